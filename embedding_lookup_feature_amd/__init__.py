@@ -35,3 +35,16 @@ from .embcore import (  # noqa: F401
     relu_bwd,
     sgd_dense,
 )
+from .tower import (  # noqa: F401
+    Dropout,
+    act_dropout_bwd,
+    act_dropout_fwd,
+    dense_bwd,
+    dense_bwd_workspace_bytes,
+    dense_fwd,
+    dense_fwd_workspace_bytes,
+    group_norm_bwd,
+    group_norm_bwd_workspace_bytes,
+    group_norm_fwd,
+    group_norm_fwd_workspace_bytes,
+)

@@ -1,0 +1,150 @@
+// act_dropout.hip -- activation, dropout from a counter-based generator and residual, forward
+// and backward, as one pass over the data.
+//
+//   y  = residual + drop(act(x)),      dx = drop(dy * act'(x))
+//
+// One thread owns eight consecutive columns of a row, which share one Philox4x32-10 call (eight
+// 16-bit numbers), so the mask costs ten rounds of two 32 x 32 -> 64 bit products per eight
+// elements and is never read or written.
+#include "tower_common.hpp"
+
+namespace el {
+namespace {
+
+struct RowsArgs {
+  const void *a, *b;  // forward: x, residual; backward: dy, x
+  void* y;
+  long lda, ldb, ldy;
+  int N, groups;      // columns, ceil(N / 8)
+  int64_t items;      // M * groups
+  DropArgs drop;
+};
+
+constexpr int kThreads = 256;
+
+// `U` groups of eight columns per thread, `kThreads` groups apart; all loads are issued before
+// the first use.
+template <class T, int ACT, bool BWD, int U>
+__global__ __launch_bounds__(kThreads) void k_act_dropout(RowsArgs p) {
+  using S = typename T::S;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * U);
+  const int64_t row0 = first / p.groups;  // uniform: one 64-bit division per workgroup
+  const uint32_t rem = static_cast<uint32_t>(first - row0 * p.groups);
+  const S* a = static_cast<const S*>(p.a);
+  const S* b = static_cast<const S*>(p.b);
+  const uint64_t offset = p.drop.threshold ? drop_offset(p.drop) : 0;
+  Raw8<T> ra[U], rb[U];
+  int64_t row[U];
+  uint32_t grp[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t local = rem + threadIdx.x + u * kThreads;
+    const uint32_t dr = local / static_cast<uint32_t>(p.groups);
+    row[u] = row0 + dr;
+    grp[u] = local - dr * p.groups;
+    if (first + threadIdx.x + u * kThreads < p.items) {
+      const int n = p.N - static_cast<int>(grp[u]) * 8;
+      ra[u] = load8_raw<T>(a + row[u] * p.lda + grp[u] * 8l, n);
+      if (b) rb[u] = load8_raw<T>(b + row[u] * p.ldb + grp[u] * 8l, n);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (first + threadIdx.x + u * kThreads >= p.items) continue;
+    const int n = p.N - static_cast<int>(grp[u]) * 8;
+    float x[8], r[8], y[8];
+    to_floats<T>(ra[u], x);
+    if (b) to_floats<T>(rb[u], r);
+    u32x4 bits = {};
+    if (p.drop.threshold) bits = philox8(grp[u], static_cast<uint32_t>(row[u]), offset, p.drop.k0, p.drop.k1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = BWD ? (ACT == EL_ACT_NONE ? x[i] : x[i] * act_df<ACT>(r[i])) : act_f<ACT>(x[i]);
+      if (p.drop.threshold) v = keep_of(bits, i, p.drop.threshold) ? v * p.drop.scale : 0.f;
+      if (!BWD && b) v += r[i];
+      y[i] = v;
+    }
+    store8<T>(static_cast<S*>(p.y) + row[u] * p.ldy + grp[u] * 8l, y, n);
+  }
+}
+
+template <class T, bool BWD>
+void launch_typed(const RowsArgs& p, uint32_t act, hipStream_t st) {
+  tower::with_act(act, [&](auto A) {
+    constexpr int ACT = decltype(A)::value;
+    const int64_t blocks = (p.items + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL((k_act_dropout<T, ACT, BWD, 1>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, p);
+  });
+}
+
+el_status launch_rows(const char* fn, RowsArgs p, int M, uint32_t act, el_dtype dtype, bool bwd, hipStream_t st) {
+  p.groups = (p.N + 7) / 8;
+  p.items = static_cast<int64_t>(M) * p.groups;
+  if (p.items > 0xffffff00ll) return tower::unsupported(fn, "M * ceil(N / 8) must be < 2^32 - 255");  // threads of one launch
+  const auto go = [&](auto t) {
+    using T = decltype(t);
+    bwd ? launch_typed<T, true>(p, act, st) : launch_typed<T, false>(p, act, st);
+  };
+  if (dtype == EL_F32) go(F32T{});
+  else if (dtype == EL_F16) go(F16T{});
+  else go(BF16T{});
+  return check_launch(fn);
+}
+
+el_status check_common(const char* fn, int32_t M, int32_t N, uint32_t act, el_dtype dtype) {
+  if (M < 0) return tower::bad(fn, "M must be >= 0");
+  if (N < 1) return tower::bad(fn, "N must be >= 1");
+  if (!dtype_valid(dtype)) return tower::bad(fn, "unknown dtype");
+  return tower::check_act(fn, act);
+}
+
+}  // namespace
+}  // namespace el
+
+using namespace el;
+
+#define EL_TRY(x)                    \
+  do {                               \
+    const el_status st_ = (x);       \
+    if (st_ != EL_OK) return st_;    \
+  } while (0)
+
+extern "C" {
+
+el_status el_act_dropout_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t M,
+                             int32_t N, uint32_t act, const el_dropout* drop, void* y, int64_t ldy,
+                             el_dtype dtype, hipStream_t stream) {
+  const char* fn = "el_act_dropout_fwd";
+  return tower::guarded(fn, [&]() -> el_status {
+    EL_TRY(check_common(fn, M, N, act, dtype));
+    RowsArgs p{};
+    EL_TRY(tower::drop_args(fn, drop, &p.drop));
+    const size_t e = dtype_size(dtype);
+    EL_TRY(tower::check_rows(fn, "x", x, ldx, N, M > 0, e));
+    EL_TRY(tower::check_rows(fn, "residual", residual, ldr, N, false, e));
+    EL_TRY(tower::check_rows(fn, "y", y, ldy, N, M > 0, e));
+    if (M == 0) return EL_OK;
+    p.a = x, p.b = residual, p.y = y, p.lda = ldx, p.ldb = ldr, p.ldy = ldy, p.N = N;
+    return launch_rows(fn, p, M, act, dtype, false, stream);
+  });
+}
+
+el_status el_act_dropout_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, int32_t M, int32_t N,
+                             uint32_t act, const el_dropout* drop, void* dx, int64_t lddx, el_dtype dtype,
+                             hipStream_t stream) {
+  const char* fn = "el_act_dropout_bwd";
+  return tower::guarded(fn, [&]() -> el_status {
+    EL_TRY(check_common(fn, M, N, act, dtype));
+    RowsArgs p{};
+    EL_TRY(tower::drop_args(fn, drop, &p.drop));
+    const size_t e = dtype_size(dtype);
+    EL_TRY(tower::check_rows(fn, "dy", dy, lddy, N, M > 0, e));
+    EL_TRY(tower::check_rows(fn, "x", x, ldx, N, M > 0 && act != EL_ACT_NONE, e));
+    EL_TRY(tower::check_rows(fn, "dx", dx, lddx, N, M > 0, e));
+    if (M == 0) return EL_OK;
+    p.a = dy, p.b = act == EL_ACT_NONE ? nullptr : x, p.y = dx, p.lda = lddy, p.ldb = ldx, p.ldy = lddx, p.N = N;
+    return launch_rows(fn, p, M, act, dtype, true, stream);
+  });
+}
+
+}  // extern "C"

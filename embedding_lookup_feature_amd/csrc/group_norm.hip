@@ -1,0 +1,789 @@
+// group_norm.hip -- channels-last group norm with an activation, forward and backward.
+//
+// Per sample b and group g, over the n = len Cg values of the group's Cg channels at the
+// sample's first len positions:
+//   mean = sum x / n,  var = sum (x - mean)^2 / n,  rstd = 1 / sqrt(var + eps)
+//   y    = act(u),  u = gamma xh + beta,  xh = (x - mean) rstd
+// and backward, with du = dy act'(u), dh = du gamma:
+//   dx     = rstd (dh - avg(dh) - xh avg(dh xh))
+//   dgamma = sum_{b,s} du xh,  dbeta = sum_{b,s} du
+//
+// Bound by memory: x in, y out (forward); x, dy in, dx out (backward).  Two forms:
+//   resident  a sample's values stay in the registers of one workgroup's threads between the
+//             statistics and their use, so everything is read once;
+//   streamed  samples too large for that are cut into chunks of positions: one kernel leaves
+//             per-channel statistics of each chunk, one joins them per group, one applies them
+//             (x, and dy, are read twice).
+// A thread owns eight consecutive channels of some positions, so every access is a 16-byte
+// vector whatever the group width; sums are kept per channel and joined into groups afterwards
+// where a vector crosses groups.
+#include <algorithm>
+
+#include "tower_common.hpp"
+
+namespace el {
+namespace {
+
+constexpr int kResident = 512;  // most threads of a resident workgroup
+
+struct GnArgs {
+  const void *x, *dy;
+  void* out;  // y or dx
+  long ldx, lddy, ldo;
+  int B, S, C, G, Cg, CV;  // CV: vectors of eight channels per position
+  const int32_t* lengths;
+  const float *gamma, *beta;
+  float eps;
+  uint32_t act;
+  float *mean, *rstd;  // written by the forward, read by the backward
+  float2* part;        // workspace, see the kernels
+  float2* gsum;
+  // resident
+  int TR, team, spw, E, E1;
+  int blocks;
+  // streamed
+  int chunks, per_chunk, colblocks, TC;
+};
+
+__device__ inline int sample_len(const GnArgs& a, int b) {
+  return a.lengths ? min(max(a.lengths[b], 0), a.S) : a.S;
+}
+
+// ---------------------------------------------------------------------------------------
+// Resident form.
+// ---------------------------------------------------------------------------------------
+// Sums over the group, for NVAL values at once.  In: the thread's sums p[v][i] for its
+// channels (i < 8), or p[v][0] for all eight where a vector lies inside one group (VECG).
+// Out: p[v][i] = the sum over the group of channel i (VECG: p[v][0]).  Every thread of the
+// workgroup calls it; the order of additions is fixed.  LDS: `red` holds NVAL arrays of one
+// entry per thread (VECG) or eight, then `mid` NVAL x spw x G x E1, then `tot` NVAL x spw x G.
+template <bool VECG, int NVAL>
+__device__ inline void group_sums(const GnArgs& a, float* lds, int tid, int team_id, int r, int cv, bool on,
+                                  float (&p)[NVAL][8]) {
+  const int nt = blockDim.x;
+  const int per_thread = VECG ? 1 : 8;
+  const int cols = VECG ? a.CV : a.CV * 8;        // entries of one thread row of a team
+  const int gc = VECG ? a.Cg / 8 : a.Cg;          // of them in one group
+  const int red_n = nt * per_thread, items = a.spw * a.G;
+  float* red = lds;
+  float* mid = lds + NVAL * red_n;
+  float* tot = mid + NVAL * items * a.E1;
+  __syncthreads();
+  if (on) {
+#pragma unroll
+    for (int v = 0; v < NVAL; ++v)
+#pragma unroll
+      for (int i = 0; i < (VECG ? 1 : 8); ++i) red[v * red_n + (team_id * a.team + r) * per_thread + i] = p[v][i];
+  }
+  __syncthreads();
+  for (int j = tid; j < items * a.E1; j += nt) {
+    const int it = j / a.E1, e0 = j - it * a.E1;
+    const int smp = it / a.G, g = it - smp * a.G;
+    float s[NVAL] = {};
+    for (int e = e0; e < a.E; e += a.E1) {
+      const int row = e / gc;
+      const int at = smp * a.team * per_thread + row * cols + g * gc + (e - row * gc);
+#pragma unroll
+      for (int v = 0; v < NVAL; ++v) s[v] += red[v * red_n + at];
+    }
+#pragma unroll
+    for (int v = 0; v < NVAL; ++v) mid[v * items * a.E1 + j] = s[v];
+  }
+  __syncthreads();
+  for (int j = tid; j < items; j += nt) {
+#pragma unroll
+    for (int v = 0; v < NVAL; ++v) {
+      float s = 0.f;
+      for (int e = 0; e < a.E1; ++e) s += mid[(v * items + j) * a.E1 + e];
+      tot[v * items + j] = s;
+    }
+  }
+  __syncthreads();
+  if (on) {
+#pragma unroll
+    for (int v = 0; v < NVAL; ++v)
+#pragma unroll
+      for (int i = 0; i < (VECG ? 1 : 8); ++i) {
+        const int c = min(cv * 8 + i, a.C - 1);
+        p[v][i] = tot[v * items + team_id * a.G + c / a.Cg];
+      }
+  }
+}
+
+template <bool VECG>
+__device__ inline float of_channel(const float (&p)[8], int i) { return p[VECG ? 0 : i]; }
+
+__device__ inline void load_params(const GnArgs& a, int cv, float (&gamma)[8], float (&beta)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = cv * 8 + i;
+    gamma[i] = a.gamma && c < a.C ? a.gamma[c] : 1.f;
+    beta[i] = a.beta && c < a.C ? a.beta[c] : 0.f;
+  }
+}
+
+template <class T, int NV, bool VECG>
+__global__ __launch_bounds__(kResident) void k_gn_fwd_resident(GnArgs a) {
+  extern __shared__ float lds[];
+  using St = typename T::S;
+  const int tid = threadIdx.x, team_id = tid / a.team, r = tid - team_id * a.team;
+  const int tr = r / a.CV, cv = r - tr * a.CV;
+  const long b = static_cast<long>(blockIdx.x) * a.spw + team_id;
+  const bool on = team_id < a.spw && b < a.B;
+  const int n = min(8, a.C - cv * 8);
+  const int len = on ? sample_len(a, static_cast<int>(b)) : 0;
+  const St* x = static_cast<const St*>(a.x) + (on ? b * a.S * a.ldx : 0) + cv * 8;
+  Raw8<T> raw[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int s = tr + i * a.TR;
+    if (s < len) raw[i] = load8_raw<T>(x + s * a.ldx, n);
+  }
+  const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
+  float p[1][8] = {};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (tr + i * a.TR < len) {
+      float f[8];
+      to_floats<T>(raw[i], f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) p[0][VECG ? 0 : q] += f[q];
+    }
+  group_sums<VECG, 1>(a, lds, tid, team_id, r, cv, on, p);
+  float mean[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) mean[q] = of_channel<VECG>(p[0], q) * inv_n;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) p[0][q] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (tr + i * a.TR < len) {
+      float f[8];
+      to_floats<T>(raw[i], f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (VECG || q < n) p[0][VECG ? 0 : q] += (f[q] - mean[q]) * (f[q] - mean[q]);
+    }
+  group_sums<VECG, 1>(a, lds, tid, team_id, r, cv, on, p);
+  if (!on) return;
+  float rstd[8], gamma[8], beta[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) rstd[q] = 1.f / sqrtf(of_channel<VECG>(p[0], q) * inv_n + a.eps);
+  load_params(a, cv, gamma, beta);
+  if (tr == 0)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int c = cv * 8 + q;
+      if (c < a.C && c % a.Cg == 0) {
+        a.mean[b * a.G + c / a.Cg] = mean[q];
+        a.rstd[b * a.G + c / a.Cg] = rstd[q];
+      }
+    }
+  St* y = static_cast<St*>(a.out) + b * a.S * a.ldo + cv * 8;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int s = tr + i * a.TR;
+    if (s >= a.S) continue;
+    float f[8] = {};
+    if (s < len) {
+      to_floats<T>(raw[i], f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] = (f[q] - mean[q]) * rstd[q] * gamma[q] + beta[q];
+      act8(a.act, f);
+    }
+    store8<T>(y + s * a.ldo, f, n);
+  }
+}
+
+// Every workgroup takes samples blockIdx.x * spw + team, then gridDim.x * spw further on, and
+// keeps dgamma / dbeta of its samples in registers; part[workgroup][c] = (dbeta, dgamma).
+template <class T, int NV, bool VECG>
+__global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
+  extern __shared__ float lds[];
+  using St = typename T::S;
+  const int tid = threadIdx.x, team_id = tid / a.team, r = tid - team_id * a.team;
+  const int tr = r / a.CV, cv = r - tr * a.CV;
+  const int n = min(8, a.C - cv * 8);
+  float gamma[8], beta[8], sb[8] = {}, sg[8] = {};
+  load_params(a, cv, gamma, beta);
+  for (long b0 = static_cast<long>(blockIdx.x) * a.spw; b0 < a.B; b0 += static_cast<long>(gridDim.x) * a.spw) {
+    const long b = b0 + team_id;
+    const bool on = team_id < a.spw && b < a.B;
+    const int len = on ? sample_len(a, static_cast<int>(b)) : 0;
+    const St* x = static_cast<const St*>(a.x) + (on ? b * a.S * a.ldx : 0) + cv * 8;
+    const St* dy = static_cast<const St*>(a.dy) + (on ? b * a.S * a.lddy : 0) + cv * 8;
+    Raw8<T> rx[NV], rd[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int s = tr + i * a.TR;
+      if (s < len) {
+        rx[i] = load8_raw<T>(x + s * a.ldx, n);
+        rd[i] = load8_raw<T>(dy + s * a.lddy, n);
+      }
+    }
+    float mean[8], rstd[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const long at = on ? b * a.G + min(cv * 8 + q, a.C - 1) / a.Cg : 0;
+      mean[q] = a.mean[at];
+      rstd[q] = a.rstd[at];
+    }
+    const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
+    float p[2][8] = {};
+    float xh[NV][8], dh[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (tr + i * a.TR < len) {
+        to_floats<T>(rx[i], xh[i]);
+        to_floats<T>(rd[i], dh[i]);
+        float u[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          xh[i][q] = (xh[i][q] - mean[q]) * rstd[q];
+          u[q] = xh[i][q] * gamma[q] + beta[q];
+        }
+        act8_grad(a.act, u, dh[i]);  // du; zero past the last channel, where dy was read as zero
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          sb[q] += dh[i][q];
+          sg[q] += dh[i][q] * xh[i][q];
+          dh[i][q] *= gamma[q];
+          p[0][VECG ? 0 : q] += dh[i][q];
+          p[1][VECG ? 0 : q] += dh[i][q] * xh[i][q];
+        }
+      }
+    group_sums<VECG, 2>(a, lds, tid, team_id, r, cv, on, p);
+    if (on) {
+      St* dx = static_cast<St*>(a.out) + b * a.S * a.ldo + cv * 8;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int s = tr + i * a.TR;
+        if (s >= a.S) continue;
+        float f[8] = {};
+        if (s < len) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            f[q] = rstd[q] * (dh[i][q] - of_channel<VECG>(p[0], q) * inv_n - xh[i][q] * (of_channel<VECG>(p[1], q) * inv_n));
+        }
+        store8<T>(dx + s * a.ldo, f, n);
+      }
+    }
+  }
+  if (!a.part) return;
+  // the threads of one channel vector: all teams, all thread rows, in that order
+  float2* red = reinterpret_cast<float2*>(lds);
+  const int rows = a.spw * a.TR;
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    __syncthreads();
+    float vb = 0.f, vg = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k == q) vb = sb[k], vg = sg[k];
+    if (team_id < a.spw) red[(team_id * a.TR + tr) * a.CV + cv] = make_float2(vb, vg);
+    __syncthreads();
+    if (tid < a.CV && tid * 8 + q < a.C) {
+      float2 s = make_float2(0.f, 0.f);
+      for (int k = 0; k < rows; ++k) {
+        const float2 v = red[k * a.CV + tid];
+        s.x += v.x;
+        s.y += v.y;
+      }
+      a.part[static_cast<long>(blockIdx.x) * a.C + tid * 8 + q] = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Streamed form.
+// ---------------------------------------------------------------------------------------
+constexpr int kStream = 256;
+
+struct StreamPos {
+  int b, chunk, cv, tr, TR, s0, s1, n;
+  bool on;
+};
+__device__ inline StreamPos stream_pos(const GnArgs& a) {
+  StreamPos q;
+  long id = blockIdx.x;
+  const int cb = static_cast<int>(id % a.colblocks);
+  id /= a.colblocks;
+  q.chunk = static_cast<int>(id % a.chunks);
+  q.b = static_cast<int>(id / a.chunks);
+  q.TR = kStream / a.TC;
+  q.tr = threadIdx.x / a.TC;
+  q.cv = cb * a.TC + threadIdx.x - q.tr * a.TC;
+  q.on = q.tr < q.TR && q.cv < a.CV;
+  q.s0 = q.chunk * a.per_chunk;
+  q.s1 = min(a.S, q.s0 + a.per_chunk);
+  q.n = min(8, a.C - q.cv * 8);
+  return q;
+}
+
+// part[b][chunk][c] = (mean, sum of squares about it) of channel c over the chunk's valid
+// positions.  A thread sums differences from its first value; threads are joined by the
+// pairwise update of Chan, Golub and LeVeque (1979).
+template <class T>
+__global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
+  __shared__ float2 red[kStream * 8];
+  using St = typename T::S;
+  const StreamPos q = stream_pos(a);
+  const int end = min(q.s1, sample_len(a, q.b));
+  if (q.on) {
+    const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
+    float k[8] = {}, s1[8] = {}, s2[8] = {};
+    int cnt = 0;
+    for (int s = q.s0 + q.tr; s < end; s += q.TR) {
+      float f[8];
+      to_floats<T>(load8_raw<T>(x + s * a.ldx, q.n), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (cnt == 0) k[i] = f[i];
+        const float d = f[i] - k[i];
+        s1[i] += d;
+        s2[i] += d * d;
+      }
+      ++cnt;
+    }
+    const float inv = cnt ? 1.f / cnt : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = s1[i] * inv;
+      red[(q.tr * a.TC + q.cv % a.TC) * 8 + i] = make_float2(k[i] + d, fmaxf(s2[i] - s1[i] * d, 0.f));
+    }
+  }
+  __syncthreads();
+  const int cb0 = (q.cv / a.TC) * a.TC;  // first vector of this column block
+  const int width = min(a.TC, a.CV - cb0) * 8;
+  const int span = max(0, end - q.s0);
+  for (int j = threadIdx.x; j < width; j += kStream) {
+    const int c = cb0 * 8 + j;
+    if (c >= a.C) continue;
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    for (int t = 0; t < q.TR && t < span; ++t) {
+      const float2 v = red[t * a.TC * 8 + j];
+      const float nb = static_cast<float>((span - t + q.TR - 1) / q.TR);
+      const float d = v.x - mean, tot = n + nb;
+      mean += d * (nb / tot);
+      m2 += v.y + d * d * (n * nb / tot);
+      n = tot;
+    }
+    a.part[(static_cast<long>(q.b) * a.chunks + q.chunk) * a.C + c] = make_float2(mean, m2);
+  }
+}
+
+// One wavefront per (sample, group): mean and rstd from the chunks' channel statistics.
+__global__ __launch_bounds__(64) void k_gn_join(GnArgs a) {
+  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G, lane = threadIdx.x;
+  const int len = sample_len(a, b);
+  const int full = a.chunks * a.Cg;
+  const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
+  const float2* part = a.part + static_cast<long>(b) * a.chunks * a.C + g * a.Cg;
+  float s = 0.f;
+  for (int j = lane; j < full; j += 64) {
+    const int ch = j / a.Cg;
+    const int cnt = min(max(len - ch * a.per_chunk, 0), a.per_chunk);
+    if (cnt > 0) s += cnt * inv_n * part[static_cast<long>(ch) * a.C + j - ch * a.Cg].x;
+  }
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  const float mean = s;
+  float v = 0.f;
+  for (int j = lane; j < full; j += 64) {
+    const int ch = j / a.Cg;
+    const int cnt = min(max(len - ch * a.per_chunk, 0), a.per_chunk);
+    if (cnt > 0) {
+      const float2 q = part[static_cast<long>(ch) * a.C + j - ch * a.Cg];
+      v += q.y + cnt * (q.x - mean) * (q.x - mean);
+    }
+  }
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if (lane == 0) {
+    a.mean[blockIdx.x] = mean;
+    a.rstd[blockIdx.x] = 1.f / sqrtf(v * inv_n + a.eps);
+  }
+}
+
+__device__ inline void load_stats(const GnArgs& a, const StreamPos& q, float (&mean)[8], float (&rstd)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const long at = static_cast<long>(q.b) * a.G + min(q.cv * 8 + i, a.C - 1) / a.Cg;
+    mean[i] = a.mean[at];
+    rstd[i] = a.rstd[at];
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kStream) void k_gn_apply(GnArgs a) {
+  using St = typename T::S;
+  const StreamPos q = stream_pos(a);
+  if (!q.on) return;
+  const int len = sample_len(a, q.b);
+  const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
+  St* y = static_cast<St*>(a.out) + static_cast<long>(q.b) * a.S * a.ldo + q.cv * 8;
+  float gamma[8], beta[8], mean[8], rstd[8];
+  load_params(a, q.cv, gamma, beta);
+  load_stats(a, q, mean, rstd);
+  for (int s = q.s0 + q.tr; s < q.s1; s += q.TR) {
+    float f[8] = {};
+    if (s < len) {
+      to_floats<T>(load8_raw<T>(x + s * a.ldx, q.n), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = (f[i] - mean[i]) * rstd[i] * gamma[i] + beta[i];
+      act8(a.act, f);
+    }
+    store8<T>(y + s * a.ldo, f, q.n);
+  }
+}
+
+// part[b][chunk][c] = (sum du, sum du xh) of channel c over the chunk's valid positions.
+template <class T>
+__global__ __launch_bounds__(kStream) void k_gn_bwd_stats(GnArgs a) {
+  __shared__ float2 red[kStream * 8];
+  using St = typename T::S;
+  const StreamPos q = stream_pos(a);
+  const int end = min(q.s1, sample_len(a, q.b));
+  if (q.on) {
+    const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
+    const St* dy = static_cast<const St*>(a.dy) + static_cast<long>(q.b) * a.S * a.lddy + q.cv * 8;
+    float gamma[8], beta[8], mean[8], rstd[8], s1[8] = {}, s2[8] = {};
+    load_params(a, q.cv, gamma, beta);
+    load_stats(a, q, mean, rstd);
+    for (int s = q.s0 + q.tr; s < end; s += q.TR) {
+      float f[8], d[8];
+      to_floats<T>(load8_raw<T>(x + s * a.ldx, q.n), f);
+      to_floats<T>(load8_raw<T>(dy + s * a.lddy, q.n), d);
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] = (f[i] - mean[i]) * rstd[i];
+        u[i] = f[i] * gamma[i] + beta[i];
+      }
+      act8_grad(a.act, u, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s1[i] += d[i];
+        s2[i] += d[i] * f[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[(q.tr * a.TC + q.cv % a.TC) * 8 + i] = make_float2(s1[i], s2[i]);
+  }
+  __syncthreads();
+  const int cb0 = (q.cv / a.TC) * a.TC;
+  const int width = min(a.TC, a.CV - cb0) * 8;
+  for (int j = threadIdx.x; j < width; j += kStream) {
+    const int c = cb0 * 8 + j;
+    if (c >= a.C) continue;
+    float2 s = make_float2(0.f, 0.f);
+    for (int t = 0; t < q.TR; ++t) {
+      const float2 v = red[t * a.TC * 8 + j];
+      s.x += v.x;
+      s.y += v.y;
+    }
+    a.part[(static_cast<long>(q.b) * a.chunks + q.chunk) * a.C + c] = s;
+  }
+}
+
+// One wavefront per (sample, group): (avg dh, avg dh xh) from the chunks' channel sums.
+__global__ __launch_bounds__(64) void k_gn_bwd_join(GnArgs a) {
+  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G, lane = threadIdx.x;
+  const int len = sample_len(a, b), full = a.chunks * a.Cg;
+  const float2* part = a.part + static_cast<long>(b) * a.chunks * a.C + g * a.Cg;
+  float s1 = 0.f, s2 = 0.f;
+  for (int j = lane; j < full; j += 64) {
+    const int ch = j / a.Cg, c = j - ch * a.Cg;
+    const float2 v = part[static_cast<long>(ch) * a.C + c];
+    const float gm = a.gamma ? a.gamma[g * a.Cg + c] : 1.f;
+    s1 += gm * v.x;
+    s2 += gm * v.y;
+  }
+  for (int o = 32; o > 0; o >>= 1) s1 += __shfl_xor(s1, o), s2 += __shfl_xor(s2, o);
+  const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
+  if (lane == 0) a.gsum[blockIdx.x] = make_float2(s1 * inv_n, s2 * inv_n);
+}
+
+template <class T>
+__global__ __launch_bounds__(kStream) void k_gn_bwd_apply(GnArgs a) {
+  using St = typename T::S;
+  const StreamPos q = stream_pos(a);
+  if (!q.on) return;
+  const int len = sample_len(a, q.b);
+  const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
+  const St* dy = static_cast<const St*>(a.dy) + static_cast<long>(q.b) * a.S * a.lddy + q.cv * 8;
+  St* dx = static_cast<St*>(a.out) + static_cast<long>(q.b) * a.S * a.ldo + q.cv * 8;
+  float gamma[8], beta[8], mean[8], rstd[8], m1[8], m2[8];
+  load_params(a, q.cv, gamma, beta);
+  load_stats(a, q, mean, rstd);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 v = a.gsum[static_cast<long>(q.b) * a.G + min(q.cv * 8 + i, a.C - 1) / a.Cg];
+    m1[i] = v.x;
+    m2[i] = v.y;
+  }
+  for (int s = q.s0 + q.tr; s < q.s1; s += q.TR) {
+    float f[8] = {};
+    if (s < len) {
+      float d[8];
+      to_floats<T>(load8_raw<T>(x + s * a.ldx, q.n), f);
+      to_floats<T>(load8_raw<T>(dy + s * a.lddy, q.n), d);
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] = (f[i] - mean[i]) * rstd[i];
+        u[i] = f[i] * gamma[i] + beta[i];
+      }
+      act8_grad(a.act, u, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = rstd[i] * (d[i] * gamma[i] - m1[i] - f[i] * m2[i]);
+    }
+    store8<T>(dx + s * a.ldo, f, q.n);
+  }
+}
+
+// dbeta[c], dgamma[c] = the sums over `rows` of part[row][c]: 16 channels per workgroup, 64
+// threads per channel whose sums are then added in order.
+__global__ __launch_bounds__(1024) void k_gn_params(const float2* part, long rows, int C, float* dgamma, float* dbeta) {
+  __shared__ float2 red[64][16];
+  const int c = blockIdx.x * 16 + (threadIdx.x & 15), t = threadIdx.x >> 4;
+  float2 s = make_float2(0.f, 0.f);
+  if (c < C)
+    for (long r = t; r < rows; r += 64) {
+      const float2 v = part[r * C + c];
+      s.x += v.x;
+      s.y += v.y;
+    }
+  red[t][threadIdx.x & 15] = s;
+  __syncthreads();
+  if (t == 0 && c < C) {
+    for (int k = 1; k < 64; ++k) s.x += red[k][threadIdx.x].x, s.y += red[k][threadIdx.x].y;
+    if (dbeta) dbeta[c] = s.x;
+    if (dgamma) dgamma[c] = s.y;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Plans and launches.
+// ---------------------------------------------------------------------------------------
+struct GnPlan {
+  bool resident = false;
+  int NV = 1, TR = 0, team = 0, spw = 1, threads = 0, blocks_fwd = 0, blocks_bwd = 0;
+  int chunks = 1, per_chunk = 1, colblocks = 1, TC = 1;
+  size_t fwd_bytes = 0, bwd_bytes = 0;
+};
+
+GnPlan plan_gn(int B, int S, int C, int G) {
+  GnPlan p;
+  const long CV = (C + 7l) / 8;
+  const auto round256 = [](size_t n) { return (n + 255) / 256 * 256; };
+  // resident: the smallest number of vectors per thread (1, 2, 4) that leaves a sample to at
+  // most 256 threads, or, for larger samples, to kResident
+  for (int limit : {256, kResident}) {
+    for (int nv = 1; nv <= 4 && !p.resident; nv *= 2) {
+      const long tr = (S + nv - 1l) / nv;
+      if (tr * CV <= limit) {
+        p.resident = true;
+        p.NV = nv;
+        p.TR = static_cast<int>(tr);
+        p.team = static_cast<int>(tr * CV);
+        p.spw = limit == 256 ? std::max(1, 256 / p.team) : 1;
+        p.threads = limit == 256 ? 256 : (p.team + 63) / 64 * 64;
+      }
+    }
+  }
+  if (p.resident) {
+    const long wgs = (B + p.spw - 1l) / p.spw;
+    p.blocks_fwd = static_cast<int>(wgs);
+    p.blocks_bwd = static_cast<int>(std::min<long>(wgs, std::max<long>(256, std::min<long>(2048, (1l << 20) / C))));
+    p.bwd_bytes = round256(static_cast<size_t>(p.blocks_bwd) * C * sizeof(float2));
+    return p;
+  }
+  p.TC = static_cast<int>(std::min<long>(CV, kStream));
+  p.colblocks = static_cast<int>((CV + p.TC - 1) / p.TC);
+  const long rows = kStream / p.TC;
+  const long want = std::max<long>(1, 2048 / (static_cast<long>(B) * p.colblocks));
+  const long most = std::max<long>(1, S / (rows * 8));  // at least eight positions per thread
+  p.chunks = static_cast<int>(std::min(want, most));
+  p.per_chunk = static_cast<int>((S + static_cast<long>(p.chunks) - 1) / p.chunks);
+  p.chunks = static_cast<int>((S + static_cast<long>(p.per_chunk) - 1) / p.per_chunk);
+  p.fwd_bytes = round256(static_cast<size_t>(B) * p.chunks * C * sizeof(float2));
+  p.bwd_bytes = p.fwd_bytes + round256(static_cast<size_t>(B) * G * sizeof(float2));
+  return p;
+}
+
+void fill(GnArgs& a, const GnPlan& p) {
+  a.CV = (a.C + 7) / 8;
+  a.Cg = a.C / a.G;
+  a.TR = p.TR, a.team = p.team, a.spw = p.spw;
+  a.chunks = p.chunks, a.per_chunk = p.per_chunk, a.colblocks = p.colblocks, a.TC = p.TC;
+  if (p.resident) {
+    a.E = p.TR * (a.Cg % 8 == 0 ? a.Cg / 8 : a.Cg);
+    a.E1 = (a.E + 15) / 16;
+  }
+}
+
+size_t lds_bytes(const GnArgs& a, const GnPlan& p, int nval) {
+  const size_t per = a.Cg % 8 == 0 ? 1 : 8;
+  const size_t items = static_cast<size_t>(p.spw) * a.G;
+  return sizeof(float) * nval * (p.threads * per + items * a.E1 + items);
+}
+
+template <class T, bool BWD, bool VECG>
+void launch_resident(const GnArgs& a, const GnPlan& p, hipStream_t st) {
+  const size_t lds = std::max(lds_bytes(a, p, BWD ? 2 : 1), BWD ? p.threads * sizeof(float2) : 0);
+  const dim3 grid(BWD ? p.blocks_bwd : p.blocks_fwd), block(p.threads);
+#define GN_CASE(NV)                                                                                        \
+  case NV:                                                                                                 \
+    if constexpr (BWD) hipLaunchKernelGGL((k_gn_bwd_resident<T, NV, VECG>), grid, block, lds, st, a); \
+    else hipLaunchKernelGGL((k_gn_fwd_resident<T, NV, VECG>), grid, block, lds, st, a);               \
+    break;
+  switch (p.NV) { GN_CASE(1) GN_CASE(2) GN_CASE(4) }
+#undef GN_CASE
+}
+
+template <class T, bool BWD>
+void launch_gn(const GnArgs& a, const GnPlan& p, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(static_cast<long>(a.B) * p.chunks * p.colblocks)), block(kStream);
+  const dim3 groups(static_cast<unsigned>(static_cast<long>(a.B) * a.G));
+  if (p.resident) {
+    a.Cg % 8 == 0 ? launch_resident<T, BWD, true>(a, p, st) : launch_resident<T, BWD, false>(a, p, st);
+  } else if constexpr (BWD) {
+    hipLaunchKernelGGL((k_gn_bwd_stats<T>), grid, block, 0, st, a);
+    hipLaunchKernelGGL(k_gn_bwd_join, groups, dim3(64), 0, st, a);
+    hipLaunchKernelGGL((k_gn_bwd_apply<T>), grid, block, 0, st, a);
+  } else {
+    hipLaunchKernelGGL((k_gn_stats<T>), grid, block, 0, st, a);
+    hipLaunchKernelGGL(k_gn_join, groups, dim3(64), 0, st, a);
+    hipLaunchKernelGGL((k_gn_apply<T>), grid, block, 0, st, a);
+  }
+}
+
+template <bool BWD>
+el_status run_gn(const char* fn, const GnArgs& a, const GnPlan& p, el_dtype dtype, hipStream_t st) {
+  if (dtype == EL_F32) launch_gn<F32T, BWD>(a, p, st);
+  else if (dtype == EL_F16) launch_gn<F16T, BWD>(a, p, st);
+  else launch_gn<BF16T, BWD>(a, p, st);
+  return check_launch(fn);
+}
+
+bool gn_sizes_ok(int32_t B, int32_t S, int32_t C, int32_t G) {
+  return B >= 1 && S >= 1 && C >= 1 && G >= 1 && C % G == 0 && C <= (1 << 24) &&
+         static_cast<int64_t>(B) * S < (int64_t{1} << 40) && static_cast<int64_t>(B) * G < (int64_t{1} << 25);
+}
+
+el_status check_gn(const char* fn, const void* x, int64_t ldx, int32_t B, int32_t S, int32_t C, int32_t G,
+                   const int32_t* lengths, const float* gamma, const float* beta, const float* mean, const float* rstd,
+                   uint32_t act, el_dtype dtype) {
+  if (B < 0) return tower::bad(fn, "B must be >= 0");
+  if (S < 0) return tower::bad(fn, "S must be >= 0");
+  if (C < 1) return tower::bad(fn, "C must be >= 1");
+  if (G < 1 || C % G != 0) return tower::bad(fn, "G must be >= 1 and divide C");
+  if (!dtype_valid(dtype)) return tower::bad(fn, "unknown dtype");
+  if (B > 0 && S > 0 && !gn_sizes_ok(B, S, C, G))
+    return tower::unsupported(fn, "C must be <= 2^24, B * S < 2^40 and B * G < 2^25");
+  const el_status s = tower::check_act(fn, act);
+  if (s != EL_OK) return s;
+  if (!tower::al(lengths, 4) || !tower::al(gamma, 4) || !tower::al(beta, 4))
+    return tower::bad(fn, "lengths, gamma and beta must be aligned to their elements");
+  if (B > 0 && (!mean || !rstd)) return tower::bad(fn, "mean or rstd is null");
+  if (!tower::al(mean, 4) || !tower::al(rstd, 4)) return tower::bad(fn, "mean and rstd must be aligned to their elements");
+  return tower::check_rows(fn, "x", x, ldx, C, B > 0 && S > 0, dtype_size(dtype));
+}
+
+// No positions at all: mean 0, rstd 1 / sqrt(eps); zero parameter gradients.
+__global__ __launch_bounds__(256) void k_gn_empty(float* mean, float* rstd, long n, float r, float* a, float* b, long c) {
+  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) mean[i] = 0.f, rstd[i] = r;
+  if (i < c) {
+    if (a) a[i] = 0.f;
+    if (b) b[i] = 0.f;
+  }
+}
+
+}  // namespace
+}  // namespace el
+
+using namespace el;
+
+#define EL_TRY(x)                    \
+  do {                               \
+    const el_status st_ = (x);       \
+    if (st_ != EL_OK) return st_;    \
+  } while (0)
+
+extern "C" {
+
+size_t el_group_norm_fwd_workspace_bytes(int32_t B, int32_t S, int32_t C, int32_t G) {
+  return gn_sizes_ok(B, S, C, G) ? plan_gn(B, S, C, G).fwd_bytes : 0;
+}
+
+size_t el_group_norm_bwd_workspace_bytes(int32_t B, int32_t S, int32_t C, int32_t G) {
+  return gn_sizes_ok(B, S, C, G) ? plan_gn(B, S, C, G).bwd_bytes : 0;
+}
+
+el_status el_group_norm_fwd(const void* x, int64_t ldx, int32_t B, int32_t S, int32_t C, int32_t G,
+                            const int32_t* lengths, const float* gamma, const float* beta, float eps, uint32_t act,
+                            void* y, int64_t ldy, float* mean, float* rstd, el_dtype dtype, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "el_group_norm_fwd";
+  return tower::guarded(fn, [&]() -> el_status {
+    EL_TRY(check_gn(fn, x, ldx, B, S, C, G, lengths, gamma, beta, mean, rstd, act, dtype));
+    if (!(eps >= 0.f) || std::isinf(eps)) return tower::bad(fn, "eps must be >= 0 and finite");
+    EL_TRY(tower::check_rows(fn, "y", y, ldy, C, B > 0 && S > 0, dtype_size(dtype)));
+    if (B == 0) return EL_OK;
+    if (S == 0) {
+      const long n = static_cast<long>(B) * G;
+      hipLaunchKernelGGL(k_gn_empty, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, mean, rstd, n,
+                         1.f / std::sqrt(eps), nullptr, nullptr, 0l);
+      return check_launch(fn);
+    }
+    const GnPlan p = plan_gn(B, S, C, G);
+    EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, p.fwd_bytes));
+    GnArgs a{};
+    a.x = x, a.ldx = ldx, a.out = y, a.ldo = ldy, a.B = B, a.S = S, a.C = C, a.G = G;
+    a.lengths = lengths, a.gamma = gamma, a.beta = beta, a.eps = eps, a.act = act, a.mean = mean, a.rstd = rstd;
+    a.part = static_cast<float2*>(workspace);
+    fill(a, p);
+    return run_gn<false>(fn, a, p, dtype, stream);
+  });
+}
+
+el_status el_group_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, int32_t B, int32_t S, int32_t C,
+                            int32_t G, const int32_t* lengths, const float* gamma, const float* beta,
+                            const float* mean, const float* rstd, uint32_t act, void* dx, int64_t lddx, float* dgamma,
+                            float* dbeta, el_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "el_group_norm_bwd";
+  return tower::guarded(fn, [&]() -> el_status {
+    EL_TRY(check_gn(fn, x, ldx, B, S, C, G, lengths, gamma, beta, mean, rstd, act, dtype));
+    EL_TRY(tower::check_rows(fn, "dy", dy, lddy, C, B > 0 && S > 0, dtype_size(dtype)));
+    EL_TRY(tower::check_rows(fn, "dx", dx, lddx, C, B > 0 && S > 0, dtype_size(dtype)));
+    if (!tower::al(dgamma, 4) || !tower::al(dbeta, 4)) return tower::bad(fn, "dgamma and dbeta must be aligned to their elements");
+    if (B == 0 || S == 0) {
+      hipLaunchKernelGGL(k_gn_empty, dim3(static_cast<unsigned>((C + 255) / 256)), dim3(256), 0, stream, nullptr, nullptr,
+                         0l, 0.f, dgamma, dbeta, static_cast<long>(C));
+      return check_launch(fn);
+    }
+    const GnPlan p = plan_gn(B, S, C, G);
+    EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, p.bwd_bytes));
+    GnArgs a{};
+    a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.out = dx, a.ldo = lddx, a.B = B, a.S = S, a.C = C, a.G = G;
+    a.lengths = lengths, a.gamma = gamma, a.beta = beta, a.act = act, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
+    fill(a, p);
+    const bool params = dgamma || dbeta;
+    if (p.resident) {
+      a.part = params ? static_cast<float2*>(workspace) : nullptr;
+    } else {
+      a.part = static_cast<float2*>(workspace);
+      a.gsum = reinterpret_cast<float2*>(static_cast<char*>(workspace) + p.fwd_bytes);
+    }
+    EL_TRY(run_gn<true>(fn, a, p, dtype, stream));
+    if (params) {
+      const long rows = p.resident ? p.blocks_bwd : static_cast<long>(B) * p.chunks;
+      hipLaunchKernelGGL(k_gn_params, dim3(static_cast<unsigned>((C + 15) / 16)), dim3(1024), 0, stream, a.part, rows, C,
+                         dgamma, dbeta);
+      return check_launch(fn);
+    }
+    return EL_OK;
+  });
+}
+
+}  // extern "C"

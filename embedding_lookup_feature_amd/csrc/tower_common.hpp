@@ -1,0 +1,291 @@
+// tower_common.hpp -- what the dense-tower operators share: activations and their
+// derivatives, the counter-based dropout mask, vectors of eight columns at any alignment, and
+// the entry points' host-side checks.
+#pragma once
+
+#include <cmath>
+#include <cstdio>
+#include <exception>
+#include <string>
+#include <type_traits>
+
+#include "el_internal.hpp"
+#include "el_mfma.hpp"
+#include "embtower.h"
+
+namespace el {
+
+// ---------------------------------------------------------------------------------------
+// Eight consecutive columns as floats.  gfx950 takes 16-byte accesses at any element
+// alignment, so one vector type serves aligned and unaligned rows; `n` < 8 (the last columns
+// of a row that is no multiple of 8 wide) goes element by element and never touches memory
+// past the row.
+// ---------------------------------------------------------------------------------------
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_f32 __attribute__((aligned(4)));
+
+// The raw bits of eight columns: one 16-byte vector for 16-bit types, two for fp32.
+template <class T>
+struct Raw8 {
+  static constexpr int W = sizeof(typename T::S) == 4 ? 2 : 1;
+  u32x4 v[W];
+};
+
+template <class T>
+__device__ inline Raw8<T> load8_raw(const typename T::S* p) {
+  Raw8<T> r;
+  if constexpr (Raw8<T>::W == 2) {
+    r.v[0] = *reinterpret_cast<const u32x4_f32*>(p);
+    r.v[1] = *reinterpret_cast<const u32x4_f32*>(p + 4);
+  } else {
+    r.v[0] = *reinterpret_cast<const u32x4_any*>(p);
+  }
+  return r;
+}
+
+// The first n (1 .. 8) of the eight, zeros after them.
+template <class T>
+__device__ inline Raw8<T> load8_raw(const typename T::S* p, int n) {
+  if (n >= 8) return load8_raw<T>(p);
+  Raw8<T> r;
+#pragma unroll
+  for (int w = 0; w < Raw8<T>::W; ++w) r.v[w] = u32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) {
+      if constexpr (Raw8<T>::W == 2)
+        r.v[i / 4][i % 4] = __float_as_uint(p[i]);
+      else
+        r.v[0][i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
+    }
+  return r;
+}
+
+template <class T>
+__device__ inline void to_floats(const Raw8<T>& r, float* f) {
+  if constexpr (Raw8<T>::W == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.v[i / 4][i % 4]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = T::to_f(static_cast<uint16_t>(r.v[0][i] & 0xffffu));
+      f[2 * i + 1] = T::to_f(static_cast<uint16_t>(r.v[0][i] >> 16));
+    }
+  }
+}
+
+template <class T>
+__device__ inline void store8(typename T::S* p, const float* f, int n) {
+  if (n >= 8) {
+    if constexpr (sizeof(typename T::S) == 4) {
+      u32x4 a, b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(f[i]), b[i] = __float_as_uint(f[4 + i]);
+      *reinterpret_cast<u32x4_f32*>(p) = a;
+      *reinterpret_cast<u32x4_f32*>(p + 4) = b;
+    } else {
+      u32x4 a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a[i] = static_cast<uint32_t>(T::from_f(f[2 * i])) | (static_cast<uint32_t>(T::from_f(f[2 * i + 1])) << 16);
+      *reinterpret_cast<u32x4_any*>(p) = a;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = T::from_f(f[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Activations: one function for the value and one for the derivative, the kind known at
+// compile time.
+// ---------------------------------------------------------------------------------------
+// Phi(u) and phi(u) sqrt(2 pi) = exp(-u^2 / 2): the normal distribution function by the
+// rational form 7.1.26 of Abramowitz and Stegun's Handbook (absolute error 1.5e-7 on erf,
+// below half an fp32 step of values near 1), which shares its exponential with the derivative
+// and costs about 20 instructions where erff takes more than twice as many.
+__device__ inline void normal_cdf(float u, float& cdf, float& ex) {
+  const float x = fabsf(u) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  ex = __expf(-x * x);
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  const float q = 0.5f * p * t * ex;  // Phi(-|u|)
+  cdf = u < 0.f ? q : 1.f - q;
+}
+
+template <int ACT>
+__device__ inline float act_f(float u) {
+  if constexpr (ACT == EL_ACT_RELU) return u > 0.f ? u : 0.f;
+  if constexpr (ACT == EL_ACT_GELU) {
+    float cdf, ex;
+    normal_cdf(u, cdf, ex);
+    return u * cdf;
+  }
+  if constexpr (ACT == EL_ACT_SILU) return u * __builtin_amdgcn_rcpf(1.f + __expf(-u));
+  return u;
+}
+
+template <int ACT>
+__device__ inline float act_df(float u) {
+  if constexpr (ACT == EL_ACT_RELU) return u > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == EL_ACT_GELU) {
+    float cdf, ex;
+    normal_cdf(u, cdf, ex);
+    return fmaf(u * ex, 0.39894228040143268f, cdf);
+  }
+  if constexpr (ACT == EL_ACT_SILU) {
+    const float s = __builtin_amdgcn_rcpf(1.f + __expf(-u));
+    return s * fmaf(u, 1.f - s, 1.f);
+  }
+  return 1.f;
+}
+
+// Eight values at once with the kind known at run time: one uniform branch per vector, for
+// kernels whose other variants would be multiplied by the number of activations.
+__device__ inline void act8(uint32_t act, float (&u)[8]) {
+  switch (act) {
+#define EL_ACT8_CASE(K)                                  \
+  case K:                                                \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) u[i] = act_f<K>(u[i]); \
+    break;
+    EL_ACT8_CASE(EL_ACT_RELU)
+    EL_ACT8_CASE(EL_ACT_GELU)
+    EL_ACT8_CASE(EL_ACT_SILU)
+#undef EL_ACT8_CASE
+  }
+}
+// d[i] *= act'(u[i])
+__device__ inline void act8_grad(uint32_t act, const float (&u)[8], float (&d)[8]) {
+  switch (act) {
+#define EL_ACT8_CASE(K)                                  \
+  case K:                                                \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) d[i] *= act_df<K>(u[i]); \
+    break;
+    EL_ACT8_CASE(EL_ACT_RELU)
+    EL_ACT8_CASE(EL_ACT_GELU)
+    EL_ACT8_CASE(EL_ACT_SILU)
+#undef EL_ACT8_CASE
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// The dropout mask (definition in embtower.h).
+// ---------------------------------------------------------------------------------------
+struct DropArgs {
+  uint32_t threshold = 0;  // T, 0 .. 65536; 0: nothing is dropped
+  float scale = 1.f;
+  uint32_t k0 = 0, k1 = 0;
+  uint64_t offset = 0;
+  const uint64_t* step = nullptr;
+};
+
+__device__ inline uint64_t drop_offset(const DropArgs& d) { return d.offset + (d.step ? d.step[0] : 0); }
+
+// The eight 16-bit numbers of columns 8 group .. 8 group + 7 of row `row`, two per word.
+__device__ inline u32x4 philox8(uint32_t group, uint32_t row, uint64_t offset, uint32_t k0, uint32_t k1) {
+  uint32_t c0 = group, c1 = row, c2 = static_cast<uint32_t>(offset), c3 = static_cast<uint32_t>(offset >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return u32x4{c0, c1, c2, c3};
+}
+
+// Number i (0 .. 7) of the eight is kept.
+__device__ inline bool keep_of(const u32x4& bits, int i, uint32_t threshold) {
+  return ((i & 1) ? bits[i >> 1] >> 16 : bits[i >> 1] & 0xffffu) >= threshold;
+}
+
+// ---------------------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------------------
+namespace tower {
+
+inline bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline el_status bad(const char* fn, const std::string& what) {
+  return set_error(EL_ERR_INVALID_ARG, std::string(fn) + ": " + what);
+}
+inline el_status unsupported(const char* fn, const std::string& what) {
+  return set_error(EL_ERR_UNSUPPORTED, std::string(fn) + ": " + what);
+}
+
+// Runs an entry point's body; no C++ exception leaves the C ABI.
+template <class F>
+el_status guarded(const char* fn, F&& body) noexcept {
+  try {
+    return body();
+  } catch (const std::exception& e) {
+    try {
+      return set_error(EL_ERR_HIP, std::string(fn) + ": " + e.what());
+    } catch (...) {
+    }
+  } catch (...) {
+  }
+  return EL_ERR_HIP;
+}
+
+// One [rows] x [cols] operand with row stride ld.
+inline el_status check_rows(const char* fn, const char* name, const void* p, int64_t ld, int64_t cols,
+                            bool needed, size_t elem) {
+  if (!p) return needed ? bad(fn, std::string(name) + " is null") : EL_OK;
+  if (!al(p, elem)) return bad(fn, std::string(name) + " must be aligned to its elements");
+  if (ld < cols) return bad(fn, std::string("the row stride of ") + name + " must be >= its columns");
+  if (ld >= (int64_t{1} << 40)) return bad(fn, std::string("the row stride of ") + name + " must be < 2^40");
+  return EL_OK;
+}
+
+inline el_status check_act(const char* fn, uint32_t act) {
+  return act <= EL_ACT_SILU ? EL_OK : bad(fn, "unknown activation");
+}
+
+// drop (or NULL) as the kernels take it.
+inline el_status drop_args(const char* fn, const el_dropout* drop, DropArgs* out) {
+  *out = DropArgs{};
+  if (!drop) return EL_OK;
+  if (!(drop->p >= 0.0 && drop->p <= 1.0)) return bad(fn, "the dropout probability must be in [0, 1]");
+  if (!al(drop->step, 8)) return bad(fn, "dropout step must be 8-byte aligned");
+  out->threshold = static_cast<uint32_t>(std::nearbyint(drop->p * 65536.0));
+  out->scale = out->threshold < 65536u ? static_cast<float>(65536.0 / (65536.0 - out->threshold)) : 0.f;
+  out->k0 = static_cast<uint32_t>(drop->seed);
+  out->k1 = static_cast<uint32_t>(drop->seed >> 32);
+  out->offset = drop->offset;
+  out->step = drop->step;
+  return EL_OK;
+}
+
+inline el_status check_workspace(const char* fn, const void* ws, size_t have, size_t need) {
+  if (need == 0) return EL_OK;
+  if (!ws || !al(ws, 256))
+    return set_error(EL_ERR_WORKSPACE, std::string(fn) + ": workspace must be non-null and 256-byte aligned");
+  if (have < need) {
+    char buf[160];
+    std::snprintf(buf, sizeof buf, "%s: workspace of %zu bytes, %zu needed", fn, have, need);
+    return set_error(EL_ERR_WORKSPACE, buf);
+  }
+  return EL_OK;
+}
+
+// Calls f with the activation as a compile-time constant.
+template <class F>
+void with_act(uint32_t act, F&& f) {
+  switch (act) {
+    case EL_ACT_RELU: f(std::integral_constant<int, EL_ACT_RELU>{}); break;
+    case EL_ACT_GELU: f(std::integral_constant<int, EL_ACT_GELU>{}); break;
+    case EL_ACT_SILU: f(std::integral_constant<int, EL_ACT_SILU>{}); break;
+    default: f(std::integral_constant<int, EL_ACT_NONE>{}); break;
+  }
+}
+
+}  // namespace tower
+}  // namespace el
