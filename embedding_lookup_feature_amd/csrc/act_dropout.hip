@@ -32,7 +32,7 @@ __global__ __launch_bounds__(kThreads) void k_act_dropout(RowsArgs p) {
   const uint32_t rem = static_cast<uint32_t>(first - row0 * p.groups);
   const S* a = static_cast<const S*>(p.a);
   const S* b = static_cast<const S*>(p.b);
-  const uint64_t offset = p.drop.threshold ? drop_offset(p.drop) : 0;
+  const uint64_t offset = p.drop.top ? drop_offset(p.drop) : 0;
   Raw8<T> ra[U], rb[U];
   int64_t row[U];
   uint32_t grp[U];
@@ -56,11 +56,11 @@ __global__ __launch_bounds__(kThreads) void k_act_dropout(RowsArgs p) {
     to_floats<T>(ra[u], x);
     if (b) to_floats<T>(rb[u], r);
     u32x4 bits = {};
-    if (p.drop.threshold) bits = philox8(grp[u], static_cast<uint32_t>(row[u]), offset, p.drop.k0, p.drop.k1);
+    if (p.drop.top) bits = philox8(grp[u], static_cast<uint32_t>(row[u]), offset, p.drop.k0, p.drop.k1);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float v = BWD ? (ACT == EL_ACT_NONE ? x[i] : x[i] * act_df<ACT>(r[i])) : act_f<ACT>(x[i]);
-      if (p.drop.threshold) v = keep_of(bits, i, p.drop.threshold) ? v * p.drop.scale : 0.f;
+      if (p.drop.top) v = keep_of(bits, i, p.drop.top) ? v * p.drop.scale : 0.f;
       if (!BWD && b) v += r[i];
       y[i] = v;
     }

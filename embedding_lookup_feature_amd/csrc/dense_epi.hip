@@ -7,7 +7,15 @@
 //
 // The three products are one kernel over operands P (output rows) and Q (output columns),
 // out[r][c] = sum_k P(r, k) Q(c, k), each operand either reduction-contiguous (element (i, k)
-// at i * ld + k) or output-contiguous (at k * ld + i).
+// at i * ld + k: x, dz and w in the first two) or output-contiguous (at k * ld + i).
+//
+// Operands travel from global memory straight into LDS (no staging registers, no LDS store
+// instructions), `ST` stages of BK reductions in a ring; a stage's slot is refilled as soon as
+// every wavefront holds its last fragments in registers.  Reduction-contiguous fragments are
+// plain 16-byte LDS reads, output-contiguous ones gfx950's transposing LDS reads, both from
+// layouts whose 16-byte units are permuted so that the reads touch every bank once.
+#include <algorithm>
+
 #include "tower_common.hpp"
 
 namespace el {
@@ -19,130 +27,504 @@ struct GemmArgs {
   const uint16_t *P, *Q;
   long ldp, ldq;
   int R, C;        // output rows, columns
-  int red;         // reduction length
-  int per_split;   // reduction per split (weight gradient)
+  int red;         // reduction length (of P's rows, zeros included)
+  int red_q;       // of Q
+  int per_split;   // reduction per split (weight gradient; a multiple of BK)
   int tiles_c;     // column tiles
   int tiles;       // tiles of one split
-  int total;       // tiles of all splits
   // forward: out = y, aux = pre (or null), add = residual (or null)
   // data gradient: out = dx, aux = dzb (or null), add = dres (or null), pre = the layer below's
-  // weight gradient: part = fp32 [split][R][C]
+  // weight gradient: part = fp32 [split][R][C], dbp = fp32 [split * tiles_c * WC][R] (or null)
   const uint16_t *add, *pre;
   uint16_t *out, *aux;
   long ldadd, ldpre, ldo, ldaux;
   const float* bias;
-  float* part;
+  float *part, *dbp;
   DropArgs drop;
+  uint32_t act;
 };
 
-// The epilogue of one output group: columns c .. c+n-1 (c a multiple of 8, n <= 8) of row r.
-template <class T, int PROD, int ACT>
-__device__ inline void epilogue8(const GemmArgs& a, uint64_t offset, int r, int c, int n, float (&v)[8]) {
-  float add[8], y[8];
-  if (a.add) to_floats<T>(load8_raw<T>(a.add + r * a.ldadd + c, n), add);
-  u32x4 bits = {};
-  if (a.drop.threshold) bits = philox8(static_cast<uint32_t>(c) >> 3, static_cast<uint32_t>(r), offset, a.drop.k0, a.drop.k1);
+// ---------------------------------------------------------------------------------------
+// Epilogue of eight columns c .. c+7 (the first n of them exist) of row r, from the product v;
+// `add` and `pre` are the eight values already loaded.  Non-temporal stores (NT) where the
+// outputs are larger than the caches.
+// ---------------------------------------------------------------------------------------
+template <class T, bool NT>
+__device__ inline void put8(uint16_t* p, const float (&f)[8], int n) {
+  if (NT && n >= 8) {
+    u32x4 a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[i] = static_cast<uint32_t>(T::from_f(f[2 * i])) | (static_cast<uint32_t>(T::from_f(f[2 * i + 1])) << 16);
+    __builtin_nontemporal_store(a, reinterpret_cast<u32x4_any*>(p));
+  } else {
+    store8<T>(p, f, n);
+  }
+}
+
+template <class T, int PROD, bool NT>
+__device__ inline void epilogue8(const GemmArgs& a, uint64_t offset, long r, int c, int n, float (&v)[8],
+                                 const float (&bias)[8], const Raw8<T>& add, const Raw8<T>& pre) {
+  float f[8];
   if constexpr (PROD == FWD) {
-    if (a.bias)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) v[i] += a.bias[c + i];
-    if (a.aux) store8<T>(a.aux + r * a.ldaux + c, v, n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[i] = act_f<ACT>(v[i]);
-      if (a.drop.threshold) y[i] = keep_of(bits, i, a.drop.threshold) ? y[i] * a.drop.scale : 0.f;
-      if (a.add) y[i] += add[i];
-    }
-    store8<T>(a.out + r * a.ldo + c, y, n);
+    for (int e = 0; e < 8; ++e) v[e] += bias[e];
+    if (a.aux) put8<T, NT>(a.aux + r * a.ldaux + c, v, n);
+    act8(a.act, v);
   } else {
-    if (a.add)
+    if (a.add) {
+      to_floats<T>(add, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += add[i];
-    store8<T>(a.out + r * a.ldo + c, v, n);
-    if (a.aux) {
-      float p[8];
-      if (ACT != EL_ACT_NONE) to_floats<T>(load8_raw<T>(a.pre + r * a.ldpre + c, n), p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = ACT == EL_ACT_NONE ? v[i] : v[i] * act_df<ACT>(p[i]);
-        if (a.drop.threshold) y[i] = keep_of(bits, i, a.drop.threshold) ? y[i] * a.drop.scale : 0.f;
-      }
-      store8<T>(a.aux + r * a.ldaux + c, y, n);
+      for (int e = 0; e < 8; ++e) v[e] += f[e];
+    }
+    put8<T, NT>(a.out + r * a.ldo + c, v, n);
+    if (!a.aux) return;
+    if (a.act != EL_ACT_NONE) {
+      to_floats<T>(pre, f);
+      act8_grad(a.act, f, v);
     }
   }
-}
-
-// Eight consecutive reduction elements of operand row i, zeros outside.
-template <bool RC>
-__device__ inline u32x4 frag(const uint16_t* p, long ld, int i, int rows, int k, int kend) {
-  u32x4 v = {};
-  if (i < rows)
+  if (a.drop.top) {
+    const u32x4 bits = philox8(static_cast<uint32_t>(c) >> 3, static_cast<uint32_t>(r), offset, a.drop.k0, a.drop.k1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k + e < kend) {
-        const long at = RC ? i * ld + (k + e) : (k + e) * ld + i;
-        v[e / 2] |= static_cast<uint32_t>(p[at]) << (16 * (e % 2));
-      }
-  return v;
-}
-
-// One 32 x 32 output tile per wavefront, fragments straight from global memory.
-template <class T, bool P_RC, bool Q_RC, int PROD, int ACT>
-__global__ __launch_bounds__(256) void k_dense_simple(GemmArgs a) {
-  __shared__ float lds[4][32][36];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, l32 = lane & 31;
-  const int tile = blockIdx.x * 4 + wave;  // the last workgroup's may lie past the end
-  const int split = tile / a.tiles, t = tile - split * a.tiles;
-  const int row0 = t / a.tiles_c * 32, col0 = t % a.tiles_c * 32;
-  const int kbeg = split * a.per_split, kend = tile < a.total ? min(a.red, kbeg + a.per_split) : kbeg;
-  f32x16 acc = {};
-  for (int k = kbeg; k < kend; k += 16) {
-    const u32x4 q = frag<Q_RC>(a.Q, a.ldq, col0 + l32, a.C, k + half * 8, kend);
-    const u32x4 p = frag<P_RC>(a.P, a.ldp, row0 + l32, a.R, k + half * 8, kend);
-    acc = mfma32<T>(q, p, acc);
+    for (int e = 0; e < 8; ++e) v[e] = keep_of(bits, e, a.drop.top) ? v[e] * a.drop.scale : 0.f;
   }
-  // register r of the accumulator: column 8 (r / 4) + 4 half + r % 4, row l32
+  if constexpr (PROD == FWD) {
+    if (a.add) {
+      to_floats<T>(add, f);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) lds[wave][l32][acc_row(r, lane)] = acc[r];
-  __syncthreads();
-  if (tile >= a.total) return;
-  if (PROD == WGRAD) {
-    for (int i = lane; i < 1024; i += 64) {
-      const int r = row0 + i / 32, c = col0 + i % 32;
-      if (r < a.R && c < a.C) a.part[(static_cast<long>(split) * a.R + r) * a.C + c] = lds[wave][i / 32][i % 32];
+      for (int e = 0; e < 8; ++e) v[e] += f[e];
+    }
+    put8<T, NT>(a.out + r * a.ldo + c, v, n);
+  } else {
+    put8<T, NT>(a.aux + r * a.ldaux + c, v, n);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Operand tiles: global memory -> LDS -> fragments.
+// ---------------------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// A buffer offset past the end of every buffer used here (their sizes are cut to less than 2^31;
+// a stage spans at most 2^30 bytes): the load reads zeros and touches no memory.
+constexpr uint32_t kOut = 0x80000000u;
+
+__device__ inline uint32_t uniform(uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); }
+
+// 64 lanes x 16 bytes from the buffer to LDS at `lds` + 16 lane.  (One wait state between the
+// write of M0 and its use.)  The load has no register result; wait_and_meet waits for it.
+__device__ inline void load_lds16(uint32_t lds, uint32_t voff, const u32x4& rsrc) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               ::"s"(lds), "v"(voff), "s"(rsrc) : "memory");
+}
+
+// At most N of this wavefront's loads to LDS are still in flight and its LDS reads are done;
+// then the same holds for every wavefront of the workgroup.
+template <int N>
+__device__ inline void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// One operand's W x BK share of the stages, loaded by NW wavefronts in pieces of 1 KiB.
+//   RC: [W rows][BK], row r's 16-byte unit c at position c ^ (r / rows per 256 bytes), so that
+//       the 32 rows of a fragment read (one unit each) spread over all banks;
+//   OC: [BK][W], row k's unit c at c ^ (4 * place of k among the 4 rows of a transposing read),
+//       so that the 64-byte pieces which such a read takes from four rows lie in four places.
+// Rows past the operand's end fall behind the buffer's size and read as zeros; vectors past the
+// reduction's end (RC) or past the last column (OC) are sent to kOut.
+template <int W, int BK, bool RC, int NW>
+struct Operand {
+  static_assert(BK == 64, "the permutations below are for rows of 64 reductions");
+  static constexpr int BYTES = W * BK * 2;
+  static constexpr int N = BYTES / 1024 / NW;  // pieces per wavefront
+  static_assert(N >= 1 && BYTES % (1024 * NW) == 0, "whole pieces");
+  uint64_t base;   // where the next stage to load begins
+  uint64_t left;   // bytes from there to the operand's end
+  uint32_t step;   // bytes per stage
+  int rem;         // reductions left
+  uint32_t voff[N];
+  int kc[N];       // RC: the reduction index of this lane's vector inside the stage
+
+  __device__ static inline int perm(int row_or_k) {
+    if constexpr (RC) return (row_or_k >> 1) & 7;
+    return W == 64 ? ((row_or_k >> 1) & 1) << 2 : (row_or_k & 3) << 2;
+  }
+  // rows i0 .. i0+W-1 of n, reductions kbeg .. kend-1
+  __device__ inline void init(const uint16_t* p, long ld, int i0, int n, int kbeg, int kend, int wave, int lane) {
+    const int rows = min(W, n - i0);
+    rem = kend - kbeg;
+    if constexpr (RC) {
+      left = static_cast<uint64_t>((rows - 1) * ld + rem) * 2;
+      base = reinterpret_cast<uint64_t>(p + i0 * ld + kbeg);
+      step = BK * 2;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int u = (j * NW + wave) * 64 + lane;
+        const int row = u / (BK / 8), c = (u % (BK / 8)) ^ perm(row);
+        voff[j] = static_cast<uint32_t>(row * ld * 2) + c * 16;
+        kc[j] = c * 8;
+      }
+    } else {
+      left = static_cast<uint64_t>((rem - 1l) * ld + ((n + 7) / 8 * 8 - i0)) * 2;  // rows hold whole vectors
+      base = reinterpret_cast<uint64_t>(p + kbeg * ld + i0);
+      step = static_cast<uint32_t>(BK * ld * 2);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int u = (j * NW + wave) * 64 + lane;
+        const int k = u / (W / 8), c = (u % (W / 8)) ^ perm(k);
+        voff[j] = c * 8 < rows ? static_cast<uint32_t>(k * ld * 2) + c * 16 : kOut;
+      }
+    }
+  }
+  __device__ inline u32x4 rsrc() const {
+    return u32x4{uniform(static_cast<uint32_t>(base)), uniform(static_cast<uint32_t>(base >> 32) & 0xffffu),
+                 uniform(rem > 0 ? static_cast<uint32_t>(min(left, uint64_t{0x7fffffff})) : 0u), 0x00027000u};
+  }
+  __device__ inline void load(uint32_t lds, int j, const u32x4& rs) const {
+    uint32_t v = voff[j];
+    if constexpr (RC) v = kc[j] < rem ? v : kOut;
+    load_lds16(lds + j * NW * 1024, v, rs);
+  }
+  __device__ inline void advance() {
+    base += step;
+    left -= step;
+    rem -= BK;
+  }
+  // The fragment of 32 rows from `i`, reductions 16 kk .. 16 kk + 15: lane l holds row l % 32,
+  // eight reductions from 8 (l / 32).
+  __device__ static inline u32x4 frag(const lds_char* tile, int i, int kk, int lane) {
+    if constexpr (RC) {
+      const int r = i + (lane & 31), c = (kk * 2 + (lane >> 5)) ^ perm(r);
+      return *reinterpret_cast<const lds_u32x4*>(tile + r * (BK * 2) + c * 16);
+    } else {
+      // each group of 16 lanes reads a 4 x 16 block (lane q: row q / 4, columns 4 (q % 4) .. +3)
+      // and gets it transposed (lane q: column q, four rows)
+      const int g = lane >> 4, q = lane & 15;
+      const int k = kk * 16 + (g >> 1) * 8 + (q >> 2);
+      const int col = i + (g & 1) * 16 + (q & 3) * 4;
+      const lds_char* p = tile + k * (W * 2) + ((col >> 3) ^ perm(k)) * 16 + (col & 7) * 2;
+      struct { s16x4 lo, hi; } v;
+      v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+      v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * (W * 2)));  // perm(k + 4) = perm(k)
+      return __builtin_bit_cast(u32x4, v);
+    }
+  }
+};
+
+// Orders this wavefront's LDS writes before its later reads by other lanes (the hardware keeps a
+// wavefront's LDS accesses in order; this keeps the compiler from moving them).
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The hardware hands workgroups to the 8 XCDs in turn; this gives each XCD one contiguous run of
+// the n logical ones, so that tiles which share operand panels share an L2.
+__device__ inline int xcd_order(int bid, int n) {
+  const int x = bid & 7, per = n >> 3, rem = n & 7;
+  return x * per + min(x, rem) + (bid >> 3);
+}
+
+// Tile shapes: WR x WC wavefronts own BR x BC outputs of a workgroup; ST stages of 64 reductions.
+template <int BR_, int BC_, int WR_, int WC_, int ST_, int WPE_, bool NT_>
+struct Cfg {
+  static constexpr int BR = BR_, BC = BC_, BK = 64, WR = WR_, WC = WC_, ST = ST_, NW = WR * WC;
+  static constexpr int FR = BR / WR / 32, FC = BC / WC / 32;  // 32 x 32 blocks per wavefront
+  static constexpr int WPE = WPE_;                            // wavefronts per SIMD the registers allow
+  static constexpr bool NT = NT_;
+};
+using CfgL = Cfg<256, 256, 2, 4, 2, 2, true>;   // 128 KB of LDS, one workgroup per CU
+using CfgM = Cfg<128, 128, 2, 2, 2, 2, false>;  // 64 KB, two per CU
+using CfgS = Cfg<64, 64, 2, 2, 4, 2, false>;    // 64 KB, two per CU
+
+template <class T, class C, int PROD>
+__global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
+  constexpr int NW = C::NW, FR = C::FR, FC = C::FC, BK = C::BK, ST = C::ST, WC = C::WC;
+  using OP = Operand<C::BR, BK, PROD != WGRAD, NW>;
+  using OQ = Operand<C::BC, BK, PROD == FWD, NW>;
+  constexpr int SB = OP::BYTES + OQ::BYTES, LOADS = OP::N + OQ::N;
+  __shared__ __attribute__((aligned(1024))) char lds[ST * SB];
+  const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+  const int wave = static_cast<int>(uniform(threadIdx.x >> 6));
+  const int lid = xcd_order(blockIdx.x, gridDim.x);
+  const int split = lid / a.tiles, t = lid - split * a.tiles;
+  const int tr = t / a.tiles_c, tc = t - tr * a.tiles_c;
+  const int row0 = tr * C::BR, col0 = tc * C::BC;
+  const int kbeg = split * a.per_split, kend = min(a.red, kbeg + a.per_split);
+  const int nk = (kend - kbeg + BK - 1) / BK;
+  const int wr = wave / WC, wc = wave % WC;
+  OP op;
+  OQ oq;
+  op.init(a.P, a.ldp, row0, a.R, kbeg, kend, wave, lane);
+  oq.init(a.Q, a.ldq, col0, a.C, kbeg, min(kend, a.red_q), wave, lane);
+  const lds_char* base = (const lds_char*)lds;
+  const uint32_t mine = uniform(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base)) + wave * 1024);
+  const auto load_one = [&](int m, uint32_t slot, const u32x4& rp, const u32x4& rq) {
+    if (m < OP::N) op.load(mine + slot, m, rp);
+    else oq.load(mine + slot + OP::BYTES, m - OP::N, rq);
+  };
+  f32x16 acc[FC][FR];
+#pragma unroll
+  for (int i = 0; i < FC; ++i)
+#pragma unroll
+    for (int j = 0; j < FR; ++j) acc[i][j] = f32x16{};
+  float dbs[FR] = {};
+
+  // Fill the ring.  Stages past the reduction's end load zeros without touching memory, so the
+  // number of loads in flight at every wait is known at compile time.
+#pragma unroll
+  for (int s = 0; s < ST; ++s) {
+    const u32x4 rp = op.rsrc(), rq = oq.rsrc();
+#pragma unroll
+    for (int m = 0; m < LOADS; ++m) load_one(m, s * SB, rp, rq);
+    op.advance();
+    oq.advance();
+  }
+
+  // Two register sets of fragments: while one K16 step multiplies, the next one's are read.  The
+  // matrix A operand is Q's fragment, so a lane's accumulators are consecutive output columns.
+  constexpr int KK = BK / 16;
+  u32x4 q[2][FC], p[2][FR];
+  const auto read = [&](int set, uint32_t slot, int kk) {
+#pragma unroll
+    for (int i = 0; i < FC; ++i) q[set][i] = OQ::frag(base + slot + OP::BYTES, (wc * FC + i) * 32, kk, lane);
+#pragma unroll
+    for (int j = 0; j < FR; ++j) p[set][j] = OP::frag(base + slot, (wr * FR + j) * 32, kk, lane);
+  };
+  // Bias gradient: the column tiles and their wavefront columns share the stages out, so every
+  // row's sum is taken once and no tile does more than its part.
+  const auto add_rows = [&](int set, int kt) {
+    if (PROD == WGRAD && a.dbp && kt % (a.tiles_c * WC) == tc * WC + wc)
+#pragma unroll
+      for (int j = 0; j < FR; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dbs[j] += T::to_f(static_cast<uint16_t>(p[set][j][e] & 0xffffu)) + T::to_f(static_cast<uint16_t>(p[set][j][e] >> 16));
+  };
+  wait_and_meet<LOADS*(ST - 1)>();
+  __builtin_amdgcn_sched_barrier(0);
+  read(0, 0, 0);
+  uint32_t slot = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+    for (int kk = 0; kk < KK - 1; ++kk) {
+      read((kk + 1) & 1, slot, kk + 1);
+#pragma unroll
+      for (int j = 0; j < FR; ++j)
+#pragma unroll
+        for (int i = 0; i < FC; ++i) acc[i][j] = mfma32<T>(q[kk & 1][i], p[kk & 1][j], acc[i][j]);
+      add_rows(kk & 1, kt);
+      // one LDS read (two where a fragment takes two) behind each product
+#pragma unroll
+      for (int m = 0; m < FC * FR; ++m) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, PROD == FWD ? 1 : 2, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // The stage's last fragments are in registers: its slot is free, and the next stage has
+    // arrived.  The refill's loads are issued one behind each product of the last K16 step.
+    wait_and_meet<LOADS*(ST - 2)>();
+    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t freed = slot;
+    slot = slot + SB == ST * SB ? 0 : slot + SB;
+    const u32x4 rp = op.rsrc(), rq = oq.rsrc();
+    add_rows((KK - 1) & 1, kt);
+    read(0, slot, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < (FC * FR > LOADS ? FC * FR : LOADS); ++m) {
+      if (m < FC * FR) acc[m % FC][m / FC] = mfma32<T>(q[1][m % FC], p[1][m / FC], acc[m % FC][m / FC]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (m < LOADS) load_one(m, freed, rp, rq);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    op.advance();
+    oq.advance();
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  if constexpr (PROD == WGRAD) {
+    if (a.dbp) {
+#pragma unroll
+      for (int j = 0; j < FR; ++j) {
+        const float s = dbs[j] + __shfl_xor(dbs[j], 32);
+        const int r = row0 + (wr * FR + j) * 32 + l32;
+        if (half == 0 && r < a.R) a.dbp[((static_cast<long>(split) * a.tiles_c + tc) * WC + wc) * a.R + r] = s;
+      }
+    }
+    // register 4 g + e of acc[i][j]: column 32 i + 8 g + 4 half + e, row 32 j + l32
+#pragma unroll
+    for (int j = 0; j < FR; ++j) {
+      const int r = row0 + (wr * FR + j) * 32 + l32;
+      float* o = a.part + (static_cast<long>(split) * a.R + r) * a.C;
+#pragma unroll
+      for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = col0 + (wc * FC + i) * 32 + g * 8 + half * 4;
+          if (r >= a.R || c >= a.C) continue;
+          if (a.C % 4 == 0) {
+            *reinterpret_cast<u32x4_f32*>(o + c) =
+                u32x4{__float_as_uint(acc[i][j][4 * g]), __float_as_uint(acc[i][j][4 * g + 1]),
+                      __float_as_uint(acc[i][j][4 * g + 2]), __float_as_uint(acc[i][j][4 * g + 3])};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (c + e < a.C) o[c + e] = acc[i][j][4 * g + e];
+          }
+        }
     }
   } else {
-    const uint64_t offset = a.drop.threshold ? drop_offset(a.drop) : 0;
-    for (int i = lane; i < 128; i += 64) {
-      const int r = row0 + i / 4, c = col0 + i % 4 * 8;
-      if (r >= a.R || c >= a.C) continue;
-      float v[8];
+    // Accumulators go through LDS (each wavefront's own 32 x (32 FC) floats at a time), so that a
+    // lane gets eight consecutive columns: they share one call of the mask's generator, and a
+    // row's accesses to residual, pre, y, ... are whole cache lines.
+    constexpr int WCOLS = FC * 32, GR = WCOLS / 8, RPP = 64 / GR, PASS = 32 / RPP, PITCH = WCOLS + 4;
+    static_assert(NW * 32 * PITCH * 4 <= ST * SB, "the wavefronts' blocks fit into the ring");
+    constexpr int AHEAD = FR < 2 ? FR : 2;  // row blocks whose residual / pre are on their way
+    const uint64_t offset = a.drop.top ? drop_offset(a.drop) : 0;
+    float* blk = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
+    const int gr = lane % GR, rr = lane / GR;
+    const int c = col0 + wc * WCOLS + gr * 8, n = min(8, a.C - c);
+    float bias[8] = {};
+    if (PROD == FWD && a.bias && n > 0)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = lds[wave][i / 4][i % 4 * 8 + e];
-      epilogue8<T, PROD, ACT>(a, offset, r, c, min(8, a.C - c), v);
+      for (int e = 0; e < 8; ++e) bias[e] = a.bias[min(c + e, a.C - 1)];
+    Raw8<T> add[AHEAD][PASS], pre[AHEAD][PASS];
+    const auto fetch = [&](int j) {
+#pragma unroll
+      for (int s = 0; s < PASS; ++s) {
+        const long r = row0 + (wr * FR + j) * 32 + rr + s * RPP;
+        if (r < a.R && n > 0) {
+          if (a.add) add[j % AHEAD][s] = load8_raw<T>(a.add + r * a.ldadd + c, n);
+          if (PROD == DGRAD && a.pre) pre[j % AHEAD][s] = load8_raw<T>(a.pre + r * a.ldpre + c, n);
+        }
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) fetch(j);
+    __syncthreads();  // the ring is no longer read
+#pragma unroll
+    for (int j = 0; j < FR; ++j) {
+#pragma unroll
+      for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4*>(blk + l32 * PITCH + i * 32 + g * 8 + half * 4) =
+              make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+      wave_sync();
+#pragma unroll
+      for (int s = 0; s < PASS; ++s) {
+        const int r = row0 + (wr * FR + j) * 32 + rr + s * RPP;
+        float v[8];
+        const float4 lo = *reinterpret_cast<const float4*>(blk + (rr + s * RPP) * PITCH + gr * 8);
+        const float4 hi = *reinterpret_cast<const float4*>(blk + (rr + s * RPP) * PITCH + gr * 8 + 4);
+        v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+        if (r < a.R && n > 0) epilogue8<T, PROD, C::NT>(a, offset, r, c, n, v, bias, add[j % AHEAD][s], pre[j % AHEAD][s]);
+      }
+      wave_sync();
+      if (j + AHEAD < FR) fetch(j + AHEAD);
     }
   }
 }
 
-// part[split][c] = sum over the split's rows of dz[m][c].
+// ---------------------------------------------------------------------------------------
+// Few outputs (a forward of one to a few hundred rows): a workgroup's wavefronts share out the
+// reduction of one 32 x 32 tile, fragments straight from global memory, and the partial tiles
+// are added in wavefront order in LDS.  Any alignment.
+// ---------------------------------------------------------------------------------------
+constexpr int kFewWaves = 16;
+
 template <class T>
-__global__ __launch_bounds__(256) void k_colsum(const uint16_t* dz, long ld, int M, int N, int per, float* part) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= N) return;
-  const int m0 = blockIdx.y * per, m1 = min(M, m0 + per);
-  float s = 0.f;
-  for (int m = m0; m < m1; ++m) s += T::to_f(dz[m * ld + c]);
-  part[static_cast<long>(blockIdx.y) * N + c] = s;
+__global__ __launch_bounds__(kFewWaves * 64) void k_dense_few(GemmArgs a) {
+  constexpr int PITCH = 36;
+  __shared__ float lds[kFewWaves][32 * PITCH];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, l32 = lane & 31;
+  const int tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
+  const int row0 = tr * 32, col0 = tc * 32;
+  const int k0 = wave * a.per_split, kend = min(a.red, k0 + a.per_split);
+  const uint16_t* q = a.Q + static_cast<long>(min(col0 + l32, a.C - 1)) * a.ldq;  // rows past the end: never stored
+  const uint16_t* p = a.P + static_cast<long>(min(row0 + l32, a.R - 1)) * a.ldp;
+  f32x16 acc = {};
+  for (int k = k0 + half * 8; k - half * 8 < kend; k += 64) {
+    Raw8<T> fq[4], fp[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int n = kend - (k + u * 16);
+      if (n > 0) {
+        fq[u] = load8_raw<T>(q + k + u * 16, n);
+        fp[u] = load8_raw<T>(p + k + u * 16, n);
+      } else {
+        fq[u].v[0] = fp[u].v[0] = u32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc = mfma32<T>(fq[u].v[0], fp[u].v[0], acc);
+  }
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    *reinterpret_cast<float4*>(&lds[wave][l32 * PITCH + g * 8 + half * 4]) =
+        make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
+  __syncthreads();
+  if (threadIdx.x >= 128) return;
+  const int r = row0 + threadIdx.x / 4, c = col0 + threadIdx.x % 4 * 8, n = min(8, a.C - c);
+  if (r >= a.R || n <= 0) return;
+  float v[8] = {}, bias[8] = {};
+  Raw8<T> add;
+  if (a.add) add = load8_raw<T>(a.add + r * a.ldadd + c, n);
+  if (a.bias)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bias[e] = a.bias[min(c + e, a.C - 1)];
+#pragma unroll 4
+  for (int w = 0; w < kFewWaves; ++w)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += lds[w][threadIdx.x / 4 * PITCH + threadIdx.x % 4 * 8 + e];
+  epilogue8<T, FWD, false>(a, a.drop.top ? drop_offset(a.drop) : 0, r, c, n, v, bias, add, add);
 }
 
-// out[i] = sum of the splits' part[split][i], in split order.
-__global__ __launch_bounds__(256) void k_sum_parts(const float* part, long n, int splits, float* out) {
+// ---------------------------------------------------------------------------------------
+// Operands whose rows are not whole aligned vectors are copied once, rows padded with zeros.
+// ---------------------------------------------------------------------------------------
+template <class T>
+__global__ __launch_bounds__(256) void k_pack(const uint16_t* src, long ld, long rows, int cols, int vecs, uint16_t* dst) {
   const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.f;
-  for (int p = 0; p < splits; ++p) s += part[p * n + i];
-  out[i] = s;
+  const long r = i / vecs;
+  const int v = static_cast<int>(i - r * vecs);
+  if (r >= rows) return;
+  reinterpret_cast<u32x4*>(dst)[i] = load8_raw<T>(src + r * ld + v * 8, cols - v * 8).v[0];
+}
+
+// out[i] = the sum over p < parts of part[p][i], VEC consecutive i per thread: 16 threads share
+// one vector's parts (thread s: parts s, s + 16, ...), their sums are added in thread order.
+template <int VEC>
+__global__ __launch_bounds__(256) void k_sum_parts(const float* part, long n, int parts, float* out) {
+  __shared__ float red[16][16 * VEC + 1];
+  const int cv = threadIdx.x & 15, s = threadIdx.x >> 4;
+  const long c = (static_cast<long>(blockIdx.x) * 16 + cv) * VEC;
+  float v[VEC] = {};
+  if (c < n)
+#pragma unroll 4
+    for (int p = s; p < parts; p += 16) {
+      float x[VEC];
+      __builtin_memcpy(x, __builtin_assume_aligned(part + p * n + c, 4 * VEC), sizeof x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] += x[e];
+    }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) red[s][cv * VEC + e] = v[e];
+  __syncthreads();
+  if (threadIdx.x < 16 * VEC) {
+    const long i = static_cast<long>(blockIdx.x) * 16 * VEC + threadIdx.x;
+    if (i < n) {
+      float t = red[0][threadIdx.x];
+      for (int k = 1; k < 16 && k < parts; ++k) t += red[k][threadIdx.x];
+      out[i] = t;
+    }
+  }
 }
 
 __global__ __launch_bounds__(256) void k_zero(float* p, long n) {
@@ -150,40 +532,100 @@ __global__ __launch_bounds__(256) void k_zero(float* p, long n) {
   if (i < n) p[i] = 0.f;
 }
 
-int ceil_div(long a, long b) { return static_cast<int>((a + b - 1) / b); }
+// ---------------------------------------------------------------------------------------
+// Plans and launches.
+// ---------------------------------------------------------------------------------------
+long ceil_div(long a, long b) { return (a + b - 1) / b; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+long pad8(long n) { return (n + 7) / 8 * 8; }
 
-// Batch slices of the weight gradient.
+constexpr int kMaxCols = 1 << 20;  // widest layer; a stage of 256 rows then spans at most 2^30 bytes
+
+enum Shape { SHAPE_L, SHAPE_M, SHAPE_S };
+constexpr int kEdge[3] = {256, 128, 64};
+
+// Forward and data gradient: the largest tile that still gives every CU one.
+Shape plan_tiles(long R, long C) {
+  for (Shape s : {SHAPE_L, SHAPE_M})
+    if (ceil_div(R, kEdge[s]) * ceil_div(C, kEdge[s]) >= 256) return s;
+  return SHAPE_S;
+}
+
+// Weight gradient: tiles x batch slices, at least 256 rows to a slice; the largest tile that
+// fills most of the CUs.
 struct WgradPlan {
-  int splits, per;
-  size_t bytes;
+  Shape shape;
+  int splits, per, db_rows;
+  size_t dw_bytes, bytes;
 };
 WgradPlan plan_wgrad(int M, int K, int N) {
-  const long tiles = static_cast<long>(ceil_div(N, 32)) * ceil_div(K, 32);
-  long s = std::max<long>(1, 4096 / tiles);
-  s = std::min<long>(s, ceil_div(M, 256));
-  WgradPlan p;
-  p.per = static_cast<int>((ceil_div(M, s) + 15l) / 16 * 16);
-  p.splits = ceil_div(M, p.per);
-  p.bytes = static_cast<size_t>(p.splits) * (static_cast<size_t>(N) * K + N) * 4;
+  WgradPlan p{};
+  long splits = 1;
+  for (Shape s : {SHAPE_L, SHAPE_M, SHAPE_S}) {
+    const long tiles = ceil_div(N, kEdge[s]) * ceil_div(K, kEdge[s]);
+    splits = std::min(std::max<long>(1, 256 / tiles), ceil_div(M, 256));
+    p.shape = s;
+    if (tiles * splits >= 192) break;
+  }
+  p.per = static_cast<int>(ceil_div(ceil_div(M, splits), 64) * 64);
+  p.splits = static_cast<int>(ceil_div(M, p.per));
+  const int wc = p.shape == SHAPE_L ? CfgL::WC : p.shape == SHAPE_M ? CfgM::WC : CfgS::WC;
+  p.db_rows = p.splits * static_cast<int>(ceil_div(K, kEdge[p.shape])) * wc;
+  p.dw_bytes = round256(static_cast<size_t>(p.splits) * N * K * 4);
+  p.bytes = p.dw_bytes + round256(static_cast<size_t>(p.db_rows) * N * 4);
   return p;
 }
 
-template <class T, bool P_RC, bool Q_RC, int PROD>
-el_status launch_product(const char* fn, GemmArgs a, int splits, uint32_t act, hipStream_t st) {
-  a.tiles_c = ceil_div(a.C, 32);
-  const long tiles = static_cast<long>(ceil_div(a.R, 32)) * a.tiles_c;
-  if (tiles * splits >= (1l << 25)) return tower::unsupported(fn, "the output has too many tiles for one launch");
+template <class T, class C, int PROD>
+el_status launch_tiles(const char* fn, GemmArgs a, int splits, hipStream_t st) {
+  a.tiles_c = static_cast<int>(ceil_div(a.C, C::BC));
+  const long tiles = ceil_div(a.R, C::BR) * a.tiles_c;
+  if (tiles * splits >= (1l << 22)) return tower::unsupported(fn, "the output has too many tiles for one launch");
   a.tiles = static_cast<int>(tiles);
-  a.total = a.tiles * splits;
-  const dim3 grid(ceil_div(tiles * splits, 4));
-  if constexpr (PROD == WGRAD) {
-    hipLaunchKernelGGL((k_dense_simple<T, P_RC, Q_RC, PROD, EL_ACT_NONE>), grid, dim3(256), 0, st, a);
-  } else {
-    tower::with_act(act, [&](auto A) {
-      hipLaunchKernelGGL((k_dense_simple<T, P_RC, Q_RC, PROD, decltype(A)::value>), grid, dim3(256), 0, st, a);
-    });
-  }
+  hipLaunchKernelGGL((k_dense<T, C, PROD>), dim3(static_cast<unsigned>(tiles * splits)), dim3(C::NW * 64), 0, st, a);
   return check_launch(fn);
+}
+template <class T, int PROD>
+el_status launch_product(const char* fn, const GemmArgs& a, Shape s, int splits, hipStream_t st) {
+  return s == SHAPE_L   ? launch_tiles<T, CfgL, PROD>(fn, a, splits, st)
+         : s == SHAPE_M ? launch_tiles<T, CfgM, PROD>(fn, a, splits, st)
+                        : launch_tiles<T, CfgS, PROD>(fn, a, splits, st);
+}
+
+// A forward of few outputs: fewer than 64 tiles of 64 x 64.
+bool plan_few(long M, long N) { return ceil_div(M, 64) * ceil_div(N, 64) < 64; }
+
+// The operand as the tile kernels take it: 16-byte aligned rows of whole vectors.
+bool whole_vectors(const void* p, int64_t ld, int64_t cols) {
+  return tower::al(p, 16) && ld % 8 == 0 && cols % 8 == 0 && ld <= 2 * kMaxCols;
+}
+size_t packed_bytes(long rows, long cols) { return round256(static_cast<size_t>(rows) * pad8(cols) * 2); }
+
+// Copies the operand behind `ws` (and moves ws on) unless it is whole already; `done` receives
+// the pointer and stride to use.
+el_status pack(const char* fn, const uint16_t** p, long* ld, long rows, int cols, char** ws, hipStream_t st) {
+  if (whole_vectors(*p, *ld, cols)) return EL_OK;
+  const int vecs = static_cast<int>(pad8(cols) / 8);
+  const long blocks = ceil_div(rows * vecs, 256);
+  if (blocks >= (1l << 24)) return tower::unsupported(fn, "an unaligned operand of more than 2^35 elements");
+  uint16_t* dst = reinterpret_cast<uint16_t*>(*ws);
+  // (the bits are copied: one instance serves both 16-bit types)
+  hipLaunchKernelGGL((k_pack<BF16T>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, *p, *ld, rows, cols, vecs, dst);
+  *p = dst;
+  *ld = vecs * 8l;
+  *ws += packed_bytes(rows, cols);
+  return check_launch(fn);
+}
+
+void launch_sum(const float* part, long n, int parts, float* out, hipStream_t st) {
+  if (n % 4 == 0)
+    hipLaunchKernelGGL((k_sum_parts<4>), dim3(static_cast<unsigned>(ceil_div(n, 64))), dim3(256), 0, st, part, n, parts, out);
+  else
+    hipLaunchKernelGGL((k_sum_parts<1>), dim3(static_cast<unsigned>(ceil_div(n, 16))), dim3(256), 0, st, part, n, parts, out);
+}
+
+bool dense_sizes_ok(int32_t M, int32_t K, int32_t N) {
+  return M >= 1 && K >= 1 && N >= 1 && K <= kMaxCols && N <= kMaxCols && static_cast<int64_t>(N) * K < (int64_t{1} << 29);
 }
 
 el_status check_dense_layer(const char* fn, const void* x, int64_t ldx, int32_t M, int32_t K, const void* w, int32_t N,
@@ -195,8 +637,7 @@ el_status check_dense_layer(const char* fn, const void* x, int64_t ldx, int32_t 
   if (M < 0) return tower::bad(fn, "M must be >= 0");
   if (K < 1) return tower::bad(fn, "K must be >= 1");
   if (N < 1) return tower::bad(fn, "N must be >= 1");
-  // 2^31 elements of weights: partial sums and copies of them stay far inside 64-bit sizes
-  if (static_cast<int64_t>(N) * K >= (int64_t{1} << 31)) return tower::unsupported(fn, "N * K must be < 2^31");
+  if (!dense_sizes_ok(std::max(M, 1), K, N)) return tower::unsupported(fn, "K and N must be <= 2^20 and N * K < 2^29");
   if (!w) return tower::bad(fn, "w is null");
   if (!tower::al(w, 2)) return tower::bad(fn, "w must be aligned to its elements");
   const el_status s = tower::check_act(fn, act);
@@ -205,6 +646,23 @@ el_status check_dense_layer(const char* fn, const void* x, int64_t ldx, int32_t 
 }
 
 const uint16_t* u16(const void* p) { return static_cast<const uint16_t*>(p); }
+
+template <class T>
+el_status run_fwd(const char* fn, GemmArgs a, char* ws, hipStream_t st) {
+  if (plan_few(a.R, a.C)) {
+    a.tiles_c = static_cast<int>(ceil_div(a.C, 32));
+    a.per_split = static_cast<int>(ceil_div(ceil_div(a.red, kFewWaves), 64) * 64);
+    hipLaunchKernelGGL((k_dense_few<T>), dim3(static_cast<unsigned>(ceil_div(a.R, 32) * a.tiles_c)), dim3(kFewWaves * 64), 0,
+                       st, a);
+    return check_launch(fn);
+  }
+  el_status s = pack(fn, &a.P, &a.ldp, a.R, a.red, &ws, st);
+  if (s == EL_OK) s = pack(fn, &a.Q, &a.ldq, a.C, a.red, &ws, st);
+  if (s != EL_OK) return s;
+  a.red = static_cast<int>(pad8(a.red));  // the copies' padding is zero; whole rows need none
+  a.red_q = a.per_split = a.red;
+  return launch_product<T, FWD>(fn, a, plan_tiles(a.R, a.C), 1, st);
+}
 
 }  // namespace
 }  // namespace el
@@ -217,16 +675,51 @@ using namespace el;
     if (st_ != EL_OK) return st_;    \
   } while (0)
 
+namespace {
+
+// Device bytes of the copies that these operands need (none when they are whole vectors).
+size_t copy_bytes(const void* p, int64_t ld, long rows, long cols) {
+  return whole_vectors(p, ld, cols) ? 0 : packed_bytes(rows, cols);
+}
+
+template <class T>
+el_status run_bwd(const char* fn, const uint16_t* x, long ldx, int M, int K, const uint16_t* w, int N, const uint16_t* dz,
+                  long lddz, GemmArgs a, float* dw, float* db, char* ws, hipStream_t st) {
+  EL_TRY(pack(fn, &dz, &lddz, M, N, &ws, st));
+  EL_TRY(pack(fn, &x, &ldx, M, K, &ws, st));
+  if (a.out) {
+    long ldw = K;
+    EL_TRY(pack(fn, &w, &ldw, N, K, &ws, st));
+    a.P = dz, a.ldp = lddz, a.Q = w, a.ldq = ldw, a.R = M, a.C = K, a.red = N;
+    // a copied dz has rows that end in zeros; the rows of w behind N read as zeros
+    a.red = a.per_split = static_cast<int>(pad8(N));
+    a.red_q = N;
+    EL_TRY((launch_product<T, DGRAD>(fn, a, plan_tiles(M, K), 1, st)));
+  }
+  const WgradPlan pl = plan_wgrad(M, K, N);
+  GemmArgs b{};
+  b.P = dz, b.ldp = lddz, b.Q = x, b.ldq = ldx, b.R = N, b.C = K, b.red = b.red_q = M, b.per_split = pl.per;
+  b.part = pl.splits > 1 ? reinterpret_cast<float*>(ws) : dw;
+  float* dbp = reinterpret_cast<float*>(ws + pl.dw_bytes);
+  b.dbp = db ? dbp : nullptr;
+  EL_TRY((launch_product<T, WGRAD>(fn, b, pl.shape, pl.splits, st)));
+  if (pl.splits > 1) launch_sum(b.part, static_cast<long>(N) * K, pl.splits, dw, st);
+  if (db) launch_sum(dbp, N, pl.db_rows, db, st);
+  return check_launch(fn);
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t el_dense_fwd_workspace_bytes(int32_t M, int32_t K, int32_t N) {
-  (void)M, (void)K, (void)N;
-  return 0;
+  if (!dense_sizes_ok(M, K, N) || plan_few(M, N)) return 0;
+  return packed_bytes(M, K) + packed_bytes(N, K);
 }
 
 size_t el_dense_bwd_workspace_bytes(int32_t M, int32_t K, int32_t N) {
-  if (M < 1 || K < 1 || N < 1 || static_cast<int64_t>(N) * K >= (int64_t{1} << 31)) return 0;
-  return plan_wgrad(M, K, N).bytes;
+  if (!dense_sizes_ok(M, K, N)) return 0;
+  return packed_bytes(M, N) + packed_bytes(M, K) + packed_bytes(N, K) + plan_wgrad(M, K, N).bytes;
 }
 
 el_status el_dense_fwd(const void* x, int64_t ldx, int32_t M, int32_t K, const void* w, const float* bias, int32_t N,
@@ -242,13 +735,14 @@ el_status el_dense_fwd(const void* x, int64_t ldx, int32_t M, int32_t K, const v
     EL_TRY(tower::check_rows(fn, "residual", residual, ldr, N, false, 2));
     EL_TRY(tower::check_rows(fn, "pre", pre, ldpre, N, false, 2));
     EL_TRY(tower::check_rows(fn, "y", y, ldy, N, M > 0, 2));
-    EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, el_dense_fwd_workspace_bytes(M, K, N)));
     if (M == 0) return EL_OK;
-    a.P = u16(x), a.ldp = ldx, a.Q = u16(w), a.ldq = K, a.R = M, a.C = N, a.red = K, a.per_split = K;
+    const size_t need = plan_few(M, N) ? 0 : copy_bytes(x, ldx, M, K) + copy_bytes(w, K, N, K);
+    EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, need));
+    a.P = u16(x), a.ldp = ldx, a.Q = u16(w), a.ldq = K, a.R = M, a.C = N, a.red = K, a.act = act;
     a.add = u16(residual), a.ldadd = ldr, a.aux = static_cast<uint16_t*>(pre), a.ldaux = ldpre;
     a.out = static_cast<uint16_t*>(y), a.ldo = ldy, a.bias = bias;
-    return dtype == EL_BF16 ? launch_product<BF16T, true, true, FWD>(fn, a, 1, act, stream)
-                            : launch_product<F16T, true, true, FWD>(fn, a, 1, act, stream);
+    char* ws = static_cast<char*>(workspace);
+    return dtype == EL_BF16 ? run_fwd<BF16T>(fn, a, ws, stream) : run_fwd<F16T>(fn, a, ws, stream);
   });
 }
 
@@ -268,38 +762,21 @@ el_status el_dense_bwd(const void* x, int64_t ldx, int32_t M, int32_t K, const v
     EL_TRY(tower::check_rows(fn, "dzb", dzb, lddzb, K, false, 2));
     if ((dzb || dres) && !dx) return tower::bad(fn, "dzb and dres need dx");
     if (!dw || !tower::al(dw, 4) || !tower::al(db, 4)) return tower::bad(fn, "dw must be non-null, dw and db aligned to their elements");
-    EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, el_dense_bwd_workspace_bytes(M, K, N)));
     const long nk = static_cast<long>(N) * K;
     if (M == 0) {  // an empty batch: zero gradients, by a kernel (a captured fill stays a kernel node)
-      hipLaunchKernelGGL(k_zero, dim3(ceil_div(nk, 256)), dim3(256), 0, stream, dw, nk);
-      if (db) hipLaunchKernelGGL(k_zero, dim3(ceil_div(N, 256)), dim3(256), 0, stream, db, static_cast<long>(N));
+      hipLaunchKernelGGL(k_zero, dim3(static_cast<unsigned>(ceil_div(nk, 256))), dim3(256), 0, stream, dw, nk);
+      if (db) hipLaunchKernelGGL(k_zero, dim3(static_cast<unsigned>(ceil_div(N, 256))), dim3(256), 0, stream, db, static_cast<long>(N));
       return check_launch(fn);
     }
-    if (dx) {
-      a.P = u16(dz), a.ldp = lddz, a.Q = u16(w), a.ldq = K, a.R = M, a.C = K, a.red = N, a.per_split = N;
-      a.add = u16(dres), a.ldadd = lddres, a.out = static_cast<uint16_t*>(dx), a.ldo = lddx;
-      a.aux = static_cast<uint16_t*>(dzb), a.ldaux = lddzb, a.pre = u16(pre), a.ldpre = ldpre;
-      EL_TRY((dtype == EL_BF16 ? launch_product<BF16T, true, false, DGRAD>(fn, a, 1, act, stream)
-                               : launch_product<F16T, true, false, DGRAD>(fn, a, 1, act, stream)));
-    }
-    const WgradPlan pl = plan_wgrad(M, K, N);
-    float* part = static_cast<float*>(workspace);
-    float* dbp = part + static_cast<size_t>(pl.splits) * nk;
-    GemmArgs b{};
-    b.P = u16(dz), b.ldp = lddz, b.Q = u16(x), b.ldq = ldx, b.R = N, b.C = K, b.red = M, b.per_split = pl.per;
-    b.part = part;
-    EL_TRY((dtype == EL_BF16 ? launch_product<BF16T, false, false, WGRAD>(fn, b, pl.splits, 0, stream)
-                             : launch_product<F16T, false, false, WGRAD>(fn, b, pl.splits, 0, stream)));
-    hipLaunchKernelGGL(k_sum_parts, dim3(ceil_div(nk, 256)), dim3(256), 0, stream, part, nk, pl.splits, dw);
-    if (db) {
-      const dim3 grid(ceil_div(N, 256), pl.splits);
-      if (dtype == EL_BF16)
-        hipLaunchKernelGGL((k_colsum<BF16T>), grid, dim3(256), 0, stream, u16(dz), lddz, M, N, pl.per, dbp);
-      else
-        hipLaunchKernelGGL((k_colsum<F16T>), grid, dim3(256), 0, stream, u16(dz), lddz, M, N, pl.per, dbp);
-      hipLaunchKernelGGL(k_sum_parts, dim3(ceil_div(N, 256)), dim3(256), 0, stream, dbp, static_cast<long>(N), pl.splits, db);
-    }
-    return check_launch(fn);
+    const size_t need = copy_bytes(dz, lddz, M, N) + copy_bytes(x, ldx, M, K) + (dx ? copy_bytes(w, K, N, K) : 0) +
+                        plan_wgrad(M, K, N).bytes;
+    EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, need));
+    a.add = u16(dres), a.ldadd = lddres, a.out = static_cast<uint16_t*>(dx), a.ldo = lddx, a.act = act;
+    a.aux = static_cast<uint16_t*>(dzb), a.ldaux = lddzb, a.pre = dzb && act != EL_ACT_NONE ? u16(pre) : nullptr, a.ldpre = ldpre;
+    char* ws = static_cast<char*>(workspace);
+    return dtype == EL_BF16
+               ? run_bwd<BF16T>(fn, u16(x), ldx, M, K, u16(w), N, u16(dz), lddz, a, dw, db, ws, stream)
+               : run_bwd<F16T>(fn, u16(x), ldx, M, K, u16(w), N, u16(dz), lddz, a, dw, db, ws, stream);
   });
 }
 

@@ -102,31 +102,32 @@ __device__ inline void store8(typename T::S* p, const float* f, int n) {
 // Activations: one function for the value and one for the derivative, the kind known at
 // compile time.
 // ---------------------------------------------------------------------------------------
-// Phi(u) and phi(u) sqrt(2 pi) = exp(-u^2 / 2): the normal distribution function by the
-// rational form 7.1.26 of Abramowitz and Stegun's Handbook (absolute error 1.5e-7 on erf,
-// below half an fp32 step of values near 1), which shares its exponential with the derivative
-// and costs about 20 instructions where erff takes more than twice as many.
-__device__ inline void normal_cdf(float u, float& cdf, float& ex) {
-  const float x = fabsf(u) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-  ex = __expf(-x * x);
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  const float q = 0.5f * p * t * ex;  // Phi(-|u|)
-  cdf = u < 0.f ? q : 1.f - q;
+// q = Phi(-|u|) and ex = exp(-u^2 / 2) = sqrt(2 pi) phi(u): the normal distribution function by
+// the rational form 7.1.26 of Abramowitz and Stegun's Handbook (absolute error 1.5e-7 on erf,
+// about one fp32 step of values near 1).  It shares its exponential with the derivative, and
+// u Phi(u) = max(u, 0) - |u| q takes 12 plain instructions, one exp2 and one reciprocal.
+__device__ inline float normal_tail(float u, float& ex) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.23164189f, fabsf(u), 1.f));
+  ex = __builtin_amdgcn_exp2f(u * u * -0.72134752044448170f);
+  float p = fmaf(0.5307027145f, t, -0.7265760135f);
+  p = fmaf(p, t, 0.7107068705f);
+  p = fmaf(p, t, -0.142248368f);
+  p = fmaf(p, t, 0.127414796f);
+  return p * t * ex;
+}
+__device__ inline float sigmoid(float u) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u * -1.4426950408889634f));
 }
 
 template <int ACT>
 __device__ inline float act_f(float u) {
   if constexpr (ACT == EL_ACT_RELU) return u > 0.f ? u : 0.f;
   if constexpr (ACT == EL_ACT_GELU) {
-    float cdf, ex;
-    normal_cdf(u, cdf, ex);
-    return u * cdf;
+    float ex;
+    const float q = normal_tail(u, ex);
+    return fmaf(-fabsf(u), q, u < 0.f ? 0.f : u);
   }
-  if constexpr (ACT == EL_ACT_SILU) return u * __builtin_amdgcn_rcpf(1.f + __expf(-u));
+  if constexpr (ACT == EL_ACT_SILU) return u * sigmoid(u);
   return u;
 }
 
@@ -134,12 +135,12 @@ template <int ACT>
 __device__ inline float act_df(float u) {
   if constexpr (ACT == EL_ACT_RELU) return u > 0.f ? 1.f : 0.f;
   if constexpr (ACT == EL_ACT_GELU) {
-    float cdf, ex;
-    normal_cdf(u, cdf, ex);
-    return fmaf(u * ex, 0.39894228040143268f, cdf);
+    float ex;
+    const float q = normal_tail(u, ex);
+    return fmaf(u * ex, 0.39894228040143268f, u < 0.f ? q : 1.f - q);
   }
   if constexpr (ACT == EL_ACT_SILU) {
-    const float s = __builtin_amdgcn_rcpf(1.f + __expf(-u));
+    const float s = sigmoid(u);
     return s * fmaf(u, 1.f - s, 1.f);
   }
   return 1.f;
@@ -177,7 +178,7 @@ __device__ inline void act8_grad(uint32_t act, const float (&u)[8], float (&d)[8
 // The dropout mask (definition in embtower.h).
 // ---------------------------------------------------------------------------------------
 struct DropArgs {
-  uint32_t threshold = 0;  // T, 0 .. 65536; 0: nothing is dropped
+  uint32_t top = 0;  // 2^16 T - 1 for T = 1 .. 65536; 0: nothing is dropped
   float scale = 1.f;
   uint32_t k0 = 0, k1 = 0;
   uint64_t offset = 0;
@@ -202,9 +203,10 @@ __device__ inline u32x4 philox8(uint32_t group, uint32_t row, uint64_t offset, u
   return u32x4{c0, c1, c2, c3};
 }
 
-// Number i (0 .. 7) of the eight is kept.
-__device__ inline bool keep_of(const u32x4& bits, int i, uint32_t threshold) {
-  return ((i & 1) ? bits[i >> 1] >> 16 : bits[i >> 1] & 0xffffu) >= threshold;
+// Number i (0 .. 7) of the eight is kept: number >= T, compared in the upper half of a word
+// (`top` = 2^16 T - 1; T >= 1).
+__device__ inline bool keep_of(const u32x4& bits, int i, uint32_t top) {
+  return ((i & 1) ? bits[i >> 1] : bits[i >> 1] << 16) > top;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -255,8 +257,9 @@ inline el_status drop_args(const char* fn, const el_dropout* drop, DropArgs* out
   if (!drop) return EL_OK;
   if (!(drop->p >= 0.0 && drop->p <= 1.0)) return bad(fn, "the dropout probability must be in [0, 1]");
   if (!al(drop->step, 8)) return bad(fn, "dropout step must be 8-byte aligned");
-  out->threshold = static_cast<uint32_t>(std::nearbyint(drop->p * 65536.0));
-  out->scale = out->threshold < 65536u ? static_cast<float>(65536.0 / (65536.0 - out->threshold)) : 0.f;
+  const uint64_t T = static_cast<uint64_t>(std::nearbyint(drop->p * 65536.0));
+  out->top = T ? static_cast<uint32_t>((T << 16) - 1) : 0u;
+  out->scale = T < 65536u ? static_cast<float>(65536.0 / (65536.0 - T)) : 0.f;
   out->k0 = static_cast<uint32_t>(drop->seed);
   out->k1 = static_cast<uint32_t>(drop->seed >> 32);
   out->offset = drop->offset;
