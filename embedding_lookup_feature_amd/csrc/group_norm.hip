@@ -37,12 +37,12 @@ struct GnArgs {
   uint32_t act;
   float *mean, *rstd;  // written by the forward, read by the backward
   float2* part;        // workspace, see the kernels
-  float2* gsum;
+  float* gsum;         // [2][B][G]: avg(dh), avg(dh xh)
   // resident
   int TR, team, spw, E, E1;
   int blocks;
   // streamed
-  int chunks, per_chunk, colblocks, TC;
+  int chunks, per_chunk, pieces, per_piece, colblocks, TC;  // chunks: statistics; pieces: their use
 };
 
 __device__ inline int sample_len(const GnArgs& a, int b) {
@@ -102,23 +102,63 @@ __device__ inline void group_sums(const GnArgs& a, float* lds, int tid, int team
   if (on) {
 #pragma unroll
     for (int v = 0; v < NVAL; ++v)
-#pragma unroll
-      for (int i = 0; i < (VECG ? 1 : 8); ++i) {
-        const int c = min(cv * 8 + i, a.C - 1);
-        p[v][i] = tot[v * items + team_id * a.G + c / a.Cg];
-      }
+    {
+      if (VECG)
+        p[v][0] = tot[v * items + team_id * a.G + cv * 8 / a.Cg];
+      else
+        load_groups(a, tot + v * items + team_id * a.G, cv, p[v]);
+    }
   }
 }
 
 template <bool VECG>
 __device__ inline float of_channel(const float (&p)[8], int i) { return p[VECG ? 0 : i]; }
 
+// xh = x rstd + shift (shift = -mean rstd) and du of eight values.
+template <class T, bool VECG>
+__device__ inline void grad8(const GnArgs& a, const Raw8<T>& rx, const Raw8<T>& rd, const float (&shift)[8],
+                             const float (&rstd)[8], const float (&gamma)[8], const float (&beta)[8], float (&xh)[8],
+                             float (&du)[8]) {
+  float u[8];
+  to_floats<T>(rx, xh);
+  to_floats<T>(rd, du);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    xh[q] = fmaf(xh[q], of_channel<VECG>(rstd, q), of_channel<VECG>(shift, q));
+    u[q] = fmaf(xh[q], gamma[q], beta[q]);
+  }
+  act8_grad(a.act, u, du);
+}
+
+// Hides a vector's value from the compiler: what was computed from it before is computed again
+// instead of being kept.  (The backward holds a sample as raw 16-byte vectors; its fp32 values
+// would take four times the registers and halve the wavefronts in flight.)
+template <class T>
+__device__ inline void forget(Raw8<T>& r) {
+#pragma unroll
+  for (int w = 0; w < Raw8<T>::W; ++w) asm volatile("" : "+v"(r.v[w]));
+}
+
 __device__ inline void load_params(const GnArgs& a, int cv, float (&gamma)[8], float (&beta)[8]) {
+  const auto load = [&](const float* p, float (&v)[8], float other) {
+    if (p && cv * 8 + 8 <= a.C) {
+      to_floats<F32T>(load8_raw<F32T>(p + cv * 8), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p && cv * 8 + i < a.C ? p[cv * 8 + i] : other;
+    }
+  };
+  load(a.gamma, gamma, 1.f);
+  load(a.beta, beta, 0.f);
+}
+
+// v[i] = p[group of channel 8 cv + i] (of the last channel past it), with one division.
+__device__ inline void load_groups(const GnArgs& a, const float* p, int cv, float (&v)[8]) {
+  int g = cv * 8 / a.Cg, r = cv * 8 - g * a.Cg;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int c = cv * 8 + i;
-    gamma[i] = a.gamma && c < a.C ? a.gamma[c] : 1.f;
-    beta[i] = a.beta && c < a.C ? a.beta[c] : 0.f;
+    v[i] = p[min(g, a.G - 1)];
+    if (++r == a.Cg) r = 0, ++g;
   }
 }
 
@@ -221,37 +261,31 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
         rd[i] = load8_raw<T>(dy + s * a.lddy, n);
       }
     }
-    float mean[8], rstd[8];
+    float shift[8], rstd[8];
+    load_groups(a, a.rstd + (on ? b * a.G : 0), cv, rstd);
+    load_groups(a, a.mean + (on ? b * a.G : 0), cv, shift);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const long at = on ? b * a.G + min(cv * 8 + q, a.C - 1) / a.Cg : 0;
-      mean[q] = a.mean[at];
-      rstd[q] = a.rstd[at];
-    }
+    for (int q = 0; q < 8; ++q) shift[q] *= -rstd[q];
     const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
-    float p[2][8] = {};
-    float xh[NV][8], dh[NV][8];
+    float p[2][8] = {}, cb[8] = {}, cg[8] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (tr + i * a.TR < len) {
-        to_floats<T>(rx[i], xh[i]);
-        to_floats<T>(rd[i], dh[i]);
-        float u[8];
+        float xh[8], du[8];
+        grad8<T, false>(a, rx[i], rd[i], shift, rstd, gamma, beta, xh, du);  // du is zero past the last channel
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          xh[i][q] = (xh[i][q] - mean[q]) * rstd[q];
-          u[q] = xh[i][q] * gamma[q] + beta[q];
-        }
-        act8_grad(a.act, u, dh[i]);  // du; zero past the last channel, where dy was read as zero
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          sb[q] += dh[i][q];
-          sg[q] += dh[i][q] * xh[i][q];
-          dh[i][q] *= gamma[q];
-          p[0][VECG ? 0 : q] += dh[i][q];
-          p[1][VECG ? 0 : q] += dh[i][q] * xh[i][q];
+          cb[q] += du[q];
+          cg[q] = fmaf(du[q], xh[q], cg[q]);
         }
       }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {  // the sample's channel sums serve both the groups and the parameters
+      sb[q] += cb[q];
+      sg[q] += cg[q];
+      p[0][VECG ? 0 : q] = fmaf(cb[q], gamma[q], p[0][VECG ? 0 : q]);
+      p[1][VECG ? 0 : q] = fmaf(cg[q], gamma[q], p[1][VECG ? 0 : q]);
+    }
     group_sums<VECG, 2>(a, lds, tid, team_id, r, cv, on, p);
     if (on) {
       St* dx = static_cast<St*>(a.out) + b * a.S * a.ldo + cv * 8;
@@ -261,9 +295,13 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
         if (s >= a.S) continue;
         float f[8] = {};
         if (s < len) {
+          float du[8];
+          forget(rx[i]);
+          forget(rd[i]);
+          grad8<T, false>(a, rx[i], rd[i], shift, rstd, gamma, beta, f, du);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            f[q] = rstd[q] * (dh[i][q] - of_channel<VECG>(p[0], q) * inv_n - xh[i][q] * (of_channel<VECG>(p[1], q) * inv_n));
+            f[q] = rstd[q] * (du[q] * gamma[q] - of_channel<VECG>(p[0], q) * inv_n - f[q] * (of_channel<VECG>(p[1], q) * inv_n));
         }
         store8<T>(dx + s * a.ldo, f, n);
       }
@@ -295,27 +333,236 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------
+// Wavefront form: a sample of at most 512 vectors whose channels and groups are powers of two.
+// 2^k lanes (a team) own a sample: lane = row * CV + cv inside the team, `TR` rows, so a group's
+// values sit in lanes that differ in some bits of their number and its sums are exchanges
+// between lanes, with no LDS and no barrier.  A wavefront holds 64 / team samples.
+// ---------------------------------------------------------------------------------------
+constexpr int kWave = 256;  // threads of a workgroup: four independent wavefronts
+
+struct WavePos {
+  long b;
+  int cv, tr, len;
+  bool on;
+};
+__device__ inline WavePos wave_pos(const GnArgs& a, long first) {
+  WavePos q;
+  const int t = threadIdx.x;
+  q.b = first + t / a.team;
+  q.cv = t & (a.CV - 1);
+  q.tr = (t & (a.team - 1)) / a.CV;
+  q.on = q.b < a.B;
+  q.len = q.on ? sample_len(a, static_cast<int>(q.b)) : 0;
+  return q;
+}
+
+// Sums over the group of each channel, over its lanes and rows.  VECG: p[0] stands for all eight
+// channels; otherwise Cg is 1, 2 or 4 and p[i] becomes the sum of channel i's group.
+template <bool VECG>
+__device__ inline void lane_sums(const GnArgs& a, float (&p)[8]) {
+#pragma unroll
+  for (int i = 0; i < (VECG ? 1 : 8); ++i) {
+    if (VECG)
+      for (int m = 1; m * 8 < a.Cg; m <<= 1) p[i] += __shfl_xor(p[i], m);
+    for (int m = a.CV; m < a.team; m <<= 1) p[i] += __shfl_xor(p[i], m);
+  }
+  if (!VECG && a.Cg > 1) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) p[i] = p[i + 1] = p[i] + p[i + 1];
+    if (a.Cg > 2)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) p[i] = p[i + 1] = p[i + 2] = p[i + 3] = p[i] + p[i + 2];
+  }
+}
+
+template <class T, int NV, bool VECG>
+__global__ __launch_bounds__(kWave) void k_gn_fwd_wave(GnArgs a) {
+  using St = typename T::S;
+  const WavePos w = wave_pos(a, static_cast<long>(blockIdx.x) * (kWave / a.team));
+  const St* x = static_cast<const St*>(a.x) + w.b * a.S * a.ldx + w.cv * 8;
+  Raw8<T> raw[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int s = w.tr + i * a.TR;
+    if (s < w.len) raw[i] = load8_raw<T>(x + s * a.ldx);
+  }
+  float gamma[8], beta[8];
+  load_params(a, w.cv, gamma, beta);
+  const float inv_n = w.len > 0 ? 1.f / (static_cast<float>(w.len) * a.Cg) : 0.f;
+  float f[NV][8], p[8] = {}, mean[8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (w.tr + i * a.TR < w.len) {
+      to_floats<T>(raw[i], f[i]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) p[VECG ? 0 : q] += f[i][q];
+    }
+  lane_sums<VECG>(a, p);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) mean[q] = of_channel<VECG>(p, q) * inv_n;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) p[q] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (w.tr + i * a.TR < w.len) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        f[i][q] -= mean[q];
+        p[VECG ? 0 : q] += f[i][q] * f[i][q];
+      }
+    }
+  lane_sums<VECG>(a, p);
+  if (!w.on) return;
+  float rstd[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) rstd[q] = VECG && q > 0 ? rstd[0] : 1.f / sqrtf(p[q] * inv_n + a.eps);
+  if (w.tr == 0)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int c = w.cv * 8 + q;
+      if ((c & (a.Cg - 1)) == 0) {
+        a.mean[w.b * a.G + c / a.Cg] = mean[q];
+        a.rstd[w.b * a.G + c / a.Cg] = rstd[q];
+      }
+    }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) gamma[q] *= rstd[q];
+  St* y = static_cast<St*>(a.out) + w.b * a.S * a.ldo + w.cv * 8;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int s = w.tr + i * a.TR;
+    if (s >= a.S) continue;
+    if (s < w.len) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[i][q] = f[i][q] * gamma[q] + beta[q];
+      act8(a.act, f[i]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
+    }
+    store8<T>(y + s * a.ldo, f[i], 8);
+  }
+}
+
+// part[workgroup][c] = (dbeta, dgamma) of the workgroup's samples, as in the resident form.
+template <class T, int NV, bool VECG>
+__global__ __launch_bounds__(kWave, 2) void k_gn_bwd_wave(GnArgs a) {
+  using St = typename T::S;
+  float gamma[8], beta[8], sb[8] = {}, sg[8] = {};
+  load_params(a, threadIdx.x & (a.CV - 1), gamma, beta);
+  const int per = kWave / a.team;
+  for (long first = static_cast<long>(blockIdx.x) * per; first < a.B; first += static_cast<long>(gridDim.x) * per) {
+    const WavePos w = wave_pos(a, first);
+    const St* x = static_cast<const St*>(a.x) + w.b * a.S * a.ldx + w.cv * 8;
+    const St* dy = static_cast<const St*>(a.dy) + w.b * a.S * a.lddy + w.cv * 8;
+    Raw8<T> rx[NV], rd[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int s = w.tr + i * a.TR;
+      if (s < w.len) {
+        rx[i] = load8_raw<T>(x + s * a.ldx);
+        rd[i] = load8_raw<T>(dy + s * a.lddy);
+      }
+    }
+    float shift[8], rstd[8], p0[8] = {}, p1[8] = {}, cb[8] = {}, cg[8] = {};
+#pragma unroll
+    for (int q = 0; q < (VECG ? 1 : 8); ++q) {
+      const long at = w.on ? w.b * a.G + (w.cv * 8 + q) / a.Cg : 0;
+      rstd[q] = a.rstd[at];
+      shift[q] = -a.mean[at] * rstd[q];
+    }
+    const float inv_n = w.len > 0 ? 1.f / (static_cast<float>(w.len) * a.Cg) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (w.tr + i * a.TR < w.len) {
+        float xh[8], du[8];
+        grad8<T, VECG>(a, rx[i], rd[i], shift, rstd, gamma, beta, xh, du);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          cb[q] += du[q];
+          cg[q] = fmaf(du[q], xh[q], cg[q]);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one vector's values in registers at a time
+      }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {  // the sample's channel sums serve both the groups and the parameters
+      sb[q] += cb[q];
+      sg[q] += cg[q];
+      p0[VECG ? 0 : q] = fmaf(cb[q], gamma[q], p0[VECG ? 0 : q]);
+      p1[VECG ? 0 : q] = fmaf(cg[q], gamma[q], p1[VECG ? 0 : q]);
+    }
+    lane_sums<VECG>(a, p0);
+    lane_sums<VECG>(a, p1);
+    if (!w.on) continue;
+#pragma unroll
+    for (int q = 0; q < (VECG ? 1 : 8); ++q) p0[q] *= -inv_n, p1[q] *= -inv_n;
+    St* dx = static_cast<St*>(a.out) + w.b * a.S * a.ldo + w.cv * 8;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int s = w.tr + i * a.TR;
+      if (s >= a.S) continue;
+      float f[8] = {};
+      if (s < w.len) {
+        float du[8];
+        forget(rx[i]);
+        forget(rd[i]);
+        grad8<T, VECG>(a, rx[i], rd[i], shift, rstd, gamma, beta, f, du);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          f[q] = of_channel<VECG>(rstd, q) * fmaf(du[q], gamma[q], fmaf(f[q], of_channel<VECG>(p1, q), of_channel<VECG>(p0, q)));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      store8<T>(dx + s * a.ldo, f, 8);
+    }
+  }
+  if (!a.part) return;
+  // all lanes of a channel vector: the wavefront's, then the four wavefronts'
+  __shared__ float2 red[4][64][9];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    for (int m = a.CV; m < 64; m <<= 1) {
+      sb[q] += __shfl_xor(sb[q], m);
+      sg[q] += __shfl_xor(sg[q], m);
+    }
+    if (lane < a.CV) red[wave][lane][q] = make_float2(sb[q], sg[q]);
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.C; c += kWave) {
+    float2 s = red[0][c >> 3][c & 7];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      s.x += red[k][c >> 3][c & 7].x;
+      s.y += red[k][c >> 3][c & 7].y;
+    }
+    a.part[static_cast<long>(blockIdx.x) * a.C + c] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
 // Streamed form.
 // ---------------------------------------------------------------------------------------
 constexpr int kStream = 256;
+constexpr int kAhead = 4;  // positions whose loads a thread has in flight
 
 struct StreamPos {
   int b, chunk, cv, tr, TR, s0, s1, n;
   bool on;
 };
-__device__ inline StreamPos stream_pos(const GnArgs& a) {
+// The workgroup's chunk of `per` positions, `chunks` of them to a sample.
+__device__ inline StreamPos stream_pos(const GnArgs& a, int chunks, int per) {
   StreamPos q;
   long id = blockIdx.x;
   const int cb = static_cast<int>(id % a.colblocks);
   id /= a.colblocks;
-  q.chunk = static_cast<int>(id % a.chunks);
-  q.b = static_cast<int>(id / a.chunks);
+  q.chunk = static_cast<int>(id % chunks);
+  q.b = static_cast<int>(id / chunks);
   q.TR = kStream / a.TC;
   q.tr = threadIdx.x / a.TC;
   q.cv = cb * a.TC + threadIdx.x - q.tr * a.TC;
   q.on = q.tr < q.TR && q.cv < a.CV;
-  q.s0 = q.chunk * a.per_chunk;
-  q.s1 = min(a.S, q.s0 + a.per_chunk);
+  q.s0 = q.chunk * per;
+  q.s1 = min(a.S, q.s0 + per);
   q.n = min(8, a.C - q.cv * 8);
   return q;
 }
@@ -327,23 +574,31 @@ template <class T>
 __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
   __shared__ float2 red[kStream * 8];
   using St = typename T::S;
-  const StreamPos q = stream_pos(a);
+  const StreamPos q = stream_pos(a, a.chunks, a.per_chunk);
   const int end = min(q.s1, sample_len(a, q.b));
   if (q.on) {
     const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
     float k[8] = {}, s1[8] = {}, s2[8] = {};
     int cnt = 0;
-    for (int s = q.s0 + q.tr; s < end; s += q.TR) {
-      float f[8];
-      to_floats<T>(load8_raw<T>(x + s * a.ldx, q.n), f);
+    for (int s = q.s0 + q.tr; s < end; s += kAhead * q.TR) {
+      Raw8<T> r[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (cnt == 0) k[i] = f[i];
-        const float d = f[i] - k[i];
-        s1[i] += d;
-        s2[i] += d * d;
+      for (int u = 0; u < kAhead; ++u)
+        if (s + u * q.TR < end) r[u] = load8_raw<T>(x + (s + u * q.TR) * a.ldx, q.n);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (s + u * q.TR >= end) break;
+        float f[8];
+        to_floats<T>(r[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (cnt == 0) k[i] = f[i];
+          const float d = f[i] - k[i];
+          s1[i] += d;
+          s2[i] += d * d;
+        }
+        ++cnt;
       }
-      ++cnt;
     }
     const float inv = cnt ? 1.f / cnt : 0.f;
 #pragma unroll
@@ -372,23 +627,32 @@ __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
   }
 }
 
-// One wavefront per (sample, group): mean and rstd from the chunks' channel statistics.
-__global__ __launch_bounds__(64) void k_gn_join(GnArgs a) {
-  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G, lane = threadIdx.x;
+// Sum of v over the 256 threads of a workgroup, in a fixed order, for every thread.
+__device__ inline float sum256(float v) {
+  __shared__ float red[4];
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// One workgroup per (sample, group): mean and rstd from the chunks' channel statistics.
+__global__ __launch_bounds__(256) void k_gn_join(GnArgs a) {
+  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G, t = threadIdx.x;
   const int len = sample_len(a, b);
   const int full = a.chunks * a.Cg;
   const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
   const float2* part = a.part + static_cast<long>(b) * a.chunks * a.C + g * a.Cg;
   float s = 0.f;
-  for (int j = lane; j < full; j += 64) {
+  for (int j = t; j < full; j += 256) {
     const int ch = j / a.Cg;
     const int cnt = min(max(len - ch * a.per_chunk, 0), a.per_chunk);
     if (cnt > 0) s += cnt * inv_n * part[static_cast<long>(ch) * a.C + j - ch * a.Cg].x;
   }
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-  const float mean = s;
+  const float mean = sum256(s);
   float v = 0.f;
-  for (int j = lane; j < full; j += 64) {
+  for (int j = t; j < full; j += 256) {
     const int ch = j / a.Cg;
     const int cnt = min(max(len - ch * a.per_chunk, 0), a.per_chunk);
     if (cnt > 0) {
@@ -396,42 +660,52 @@ __global__ __launch_bounds__(64) void k_gn_join(GnArgs a) {
       v += q.y + cnt * (q.x - mean) * (q.x - mean);
     }
   }
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if (lane == 0) {
+  v = sum256(v);
+  if (t == 0) {
     a.mean[blockIdx.x] = mean;
     a.rstd[blockIdx.x] = 1.f / sqrtf(v * inv_n + a.eps);
   }
 }
 
+// (mean, rstd) of the thread's channels; SHIFT: -mean rstd in the mean's place.
+template <bool SHIFT>
 __device__ inline void load_stats(const GnArgs& a, const StreamPos& q, float (&mean)[8], float (&rstd)[8]) {
+  load_groups(a, a.rstd + static_cast<long>(q.b) * a.G, q.cv, rstd);
+  load_groups(a, a.mean + static_cast<long>(q.b) * a.G, q.cv, mean);
+  if (SHIFT)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const long at = static_cast<long>(q.b) * a.G + min(q.cv * 8 + i, a.C - 1) / a.Cg;
-    mean[i] = a.mean[at];
-    rstd[i] = a.rstd[at];
-  }
+    for (int i = 0; i < 8; ++i) mean[i] *= -rstd[i];
 }
 
 template <class T>
 __global__ __launch_bounds__(kStream) void k_gn_apply(GnArgs a) {
   using St = typename T::S;
-  const StreamPos q = stream_pos(a);
+  const StreamPos q = stream_pos(a, a.pieces, a.per_piece);
   if (!q.on) return;
   const int len = sample_len(a, q.b);
   const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
   St* y = static_cast<St*>(a.out) + static_cast<long>(q.b) * a.S * a.ldo + q.cv * 8;
   float gamma[8], beta[8], mean[8], rstd[8];
   load_params(a, q.cv, gamma, beta);
-  load_stats(a, q, mean, rstd);
-  for (int s = q.s0 + q.tr; s < q.s1; s += q.TR) {
-    float f[8] = {};
-    if (s < len) {
-      to_floats<T>(load8_raw<T>(x + s * a.ldx, q.n), f);
+  load_stats<false>(a, q, mean, rstd);
+  for (int s0 = q.s0 + q.tr; s0 < q.s1; s0 += kAhead * q.TR) {
+    Raw8<T> r[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = (f[i] - mean[i]) * rstd[i] * gamma[i] + beta[i];
-      act8(a.act, f);
+    for (int u = 0; u < kAhead; ++u)
+      if (s0 + u * q.TR < min(len, q.s1)) r[u] = load8_raw<T>(x + (s0 + u * q.TR) * a.ldx, q.n);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int s = s0 + u * q.TR;
+      if (s >= q.s1) break;
+      float f[8] = {};
+      if (s < len) {
+        to_floats<T>(r[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (f[i] - mean[i]) * rstd[i] * gamma[i] + beta[i];
+        act8(a.act, f);
+      }
+      store8<T>(y + s * a.ldo, f, q.n);
     }
-    store8<T>(y + s * a.ldo, f, q.n);
   }
 }
 
@@ -440,29 +714,32 @@ template <class T>
 __global__ __launch_bounds__(kStream) void k_gn_bwd_stats(GnArgs a) {
   __shared__ float2 red[kStream * 8];
   using St = typename T::S;
-  const StreamPos q = stream_pos(a);
+  const StreamPos q = stream_pos(a, a.chunks, a.per_chunk);
   const int end = min(q.s1, sample_len(a, q.b));
   if (q.on) {
     const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
     const St* dy = static_cast<const St*>(a.dy) + static_cast<long>(q.b) * a.S * a.lddy + q.cv * 8;
-    float gamma[8], beta[8], mean[8], rstd[8], s1[8] = {}, s2[8] = {};
+    float gamma[8], beta[8], shift[8], rstd[8], s1[8] = {}, s2[8] = {};
     load_params(a, q.cv, gamma, beta);
-    load_stats(a, q, mean, rstd);
-    for (int s = q.s0 + q.tr; s < end; s += q.TR) {
-      float f[8], d[8];
-      to_floats<T>(load8_raw<T>(x + s * a.ldx, q.n), f);
-      to_floats<T>(load8_raw<T>(dy + s * a.lddy, q.n), d);
-      float u[8];
+    load_stats<true>(a, q, shift, rstd);
+    for (int s = q.s0 + q.tr; s < end; s += kAhead * q.TR) {
+      Raw8<T> rx[kAhead], rd[kAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] = (f[i] - mean[i]) * rstd[i];
-        u[i] = f[i] * gamma[i] + beta[i];
-      }
-      act8_grad(a.act, u, d);
+      for (int u = 0; u < kAhead; ++u)
+        if (s + u * q.TR < end) {
+          rx[u] = load8_raw<T>(x + (s + u * q.TR) * a.ldx, q.n);
+          rd[u] = load8_raw<T>(dy + (s + u * q.TR) * a.lddy, q.n);
+        }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s1[i] += d[i];
-        s2[i] += d[i] * f[i];
+      for (int u = 0; u < kAhead; ++u) {
+        if (s + u * q.TR >= end) break;
+        float f[8], d[8];
+        grad8<T, false>(a, rx[u], rd[u], shift, rstd, gamma, beta, f, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s1[i] += d[i];
+          s2[i] += d[i] * f[i];
+        }
       }
     }
 #pragma unroll
@@ -484,78 +761,89 @@ __global__ __launch_bounds__(kStream) void k_gn_bwd_stats(GnArgs a) {
   }
 }
 
-// One wavefront per (sample, group): (avg dh, avg dh xh) from the chunks' channel sums.
-__global__ __launch_bounds__(64) void k_gn_bwd_join(GnArgs a) {
-  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G, lane = threadIdx.x;
+// One workgroup per (sample, group): (avg dh, avg dh xh) from the chunks' channel sums.
+__global__ __launch_bounds__(256) void k_gn_bwd_join(GnArgs a) {
+  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G, t = threadIdx.x;
   const int len = sample_len(a, b), full = a.chunks * a.Cg;
   const float2* part = a.part + static_cast<long>(b) * a.chunks * a.C + g * a.Cg;
   float s1 = 0.f, s2 = 0.f;
-  for (int j = lane; j < full; j += 64) {
+  for (int j = t; j < full; j += 256) {
     const int ch = j / a.Cg, c = j - ch * a.Cg;
     const float2 v = part[static_cast<long>(ch) * a.C + c];
     const float gm = a.gamma ? a.gamma[g * a.Cg + c] : 1.f;
     s1 += gm * v.x;
     s2 += gm * v.y;
   }
-  for (int o = 32; o > 0; o >>= 1) s1 += __shfl_xor(s1, o), s2 += __shfl_xor(s2, o);
+  s1 = sum256(s1);
+  s2 = sum256(s2);
   const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
-  if (lane == 0) a.gsum[blockIdx.x] = make_float2(s1 * inv_n, s2 * inv_n);
+  if (t == 0) {
+    a.gsum[blockIdx.x] = s1 * inv_n;
+    a.gsum[static_cast<long>(a.B) * a.G + blockIdx.x] = s2 * inv_n;
+  }
 }
 
 template <class T>
 __global__ __launch_bounds__(kStream) void k_gn_bwd_apply(GnArgs a) {
   using St = typename T::S;
-  const StreamPos q = stream_pos(a);
+  const StreamPos q = stream_pos(a, a.pieces, a.per_piece);
   if (!q.on) return;
   const int len = sample_len(a, q.b);
   const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
   const St* dy = static_cast<const St*>(a.dy) + static_cast<long>(q.b) * a.S * a.lddy + q.cv * 8;
   St* dx = static_cast<St*>(a.out) + static_cast<long>(q.b) * a.S * a.ldo + q.cv * 8;
-  float gamma[8], beta[8], mean[8], rstd[8], m1[8], m2[8];
+  float gamma[8], beta[8], shift[8], rstd[8], m1[8], m2[8];
   load_params(a, q.cv, gamma, beta);
-  load_stats(a, q, mean, rstd);
+  load_stats<true>(a, q, shift, rstd);
+  load_groups(a, a.gsum + static_cast<long>(q.b) * a.G, q.cv, m1);
+  load_groups(a, a.gsum + (static_cast<long>(a.B) + q.b) * a.G, q.cv, m2);
+  for (int s0 = q.s0 + q.tr; s0 < q.s1; s0 += kAhead * q.TR) {
+    Raw8<T> rx[kAhead], rd[kAhead];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 v = a.gsum[static_cast<long>(q.b) * a.G + min(q.cv * 8 + i, a.C - 1) / a.Cg];
-    m1[i] = v.x;
-    m2[i] = v.y;
-  }
-  for (int s = q.s0 + q.tr; s < q.s1; s += q.TR) {
-    float f[8] = {};
-    if (s < len) {
-      float d[8];
-      to_floats<T>(load8_raw<T>(x + s * a.ldx, q.n), f);
-      to_floats<T>(load8_raw<T>(dy + s * a.lddy, q.n), d);
-      float u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] = (f[i] - mean[i]) * rstd[i];
-        u[i] = f[i] * gamma[i] + beta[i];
+    for (int u = 0; u < kAhead; ++u)
+      if (s0 + u * q.TR < min(len, q.s1)) {
+        rx[u] = load8_raw<T>(x + (s0 + u * q.TR) * a.ldx, q.n);
+        rd[u] = load8_raw<T>(dy + (s0 + u * q.TR) * a.lddy, q.n);
       }
-      act8_grad(a.act, u, d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = rstd[i] * (d[i] * gamma[i] - m1[i] - f[i] * m2[i]);
+    for (int u = 0; u < kAhead; ++u) {
+      const int s = s0 + u * q.TR;
+      if (s >= q.s1) break;
+      float f[8] = {};
+      if (s < len) {
+        float d[8];
+        grad8<T, false>(a, rx[u], rd[u], shift, rstd, gamma, beta, f, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = rstd[i] * (d[i] * gamma[i] - m1[i] - f[i] * m2[i]);
+      }
+      store8<T>(dx + s * a.ldo, f, q.n);
     }
-    store8<T>(dx + s * a.ldo, f, q.n);
   }
 }
 
-// dbeta[c], dgamma[c] = the sums over `rows` of part[row][c]: 16 channels per workgroup, 64
-// threads per channel whose sums are then added in order.
+// dbeta[c], dgamma[c] = the sums over `rows` of part[row][c]: 4 channels per workgroup, 256
+// threads per channel (thread t: rows t, t + 256, ...), whose sums are joined in a fixed tree.
 __global__ __launch_bounds__(1024) void k_gn_params(const float2* part, long rows, int C, float* dgamma, float* dbeta) {
-  __shared__ float2 red[64][16];
-  const int c = blockIdx.x * 16 + (threadIdx.x & 15), t = threadIdx.x >> 4;
+  __shared__ float2 red[256][4];
+  const int q = threadIdx.x & 3, c = blockIdx.x * 4 + q, t = threadIdx.x >> 2;
   float2 s = make_float2(0.f, 0.f);
   if (c < C)
-    for (long r = t; r < rows; r += 64) {
+#pragma unroll 4
+    for (long r = t; r < rows; r += 256) {
       const float2 v = part[r * C + c];
       s.x += v.x;
       s.y += v.y;
     }
-  red[t][threadIdx.x & 15] = s;
-  __syncthreads();
+  red[t][q] = s;
+  for (int h = 128; h > 0; h >>= 1) {
+    __syncthreads();
+    if (t < h) {
+      s.x += red[t + h][q].x;
+      s.y += red[t + h][q].y;
+      red[t][q] = s;
+    }
+  }
   if (t == 0 && c < C) {
-    for (int k = 1; k < 64; ++k) s.x += red[k][threadIdx.x].x, s.y += red[k][threadIdx.x].y;
     if (dbeta) dbeta[c] = s.x;
     if (dgamma) dgamma[c] = s.y;
   }
@@ -564,10 +852,12 @@ __global__ __launch_bounds__(1024) void k_gn_params(const float2* part, long row
 // ---------------------------------------------------------------------------------------
 // Plans and launches.
 // ---------------------------------------------------------------------------------------
+enum Form { WAVE, RESIDENT, STREAMED };
+
 struct GnPlan {
-  bool resident = false;
+  Form form = STREAMED;
   int NV = 1, TR = 0, team = 0, spw = 1, threads = 0, blocks_fwd = 0, blocks_bwd = 0;
-  int chunks = 1, per_chunk = 1, colblocks = 1, TC = 1;
+  int chunks = 1, per_chunk = 1, pieces = 1, per_piece = 1, colblocks = 1, TC = 1;
   size_t fwd_bytes = 0, bwd_bytes = 0;
 };
 
@@ -575,13 +865,26 @@ GnPlan plan_gn(int B, int S, int C, int G) {
   GnPlan p;
   const long CV = (C + 7l) / 8;
   const auto round256 = [](size_t n) { return (n + 255) / 256 * 256; };
+  // wavefront: powers of two all the way, at most eight vectors per lane
+  const long Cg = C / G;
+  const auto pow2 = [](long n) { return (n & (n - 1)) == 0; };
+  if (C % 8 == 0 && CV <= 64 && pow2(CV) && pow2(Cg) && S <= 8 * (64 / CV)) {
+    p.form = WAVE;
+    p.TR = static_cast<int>(64 / CV);
+    while (p.TR > 1 && p.TR / 2 >= S) p.TR /= 2;
+    p.team = static_cast<int>(p.TR * CV);
+    p.NV = 1;
+    while (p.NV * p.TR < S) p.NV *= 2;
+    p.threads = kWave;
+    p.spw = kWave / p.team;
+  }
   // resident: the smallest number of vectors per thread (1, 2, 4) that leaves a sample to at
   // most 256 threads, or, for larger samples, to kResident
   for (int limit : {256, kResident}) {
-    for (int nv = 1; nv <= 4 && !p.resident; nv *= 2) {
+    for (int nv = 1; nv <= 4 && p.form == STREAMED; nv *= 2) {
       const long tr = (S + nv - 1l) / nv;
       if (tr * CV <= limit) {
-        p.resident = true;
+        p.form = RESIDENT;
         p.NV = nv;
         p.TR = static_cast<int>(tr);
         p.team = static_cast<int>(tr * CV);
@@ -590,10 +893,10 @@ GnPlan plan_gn(int B, int S, int C, int G) {
       }
     }
   }
-  if (p.resident) {
+  if (p.form != STREAMED) {
     const long wgs = (B + p.spw - 1l) / p.spw;
     p.blocks_fwd = static_cast<int>(wgs);
-    p.blocks_bwd = static_cast<int>(std::min<long>(wgs, std::max<long>(256, std::min<long>(2048, (1l << 20) / C))));
+    p.blocks_bwd = static_cast<int>(std::min<long>(wgs, std::max<long>(256, std::min<long>(p.NV == 8 ? 512 : 1024, (1l << 20) / C))));
     p.bwd_bytes = round256(static_cast<size_t>(p.blocks_bwd) * C * sizeof(float2));
     return p;
   }
@@ -602,11 +905,19 @@ GnPlan plan_gn(int B, int S, int C, int G) {
   const long rows = kStream / p.TC;
   const long want = std::max<long>(1, 2048 / (static_cast<long>(B) * p.colblocks));
   const long most = std::max<long>(1, S / (rows * 8));  // at least eight positions per thread
-  p.chunks = static_cast<int>(std::min(want, most));
+  // and channel statistics of at most 8 MB where the samples alone do not take more
+  const long cap = std::max<long>(1, (1l << 20) / (static_cast<long>(B) * C));
+  p.chunks = static_cast<int>(std::min({want, most, cap}));
   p.per_chunk = static_cast<int>((S + static_cast<long>(p.chunks) - 1) / p.chunks);
   p.chunks = static_cast<int>((S + static_cast<long>(p.per_chunk) - 1) / p.per_chunk);
+  // the passes that use the statistics leave nothing behind, so their pieces are smaller: one
+  // batch of loads per thread, more where the launch would have over 2^22 workgroups
+  p.per_piece = static_cast<int>(std::min<long>(S, rows * kAhead));
+  while (static_cast<long>(B) * p.colblocks * ((S + static_cast<long>(p.per_piece) - 1) / p.per_piece) > (1l << 22) && p.per_piece < S)
+    p.per_piece = static_cast<int>(std::min<long>(S, 2l * p.per_piece));
+  p.pieces = static_cast<int>((S + static_cast<long>(p.per_piece) - 1) / p.per_piece);
   p.fwd_bytes = round256(static_cast<size_t>(B) * p.chunks * C * sizeof(float2));
-  p.bwd_bytes = p.fwd_bytes + round256(static_cast<size_t>(B) * G * sizeof(float2));
+  p.bwd_bytes = p.fwd_bytes + round256(static_cast<size_t>(B) * G * 2 * sizeof(float));
   return p;
 }
 
@@ -614,8 +925,8 @@ void fill(GnArgs& a, const GnPlan& p) {
   a.CV = (a.C + 7) / 8;
   a.Cg = a.C / a.G;
   a.TR = p.TR, a.team = p.team, a.spw = p.spw;
-  a.chunks = p.chunks, a.per_chunk = p.per_chunk, a.colblocks = p.colblocks, a.TC = p.TC;
-  if (p.resident) {
+  a.chunks = p.chunks, a.per_chunk = p.per_chunk, a.pieces = p.pieces, a.per_piece = p.per_piece, a.colblocks = p.colblocks, a.TC = p.TC;
+  if (p.form == RESIDENT) {
     a.E = p.TR * (a.Cg % 8 == 0 ? a.Cg / 8 : a.Cg);
     a.E1 = (a.E + 15) / 16;
   }
@@ -640,20 +951,35 @@ void launch_resident(const GnArgs& a, const GnPlan& p, hipStream_t st) {
 #undef GN_CASE
 }
 
+template <class T, bool BWD, bool VECG>
+void launch_wave(const GnArgs& a, const GnPlan& p, hipStream_t st) {
+  const dim3 grid(BWD ? p.blocks_bwd : p.blocks_fwd), block(kWave);
+#define GN_CASE(NV)                                                                                  \
+  case NV:                                                                                           \
+    if constexpr (BWD) hipLaunchKernelGGL((k_gn_bwd_wave<T, NV, VECG>), grid, block, 0, st, a);      \
+    else hipLaunchKernelGGL((k_gn_fwd_wave<T, NV, VECG>), grid, block, 0, st, a);                    \
+    break;
+  switch (p.NV) { GN_CASE(1) GN_CASE(2) GN_CASE(4) GN_CASE(8) }
+#undef GN_CASE
+}
+
 template <class T, bool BWD>
 void launch_gn(const GnArgs& a, const GnPlan& p, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(static_cast<long>(a.B) * p.chunks * p.colblocks)), block(kStream);
+  const dim3 pieces(static_cast<unsigned>(static_cast<long>(a.B) * p.pieces * p.colblocks));
   const dim3 groups(static_cast<unsigned>(static_cast<long>(a.B) * a.G));
-  if (p.resident) {
+  if (p.form == WAVE) {
+    a.Cg % 8 == 0 ? launch_wave<T, BWD, true>(a, p, st) : launch_wave<T, BWD, false>(a, p, st);
+  } else if (p.form == RESIDENT) {
     a.Cg % 8 == 0 ? launch_resident<T, BWD, true>(a, p, st) : launch_resident<T, BWD, false>(a, p, st);
   } else if constexpr (BWD) {
     hipLaunchKernelGGL((k_gn_bwd_stats<T>), grid, block, 0, st, a);
-    hipLaunchKernelGGL(k_gn_bwd_join, groups, dim3(64), 0, st, a);
-    hipLaunchKernelGGL((k_gn_bwd_apply<T>), grid, block, 0, st, a);
+    hipLaunchKernelGGL(k_gn_bwd_join, groups, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_gn_bwd_apply<T>), pieces, block, 0, st, a);
   } else {
     hipLaunchKernelGGL((k_gn_stats<T>), grid, block, 0, st, a);
-    hipLaunchKernelGGL(k_gn_join, groups, dim3(64), 0, st, a);
-    hipLaunchKernelGGL((k_gn_apply<T>), grid, block, 0, st, a);
+    hipLaunchKernelGGL(k_gn_join, groups, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_gn_apply<T>), pieces, block, 0, st, a);
   }
 }
 
@@ -769,16 +1095,16 @@ el_status el_group_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t
     a.lengths = lengths, a.gamma = gamma, a.beta = beta, a.act = act, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
     fill(a, p);
     const bool params = dgamma || dbeta;
-    if (p.resident) {
+    if (p.form != STREAMED) {
       a.part = params ? static_cast<float2*>(workspace) : nullptr;
     } else {
       a.part = static_cast<float2*>(workspace);
-      a.gsum = reinterpret_cast<float2*>(static_cast<char*>(workspace) + p.fwd_bytes);
+      a.gsum = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.fwd_bytes);
     }
     EL_TRY(run_gn<true>(fn, a, p, dtype, stream));
     if (params) {
-      const long rows = p.resident ? p.blocks_bwd : static_cast<long>(B) * p.chunks;
-      hipLaunchKernelGGL(k_gn_params, dim3(static_cast<unsigned>((C + 15) / 16)), dim3(1024), 0, stream, a.part, rows, C,
+      const long rows = p.form != STREAMED ? p.blocks_bwd : static_cast<long>(B) * p.chunks;
+      hipLaunchKernelGGL(k_gn_params, dim3(static_cast<unsigned>((C + 3) / 4)), dim3(1024), 0, stream, a.part, rows, C,
                          dgamma, dbeta);
       return check_launch(fn);
     }

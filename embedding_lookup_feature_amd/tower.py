@@ -90,14 +90,23 @@ def _mat(t: torch.Tensor, name: str, shape, dtype):
         return None, shape[1]
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, cs = t.stride()
+    if cs != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit column stride")
     # the row stride of one row (or none) says nothing
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
+
+
+def _stream(stream, t: torch.Tensor):
+    """The stream's handle; without one, torch's current stream on t's device (its raw handle:
+    a Stream object costs more than the rest of a small call's marshalling)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return ec._stream(stream)
 
 
 def _vec(t: torch.Tensor, name: str, n: int, dtype=torch.float32):
@@ -109,9 +118,10 @@ def _vec(t: torch.Tensor, name: str, n: int, dtype=torch.float32):
 
 
 def _rows_cols(t: torch.Tensor, name: str):
-    if t.dim() != 2:
+    s = t.shape
+    if len(s) != 2:
         raise ValueError(f"{name} must be 2-D")
-    return t.shape[0], t.shape[1]
+    return s
 
 
 def _workspace(ws, need: int, device):
@@ -125,12 +135,12 @@ def _workspace(ws, need: int, device):
 def act_dropout_fwd(x: torch.Tensor, y: torch.Tensor, act: str = "none", dropout: Dropout = None,
                     residual: torch.Tensor = None, stream=None):
     """y = residual + drop(act(x)); x, y, residual [M, N] of one dtype (fp32, fp16, bf16)."""
-    M, N = _rows_cols(x, "x")
-    xp, ldx = _mat(x, "x", (M, N), x.dtype)
-    rp, ldr = _mat(residual, "residual", (M, N), x.dtype)
-    yp, ldy = _mat(y, "y", (M, N), x.dtype)
+    shape = M, N = _rows_cols(x, "x")
+    xp, ldx = _mat(x, "x", shape, x.dtype)
+    rp, ldr = _mat(residual, "residual", shape, x.dtype)
+    yp, ldy = _mat(y, "y", shape, x.dtype)
     ec._check(lib().el_act_dropout_fwd(xp, ldx, rp, ldr, M, N, _act(act), _drop(dropout), yp, ldy,
-                                       ec._dtype(x, "x"), ec._stream(stream)))
+                                       ec._dtype(x, "x"), _stream(stream, x)))
     return y
 
 
@@ -138,12 +148,12 @@ def act_dropout_bwd(dy: torch.Tensor, x: torch.Tensor, dx: torch.Tensor, act: st
                     dropout: Dropout = None, stream=None):
     """dx = drop(dy * act'(x)), the mask of the forward with the same dropout (x may be None
     with act "none")."""
-    M, N = _rows_cols(dy, "dy")
-    dp, lddy = _mat(dy, "dy", (M, N), dy.dtype)
-    xp, ldx = _mat(x, "x", (M, N), dy.dtype)
-    op, lddx = _mat(dx, "dx", (M, N), dy.dtype)
+    shape = M, N = _rows_cols(dy, "dy")
+    dp, lddy = _mat(dy, "dy", shape, dy.dtype)
+    xp, ldx = _mat(x, "x", shape, dy.dtype)
+    op, lddx = _mat(dx, "dx", shape, dy.dtype)
     ec._check(lib().el_act_dropout_bwd(dp, lddy, xp, ldx, M, N, _act(act), _drop(dropout), op, lddx,
-                                       ec._dtype(dy, "dy"), ec._stream(stream)))
+                                       ec._dtype(dy, "dy"), _stream(stream, dy)))
     return dx
 
 
@@ -162,7 +172,7 @@ def dense_fwd(x: torch.Tensor, w: torch.Tensor, bias, y: torch.Tensor, act: str 
     contiguous, bias fp32 [N] or None, y / residual / pre [M, N], bf16 or fp16."""
     M, K = _rows_cols(x, "x")
     N = _rows_cols(w, "w")[0]
-    if tuple(w.shape) != (N, K) or w.dtype != x.dtype:
+    if w.shape != (N, K) or w.dtype is not x.dtype:
         raise ValueError(f"w must be [N, {K}] of {x.dtype}")
     xp, ldx = _mat(x, "x", (M, K), x.dtype)
     rp, ldr = _mat(residual, "residual", (M, N), x.dtype)
@@ -170,7 +180,7 @@ def dense_fwd(x: torch.Tensor, w: torch.Tensor, bias, y: torch.Tensor, act: str 
     yp, ldy = _mat(y, "y", (M, N), x.dtype)
     wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_fwd_workspace_bytes(M, K, N), x.device)
     ec._check(lib().el_dense_fwd(xp, ldx, M, K, ec._dev(w, "w"), _vec(bias, "bias", N), N, _act(act), _drop(dropout),
-                                 rp, ldr, pp, ldp, yp, ldy, ec._dtype(x, "x"), wsp, wsn, ec._stream(stream)))
+                                 rp, ldr, pp, ldp, yp, ldy, ec._dtype(x, "x"), wsp, wsn, _stream(stream, x)))
     return y
 
 
@@ -182,7 +192,7 @@ def dense_bwd(x: torch.Tensor, w: torch.Tensor, dz: torch.Tensor, dw: torch.Tens
     dz of the layer below (act, dropout and pre are that layer's).  dx, dres, dzb, pre [M, K]."""
     M, K = _rows_cols(x, "x")
     N = _rows_cols(w, "w")[0]
-    if tuple(w.shape) != (N, K) or w.dtype != x.dtype:
+    if w.shape != (N, K) or w.dtype is not x.dtype:
         raise ValueError(f"w must be [N, {K}] of {x.dtype}")
     xp, ldx = _mat(x, "x", (M, K), x.dtype)
     zp, ldz = _mat(dz, "dz", (M, N), x.dtype)
@@ -195,7 +205,7 @@ def dense_bwd(x: torch.Tensor, w: torch.Tensor, dz: torch.Tensor, dw: torch.Tens
         raise ValueError(f"dw must be [{N}, {K}]")
     ec._check(lib().el_dense_bwd(xp, ldx, M, K, ec._dev(w, "w"), N, zp, ldz, rp, ldr, dxp, lddx, _act(act),
                                  _drop(dropout), pp, ldp, bp, ldb, _vec(dw, "dw", N * K), _vec(db, "db", N),
-                                 ec._dtype(x, "x"), wsp, wsn, ec._stream(stream)))
+                                 ec._dtype(x, "x"), wsp, wsn, _stream(stream, x)))
     return dx, dw, db
 
 
@@ -228,7 +238,7 @@ def group_norm_fwd(x: torch.Tensor, gamma, beta, y: torch.Tensor, mean: torch.Te
     ec._check(lib().el_group_norm_fwd(xp, ldx, B, S, C, G, _vec(lengths, "lengths", B, torch.int32),
                                       _vec(gamma, "gamma", C), _vec(beta, "beta", C), float(eps), _act(act), yp, ldy,
                                       _vec(mean, "mean", B * G), _vec(rstd, "rstd", B * G), ec._dtype(x, "x"), wsp,
-                                      wsn, ec._stream(stream)))
+                                      wsn, _stream(stream, x)))
     return y
 
 
@@ -245,5 +255,5 @@ def group_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma, beta, mean: torch.T
     ec._check(lib().el_group_norm_bwd(dp, lddy, xp, ldx, B, S, C, G, _vec(lengths, "lengths", B, torch.int32),
                                       _vec(gamma, "gamma", C), _vec(beta, "beta", C), _vec(mean, "mean", B * G),
                                       _vec(rstd, "rstd", B * G), _act(act), op, lddx, _vec(dgamma, "dgamma", C),
-                                      _vec(dbeta, "dbeta", C), ec._dtype(x, "x"), wsp, wsn, ec._stream(stream)))
+                                      _vec(dbeta, "dbeta", C), ec._dtype(x, "x"), wsp, wsn, _stream(stream, x)))
     return dx, dgamma, dbeta
