@@ -46,8 +46,8 @@ struct GemmArgs {
 
 // ---------------------------------------------------------------------------------------
 // Epilogue of eight columns c .. c+7 (the first n of them exist) of row r, from the product v;
-// `add` and `pre` are the eight values already loaded.  Non-temporal stores (NT) where the
-// outputs are larger than the caches.
+// `add` and `pre` are the eight values already loaded.  Non-temporal accesses (NT) where the
+// arrays are larger than the caches.
 // ---------------------------------------------------------------------------------------
 template <class T, bool NT>
 __device__ inline void put8(uint16_t* p, const float (&f)[8], int n) {
@@ -62,21 +62,26 @@ __device__ inline void put8(uint16_t* p, const float (&f)[8], int n) {
   }
 }
 
+template <class T, bool NT>
+__device__ inline Raw8<T> get8(const uint16_t* p, int n) {
+  if (!NT || n < 8) return load8_raw<T>(p, n);
+  Raw8<T> r;
+  r.v[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+  return r;
+}
+
 template <class T, int PROD, bool NT>
 __device__ inline void epilogue8(const GemmArgs& a, uint64_t offset, long r, int c, int n, float (&v)[8],
-                                 const float (&bias)[8], const Raw8<T>& add, const Raw8<T>& pre) {
+                                 const Raw8<T>& add, const Raw8<T>& pre) {
   float f[8];
+  if (a.add) to_floats<T>(add, f);
   if constexpr (PROD == FWD) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += bias[e];
     if (a.aux) put8<T, NT>(a.aux + r * a.ldaux + c, v, n);
     act8(a.act, v);
   } else {
-    if (a.add) {
-      to_floats<T>(add, f);
+    if (a.add)
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += f[e];
-    }
     put8<T, NT>(a.out + r * a.ldo + c, v, n);
     if (!a.aux) return;
     if (a.act != EL_ACT_NONE) {
@@ -84,21 +89,21 @@ __device__ inline void epilogue8(const GemmArgs& a, uint64_t offset, long r, int
       act8_grad(a.act, f, v);
     }
   }
+  float scale = 1.f;
   if (a.drop.top) {
     const u32x4 bits = philox8(static_cast<uint32_t>(c) >> 3, static_cast<uint32_t>(r), offset, a.drop.k0, a.drop.k1);
+    scale = a.drop.scale;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = keep_of(bits, e, a.drop.top) ? v[e] * a.drop.scale : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = keep_of(bits, e, a.drop.top) ? v[e] : 0.f;
   }
-  if constexpr (PROD == FWD) {
-    if (a.add) {
-      to_floats<T>(add, f);
+  if (PROD == FWD && a.add) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += f[e];
-    }
-    put8<T, NT>(a.out + r * a.ldo + c, v, n);
-  } else {
-    put8<T, NT>(a.aux + r * a.ldaux + c, v, n);
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], scale, f[e]);
+  } else if (a.drop.top) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= scale;
   }
+  put8<T, NT>((PROD == FWD ? a.out : a.aux) + r * (PROD == FWD ? a.ldo : a.ldaux) + c, v, n);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -230,27 +235,29 @@ __device__ inline int xcd_order(int bid, int n) {
 }
 
 // Tile shapes: WR x WC wavefronts own BR x BC outputs of a workgroup; ST stages of 64 reductions.
-template <int BR_, int BC_, int WR_, int WC_, int ST_, int WPE_, bool NT_>
+template <int BR_, int BC_, int WR_, int WC_, int ST_, int WPE_, bool NT_, int AHEAD_>
 struct Cfg {
   static constexpr int BR = BR_, BC = BC_, BK = 64, WR = WR_, WC = WC_, ST = ST_, NW = WR * WC;
   static constexpr int FR = BR / WR / 32, FC = BC / WC / 32;  // 32 x 32 blocks per wavefront
   static constexpr int WPE = WPE_;                            // wavefronts per SIMD the registers allow
-  static constexpr bool NT = NT_;
+  static constexpr bool NT = NT_;                             // non-temporal epilogue
+  static constexpr int AHEAD = AHEAD_;                        // row blocks whose residual / pre are on their way
+  static constexpr int PITCH = FC * 32 + 4;                   // floats per row of the epilogue's LDS blocks
+  static constexpr int LDS = std::max(ST * (BR + BC) * BK * 2, NW * 32 * PITCH * 4);
 };
-using CfgL = Cfg<256, 256, 2, 4, 2, 2, true>;   // 128 KB of LDS, one workgroup per CU
-using CfgM = Cfg<128, 128, 2, 2, 2, 2, false>;  // 64 KB, two per CU
-using CfgS = Cfg<64, 64, 2, 2, 4, 2, false>;    // 64 KB, two per CU
+using CfgL = Cfg<256, 256, 4, 4, 2, 4, true, 1>;   // 136 KB of LDS, one workgroup of 16 wavefronts per CU
+using CfgM = Cfg<128, 128, 2, 2, 2, 2, false, 2>;  // 64 KB, two per CU
+using CfgS = Cfg<64, 64, 2, 2, 4, 2, false, 1>;    // 64 KB, two per CU
 
+// One tile (of one split): `lid` in tiles of all splits, in the order that shares panels.
 template <class T, class C, int PROD>
-__global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
+__device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds) {
   constexpr int NW = C::NW, FR = C::FR, FC = C::FC, BK = C::BK, ST = C::ST, WC = C::WC;
   using OP = Operand<C::BR, BK, PROD != WGRAD, NW>;
   using OQ = Operand<C::BC, BK, PROD == FWD, NW>;
   constexpr int SB = OP::BYTES + OQ::BYTES, LOADS = OP::N + OQ::N;
-  __shared__ __attribute__((aligned(1024))) char lds[ST * SB];
   const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = static_cast<int>(uniform(threadIdx.x >> 6));
-  const int lid = xcd_order(blockIdx.x, gridDim.x);
   const int split = lid / a.tiles, t = lid - split * a.tiles;
   const int tr = t / a.tiles_c, tc = t - tr * a.tiles_c;
   const int row0 = tr * C::BR, col0 = tc * C::BC;
@@ -268,10 +275,17 @@ __global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
     else oq.load(mine + slot + OP::BYTES, m - OP::N, rq);
   };
   f32x16 acc[FC][FR];
+  // register 4 g + e of acc[i][j]: column 32 i + 8 g + 4 half + e of row 32 j + l32; the forward's
+  // accumulators start from the bias
 #pragma unroll
-  for (int i = 0; i < FC; ++i)
+  for (int i = 0; i < FC; ++i) {
+    f32x16 z = f32x16{};
+    if (PROD == FWD && a.bias)
 #pragma unroll
-    for (int j = 0; j < FR; ++j) acc[i][j] = f32x16{};
+      for (int k = 0; k < 16; ++k) z[k] = a.bias[min(col0 + (wc * FC + i) * 32 + acc_row(k, lane), a.C - 1)];
+#pragma unroll
+    for (int j = 0; j < FR; ++j) acc[i][j] = z;
+  }
   float dbs[FR] = {};
 
   // Fill the ring.  Stages past the reduction's end load zeros without touching memory, so the
@@ -357,7 +371,6 @@ __global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
         if (half == 0 && r < a.R) a.dbp[((static_cast<long>(split) * a.tiles_c + tc) * WC + wc) * a.R + r] = s;
       }
     }
-    // register 4 g + e of acc[i][j]: column 32 i + 8 g + 4 half + e, row 32 j + l32
 #pragma unroll
     for (int j = 0; j < FR; ++j) {
       const int r = row0 + (wr * FR + j) * 32 + l32;
@@ -383,25 +396,21 @@ __global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
     // Accumulators go through LDS (each wavefront's own 32 x (32 FC) floats at a time), so that a
     // lane gets eight consecutive columns: they share one call of the mask's generator, and a
     // row's accesses to residual, pre, y, ... are whole cache lines.
-    constexpr int WCOLS = FC * 32, GR = WCOLS / 8, RPP = 64 / GR, PASS = 32 / RPP, PITCH = WCOLS + 4;
-    static_assert(NW * 32 * PITCH * 4 <= ST * SB, "the wavefronts' blocks fit into the ring");
-    constexpr int AHEAD = FR < 2 ? FR : 2;  // row blocks whose residual / pre are on their way
+    constexpr int WCOLS = FC * 32, GR = WCOLS / 8, RPP = 64 / GR, PASS = 32 / RPP, PITCH = C::PITCH, AHEAD = C::AHEAD;
+    static_assert(AHEAD <= FR, "no block is fetched twice");
     const uint64_t offset = a.drop.top ? drop_offset(a.drop) : 0;
     float* blk = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
     const int gr = lane % GR, rr = lane / GR;
     const int c = col0 + wc * WCOLS + gr * 8, n = min(8, a.C - c);
-    float bias[8] = {};
-    if (PROD == FWD && a.bias && n > 0)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) bias[e] = a.bias[min(c + e, a.C - 1)];
     Raw8<T> add[AHEAD][PASS], pre[AHEAD][PASS];
     const auto fetch = [&](int j) {
 #pragma unroll
       for (int s = 0; s < PASS; ++s) {
         const long r = row0 + (wr * FR + j) * 32 + rr + s * RPP;
         if (r < a.R && n > 0) {
-          if (a.add) add[j % AHEAD][s] = load8_raw<T>(a.add + r * a.ldadd + c, n);
-          if (PROD == DGRAD && a.pre) pre[j % AHEAD][s] = load8_raw<T>(a.pre + r * a.ldpre + c, n);
+          constexpr bool NTL = C::NT && PROD == DGRAD;
+          if (a.add) add[j % AHEAD][s] = get8<T, NTL>(a.add + r * a.ldadd + c, n);
+          if (PROD == DGRAD && a.pre) pre[j % AHEAD][s] = get8<T, NTL>(a.pre + r * a.ldpre + c, n);
         }
       }
     };
@@ -424,12 +433,37 @@ __global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
         const float4 lo = *reinterpret_cast<const float4*>(blk + (rr + s * RPP) * PITCH + gr * 8);
         const float4 hi = *reinterpret_cast<const float4*>(blk + (rr + s * RPP) * PITCH + gr * 8 + 4);
         v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-        if (r < a.R && n > 0) epilogue8<T, PROD, C::NT>(a, offset, r, c, n, v, bias, add[j % AHEAD][s], pre[j % AHEAD][s]);
+        if (r < a.R && n > 0) epilogue8<T, PROD, C::NT>(a, offset, r, c, n, v, add[j % AHEAD][s], pre[j % AHEAD][s]);
       }
       wave_sync();
       if (j + AHEAD < FR) fetch(j + AHEAD);
     }
   }
+}
+
+template <class T, class C, int PROD>
+__global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  dense_tile<T, C, PROD>(a, xcd_order(blockIdx.x, gridDim.x), lds);
+}
+
+// The two products of the backward in one launch: nd tiles of the data gradient `d`, and the
+// weight gradient `w`'s, which do not depend on them.  Each XCD gets its run of both, the weight
+// gradient's long tiles first, so that the data gradient's short ones fill the gaps behind them
+// and one tail replaces two (65536 x 1024 x 1024: 374 us; two launches 383; every third
+// workgroup a weight gradient's 394).
+template <class T, class CD, class CW>
+__global__ __launch_bounds__(CD::NW * 64, CD::WPE) void k_dense_bwd(GemmArgs d, GemmArgs w, int nd) {
+  static_assert(CD::NW == CW::NW, "one workgroup shape");
+  __shared__ __attribute__((aligned(1024))) char lds[std::max(CD::LDS, CW::LDS)];
+  const int n = gridDim.x, x = blockIdx.x & 7, i = blockIdx.x >> 3;
+  const int count = (n >> 3) + (x < (n & 7)), first = x * (n >> 3) + min(x, n & 7);  // this XCD's workgroups
+  const int dcount = (nd >> 3) + (x < (nd & 7)), dfirst = x * (nd >> 3) + min(x, nd & 7);
+  const int wcount = count - dcount;
+  if (i < wcount)
+    dense_tile<T, CW, WGRAD>(w, first - dfirst + i, lds);
+  else
+    dense_tile<T, CD, DGRAD>(d, dfirst + i - wcount, lds);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -473,17 +507,17 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_dense_few(GemmArgs a) {
   if (threadIdx.x >= 128) return;
   const int r = row0 + threadIdx.x / 4, c = col0 + threadIdx.x % 4 * 8, n = min(8, a.C - c);
   if (r >= a.R || n <= 0) return;
-  float v[8] = {}, bias[8] = {};
+  float v[8] = {};
   Raw8<T> add;
   if (a.add) add = load8_raw<T>(a.add + r * a.ldadd + c, n);
   if (a.bias)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) bias[e] = a.bias[min(c + e, a.C - 1)];
+    for (int e = 0; e < 8; ++e) v[e] = a.bias[min(c + e, a.C - 1)];
 #pragma unroll 4
   for (int w = 0; w < kFewWaves; ++w)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += lds[w][threadIdx.x / 4 * PITCH + threadIdx.x % 4 * 8 + e];
-  epilogue8<T, FWD, false>(a, a.drop.top ? drop_offset(a.drop) : 0, r, c, n, v, bias, add, add);
+  epilogue8<T, FWD, false>(a, a.drop.top ? drop_offset(a.drop) : 0, r, c, n, v, add, add);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -498,19 +532,24 @@ __global__ __launch_bounds__(256) void k_pack(const uint16_t* src, long ld, long
   reinterpret_cast<u32x4*>(dst)[i] = load8_raw<T>(src + r * ld + v * 8, cols - v * 8).v[0];
 }
 
-// out[i] = the sum over p < parts of part[p][i], VEC consecutive i per thread: 16 threads share
-// one vector's parts (thread s: parts s, s + 16, ...), their sums are added in thread order.
+// out[i] = the sum over p < parts of part[p][i], i < n: 16 threads share one vector's parts
+// (thread s: parts s, s + 16, ...), their sums are added in thread order.
+struct Sums {
+  const float* part;
+  float* out;
+  long n;
+  int parts;
+};
 template <int VEC>
-__global__ __launch_bounds__(256) void k_sum_parts(const float* part, long n, int parts, float* out) {
-  __shared__ float red[16][16 * VEC + 1];
+__device__ inline void sum_parts(const Sums& a, long blk, float (&red)[16][65]) {
   const int cv = threadIdx.x & 15, s = threadIdx.x >> 4;
-  const long c = (static_cast<long>(blockIdx.x) * 16 + cv) * VEC;
+  const long c = (blk * 16 + cv) * VEC;
   float v[VEC] = {};
-  if (c < n)
+  if (c < a.n)
 #pragma unroll 4
-    for (int p = s; p < parts; p += 16) {
+    for (int p = s; p < a.parts; p += 16) {
       float x[VEC];
-      __builtin_memcpy(x, __builtin_assume_aligned(part + p * n + c, 4 * VEC), sizeof x);
+      __builtin_memcpy(x, __builtin_assume_aligned(a.part + p * a.n + c, 4 * VEC), sizeof x);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] += x[e];
     }
@@ -518,13 +557,21 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* part, long n, in
   for (int e = 0; e < VEC; ++e) red[s][cv * VEC + e] = v[e];
   __syncthreads();
   if (threadIdx.x < 16 * VEC) {
-    const long i = static_cast<long>(blockIdx.x) * 16 * VEC + threadIdx.x;
-    if (i < n) {
+    const long i = blk * 16 * VEC + threadIdx.x;
+    if (i < a.n) {
       float t = red[0][threadIdx.x];
-      for (int k = 1; k < 16 && k < parts; ++k) t += red[k][threadIdx.x];
-      out[i] = t;
+      for (int k = 1; k < 16 && k < a.parts; ++k) t += red[k][threadIdx.x];
+      a.out[i] = t;
     }
   }
+}
+// The weight gradient's partials (the first `blocks` workgroups) and the bias gradient's.
+template <int VEC>
+__global__ __launch_bounds__(256) void k_sum_parts(Sums w, Sums b, int blocks) {
+  __shared__ float red[16][65];
+  const int blk = blockIdx.x;
+  if (blk < blocks) sum_parts<VEC>(w, blk, red);
+  else sum_parts<1>(b, blk - blocks, red);
 }
 
 __global__ __launch_bounds__(256) void k_zero(float* p, long n) {
@@ -551,8 +598,10 @@ Shape plan_tiles(long R, long C) {
   return SHAPE_S;
 }
 
-// Weight gradient: tiles x batch slices, at least 256 rows to a slice; the largest tile that
-// fills most of the CUs.
+// Weight gradient: tiles x batch slices that fill the CUs once (L) or twice.  A slice has to be
+// long enough to pay for its fp32 partial tile, which is written and read again: at 1024 x 1024
+// the shapes meet near 2048 rows a slice for L (16384 rows: L 63 us, M 55; 65536: 156, 167) and
+// near 512 for M (4096 rows: M 32, S 33; 2048: 31, 27).
 struct WgradPlan {
   Shape shape;
   int splits, per, db_rows;
@@ -563,9 +612,10 @@ WgradPlan plan_wgrad(int M, int K, int N) {
   long splits = 1;
   for (Shape s : {SHAPE_L, SHAPE_M, SHAPE_S}) {
     const long tiles = ceil_div(N, kEdge[s]) * ceil_div(K, kEdge[s]);
-    splits = std::min(std::max<long>(1, 256 / tiles), ceil_div(M, 256));
+    splits = std::max<long>(1, (s == SHAPE_L ? 256 : 512) / tiles);
     p.shape = s;
-    if (tiles * splits >= 192) break;
+    if (s == SHAPE_S) splits = std::min(splits, ceil_div(M, 256));
+    else if (M / splits >= (s == SHAPE_L ? 2048 : 512)) break;
   }
   p.per = static_cast<int>(ceil_div(ceil_div(M, splits), 64) * 64);
   p.splits = static_cast<int>(ceil_div(M, p.per));
@@ -576,13 +626,22 @@ WgradPlan plan_wgrad(int M, int K, int N) {
   return p;
 }
 
-template <class T, class C, int PROD>
-el_status launch_tiles(const char* fn, GemmArgs a, int splits, hipStream_t st) {
+// Tiles of `a` (all splits) in shape C; 0 if there are too many for one launch.
+template <class C>
+int set_tiles(GemmArgs& a, int splits) {
   a.tiles_c = static_cast<int>(ceil_div(a.C, C::BC));
   const long tiles = ceil_div(a.R, C::BR) * a.tiles_c;
-  if (tiles * splits >= (1l << 22)) return tower::unsupported(fn, "the output has too many tiles for one launch");
+  if (tiles * splits >= (1l << 21)) return 0;
   a.tiles = static_cast<int>(tiles);
-  hipLaunchKernelGGL((k_dense<T, C, PROD>), dim3(static_cast<unsigned>(tiles * splits)), dim3(C::NW * 64), 0, st, a);
+  return a.tiles * splits;
+}
+el_status too_many_tiles(const char* fn) { return tower::unsupported(fn, "the output has too many tiles for one launch"); }
+
+template <class T, class C, int PROD>
+el_status launch_tiles(const char* fn, GemmArgs a, int splits, hipStream_t st) {
+  const int n = set_tiles<C>(a, splits);
+  if (!n) return too_many_tiles(fn);
+  hipLaunchKernelGGL((k_dense<T, C, PROD>), dim3(n), dim3(C::NW * 64), 0, st, a);
   return check_launch(fn);
 }
 template <class T, int PROD>
@@ -590,6 +649,25 @@ el_status launch_product(const char* fn, const GemmArgs& a, Shape s, int splits,
   return s == SHAPE_L   ? launch_tiles<T, CfgL, PROD>(fn, a, splits, st)
          : s == SHAPE_M ? launch_tiles<T, CfgM, PROD>(fn, a, splits, st)
                         : launch_tiles<T, CfgS, PROD>(fn, a, splits, st);
+}
+
+template <class T, class CD, class CW>
+el_status launch_both(const char* fn, GemmArgs d, GemmArgs w, int splits, hipStream_t st) {
+  const int nd = set_tiles<CD>(d, 1), nw = set_tiles<CW>(w, splits);
+  if (!nd || !nw) return too_many_tiles(fn);
+  hipLaunchKernelGGL((k_dense_bwd<T, CD, CW>), dim3(nd + nw), dim3(CD::NW * 64), 0, st, d, w, nd);
+  return check_launch(fn);
+}
+// The backward's two products: in one launch where their workgroups have one shape.
+template <class T>
+el_status launch_backward(const char* fn, const GemmArgs& d, Shape sd, const GemmArgs& w, Shape sw, int splits, hipStream_t st) {
+  if (sd == SHAPE_L && sw == SHAPE_L) return launch_both<T, CfgL, CfgL>(fn, d, w, splits, st);
+  if (sd == SHAPE_M && sw == SHAPE_M) return launch_both<T, CfgM, CfgM>(fn, d, w, splits, st);
+  if (sd == SHAPE_M && sw == SHAPE_S) return launch_both<T, CfgM, CfgS>(fn, d, w, splits, st);
+  if (sd == SHAPE_S && sw == SHAPE_M) return launch_both<T, CfgS, CfgM>(fn, d, w, splits, st);
+  if (sd == SHAPE_S && sw == SHAPE_S) return launch_both<T, CfgS, CfgS>(fn, d, w, splits, st);
+  const el_status s = launch_product<T, DGRAD>(fn, d, sd, 1, st);
+  return s == EL_OK ? launch_product<T, WGRAD>(fn, w, sw, splits, st) : s;
 }
 
 // A forward of few outputs: fewer than 64 tiles of 64 x 64.
@@ -617,11 +695,13 @@ el_status pack(const char* fn, const uint16_t** p, long* ld, long rows, int cols
   return check_launch(fn);
 }
 
-void launch_sum(const float* part, long n, int parts, float* out, hipStream_t st) {
-  if (n % 4 == 0)
-    hipLaunchKernelGGL((k_sum_parts<4>), dim3(static_cast<unsigned>(ceil_div(n, 64))), dim3(256), 0, st, part, n, parts, out);
-  else
-    hipLaunchKernelGGL((k_sum_parts<1>), dim3(static_cast<unsigned>(ceil_div(n, 16))), dim3(256), 0, st, part, n, parts, out);
+void launch_sums(const Sums& w, const Sums& b, hipStream_t st) {
+  const bool vec = w.n % 4 == 0;
+  const long nw = ceil_div(w.n, vec ? 64 : 16), nb = ceil_div(b.n, 16);
+  if (nw + nb == 0) return;
+  const dim3 grid(static_cast<unsigned>(nw + nb));
+  if (vec) hipLaunchKernelGGL((k_sum_parts<4>), grid, dim3(256), 0, st, w, b, static_cast<int>(nw));
+  else hipLaunchKernelGGL((k_sum_parts<1>), grid, dim3(256), 0, st, w, b, static_cast<int>(nw));
 }
 
 bool dense_sizes_ok(int32_t M, int32_t K, int32_t N) {
@@ -687,24 +767,25 @@ el_status run_bwd(const char* fn, const uint16_t* x, long ldx, int M, int K, con
                   long lddz, GemmArgs a, float* dw, float* db, char* ws, hipStream_t st) {
   EL_TRY(pack(fn, &dz, &lddz, M, N, &ws, st));
   EL_TRY(pack(fn, &x, &ldx, M, K, &ws, st));
-  if (a.out) {
-    long ldw = K;
-    EL_TRY(pack(fn, &w, &ldw, N, K, &ws, st));
-    a.P = dz, a.ldp = lddz, a.Q = w, a.ldq = ldw, a.R = M, a.C = K, a.red = N;
-    // a copied dz has rows that end in zeros; the rows of w behind N read as zeros
-    a.red = a.per_split = static_cast<int>(pad8(N));
-    a.red_q = N;
-    EL_TRY((launch_product<T, DGRAD>(fn, a, plan_tiles(M, K), 1, st)));
-  }
+  long ldw = K;
+  if (a.out) EL_TRY(pack(fn, &w, &ldw, N, K, &ws, st));
   const WgradPlan pl = plan_wgrad(M, K, N);
   GemmArgs b{};
   b.P = dz, b.ldp = lddz, b.Q = x, b.ldq = ldx, b.R = N, b.C = K, b.red = b.red_q = M, b.per_split = pl.per;
   b.part = pl.splits > 1 ? reinterpret_cast<float*>(ws) : dw;
   float* dbp = reinterpret_cast<float*>(ws + pl.dw_bytes);
   b.dbp = db ? dbp : nullptr;
-  EL_TRY((launch_product<T, WGRAD>(fn, b, pl.shape, pl.splits, st)));
-  if (pl.splits > 1) launch_sum(b.part, static_cast<long>(N) * K, pl.splits, dw, st);
-  if (db) launch_sum(dbp, N, pl.db_rows, db, st);
+  if (a.out) {
+    // a copied dz has rows that end in zeros; the rows of w behind N read as zeros
+    a.P = dz, a.ldp = lddz, a.Q = w, a.ldq = ldw, a.R = M, a.C = K;
+    a.red = a.per_split = static_cast<int>(pad8(N));
+    a.red_q = N;
+    EL_TRY(launch_backward<T>(fn, a, plan_tiles(M, K), b, pl.shape, pl.splits, st));
+  } else {
+    EL_TRY((launch_product<T, WGRAD>(fn, b, pl.shape, pl.splits, st)));
+  }
+  launch_sums(Sums{b.part, dw, pl.splits > 1 ? static_cast<long>(N) * K : 0, pl.splits},
+              Sums{dbp, db, db ? static_cast<long>(N) : 0, pl.db_rows}, st);
   return check_launch(fn);
 }
 

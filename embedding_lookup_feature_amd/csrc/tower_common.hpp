@@ -105,7 +105,7 @@ __device__ inline void store8(typename T::S* p, const float* f, int n) {
 // q = Phi(-|u|) and ex = exp(-u^2 / 2) = sqrt(2 pi) phi(u): the normal distribution function by
 // the rational form 7.1.26 of Abramowitz and Stegun's Handbook (absolute error 1.5e-7 on erf,
 // about one fp32 step of values near 1).  It shares its exponential with the derivative, and
-// u Phi(u) = max(u, 0) - |u| q takes 12 plain instructions, one exp2 and one reciprocal.
+// u Phi(u) = max(u, 0) - |u| q takes 13 plain instructions, one exp2 and one reciprocal.
 __device__ inline float normal_tail(float u, float& ex) {
   const float t = __builtin_amdgcn_rcpf(fmaf(0.23164189f, fabsf(u), 1.f));
   ex = __builtin_amdgcn_exp2f(u * u * -0.72134752044448170f);
@@ -124,8 +124,9 @@ __device__ inline float act_f(float u) {
   if constexpr (ACT == EL_ACT_RELU) return u > 0.f ? u : 0.f;
   if constexpr (ACT == EL_ACT_GELU) {
     float ex;
-    const float q = normal_tail(u, ex);
-    return fmaf(-fabsf(u), q, u < 0.f ? 0.f : u);
+    // Phi(-64) is 0 in fp32, and no infinity meets it; minimum and maximum keep NaN
+    const float a = __builtin_elementwise_minimum(fabsf(u), 64.f);
+    return fmaf(-a, normal_tail(a, ex), __builtin_elementwise_maximum(u, 0.f));
   }
   if constexpr (ACT == EL_ACT_SILU) return u * sigmoid(u);
   return u;
