@@ -22,63 +22,50 @@ struct RowsArgs {
 
 constexpr int kThreads = 256;
 
-// `U` groups of eight columns per thread, `kThreads` groups apart; all loads are issued before
-// the first use.
-template <class T, int ACT, bool BWD, int U>
+template <class T, int ACT, bool BWD>
 __global__ __launch_bounds__(kThreads) void k_act_dropout(RowsArgs p) {
   using S = typename T::S;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * U);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads;
+  if (first + threadIdx.x >= p.items) return;
   const int64_t row0 = first / p.groups;  // uniform: one 64-bit division per workgroup
-  const uint32_t rem = static_cast<uint32_t>(first - row0 * p.groups);
-  const S* a = static_cast<const S*>(p.a);
-  const S* b = static_cast<const S*>(p.b);
-  const uint64_t offset = p.drop.top ? drop_offset(p.drop) : 0;
-  Raw8<T> ra[U], rb[U];
-  int64_t row[U];
-  uint32_t grp[U];
+  const uint32_t local = static_cast<uint32_t>(first - row0 * p.groups) + threadIdx.x;
+  const uint32_t dr = local / static_cast<uint32_t>(p.groups), grp = local - dr * p.groups;
+  const int64_t row = row0 + dr;
+  const int n = p.N - static_cast<int>(grp) * 8;
+  Raw8<T> ra = load8_raw<T>(static_cast<const S*>(p.a) + row * p.lda + grp * 8l, n), rb;
+  if (p.b) rb = load8_raw<T>(static_cast<const S*>(p.b) + row * p.ldb + grp * 8l, n);
+  float x[8], r[8];
+  to_floats<T>(ra, x);
+  if (p.b) to_floats<T>(rb, r);
+  if constexpr (!BWD) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const uint32_t local = rem + threadIdx.x + u * kThreads;
-    const uint32_t dr = local / static_cast<uint32_t>(p.groups);
-    row[u] = row0 + dr;
-    grp[u] = local - dr * p.groups;
-    if (first + threadIdx.x + u * kThreads < p.items) {
-      const int n = p.N - static_cast<int>(grp[u]) * 8;
-      ra[u] = load8_raw<T>(a + row[u] * p.lda + grp[u] * 8l, n);
-      if (b) rb[u] = load8_raw<T>(b + row[u] * p.ldb + grp[u] * 8l, n);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = act_f<ACT>(x[i]);
+  } else if constexpr (ACT != EL_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= act_df<ACT>(r[i]);
   }
+  if (p.drop.top) {
+    const u32x4 bits = philox8(grp, static_cast<uint32_t>(row), drop_offset(p.drop), p.drop.k0, p.drop.k1);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (first + threadIdx.x + u * kThreads >= p.items) continue;
-    const int n = p.N - static_cast<int>(grp[u]) * 8;
-    float x[8], r[8], y[8];
-    to_floats<T>(ra[u], x);
-    if (b) to_floats<T>(rb[u], r);
-    u32x4 bits = {};
-    if (p.drop.top) bits = philox8(grp[u], static_cast<uint32_t>(row[u]), offset, p.drop.k0, p.drop.k1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = BWD ? (ACT == EL_ACT_NONE ? x[i] : x[i] * act_df<ACT>(r[i])) : act_f<ACT>(x[i]);
-      if (p.drop.top) v = keep_of(bits, i, p.drop.top) ? v * p.drop.scale : 0.f;
-      if (!BWD && b) v += r[i];
-      y[i] = v;
-    }
-    store8<T>(static_cast<S*>(p.y) + row[u] * p.ldy + grp[u] * 8l, y, n);
+    for (int i = 0; i < 8; ++i) x[i] = keep_of(bits, i, p.drop.top) ? x[i] * p.drop.scale : 0.f;
   }
+  if (!BWD && p.b)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] += r[i];
+  store8<T>(static_cast<S*>(p.y) + row * p.ldy + grp * 8l, x, n);
 }
 
 template <class T, bool BWD>
 void launch_typed(const RowsArgs& p, uint32_t act, hipStream_t st) {
   tower::with_act(act, [&](auto A) {
-    constexpr int ACT = decltype(A)::value;
     const int64_t blocks = (p.items + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL((k_act_dropout<T, ACT, BWD, 1>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, p);
+    hipLaunchKernelGGL((k_act_dropout<T, decltype(A)::value, BWD>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
+                       st, p);
   });
 }
 
 el_status launch_rows(const char* fn, RowsArgs p, int M, uint32_t act, el_dtype dtype, bool bwd, hipStream_t st) {
-  p.groups = (p.N + 7) / 8;
+  p.groups = p.N / 8 + (p.N % 8 != 0);
   p.items = static_cast<int64_t>(M) * p.groups;
   if (p.items > 0xffffff00ll) return tower::unsupported(fn, "M * ceil(N / 8) must be < 2^32 - 255");  // threads of one launch
   const auto go = [&](auto t) {

@@ -861,6 +861,12 @@ struct GnPlan {
   size_t fwd_bytes = 0, bwd_bytes = 0;
 };
 
+// LDS of group_sums for nval values: entries, their first sums, the groups' sums.
+size_t resident_lds(long Cg, long G, long tr, long spw, long threads, int nval) {
+  const long per = Cg % 8 == 0 ? 1 : 8, entries = tr * (Cg % 8 == 0 ? Cg / 8 : Cg);
+  return sizeof(float) * nval * (threads * per + spw * G * ((entries + 15) / 16 + 1));
+}
+
 GnPlan plan_gn(int B, int S, int C, int G) {
   GnPlan p;
   const long CV = (C + 7l) / 8;
@@ -882,13 +888,14 @@ GnPlan plan_gn(int B, int S, int C, int G) {
   // most 256 threads, or, for larger samples, to kResident
   for (int limit : {256, kResident}) {
     for (int nv = 1; nv <= 4 && p.form == STREAMED; nv *= 2) {
-      const long tr = (S + nv - 1l) / nv;
-      if (tr * CV <= limit) {
+      const long tr = (S + (nv - 1l)) / nv;
+      const long spw = tr * CV <= limit && limit == 256 ? 256 / (tr * CV) : 1;
+      if (tr * CV <= limit && resident_lds(Cg, G, tr, spw, limit, 2) <= 65536) {
         p.form = RESIDENT;
         p.NV = nv;
         p.TR = static_cast<int>(tr);
         p.team = static_cast<int>(tr * CV);
-        p.spw = limit == 256 ? std::max(1, 256 / p.team) : 1;
+        p.spw = static_cast<int>(spw);
         p.threads = limit == 256 ? 256 : (p.team + 63) / 64 * 64;
       }
     }
@@ -932,15 +939,9 @@ void fill(GnArgs& a, const GnPlan& p) {
   }
 }
 
-size_t lds_bytes(const GnArgs& a, const GnPlan& p, int nval) {
-  const size_t per = a.Cg % 8 == 0 ? 1 : 8;
-  const size_t items = static_cast<size_t>(p.spw) * a.G;
-  return sizeof(float) * nval * (p.threads * per + items * a.E1 + items);
-}
-
 template <class T, bool BWD, bool VECG>
 void launch_resident(const GnArgs& a, const GnPlan& p, hipStream_t st) {
-  const size_t lds = std::max(lds_bytes(a, p, BWD ? 2 : 1), BWD ? p.threads * sizeof(float2) : 0);
+  const size_t lds = std::max(resident_lds(a.Cg, a.G, p.TR, p.spw, p.threads, BWD ? 2 : 1), BWD ? p.threads * sizeof(float2) : 0);
   const dim3 grid(BWD ? p.blocks_bwd : p.blocks_fwd), block(p.threads);
 #define GN_CASE(NV)                                                                                        \
   case NV:                                                                                                 \
@@ -991,9 +992,15 @@ el_status run_gn(const char* fn, const GnArgs& a, const GnPlan& p, el_dtype dtyp
   return check_launch(fn);
 }
 
+// What one launch's grid can hold: samples that fit a workgroup take up to one workgroup each,
+// streamed ones a workgroup per group and per block of columns.
 bool gn_sizes_ok(int32_t B, int32_t S, int32_t C, int32_t G) {
-  return B >= 1 && S >= 1 && C >= 1 && G >= 1 && C % G == 0 && C <= (1 << 24) &&
-         static_cast<int64_t>(B) * S < (int64_t{1} << 40) && static_cast<int64_t>(B) * G < (int64_t{1} << 25);
+  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0 || C > (1 << 20) || B > (1 << 22) || S > (1 << 30))
+    return false;
+  if (static_cast<int64_t>(B) * G >= (int64_t{1} << 25)) return false;
+  const GnPlan p = plan_gn(B, S, C, G);
+  return p.form != STREAMED ||
+         (static_cast<int64_t>(B) * G < (int64_t{1} << 24) && static_cast<int64_t>(B) * p.colblocks <= (int64_t{1} << 22));
 }
 
 el_status check_gn(const char* fn, const void* x, int64_t ldx, int32_t B, int32_t S, int32_t C, int32_t G,
@@ -1005,7 +1012,7 @@ el_status check_gn(const char* fn, const void* x, int64_t ldx, int32_t B, int32_
   if (G < 1 || C % G != 0) return tower::bad(fn, "G must be >= 1 and divide C");
   if (!dtype_valid(dtype)) return tower::bad(fn, "unknown dtype");
   if (B > 0 && S > 0 && !gn_sizes_ok(B, S, C, G))
-    return tower::unsupported(fn, "C must be <= 2^24, B * S < 2^40 and B * G < 2^25");
+    return tower::unsupported(fn, "more channels (2^20), samples (2^22), positions (2^30) or groups in all than one launch takes");
   const el_status s = tower::check_act(fn, act);
   if (s != EL_OK) return s;
   if (!tower::al(lengths, 4) || !tower::al(gamma, 4) || !tower::al(beta, 4))

@@ -357,3 +357,124 @@ def test_a_captured_layer_replays_with_another_mask_each_time():
             assert torch.equal(names[n], eager[n]), (k, n)
         seen.append(names["y"].clone())
     assert not torch.equal(seen[0], seen[1]) and not torch.equal(seen[1], seen[2])
+
+
+# ------------------------------------------------------------------------- every tile shape
+@pytest.mark.parametrize("M,K,N", [
+    (33_000, 40, 264),     # forward: 256 x 256 tiles with ragged edges
+    (4_200, 72, 1_032),    # 128 x 128
+    (2_200, 72, 520),      # 64 x 64
+    (40_000, 24, 1),       # one column
+])
+def test_dense_fwd_tile_shapes(M, K, N):
+    rng = np.random.default_rng(M)
+    x, w = rows(rng, M, K, K, "bf16").contiguous(), rows(rng, N, K, K, "bf16", 1 / np.sqrt(K)).contiguous()
+    bias = torch.from_numpy(rng.normal(size=N)).float().to(DEV)
+    r, y, pre = rows(rng, M, N, N + 8, "bf16"), out(M, N, N + 8, "bf16"), out(M, N, N + 8, "bf16")
+    d, seed, offset = make_drop(0.3)
+    elf.dense_fwd(x, w, bias, y, act="gelu", dropout=d, residual=r, pre=pre)
+    f = tp.drop_factors(M, N, 0.3, seed, offset)
+    ry, ey, rz, ez = tp.dense_fwd(np64(x), np64(w), np64(bias), "gelu", f, np64(r), DT["bf16"])
+    tp.check(y, (ry, ey), "y")
+    tp.check(pre, (rz, ez), "pre")
+    assert gap_untouched(y) and gap_untouched(pre)
+
+
+@pytest.mark.parametrize("M,K,N", [
+    (24_600, 1_000, 1_032),  # both products in 256 x 256 tiles
+    (5_000, 1_032, 1_032),   # both in 128 x 128
+    (4_200, 1_032, 136),     # data gradient 128 x 128, weight gradient 64 x 64
+    (5_700, 520, 1_032),     # data gradient 64 x 64, weight gradient 128 x 128
+    (33_000, 264, 72),       # data gradient 256 x 256, weight gradient 64 x 64
+])
+def test_dense_bwd_tile_shapes(M, K, N):
+    rng = np.random.default_rng(M)
+    x, w = rows(rng, M, K, K, "bf16").contiguous(), rows(rng, N, K, K, "bf16", 1 / np.sqrt(N)).contiguous()
+    dz, dres, pre = rows(rng, M, N, N, "bf16").contiguous(), rows(rng, M, K, K, "bf16"), rows(rng, M, K, K, "bf16", 1.5)
+    dx, dzb = out(M, K, K + 8, "bf16"), out(M, K, K + 8, "bf16")
+    dw, db = torch.full((N, K), float("nan"), device=DEV), torch.full((N,), float("nan"), device=DEV)
+    d, seed, offset = make_drop(0.3)
+    elf.dense_bwd(x, w, dz, dw, db, dx=dx, dres=dres, dzb=dzb, pre=pre, act="silu", dropout=d)
+    ref = tp.dense_bwd(np64(x), np64(w), np64(dz), np64(dres), np64(pre), "silu", tp.drop_factors(M, K, 0.3, seed, offset),
+                       DT["bf16"])
+    for name, got in (("dw", dw), ("db", db), ("dx", dx), ("dzb", dzb)):
+        tp.check(got, ref[name], name)
+    assert gap_untouched(dx) and gap_untouched(dzb)
+
+
+@pytest.mark.parametrize("B,S,C,G,dt,kind", [
+    (33, 1, 8, 1, "f32", "silu"), (33, 1, 8, 4, "bf16", "none"), (20, 2, 512, 64, "f16", "gelu"), (21, 10, 64, 16, "f32", "silu"),
+    (20, 30, 32, 16, "bf16", "silu"), (10, 30, 128, 16, "f32", "gelu"), (9, 8, 512, 512, "f32", "none"),
+    (50, 20, 96, 6, "bf16", "gelu"), (40, 64, 24, 1, "f32", "silu"), (33, 60, 48, 3, "f16", "relu"), (12, 33, 320, 32, "bf16", "silu"),
+    (5, 3, 1000, 8, "f32", "gelu"), (2, 1, 4096, 4096, "f32", "none"), (3, 1, 5000, 1000, "bf16", "silu"),
+])
+def test_group_norm_forms(B, S, C, G, dt, kind):
+    """One wavefront per sample or several samples in one, one workgroup, chunks; groups inside
+    vectors, of whole vectors, across them."""
+    rng = np.random.default_rng(C + S)
+    x, dy = rows(rng, B * S, C, C, dt, 1.5, 0.7).contiguous(), rows(rng, B * S, C, C, dt).contiguous()
+    gm, bt = (torch.from_numpy(a + 0.3 * rng.normal(size=C)).float().to(DEV) for a in (1, 0))
+    y, dx = torch.full_like(x, float("nan")), torch.full_like(x, float("nan"))
+    mean, rstd = torch.empty((B, G), device=DEV), torch.empty((B, G), device=DEV)
+    dg, db = torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+    eps = 0.1  # groups of one or two values: keeps rstd and its cancellations moderate
+    elf.group_norm_fwd(x, gm, bt, y, mean, rstd, positions=S, groups=G, eps=eps, act=kind)
+    elf.group_norm_bwd(dy, x, gm, bt, mean, rstd, dx, dg, db, positions=S, groups=G, act=kind)
+    ry, ey, rm, rr = tp.gn_fwd(np64(x), S, G, None, np64(gm), np64(bt), eps, kind, DT[dt])
+    tp.check(mean, rm, "mean")
+    tp.check(rstd, rr, "rstd")
+    tp.check(y, (ry, ey), "y")
+    ref = tp.gn_bwd(np64(dy), np64(x), S, G, None, np64(gm), np64(bt), np64(mean), np64(rstd), kind, DT[dt])
+    tp.check(dx, ref["dx"], "dx")
+    tp.check(dg, ref["dgamma"], "dgamma")
+    tp.check(db, ref["dbeta"], "dbeta")
+
+
+def test_rows_past_32_bit_offsets():
+    """Row strides of 2^20 elements: the last rows of 2300 lie past 2^32 bytes."""
+    M, K, N, ld = 2_300, 64, 72, 1 << 20
+    big = torch.empty((M, ld), dtype=torch.bfloat16, device=DEV)
+    at = {"x": 0, "dz": 100, "y": 200, "pre": 300, "dx": 400, "dres": 500, "dzb": 600, "gn": 700}
+    view = lambda n, c: big[:, at[n]:at[n] + c]  # noqa: E731
+    g = torch.Generator(DEV).manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, device=DEV, generator=g).bfloat16()  # noqa: E731
+    src = {n: rnd(M, c) for n, c in (("x", K), ("dz", N), ("dres", K))}
+    for n, t in src.items():
+        view(n, t.shape[1]).copy_(t)
+    w, d = rnd(N, K), elf.Dropout(0.2, 3)
+    y, pre, dx, dzb = (torch.empty(M, c, dtype=torch.bfloat16, device=DEV) for c in (N, N, K, K))
+    dw, dw2 = torch.empty(N, K, device=DEV), torch.empty(N, K, device=DEV)
+    elf.dense_fwd(src["x"], w, None, y, act="gelu", dropout=d, pre=pre)
+    elf.dense_fwd(view("x", K), w, None, view("y", N), act="gelu", dropout=d, pre=view("pre", N))
+    assert torch.equal(y, view("y", N)) and torch.equal(pre, view("pre", N))
+    elf.dense_bwd(src["x"], w, src["dz"], dw, dx=dx, dres=src["dres"], dzb=dzb, pre=src["x"], act="silu", dropout=d)
+    elf.dense_bwd(view("x", K), w, view("dz", N), dw2, dx=view("dx", K), dres=view("dres", K), dzb=view("dzb", K),
+                  pre=view("x", K), act="silu", dropout=d)
+    assert torch.equal(dw, dw2) and torch.equal(dx, view("dx", K)) and torch.equal(dzb, view("dzb", K))
+    elf.act_dropout_fwd(src["x"], dx, act="gelu", dropout=d)
+    elf.act_dropout_fwd(view("x", K), view("dx", K), act="gelu", dropout=d)
+    assert torch.equal(dx, view("dx", K))
+    for S in (23, 1150):
+        st = [torch.empty(M // S, 4, device=DEV) for _ in range(4)]
+        elf.group_norm_fwd(src["x"], None, None, dx, st[0], st[1], positions=S, groups=4)
+        elf.group_norm_fwd(view("x", K), None, None, view("gn", K), st[2], st[3], positions=S, groups=4)
+        assert torch.equal(dx, view("gn", K)) and torch.equal(st[0], st[2]) and torch.equal(st[1], st[3])
+
+
+def test_calls_follow_the_given_stream_and_the_current_one():
+    M, K, N = 700, 128, 136
+    x, w, dz = (torch.randn(*s, device=DEV).bfloat16() for s in ((M, K), (N, K), (M, N)))
+    want = None
+    side = torch.cuda.Stream()
+    for how in ("default", "given", "current"):
+        y, dw, dx = torch.empty(M, N, device=DEV).bfloat16(), torch.empty(N, K, device=DEV), torch.empty_like(x)
+        ws = torch.empty(elf.dense_bwd_workspace_bytes(M, K, N), dtype=torch.uint8, device=DEV)
+        kw = dict(stream=side) if how == "given" else {}
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side) if how == "current" else torch.cuda.stream(None):
+            elf.dense_fwd(x, w, None, y, act="silu", **kw)
+            elf.dense_bwd(x, w, dz, dw, dx=dx, workspace=ws, **kw)
+        torch.cuda.current_stream().wait_stream(side)
+        got = (y.clone(), dw.clone(), dx.clone())
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), how
