@@ -246,7 +246,7 @@ struct Cfg {
   static constexpr int LDS = std::max(ST * (BR + BC) * BK * 2, NW * 32 * PITCH * 4);
 };
 using CfgL = Cfg<256, 256, 4, 4, 2, 4, true, 1>;   // 136 KB of LDS, one workgroup of 16 wavefronts per CU
-using CfgM = Cfg<128, 128, 2, 2, 2, 2, false, 2>;  // 64 KB, two per CU
+using CfgM = Cfg<128, 128, 2, 4, 2, 4, false, 2>;  // 64 KB, two of 8 wavefronts per CU
 using CfgS = Cfg<64, 64, 2, 2, 4, 2, false, 1>;    // 64 KB, two per CU
 
 // One tile (of one split): `lid` in tiles of all splits, in the order that shares panels.
@@ -523,13 +523,30 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_dense_few(GemmArgs a) {
 // ---------------------------------------------------------------------------------------
 // Operands whose rows are not whole aligned vectors are copied once, rows padded with zeros.
 // ---------------------------------------------------------------------------------------
-template <class T>
-__global__ __launch_bounds__(256) void k_pack(const uint16_t* src, long ld, long rows, int cols, int vecs, uint16_t* dst) {
-  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
-  const long r = i / vecs;
-  const int v = static_cast<int>(i - r * vecs);
-  if (r >= rows) return;
-  reinterpret_cast<u32x4*>(dst)[i] = load8_raw<T>(src + r * ld + v * 8, cols - v * 8).v[0];
+struct PackJob {
+  const uint16_t* src;
+  uint16_t* dst;
+  long ld, rows;
+  int cols, vecs;
+  unsigned blocks;  // 0: nothing to copy
+};
+__global__ __launch_bounds__(256) void k_pack(PackJob a, PackJob b, PackJob c) {
+  unsigned blk = blockIdx.x;
+  PackJob j = a;
+  if (blk >= a.blocks) {
+    blk -= a.blocks;
+    j = b;
+    if (blk >= b.blocks) {
+      blk -= b.blocks;
+      j = c;
+    }
+  }
+  const long i = static_cast<long>(blk) * 256 + threadIdx.x;
+  const long r = i / j.vecs;
+  const int v = static_cast<int>(i - r * j.vecs);
+  if (r >= j.rows) return;
+  // (bits: one loader serves both 16-bit types)
+  reinterpret_cast<u32x4*>(j.dst)[i] = load8_raw<BF16T>(j.src + r * j.ld + v * 8, j.cols - v * 8).v[0];
 }
 
 // out[i] = the sum over p < parts of part[p][i], i < n: 16 threads share one vector's parts
@@ -663,8 +680,6 @@ template <class T>
 el_status launch_backward(const char* fn, const GemmArgs& d, Shape sd, const GemmArgs& w, Shape sw, int splits, hipStream_t st) {
   if (sd == SHAPE_L && sw == SHAPE_L) return launch_both<T, CfgL, CfgL>(fn, d, w, splits, st);
   if (sd == SHAPE_M && sw == SHAPE_M) return launch_both<T, CfgM, CfgM>(fn, d, w, splits, st);
-  if (sd == SHAPE_M && sw == SHAPE_S) return launch_both<T, CfgM, CfgS>(fn, d, w, splits, st);
-  if (sd == SHAPE_S && sw == SHAPE_M) return launch_both<T, CfgS, CfgM>(fn, d, w, splits, st);
   if (sd == SHAPE_S && sw == SHAPE_S) return launch_both<T, CfgS, CfgS>(fn, d, w, splits, st);
   const el_status s = launch_product<T, DGRAD>(fn, d, sd, 1, st);
   return s == EL_OK ? launch_product<T, WGRAD>(fn, w, sw, splits, st) : s;
@@ -679,21 +694,28 @@ bool whole_vectors(const void* p, int64_t ld, int64_t cols) {
 }
 size_t packed_bytes(long rows, long cols) { return round256(static_cast<size_t>(rows) * pad8(cols) * 2); }
 
-// Copies the operand behind `ws` (and moves ws on) unless it is whole already; `done` receives
-// the pointer and stride to use.
-el_status pack(const char* fn, const uint16_t** p, long* ld, long rows, int cols, char** ws, hipStream_t st) {
-  if (whole_vectors(*p, *ld, cols)) return EL_OK;
-  const int vecs = static_cast<int>(pad8(cols) / 8);
-  const long blocks = ceil_div(rows * vecs, 256);
-  if (blocks >= (1l << 24)) return tower::unsupported(fn, "an unaligned operand of more than 2^35 elements");
-  uint16_t* dst = reinterpret_cast<uint16_t*>(*ws);
-  // (the bits are copied: one instance serves both 16-bit types)
-  hipLaunchKernelGGL((k_pack<BF16T>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, *p, *ld, rows, cols, vecs, dst);
-  *p = dst;
-  *ld = vecs * 8l;
-  *ws += packed_bytes(rows, cols);
-  return check_launch(fn);
-}
+// The copies that a call's operands need, in one launch: `add` an operand, its pointer and stride
+// become the copy's behind `ws` (which moves on) unless it is whole already, then `run`.
+struct Packs {
+  PackJob job[3] = {};
+  int n = 0;
+  void add(const uint16_t** p, long* ld, long rows, int cols, char** ws) {
+    if (whole_vectors(*p, *ld, cols)) return;
+    const int vecs = static_cast<int>(pad8(cols) / 8);
+    uint16_t* dst = reinterpret_cast<uint16_t*>(*ws);
+    job[n++] = PackJob{*p, dst, *ld, rows, cols, vecs, static_cast<unsigned>(std::min<long>(ceil_div(rows * vecs, 256), 1l << 24))};
+    *p = dst;
+    *ld = vecs * 8l;
+    *ws += packed_bytes(rows, cols);
+  }
+  el_status run(const char* fn, hipStream_t st) const {
+    const long blocks = static_cast<long>(job[0].blocks) + job[1].blocks + job[2].blocks;
+    if (blocks == 0) return EL_OK;
+    if (blocks >= (1l << 24)) return tower::unsupported(fn, "unaligned operands of more than 2^35 elements");
+    hipLaunchKernelGGL(k_pack, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, job[0], job[1], job[2]);
+    return check_launch(fn);
+  }
+};
 
 void launch_sums(const Sums& w, const Sums& b, hipStream_t st) {
   const bool vec = w.n % 4 == 0;
@@ -736,8 +758,10 @@ el_status run_fwd(const char* fn, GemmArgs a, char* ws, hipStream_t st) {
                        st, a);
     return check_launch(fn);
   }
-  el_status s = pack(fn, &a.P, &a.ldp, a.R, a.red, &ws, st);
-  if (s == EL_OK) s = pack(fn, &a.Q, &a.ldq, a.C, a.red, &ws, st);
+  Packs packs;
+  packs.add(&a.P, &a.ldp, a.R, a.red, &ws);
+  packs.add(&a.Q, &a.ldq, a.C, a.red, &ws);
+  const el_status s = packs.run(fn, st);
   if (s != EL_OK) return s;
   a.red = static_cast<int>(pad8(a.red));  // the copies' padding is zero; whole rows need none
   a.red_q = a.per_split = a.red;
@@ -765,10 +789,12 @@ size_t copy_bytes(const void* p, int64_t ld, long rows, long cols) {
 template <class T>
 el_status run_bwd(const char* fn, const uint16_t* x, long ldx, int M, int K, const uint16_t* w, int N, const uint16_t* dz,
                   long lddz, GemmArgs a, float* dw, float* db, char* ws, hipStream_t st) {
-  EL_TRY(pack(fn, &dz, &lddz, M, N, &ws, st));
-  EL_TRY(pack(fn, &x, &ldx, M, K, &ws, st));
+  Packs packs;
+  packs.add(&dz, &lddz, M, N, &ws);
+  packs.add(&x, &ldx, M, K, &ws);
   long ldw = K;
-  if (a.out) EL_TRY(pack(fn, &w, &ldw, N, K, &ws, st));
+  if (a.out) packs.add(&w, &ldw, N, K, &ws);
+  EL_TRY(packs.run(fn, st));
   const WgradPlan pl = plan_wgrad(M, K, N);
   GemmArgs b{};
   b.P = dz, b.ldp = lddz, b.Q = x, b.ldq = ldx, b.R = N, b.C = K, b.red = b.red_q = M, b.per_split = pl.per;
