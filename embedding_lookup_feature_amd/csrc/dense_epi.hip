@@ -21,6 +21,8 @@
 namespace el {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 enum Product { FWD = 0, DGRAD = 1, WGRAD = 2 };
 
 struct GemmArgs {
@@ -467,56 +469,66 @@ __global__ __launch_bounds__(CD::NW * 64, CD::WPE) void k_dense_bwd(GemmArgs d, 
 }
 
 // ---------------------------------------------------------------------------------------
-// Few outputs (a forward of one to a few hundred rows): a workgroup's wavefronts share out the
-// reduction of one 32 x 32 tile, fragments straight from global memory, and the partial tiles
-// are added in wavefront order in LDS.  Any alignment.
+// Few outputs (a forward of one to a few hundred rows): the weights' bytes and latency count.  A
+// workgroup's wavefronts share out the reduction of one 16 x 16 tile, fragments straight from
+// global memory (64 contiguous bytes of a row per read), and the partial tiles are added in
+// wavefront order in LDS.  Any alignment.
 // ---------------------------------------------------------------------------------------
-constexpr int kFewWaves = 16;
+constexpr int kFewWaves = 8;
+
+template <class T>
+__device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
+  if constexpr (T::code == EL_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
 
 template <class T>
 __global__ __launch_bounds__(kFewWaves * 64) void k_dense_few(GemmArgs a) {
-  constexpr int PITCH = 36;
-  __shared__ float lds[kFewWaves][32 * PITCH];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, l32 = lane & 31;
+  constexpr int PITCH = 20, AHEAD = 4;
+  __shared__ float lds[kFewWaves][16 * PITCH];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
-  const int row0 = tr * 32, col0 = tc * 32;
+  const int row0 = tr * 16, col0 = tc * 16;
   const int k0 = wave * a.per_split, kend = min(a.red, k0 + a.per_split);
-  const uint16_t* q = a.Q + static_cast<long>(min(col0 + l32, a.C - 1)) * a.ldq;  // rows past the end: never stored
-  const uint16_t* p = a.P + static_cast<long>(min(row0 + l32, a.R - 1)) * a.ldp;
-  f32x16 acc = {};
-  for (int k = k0 + half * 8; k - half * 8 < kend; k += 64) {
-    Raw8<T> fq[4], fp[4];
+  const uint16_t* q = a.Q + static_cast<long>(min(col0 + l16, a.C - 1)) * a.ldq;  // rows past the end: never stored
+  const uint16_t* p = a.P + static_cast<long>(min(row0 + l16, a.R - 1)) * a.ldp;
+  // the epilogue's operands are on their way while the products run
+  const int r = row0 + threadIdx.x / 2, c = col0 + threadIdx.x % 2 * 8, n = min(8, a.C - c);
+  const bool mine = threadIdx.x < 32 && r < a.R && n > 0;
+  float v[8] = {};
+  Raw8<T> add;
+  if (mine) {
+    if (a.add) add = load8_raw<T>(a.add + r * a.ldadd + c, n);
+    if (a.bias)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int n = kend - (k + u * 16);
-      if (n > 0) {
-        fq[u] = load8_raw<T>(q + k + u * 16, n);
-        fp[u] = load8_raw<T>(p + k + u * 16, n);
+      for (int e = 0; e < 8; ++e) v[e] = a.bias[min(c + e, a.C - 1)];
+  }
+  f32x4 acc = {};
+  for (int k = k0; k < kend; k += 32 * AHEAD) {
+    Raw8<T> fq[AHEAD], fp[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int at = k + u * 32 + g * 8;
+      if (at < kend) {
+        fq[u] = load8_raw<T>(q + at, kend - at);
+        fp[u] = load8_raw<T>(p + at, kend - at);
       } else {
         fq[u].v[0] = fp[u].v[0] = u32x4{0, 0, 0, 0};
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) acc = mfma32<T>(fq[u].v[0], fp[u].v[0], acc);
+    for (int u = 0; u < AHEAD; ++u) acc = mfma16<T>(fq[u].v[0], fp[u].v[0], acc);
   }
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-    *reinterpret_cast<float4*>(&lds[wave][l32 * PITCH + g * 8 + half * 4]) =
-        make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
+  // register e: column 4 g + e of row l16
+  *reinterpret_cast<f32x4*>(&lds[wave][l16 * PITCH + g * 4]) = acc;
   __syncthreads();
-  if (threadIdx.x >= 128) return;
-  const int r = row0 + threadIdx.x / 4, c = col0 + threadIdx.x % 4 * 8, n = min(8, a.C - c);
-  if (r >= a.R || n <= 0) return;
-  float v[8] = {};
-  Raw8<T> add;
-  if (a.add) add = load8_raw<T>(a.add + r * a.ldadd + c, n);
-  if (a.bias)
+  if (!mine) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = a.bias[min(c + e, a.C - 1)];
-#pragma unroll 4
   for (int w = 0; w < kFewWaves; ++w)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += lds[w][threadIdx.x / 4 * PITCH + threadIdx.x % 4 * 8 + e];
+    for (int e = 0; e < 8; ++e) v[e] += lds[w][threadIdx.x / 2 * PITCH + threadIdx.x % 2 * 8 + e];
   epilogue8<T, FWD, false>(a, a.drop.top ? drop_offset(a.drop) : 0, r, c, n, v, add, add);
 }
 
@@ -685,8 +697,9 @@ el_status launch_backward(const char* fn, const GemmArgs& d, Shape sd, const Gem
   return s == EL_OK ? launch_product<T, WGRAD>(fn, w, sw, splits, st) : s;
 }
 
-// A forward of few outputs: fewer than 64 tiles of 64 x 64.
-bool plan_few(long M, long N) { return ceil_div(M, 64) * ceil_div(N, 64) < 64; }
+// A forward of few outputs: at most 64 tiles of 64 x 64 (512 x 512 x 512: 7.6 us against 9.1 in
+// tiles; 300 x 1024 x 1024, 80 tiles: 14.7 against 13.8).
+bool plan_few(long M, long N) { return ceil_div(M, 64) * ceil_div(N, 64) <= 64; }
 
 // The operand as the tile kernels take it: 16-byte aligned rows of whole vectors.
 bool whole_vectors(const void* p, int64_t ld, int64_t cols) {
@@ -752,9 +765,9 @@ const uint16_t* u16(const void* p) { return static_cast<const uint16_t*>(p); }
 template <class T>
 el_status run_fwd(const char* fn, GemmArgs a, char* ws, hipStream_t st) {
   if (plan_few(a.R, a.C)) {
-    a.tiles_c = static_cast<int>(ceil_div(a.C, 32));
-    a.per_split = static_cast<int>(ceil_div(ceil_div(a.red, kFewWaves), 64) * 64);
-    hipLaunchKernelGGL((k_dense_few<T>), dim3(static_cast<unsigned>(ceil_div(a.R, 32) * a.tiles_c)), dim3(kFewWaves * 64), 0,
+    a.tiles_c = static_cast<int>(ceil_div(a.C, 16));
+    a.per_split = static_cast<int>(ceil_div(ceil_div(a.red, kFewWaves), 32) * 32);
+    hipLaunchKernelGGL((k_dense_few<T>), dim3(static_cast<unsigned>(ceil_div(a.R, 16) * a.tiles_c)), dim3(kFewWaves * 64), 0,
                        st, a);
     return check_launch(fn);
   }
