@@ -630,18 +630,20 @@ Shape plan_tiles(long R, long C) {
 // Weight gradient: tiles x batch slices that fill the CUs once (L) or twice.  A slice has to be
 // long enough to pay for its fp32 partial tile, which is written and read again: at 1024 x 1024
 // the shapes meet near 2048 rows a slice for L (16384 rows: L 63 us, M 55; 65536: 156, 167) and
-// near 512 for M (4096 rows: M 32, S 33; 2048: 31, 27).
+// near 512 for M (4096 rows: M 32, S 33; 2048: 31, 27).  Beside the data gradient's L tiles
+// (`shared`) half the CUs are enough: the others begin with those tiles, and the partials halve
+// (65536 x 1024 x 1024, both products: 382 us against 390; 65536 x 512 x 1024: 192, 206).
 struct WgradPlan {
   Shape shape;
   int splits, per, db_rows;
   size_t dw_bytes, bytes;
 };
-WgradPlan plan_wgrad(int M, int K, int N) {
+WgradPlan plan_wgrad(int M, int K, int N, bool shared) {
   WgradPlan p{};
   long splits = 1;
   for (Shape s : {SHAPE_L, SHAPE_M, SHAPE_S}) {
     const long tiles = ceil_div(N, kEdge[s]) * ceil_div(K, kEdge[s]);
-    splits = std::max<long>(1, (s == SHAPE_L ? 256 : 512) / tiles);
+    splits = std::max<long>(1, (s != SHAPE_L ? 512 : shared ? 128 : 256) / tiles);
     p.shape = s;
     if (s == SHAPE_S) splits = std::min(splits, ceil_div(M, 256));
     else if (M / splits >= (s == SHAPE_L ? 2048 : 512)) break;
@@ -696,6 +698,8 @@ el_status launch_backward(const char* fn, const GemmArgs& d, Shape sd, const Gem
   const el_status s = launch_product<T, DGRAD>(fn, d, sd, 1, st);
   return s == EL_OK ? launch_product<T, WGRAD>(fn, w, sw, splits, st) : s;
 }
+
+bool wgrad_shares(long M, long K, const void* dx) { return dx && plan_tiles(M, K) == SHAPE_L; }
 
 // A forward of few outputs: at most 64 tiles of 64 x 64 (512 x 512 x 512: 7.6 us against 9.1 in
 // tiles; 300 x 1024 x 1024, 80 tiles: 14.7 against 13.8).
@@ -808,7 +812,7 @@ el_status run_bwd(const char* fn, const uint16_t* x, long ldx, int M, int K, con
   long ldw = K;
   if (a.out) packs.add(&w, &ldw, N, K, &ws);
   EL_TRY(packs.run(fn, st));
-  const WgradPlan pl = plan_wgrad(M, K, N);
+  const WgradPlan pl = plan_wgrad(M, K, N, wgrad_shares(M, K, a.out));
   GemmArgs b{};
   b.P = dz, b.ldp = lddz, b.Q = x, b.ldq = ldx, b.R = N, b.C = K, b.red = b.red_q = M, b.per_split = pl.per;
   b.part = pl.splits > 1 ? reinterpret_cast<float*>(ws) : dw;
@@ -839,7 +843,8 @@ size_t el_dense_fwd_workspace_bytes(int32_t M, int32_t K, int32_t N) {
 
 size_t el_dense_bwd_workspace_bytes(int32_t M, int32_t K, int32_t N) {
   if (!dense_sizes_ok(M, K, N)) return 0;
-  return packed_bytes(M, N) + packed_bytes(M, K) + packed_bytes(N, K) + plan_wgrad(M, K, N).bytes;
+  return packed_bytes(M, N) + packed_bytes(M, K) + packed_bytes(N, K) +
+         std::max(plan_wgrad(M, K, N, false).bytes, plan_wgrad(M, K, N, true).bytes);
 }
 
 el_status el_dense_fwd(const void* x, int64_t ldx, int32_t M, int32_t K, const void* w, const float* bias, int32_t N,
@@ -889,7 +894,7 @@ el_status el_dense_bwd(const void* x, int64_t ldx, int32_t M, int32_t K, const v
       return check_launch(fn);
     }
     const size_t need = copy_bytes(dz, lddz, M, N) + copy_bytes(x, ldx, M, K) + (dx ? copy_bytes(w, K, N, K) : 0) +
-                        plan_wgrad(M, K, N).bytes;
+                        plan_wgrad(M, K, N, wgrad_shares(M, K, dx)).bytes;
     EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, need));
     a.add = u16(dres), a.ldadd = lddres, a.out = static_cast<uint16_t*>(dx), a.ldo = lddx, a.act = act;
     a.aux = static_cast<uint16_t*>(dzb), a.ldaux = lddzb, a.pre = dzb && act != EL_ACT_NONE ? u16(pre) : nullptr, a.ldpre = ldpre;

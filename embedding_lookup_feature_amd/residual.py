@@ -131,7 +131,7 @@ def main(argv=None):
     ap.add_argument("--rows", type=int, default=20_000, help="rows of each of the 26 tables")
     ap.add_argument("--blocks", type=int, default=2)
     ap.add_argument("--dropout", type=float, default=0.1)
-    ap.add_argument("--lr", type=float, default=0.1)
+    ap.add_argument("--lr", type=float, default=0.001)
     args = ap.parse_args(argv)
     dev = "cuda"
     wl = synth.WORKLOADS["train_step"].scaled(name="residual", batch=args.batch, rows=(args.rows,) * 26,
