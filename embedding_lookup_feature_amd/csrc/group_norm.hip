@@ -39,7 +39,7 @@ struct GnArgs {
   float2* part;        // workspace, see the kernels
   float* gsum;         // [2][B][G]: avg(dh), avg(dh xh)
   // resident
-  int TR, team, spw, E, E1;
+  int TR, team, spw, E, E1, E1_rows, E1_cols;  // E1 = E1_rows (entries of a group's row) + E1_cols
   int blocks;
   // streamed
   int chunks, per_chunk, pieces, per_piece, colblocks, TC;  // chunks: statistics; pieces: their use
@@ -80,11 +80,14 @@ __device__ inline void group_sums(const GnArgs& a, float* lds, int tid, int team
     const int it = j / a.E1, e0 = j - it * a.E1;
     const int smp = it / a.G, g = it - smp * a.G;
     float s[NVAL] = {};
+    int row = e0 / gc, col = e0 - row * gc;
+    const float* from = red + smp * a.team * per_thread + g * gc;
     for (int e = e0; e < a.E; e += a.E1) {
-      const int row = e / gc;
-      const int at = smp * a.team * per_thread + row * cols + g * gc + (e - row * gc);
 #pragma unroll
-      for (int v = 0; v < NVAL; ++v) s[v] += red[v * red_n + at];
+      for (int v = 0; v < NVAL; ++v) s[v] += from[v * red_n + row * cols + col];
+      row += a.E1_rows;
+      col += a.E1_cols;
+      if (col >= gc) col -= gc, ++row;
     }
 #pragma unroll
     for (int v = 0; v < NVAL; ++v) mid[v * items * a.E1 + j] = s[v];
@@ -567,19 +570,55 @@ __device__ inline StreamPos stream_pos(const GnArgs& a, int chunks, int per) {
   return q;
 }
 
+// Joins the eight (x, y) pairs of the workgroup's thread rows, n values behind each, into row 0 by
+// halving the rows: join(x, y, other pair, n, other's n) for each channel.
+template <class F>
+__device__ inline void join_rows(const StreamPos& q, int TC, float (&x)[8], float (&y)[8], float n, F&& join) {
+  __shared__ float2 red[kStream / 2][8];
+  __shared__ float cnt[kStream / 2];
+  const int col = q.cv % TC;
+  int h = 1;
+  while (h * 2 < q.TR) h *= 2;
+  for (int width = q.TR; width > 1; width = h, h /= 2) {  // rows 0 .. width-1 are left
+    __syncthreads();
+    if (q.on && q.tr >= h && q.tr < width) {
+      const int at = (q.tr - h) * TC + col;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) red[at][i] = make_float2(x[i], y[i]);
+      cnt[at] = n;
+    }
+    __syncthreads();
+    if (q.on && q.tr + h < width) {
+      const int at = q.tr * TC + col;
+      const float nb = cnt[at];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) join(x[i], y[i], red[at][i], n, nb);
+      n += nb;
+    }
+  }
+}
+
+// Row 0's threads write their channels' pairs.
+__device__ inline void write_part(const GnArgs& a, const StreamPos& q, const float (&x)[8], const float (&y)[8]) {
+  if (!q.on || q.tr != 0) return;
+  float2* part = a.part + (static_cast<long>(q.b) * a.chunks + q.chunk) * a.C + q.cv * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < q.n) part[i] = make_float2(x[i], y[i]);
+}
+
 // part[b][chunk][c] = (mean, sum of squares about it) of channel c over the chunk's valid
 // positions.  A thread sums differences from its first value; threads are joined by the
 // pairwise update of Chan, Golub and LeVeque (1979).
 template <class T>
 __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
-  __shared__ float2 red[kStream * 8];
   using St = typename T::S;
   const StreamPos q = stream_pos(a, a.chunks, a.per_chunk);
   const int end = min(q.s1, sample_len(a, q.b));
+  float mean[8] = {}, m2[8] = {}, cnt = 0.f;
   if (q.on) {
     const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
     float k[8] = {}, s1[8] = {}, s2[8] = {};
-    int cnt = 0;
     for (int s = q.s0 + q.tr; s < end; s += kAhead * q.TR) {
       Raw8<T> r[kAhead];
 #pragma unroll
@@ -592,76 +631,76 @@ __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
         to_floats<T>(r[u], f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (cnt == 0) k[i] = f[i];
+          if (cnt == 0.f) k[i] = f[i];
           const float d = f[i] - k[i];
           s1[i] += d;
           s2[i] += d * d;
         }
-        ++cnt;
+        cnt += 1.f;
       }
     }
-    const float inv = cnt ? 1.f / cnt : 0.f;
+    const float inv = cnt > 0.f ? 1.f / cnt : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = s1[i] * inv;
-      red[(q.tr * a.TC + q.cv % a.TC) * 8 + i] = make_float2(k[i] + d, fmaxf(s2[i] - s1[i] * d, 0.f));
+      mean[i] = k[i] + d;
+      m2[i] = fmaxf(s2[i] - s1[i] * d, 0.f);
     }
   }
-  __syncthreads();
-  const int cb0 = (q.cv / a.TC) * a.TC;  // first vector of this column block
-  const int width = min(a.TC, a.CV - cb0) * 8;
-  const int span = max(0, end - q.s0);
-  for (int j = threadIdx.x; j < width; j += kStream) {
-    const int c = cb0 * 8 + j;
-    if (c >= a.C) continue;
-    float n = 0.f, mean = 0.f, m2 = 0.f;
-    for (int t = 0; t < q.TR && t < span; ++t) {
-      const float2 v = red[t * a.TC * 8 + j];
-      const float nb = static_cast<float>((span - t + q.TR - 1) / q.TR);
-      const float d = v.x - mean, tot = n + nb;
-      mean += d * (nb / tot);
-      m2 += v.y + d * d * (n * nb / tot);
-      n = tot;
+  join_rows(q, a.TC, mean, m2, cnt, [](float& m, float& s, const float2& o, float na, float nb) {
+    if (nb > 0.f) {
+      const float w = nb / (na + nb), d = o.x - m;
+      m += d * w;
+      s += o.y + d * d * (na * w);
     }
-    a.part[(static_cast<long>(q.b) * a.chunks + q.chunk) * a.C + c] = make_float2(mean, m2);
-  }
+  });
+  write_part(a, q, mean, m2);
 }
 
-// Sum of v over the 256 threads of a workgroup, in a fixed order, for every thread.
-__device__ inline float sum256(float v) {
-  __shared__ float red[4];
+// Sum of v over the workgroup's threads, in a fixed order, for every thread.
+__device__ inline float sum_all(float v) {
+  __shared__ float red[16];
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  return (red[0] + red[1]) + (red[2] + red[3]);
+  float s = red[0];
+  for (unsigned w = 1; w < blockDim.x / 64; ++w) s += red[w];
+  return s;
+}
+
+// Walks the group's chunks * Cg channel entries, thread t from entry t in steps of the workgroup:
+// f(chunk, channel in the group).
+template <class F>
+__device__ inline void each_entry(const GnArgs& a, F&& f) {
+  const int nt = blockDim.x, rows = nt / a.Cg, cols = nt % a.Cg;
+  int ch = threadIdx.x / a.Cg, c = threadIdx.x % a.Cg;
+#pragma unroll 4
+  for (int j = threadIdx.x; j < a.chunks * a.Cg; j += nt) {
+    f(ch, c);
+    ch += rows;
+    c += cols;
+    if (c >= a.Cg) c -= a.Cg, ++ch;
+  }
 }
 
 // One workgroup per (sample, group): mean and rstd from the chunks' channel statistics.
-__global__ __launch_bounds__(256) void k_gn_join(GnArgs a) {
-  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G, t = threadIdx.x;
+__global__ __launch_bounds__(1024) void k_gn_join(GnArgs a) {
+  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G;
   const int len = sample_len(a, b);
-  const int full = a.chunks * a.Cg;
   const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
   const float2* part = a.part + static_cast<long>(b) * a.chunks * a.C + g * a.Cg;
+  const auto count = [&](int ch) { return static_cast<float>(min(max(len - ch * a.per_chunk, 0), a.per_chunk)); };
   float s = 0.f;
-  for (int j = t; j < full; j += 256) {
-    const int ch = j / a.Cg;
-    const int cnt = min(max(len - ch * a.per_chunk, 0), a.per_chunk);
-    if (cnt > 0) s += cnt * inv_n * part[static_cast<long>(ch) * a.C + j - ch * a.Cg].x;
-  }
-  const float mean = sum256(s);
+  each_entry(a, [&](int ch, int c) { s += count(ch) * inv_n * part[static_cast<long>(ch) * a.C + c].x; });
+  const float mean = sum_all(s);
   float v = 0.f;
-  for (int j = t; j < full; j += 256) {
-    const int ch = j / a.Cg;
-    const int cnt = min(max(len - ch * a.per_chunk, 0), a.per_chunk);
-    if (cnt > 0) {
-      const float2 q = part[static_cast<long>(ch) * a.C + j - ch * a.Cg];
-      v += q.y + cnt * (q.x - mean) * (q.x - mean);
-    }
-  }
-  v = sum256(v);
-  if (t == 0) {
+  each_entry(a, [&](int ch, int c) {
+    const float2 q = part[static_cast<long>(ch) * a.C + c];
+    v += q.y + count(ch) * (q.x - mean) * (q.x - mean);
+  });
+  v = sum_all(v);
+  if (threadIdx.x == 0) {
     a.mean[blockIdx.x] = mean;
     a.rstd[blockIdx.x] = 1.f / sqrtf(v * inv_n + a.eps);
   }
@@ -712,14 +751,14 @@ __global__ __launch_bounds__(kStream) void k_gn_apply(GnArgs a) {
 // part[b][chunk][c] = (sum du, sum du xh) of channel c over the chunk's valid positions.
 template <class T>
 __global__ __launch_bounds__(kStream) void k_gn_bwd_stats(GnArgs a) {
-  __shared__ float2 red[kStream * 8];
   using St = typename T::S;
   const StreamPos q = stream_pos(a, a.chunks, a.per_chunk);
   const int end = min(q.s1, sample_len(a, q.b));
+  float s1[8] = {}, s2[8] = {};
   if (q.on) {
     const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
     const St* dy = static_cast<const St*>(a.dy) + static_cast<long>(q.b) * a.S * a.lddy + q.cv * 8;
-    float gamma[8], beta[8], shift[8], rstd[8], s1[8] = {}, s2[8] = {};
+    float gamma[8], beta[8], shift[8], rstd[8];
     load_params(a, q.cv, gamma, beta);
     load_stats<true>(a, q, shift, rstd);
     for (int s = q.s0 + q.tr; s < end; s += kAhead * q.TR) {
@@ -742,42 +781,30 @@ __global__ __launch_bounds__(kStream) void k_gn_bwd_stats(GnArgs a) {
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) red[(q.tr * a.TC + q.cv % a.TC) * 8 + i] = make_float2(s1[i], s2[i]);
   }
-  __syncthreads();
-  const int cb0 = (q.cv / a.TC) * a.TC;
-  const int width = min(a.TC, a.CV - cb0) * 8;
-  for (int j = threadIdx.x; j < width; j += kStream) {
-    const int c = cb0 * 8 + j;
-    if (c >= a.C) continue;
-    float2 s = make_float2(0.f, 0.f);
-    for (int t = 0; t < q.TR; ++t) {
-      const float2 v = red[t * a.TC * 8 + j];
-      s.x += v.x;
-      s.y += v.y;
-    }
-    a.part[(static_cast<long>(q.b) * a.chunks + q.chunk) * a.C + c] = s;
-  }
+  join_rows(q, a.TC, s1, s2, 0.f, [](float& x, float& y, const float2& o, float, float) {
+    x += o.x;
+    y += o.y;
+  });
+  write_part(a, q, s1, s2);
 }
 
 // One workgroup per (sample, group): (avg dh, avg dh xh) from the chunks' channel sums.
-__global__ __launch_bounds__(256) void k_gn_bwd_join(GnArgs a) {
-  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G, t = threadIdx.x;
-  const int len = sample_len(a, b), full = a.chunks * a.Cg;
+__global__ __launch_bounds__(1024) void k_gn_bwd_join(GnArgs a) {
+  const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G;
+  const int len = sample_len(a, b);
   const float2* part = a.part + static_cast<long>(b) * a.chunks * a.C + g * a.Cg;
   float s1 = 0.f, s2 = 0.f;
-  for (int j = t; j < full; j += 256) {
-    const int ch = j / a.Cg, c = j - ch * a.Cg;
+  each_entry(a, [&](int ch, int c) {
     const float2 v = part[static_cast<long>(ch) * a.C + c];
     const float gm = a.gamma ? a.gamma[g * a.Cg + c] : 1.f;
     s1 += gm * v.x;
     s2 += gm * v.y;
-  }
-  s1 = sum256(s1);
-  s2 = sum256(s2);
+  });
+  s1 = sum_all(s1);
+  s2 = sum_all(s2);
   const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
-  if (t == 0) {
+  if (threadIdx.x == 0) {
     a.gsum[blockIdx.x] = s1 * inv_n;
     a.gsum[static_cast<long>(a.B) * a.G + blockIdx.x] = s2 * inv_n;
   }
@@ -884,34 +911,34 @@ GnPlan plan_gn(int B, int S, int C, int G) {
     p.threads = kWave;
     p.spw = kWave / p.team;
   }
-  // resident: the smallest number of vectors per thread (1, 2, 4) that leaves a sample to at
-  // most 256 threads, or, for larger samples, to kResident
-  for (int limit : {256, kResident}) {
+  // resident: the smallest number of vectors per thread (1, 2, 4) that leaves a sample to one
+  // wavefront (no other one to wait for), to 256 threads, or to kResident
+  for (int limit : {64, 256, kResident}) {
     for (int nv = 1; nv <= 4 && p.form == STREAMED; nv *= 2) {
       const long tr = (S + (nv - 1l)) / nv;
-      const long spw = tr * CV <= limit && limit == 256 ? 256 / (tr * CV) : 1;
+      const long spw = tr * CV <= limit && limit < kResident ? limit / (tr * CV) : 1;
       if (tr * CV <= limit && resident_lds(Cg, G, tr, spw, limit, 2) <= 65536) {
         p.form = RESIDENT;
         p.NV = nv;
         p.TR = static_cast<int>(tr);
         p.team = static_cast<int>(tr * CV);
         p.spw = static_cast<int>(spw);
-        p.threads = limit == 256 ? 256 : (p.team + 63) / 64 * 64;
+        p.threads = limit < kResident ? limit : (p.team + 63) / 64 * 64;
       }
     }
   }
   if (p.form != STREAMED) {
     const long wgs = (B + p.spw - 1l) / p.spw;
     p.blocks_fwd = static_cast<int>(wgs);
-    p.blocks_bwd = static_cast<int>(std::min<long>(wgs, std::max<long>(256, std::min<long>(p.NV == 8 ? 512 : 1024, (1l << 20) / C))));
+    p.blocks_bwd = static_cast<int>(std::min<long>(wgs, std::max<long>(256, std::min<long>(p.threads == 64 ? 4096 : p.NV == 8 ? 512 : 1024, (1l << 20) / C))));
     p.bwd_bytes = round256(static_cast<size_t>(p.blocks_bwd) * C * sizeof(float2));
     return p;
   }
   p.TC = static_cast<int>(std::min<long>(CV, kStream));
   p.colblocks = static_cast<int>((CV + p.TC - 1) / p.TC);
   const long rows = kStream / p.TC;
-  const long want = std::max<long>(1, 2048 / (static_cast<long>(B) * p.colblocks));
-  const long most = std::max<long>(1, S / (rows * 8));  // at least eight positions per thread
+  const long want = std::max<long>(1, 512 / (static_cast<long>(B) * p.colblocks));
+  const long most = std::max<long>(1, S / (rows * kAhead));  // at least one batch of loads per thread
   // and channel statistics of at most 8 MB where the samples alone do not take more
   const long cap = std::max<long>(1, (1l << 20) / (static_cast<long>(B) * C));
   p.chunks = static_cast<int>(std::min({want, most, cap}));
@@ -936,6 +963,9 @@ void fill(GnArgs& a, const GnPlan& p) {
   if (p.form == RESIDENT) {
     a.E = p.TR * (a.Cg % 8 == 0 ? a.Cg / 8 : a.Cg);
     a.E1 = (a.E + 15) / 16;
+    const int gc = a.Cg % 8 == 0 ? a.Cg / 8 : a.Cg;
+    a.E1_rows = a.E1 / gc;
+    a.E1_cols = a.E1 % gc;
   }
 }
 
@@ -968,6 +998,9 @@ template <class T, bool BWD>
 void launch_gn(const GnArgs& a, const GnPlan& p, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(static_cast<long>(a.B) * p.chunks * p.colblocks)), block(kStream);
   const dim3 pieces(static_cast<unsigned>(static_cast<long>(a.B) * p.pieces * p.colblocks));
+  // enough threads for a few entries each
+  const long entries = static_cast<long>(p.chunks) * a.Cg;
+  const dim3 join(entries <= 256 ? 64 : entries <= 2048 ? 256 : 1024);
   const dim3 groups(static_cast<unsigned>(static_cast<long>(a.B) * a.G));
   if (p.form == WAVE) {
     a.Cg % 8 == 0 ? launch_wave<T, BWD, true>(a, p, st) : launch_wave<T, BWD, false>(a, p, st);
@@ -975,11 +1008,11 @@ void launch_gn(const GnArgs& a, const GnPlan& p, hipStream_t st) {
     a.Cg % 8 == 0 ? launch_resident<T, BWD, true>(a, p, st) : launch_resident<T, BWD, false>(a, p, st);
   } else if constexpr (BWD) {
     hipLaunchKernelGGL((k_gn_bwd_stats<T>), grid, block, 0, st, a);
-    hipLaunchKernelGGL(k_gn_bwd_join, groups, dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_gn_bwd_join, groups, join, 0, st, a);
     hipLaunchKernelGGL((k_gn_bwd_apply<T>), pieces, block, 0, st, a);
   } else {
     hipLaunchKernelGGL((k_gn_stats<T>), grid, block, 0, st, a);
-    hipLaunchKernelGGL(k_gn_join, groups, dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_gn_join, groups, join, 0, st, a);
     hipLaunchKernelGGL((k_gn_apply<T>), pieces, block, 0, st, a);
   }
 }
@@ -1000,7 +1033,7 @@ bool gn_sizes_ok(int32_t B, int32_t S, int32_t C, int32_t G) {
   if (static_cast<int64_t>(B) * G >= (int64_t{1} << 25)) return false;
   const GnPlan p = plan_gn(B, S, C, G);
   return p.form != STREAMED ||
-         (static_cast<int64_t>(B) * G < (int64_t{1} << 24) && static_cast<int64_t>(B) * p.colblocks <= (int64_t{1} << 22));
+         (static_cast<int64_t>(B) * G < (int64_t{1} << 22) && static_cast<int64_t>(B) * p.colblocks <= (int64_t{1} << 22));
 }
 
 el_status check_gn(const char* fn, const void* x, int64_t ldx, int32_t B, int32_t S, int32_t C, int32_t G,
