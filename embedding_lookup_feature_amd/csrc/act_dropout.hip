@@ -6,6 +6,12 @@
 // One thread owns eight consecutive columns of a row, which share one Philox4x32-10 call (eight
 // 16-bit numbers), so the mask costs ten rounds of two 32 x 32 -> 64 bit products per eight
 // elements and is never read or written.
+//
+// Bound by memory: 65536 x 1024, bf16, GELU, dropout and residual (402 MB) 76.6 us, 5.3 TB/s, the
+// rate of a copy; the gradient of 16411 x 479, fp32, SiLU and dropout (94 MB) 19.7 us, 4.8 TB/s.
+// One vector per thread and no loop: the wavefronts of the next workgroups hide the loads, and
+// the smallest calls, which are latency, stay one load, the arithmetic and one store (64 x 128:
+// 2.1 us, the time of an empty kernel).
 #include "tower_common.hpp"
 
 namespace el {

@@ -14,6 +14,13 @@
 // every wavefront holds its last fragments in registers.  Reduction-contiguous fragments are
 // plain 16-byte LDS reads, output-contiguous ones gfx950's transposing LDS reads, both from
 // layouts whose 16-byte units are permuted so that the reads touch every bank once.
+//
+// What bounds it: the large products run at the matrix units' rate under the power limit (the
+// main loop alone, 65536 x 1024 x 1024 bf16, 125 us = 1.1 PFLOP/s, a library's product 121), and
+// behind each tile's products its epilogue moves residual, pre and y at the memory's rate with
+// the matrix units idle, the generator and the activation beside it: 213 us forward with GELU,
+// dropout, residual and pre, 360 us for both products of the backward, their partials' sums
+// included (floors 121 and 242 of products, 105 and 158 of memory).
 #include <algorithm>
 
 #include "tower_common.hpp"
@@ -237,6 +244,8 @@ __device__ inline int xcd_order(int bid, int n) {
 }
 
 // Tile shapes: WR x WC wavefronts own BR x BC outputs of a workgroup; ST stages of 64 reductions.
+// 16 wavefronts on the large tile and 8 on the middle one: more wavefronts share the epilogue's
+// latency (L forward 232 us at 16, 244 at 8; backward 376, 387).
 template <int BR_, int BC_, int WR_, int WC_, int ST_, int WPE_, bool NT_, int AHEAD_>
 struct Cfg {
   static constexpr int BR = BR_, BC = BC_, BK = 64, WR = WR_, WC = WC_, ST = ST_, NW = WR * WC;
@@ -397,7 +406,8 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
   } else {
     // Accumulators go through LDS (each wavefront's own 32 x (32 FC) floats at a time), so that a
     // lane gets eight consecutive columns: they share one call of the mask's generator, and a
-    // row's accesses to residual, pre, y, ... are whole cache lines.
+    // row's accesses to residual, pre, y, ... are whole cache lines (222 us against 298 with the
+    // epilogue straight from the accumulators' four columns a lane).
     constexpr int WCOLS = FC * 32, GR = WCOLS / 8, RPP = 64 / GR, PASS = 32 / RPP, PITCH = C::PITCH, AHEAD = C::AHEAD;
     static_assert(AHEAD <= FR, "no block is fetched twice");
     const uint64_t offset = a.drop.top ? drop_offset(a.drop) : 0;
@@ -472,7 +482,8 @@ __global__ __launch_bounds__(CD::NW * 64, CD::WPE) void k_dense_bwd(GemmArgs d, 
 // Few outputs (a forward of one to a few hundred rows): the weights' bytes and latency count.  A
 // workgroup's wavefronts share out the reduction of one 16 x 16 tile, fragments straight from
 // global memory (64 contiguous bytes of a row per read), and the partial tiles are added in
-// wavefront order in LDS.  Any alignment.
+// wavefront order in LDS.  Any alignment.  1 x 1024 x 1024 takes 4.2 us and 77 x 512 x 1024 4.7
+// (an empty kernel 2.1): a round of loads or two and a barrier, no longer the bytes.
 // ---------------------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 
@@ -533,7 +544,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_dense_few(GemmArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------
-// Operands whose rows are not whole aligned vectors are copied once, rows padded with zeros.
+// Operands whose rows are not whole aligned vectors are copied once, rows padded with zeros: the
+// direct loads to LDS take whole 16-byte units only (4099 x 479 and 1001 x 479: 5.1 us, beside
+// 24.7 for the product; its floor in memory 5.8 us).
 // ---------------------------------------------------------------------------------------
 struct PackJob {
   const uint16_t* src;

@@ -8,12 +8,19 @@
 //   dx     = rstd (dh - avg(dh) - xh avg(dh xh))
 //   dgamma = sum_{b,s} du xh,  dbeta = sum_{b,s} du
 //
-// Bound by memory: x in, y out (forward); x, dy in, dx out (backward).  Two forms:
-//   resident  a sample's values stay in the registers of one workgroup's threads between the
-//             statistics and their use, so everything is read once;
-//   streamed  samples too large for that are cut into chunks of positions: one kernel leaves
-//             per-channel statistics of each chunk, one joins them per group, one applies them
-//             (x, and dy, are read twice).
+// Bound by memory: x in, y out (forward); x, dy in, dx out (backward).  Three forms:
+//   wavefront  a sample sits in the registers of some lanes of one wavefront, which exchange its
+//              sums: read once, no barrier (16384 samples of 26 x 128 in 8 groups, bf16: forward
+//              41.5 us, 5.2 TB/s, the rate of a copy; backward 93 us, 3.5 TB/s, held back by the
+//              two wavefronts per SIMD that its 256 registers leave: with fewer registers, three
+//              or four per SIMD, it spills and takes 220 us and more);
+//   resident   a sample sits in the registers of one workgroup's threads, which join its sums in
+//              LDS: read once, any width and group size;
+//   streamed   samples too large for that are cut into chunks of positions: one kernel leaves
+//              per-channel statistics of each chunk, one joins them per group, one applies them
+//              (x, and dy, are read twice, the second time from the caches where they fit: 6
+//              samples of up to 5001 x 256 in 32 groups, fp16: stats 7.9 us, join 4.6, apply 9.2;
+//              backward 11.1, 3.9, 10.9 and 3.9 for the parameters: seven dependent launches).
 // A thread owns eight consecutive channels of some positions, so every access is a 16-byte
 // vector whatever the group width; sums are kept per channel and joined into groups afterwards
 // where a vector crosses groups.
@@ -38,6 +45,7 @@ struct GnArgs {
   float *mean, *rstd;  // written by the forward, read by the backward
   float2* part;        // workspace, see the kernels
   float* gsum;         // [2][B][G]: avg(dh), avg(dh xh)
+  float *dgamma, *dbeta;
   // resident
   int TR, team, spw, E, E1, E1_rows, E1_cols;  // E1 = E1_rows (entries of a group's row) + E1_cols
   int blocks;
@@ -448,8 +456,11 @@ __global__ __launch_bounds__(kWave) void k_gn_fwd_wave(GnArgs a) {
 }
 
 // part[workgroup][c] = (dbeta, dgamma) of the workgroup's samples, as in the resident form.
+// Two wavefronts per SIMD; one where eight fp32 vectors and per-channel sums would spill too much
+// (8192 samples of 26 x 128, forward and backward, 32 groups: 157 us, spilling 171; 8 groups, whose
+// sums are fewer: 142, spilling 134).
 template <class T, int NV, bool VECG>
-__global__ __launch_bounds__(kWave, 2) void k_gn_bwd_wave(GnArgs a) {
+__global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) == 4 ? 1 : 2) void k_gn_bwd_wave(GnArgs a) {
   using St = typename T::S;
   float gamma[8], beta[8], sb[8] = {}, sg[8] = {};
   load_params(a, threadIdx.x & (a.CV - 1), gamma, beta);
@@ -543,7 +554,9 @@ __global__ __launch_bounds__(kWave, 2) void k_gn_bwd_wave(GnArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------
-// Streamed form.
+// Streamed form.  The statistics want few chunks (each leaves a row of channel sums to be joined),
+// the passes that use them leave nothing behind and want many small pieces, so the two are cut
+// differently.
 // ---------------------------------------------------------------------------------------
 constexpr int kStream = 256;
 constexpr int kAhead = 4;  // positions whose loads a thread has in flight
@@ -789,8 +802,45 @@ __global__ __launch_bounds__(kStream) void k_gn_bwd_stats(GnArgs a) {
   write_part(a, q, s1, s2);
 }
 
-// One workgroup per (sample, group): (avg dh, avg dh xh) from the chunks' channel sums.
+// dbeta[c], dgamma[c] = the sums over `rows` of part[row][c]: 4 channels per workgroup, the rest
+// of its threads (T = blockDim.x / 4 per channel, thread t: rows t, t + T, ...) share out the rows,
+// and their sums are joined in a fixed tree.
+__device__ inline void sum_params(const GnArgs& a, long rows, int block) {
+  __shared__ float2 red[256][4];
+  const int q = threadIdx.x & 3, c = block * 4 + q, t = threadIdx.x >> 2, C = a.C, T = blockDim.x >> 2;
+  float2 s = make_float2(0.f, 0.f);
+  if (c < C)
+#pragma unroll 4
+    for (long r = t; r < rows; r += T) {
+      const float2 v = a.part[r * C + c];
+      s.x += v.x;
+      s.y += v.y;
+    }
+  red[t][q] = s;
+  for (int h = T / 2; h > 0; h >>= 1) {
+    __syncthreads();
+    if (t < h) {
+      s.x += red[t + h][q].x;
+      s.y += red[t + h][q].y;
+      red[t][q] = s;
+    }
+  }
+  if (t == 0 && c < C) {
+    if (a.dbeta) a.dbeta[c] = s.x;
+    if (a.dgamma) a.dgamma[c] = s.y;
+  }
+}
+
+__global__ __launch_bounds__(1024) void k_gn_params(GnArgs a, long rows) { sum_params(a, rows, blockIdx.x); }
+
+// One workgroup per (sample, group): (avg dh, avg dh xh) from the chunks' channel sums.  The
+// workgroups past those sum the parameters' gradients, where the launch has them.
 __global__ __launch_bounds__(1024) void k_gn_bwd_join(GnArgs a) {
+  const int block = blockIdx.x, groups = a.B * a.G;
+  if (block >= groups) {
+    sum_params(a, static_cast<long>(a.B) * a.chunks, block - groups);
+    return;
+  }
   const int b = blockIdx.x / a.G, g = blockIdx.x - b * a.G;
   const int len = sample_len(a, b);
   const float2* part = a.part + static_cast<long>(b) * a.chunks * a.C + g * a.Cg;
@@ -848,34 +898,6 @@ __global__ __launch_bounds__(kStream) void k_gn_bwd_apply(GnArgs a) {
   }
 }
 
-// dbeta[c], dgamma[c] = the sums over `rows` of part[row][c]: 4 channels per workgroup, 256
-// threads per channel (thread t: rows t, t + 256, ...), whose sums are joined in a fixed tree.
-__global__ __launch_bounds__(1024) void k_gn_params(const float2* part, long rows, int C, float* dgamma, float* dbeta) {
-  __shared__ float2 red[256][4];
-  const int q = threadIdx.x & 3, c = blockIdx.x * 4 + q, t = threadIdx.x >> 2;
-  float2 s = make_float2(0.f, 0.f);
-  if (c < C)
-#pragma unroll 4
-    for (long r = t; r < rows; r += 256) {
-      const float2 v = part[r * C + c];
-      s.x += v.x;
-      s.y += v.y;
-    }
-  red[t][q] = s;
-  for (int h = 128; h > 0; h >>= 1) {
-    __syncthreads();
-    if (t < h) {
-      s.x += red[t + h][q].x;
-      s.y += red[t + h][q].y;
-      red[t][q] = s;
-    }
-  }
-  if (t == 0 && c < C) {
-    if (dbeta) dbeta[c] = s.x;
-    if (dgamma) dgamma[c] = s.y;
-  }
-}
-
 // ---------------------------------------------------------------------------------------
 // Plans and launches.
 // ---------------------------------------------------------------------------------------
@@ -930,7 +952,12 @@ GnPlan plan_gn(int B, int S, int C, int G) {
   if (p.form != STREAMED) {
     const long wgs = (B + p.spw - 1l) / p.spw;
     p.blocks_fwd = static_cast<int>(wgs);
-    p.blocks_bwd = static_cast<int>(std::min<long>(wgs, std::max<long>(256, std::min<long>(p.threads == 64 ? 4096 : p.NV == 8 ? 512 : 1024, (1l << 20) / C))));
+    // the backward's workgroups walk samples and leave one row of channel sums each: as many as
+    // are resident at once (two to a CU where a thread holds eight vectors in 256 registers, 16
+    // of one wavefront, about four otherwise), fewer, down to one, where their rows take over 8 MB
+    const long most = p.threads == 64 ? 4096 : p.NV == 8 ? 512 : 1024;
+    const long few = std::max<long>(256, std::min<long>(most, (1l << 20) / C));
+    p.blocks_bwd = static_cast<int>(std::min(wgs, few));
     p.bwd_bytes = round256(static_cast<size_t>(p.blocks_bwd) * C * sizeof(float2));
     return p;
   }
@@ -1000,21 +1027,30 @@ void launch_gn(const GnArgs& a, const GnPlan& p, hipStream_t st) {
   const dim3 pieces(static_cast<unsigned>(static_cast<long>(a.B) * p.pieces * p.colblocks));
   // enough threads for a few entries each
   const long entries = static_cast<long>(p.chunks) * a.Cg;
-  const dim3 join(entries <= 256 ? 64 : entries <= 2048 ? 256 : 1024);
+  const int threads = entries <= 256 ? 64 : entries <= 2048 ? 256 : 1024;
+  const dim3 join(threads);
   const dim3 groups(static_cast<unsigned>(static_cast<long>(a.B) * a.G));
+  const unsigned quads = static_cast<unsigned>((a.C + 3) / 4);
+  const long rows = p.form != STREAMED ? p.blocks_bwd : static_cast<long>(a.B) * p.chunks;
+  bool params = BWD && (a.dgamma || a.dbeta);
   if (p.form == WAVE) {
     a.Cg % 8 == 0 ? launch_wave<T, BWD, true>(a, p, st) : launch_wave<T, BWD, false>(a, p, st);
   } else if (p.form == RESIDENT) {
     a.Cg % 8 == 0 ? launch_resident<T, BWD, true>(a, p, st) : launch_resident<T, BWD, false>(a, p, st);
   } else if constexpr (BWD) {
     hipLaunchKernelGGL((k_gn_bwd_stats<T>), grid, block, 0, st, a);
-    hipLaunchKernelGGL(k_gn_bwd_join, groups, join, 0, st, a);
+    // a parameter's sums beside the groups' where they take at most 16 rows a thread (six samples
+    // of 5001 x 256, forward and backward: 45.4 us, in a launch of their own 47.3)
+    const bool beside = params && rows <= 4 * threads;
+    hipLaunchKernelGGL(k_gn_bwd_join, dim3(groups.x + (beside ? quads : 0)), join, 0, st, a);
+    params = params && !beside;
     hipLaunchKernelGGL((k_gn_bwd_apply<T>), pieces, block, 0, st, a);
   } else {
     hipLaunchKernelGGL((k_gn_stats<T>), grid, block, 0, st, a);
     hipLaunchKernelGGL(k_gn_join, groups, join, 0, st, a);
     hipLaunchKernelGGL((k_gn_apply<T>), pieces, block, 0, st, a);
   }
+  if (params) hipLaunchKernelGGL(k_gn_params, dim3(quads), dim3(1024), 0, st, a, rows);
 }
 
 template <bool BWD>
@@ -1133,22 +1169,15 @@ el_status el_group_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t
     GnArgs a{};
     a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.out = dx, a.ldo = lddx, a.B = B, a.S = S, a.C = C, a.G = G;
     a.lengths = lengths, a.gamma = gamma, a.beta = beta, a.act = act, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
+    a.dgamma = dgamma, a.dbeta = dbeta;
     fill(a, p);
-    const bool params = dgamma || dbeta;
     if (p.form != STREAMED) {
-      a.part = params ? static_cast<float2*>(workspace) : nullptr;
+      a.part = dgamma || dbeta ? static_cast<float2*>(workspace) : nullptr;
     } else {
       a.part = static_cast<float2*>(workspace);
       a.gsum = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.fwd_bytes);
     }
-    EL_TRY(run_gn<true>(fn, a, p, dtype, stream));
-    if (params) {
-      const long rows = p.form != STREAMED ? p.blocks_bwd : static_cast<long>(B) * p.chunks;
-      hipLaunchKernelGGL(k_gn_params, dim3(static_cast<unsigned>((C + 3) / 4)), dim3(1024), 0, stream, a.part, rows, C,
-                         dgamma, dbeta);
-      return check_launch(fn);
-    }
-    return EL_OK;
+    return run_gn<true>(fn, a, p, dtype, stream);
   });
 }
 

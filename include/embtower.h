@@ -48,7 +48,8 @@ typedef struct {
  * Activation, dropout and residual on their own:
  *   y[m][n] = residual[m][n] + drop(act(x[m][n])),   m < M, n < N
  * act: EL_ACT_*; drop NULL: no dropout; residual NULL: none.  x, residual, y: rows of strides
- * ldx, ldr, ldy (elements), all of dtype; fp32 arithmetic, one rounding.
+ * ldx, ldr, ldy (elements), all of dtype; fp32 arithmetic, one rounding.  A call with
+ * M ceil(N / 8) > 2^32 - 256 is refused (EL_ERR_UNSUPPORTED).
  */
 EL_API el_status el_act_dropout_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                     int32_t M, int32_t N, uint32_t act, const el_dropout* drop,
@@ -75,7 +76,8 @@ EL_API size_t el_dense_bwd_workspace_bytes(int32_t M, int32_t K, int32_t N);
  * x: [M] rows of stride ldx (first K used); w: [N][K] row-major; bias: fp32 [N] or NULL;
  * residual, pre, y: [M] rows of strides ldr, ldpre, ldy.  dtype: EL_BF16 or EL_F16 (one for x,
  * w, residual, pre and y).  Products accumulate in fp32 (MFMA); y is computed from the fp32 z,
- * one rounding each.  Any K, N >= 1.  workspace: >= el_dense_fwd_workspace_bytes(M, K, N),
+ * one rounding each.  Any K, N from 1 to 2^20 with N K < 2^29 (EL_ERR_UNSUPPORTED beyond).
+ * workspace: >= el_dense_fwd_workspace_bytes(M, K, N),
  * 256-byte aligned, contents irrelevant (NULL when that is 0).
  */
 EL_API el_status el_dense_fwd(const void* x, int64_t ldx, int32_t M, int32_t K, const void* w,
@@ -96,7 +98,7 @@ EL_API el_status el_dense_fwd(const void* x, int64_t ldx, int32_t M, int32_t K, 
  * layer).  dzb is the dz of the layer below, whose output is x: act, drop and pre are that
  * layer's; it is computed from the fp32 dx, so a tower's backward is one call per layer.  pre
  * may be NULL with EL_ACT_NONE; dzb needs dx.  The sums over m are split into fixed slices
- * whose fp32 partials are added in slice order: bitwise reproducible.  M == 0 gives zero dw, db.
+ * whose fp32 partials are added in a fixed order: bitwise reproducible.  M == 0 gives zero dw, db.
  * workspace: >= el_dense_bwd_workspace_bytes(M, K, N), 256-byte aligned.
  */
 EL_API el_status el_dense_bwd(const void* x, int64_t ldx, int32_t M, int32_t K, const void* w,
@@ -123,7 +125,8 @@ EL_API size_t el_group_norm_bwd_workspace_bytes(int32_t B, int32_t S, int32_t C,
  * pooled vectors [B][F][D] normalises each sample's embeddings over its F tables.
  * x, y: rows of strides ldx, ldy, dtype EL_F32 / EL_F16 / EL_BF16; gamma, beta: fp32 [C] or
  * NULL (1, 0); mean, rstd: fp32 [B][G], overwritten; statistics and arithmetic in fp32, the
- * variance from centred values.  C % G == 0, eps >= 0 finite.  workspace: >=
+ * variance from centred values.  C % G == 0, eps >= 0 finite.  Up to C = 2^20, B = 2^22,
+ * S = 2^30 and B G = 2^25 (EL_ERR_UNSUPPORTED beyond).  workspace: >=
  * el_group_norm_fwd_workspace_bytes(B, S, C, G), 256-byte aligned (NULL when that is 0).
  */
 EL_API el_status el_group_norm_fwd(const void* x, int64_t ldx, int32_t B, int32_t S, int32_t C,
