@@ -319,27 +319,32 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
     }
   }
   if (!a.part) return;
-  // the threads of one channel vector: all teams, all thread rows, in that order
+  // the thread rows of all teams into row 0, by halving the rows
   float2* red = reinterpret_cast<float2*>(lds);
-  const int rows = a.spw * a.TR;
-#pragma unroll 1
-  for (int q = 0; q < 8; ++q) {
-    __syncthreads();
-    float vb = 0.f, vg = 0.f;
+  const int nt = blockDim.x, row = team_id * a.TR + tr;
+  __syncthreads();
+  for (int left = a.spw * a.TR; left > 1;) {
+    const int half = (left + 1) / 2;
+    if (row >= half && row < left) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k == q) vb = sb[k], vg = sg[k];
-    if (team_id < a.spw) red[(team_id * a.TR + tr) * a.CV + cv] = make_float2(vb, vg);
-    __syncthreads();
-    if (tid < a.CV && tid * 8 + q < a.C) {
-      float2 s = make_float2(0.f, 0.f);
-      for (int k = 0; k < rows; ++k) {
-        const float2 v = red[k * a.CV + tid];
-        s.x += v.x;
-        s.y += v.y;
-      }
-      a.part[static_cast<long>(blockIdx.x) * a.C + tid * 8 + q] = s;
+      for (int q = 0; q < 8; ++q) red[q * nt + tid] = make_float2(sb[q], sg[q]);
     }
+    __syncthreads();
+    if (row < half && row + half < left) {  // (the next rows to be written lie before these)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float2 v = red[q * nt + tid + half * a.CV];
+        sb[q] += v.x;
+        sg[q] += v.y;
+      }
+    }
+    left = half;
+  }
+  if (row == 0) {
+    float2* part = a.part + static_cast<long>(blockIdx.x) * a.C + cv * 8;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) part[q] = make_float2(sb[q], sg[q]);
   }
 }
 
@@ -587,7 +592,7 @@ __device__ inline StreamPos stream_pos(const GnArgs& a, int chunks, int per) {
 // halving the rows: join(x, y, other pair, n, other's n) for each channel.
 template <class F>
 __device__ inline void join_rows(const StreamPos& q, int TC, float (&x)[8], float (&y)[8], float n, F&& join) {
-  __shared__ float2 red[kStream / 2][8];
+  __shared__ float2 red[8][kStream / 2];
   __shared__ float cnt[kStream / 2];
   const int col = q.cv % TC;
   int h = 1;
@@ -597,7 +602,7 @@ __device__ inline void join_rows(const StreamPos& q, int TC, float (&x)[8], floa
     if (q.on && q.tr >= h && q.tr < width) {
       const int at = (q.tr - h) * TC + col;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) red[at][i] = make_float2(x[i], y[i]);
+      for (int i = 0; i < 8; ++i) red[i][at] = make_float2(x[i], y[i]);
       cnt[at] = n;
     }
     __syncthreads();
@@ -605,7 +610,7 @@ __device__ inline void join_rows(const StreamPos& q, int TC, float (&x)[8], floa
       const int at = q.tr * TC + col;
       const float nb = cnt[at];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) join(x[i], y[i], red[at][i], n, nb);
+      for (int i = 0; i < 8; ++i) join(x[i], y[i], red[i][at], n, nb);
       n += nb;
     }
   }
@@ -998,7 +1003,7 @@ void fill(GnArgs& a, const GnPlan& p) {
 
 template <class T, bool BWD, bool VECG>
 void launch_resident(const GnArgs& a, const GnPlan& p, hipStream_t st) {
-  const size_t lds = std::max(resident_lds(a.Cg, a.G, p.TR, p.spw, p.threads, BWD ? 2 : 1), BWD ? p.threads * sizeof(float2) : 0);
+  const size_t lds = std::max(resident_lds(a.Cg, a.G, p.TR, p.spw, p.threads, BWD ? 2 : 1), BWD ? 8 * p.threads * sizeof(float2) : 0);
   const dim3 grid(BWD ? p.blocks_bwd : p.blocks_fwd), block(p.threads);
 #define GN_CASE(NV)                                                                                        \
   case NV:                                                                                                 \
