@@ -142,8 +142,8 @@ __device__ inline void grad8(const GnArgs& a, const Raw8<T>& rx, const Raw8<T>& 
 }
 
 // Hides a vector's value from the compiler: what was computed from it before is computed again
-// instead of being kept.  (The backward holds a sample as raw 16-byte vectors; its fp32 values
-// would take four times the registers and halve the wavefronts in flight.)
+// instead of being kept.  (The backward holds x as raw 16-byte vectors; xh beside du in fp32 would
+// spill.)
 template <class T>
 __device__ inline void forget(Raw8<T>& r) {
 #pragma unroll
@@ -278,16 +278,16 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) shift[q] *= -rstd[q];
     const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
-    float p[2][8] = {}, cb[8] = {}, cg[8] = {};
+    float p[2][8] = {}, cb[8] = {}, cg[8] = {}, du[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (tr + i * a.TR < len) {
-        float xh[8], du[8];
-        grad8<T, false>(a, rx[i], rd[i], shift, rstd, gamma, beta, xh, du);  // du is zero past the last channel
+        float xh[8];
+        grad8<T, false>(a, rx[i], rd[i], shift, rstd, gamma, beta, xh, du[i]);  // du is zero past the last channel
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          cb[q] += du[q];
-          cg[q] = fmaf(du[q], xh[q], cg[q]);
+          cb[q] += du[i][q];
+          cg[q] = fmaf(du[i][q], xh[q], cg[q]);
         }
       }
 #pragma unroll
@@ -306,13 +306,13 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
         if (s >= a.S) continue;
         float f[8] = {};
         if (s < len) {
-          float du[8];
           forget(rx[i]);
-          forget(rd[i]);
-          grad8<T, false>(a, rx[i], rd[i], shift, rstd, gamma, beta, f, du);
+          to_floats<T>(rx[i], f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            f[q] = rstd[q] * (du[q] * gamma[q] - of_channel<VECG>(p[0], q) * inv_n - f[q] * (of_channel<VECG>(p[1], q) * inv_n));
+          for (int q = 0; q < 8; ++q) {
+            f[q] = fmaf(f[q], rstd[q], shift[q]);
+            f[q] = rstd[q] * (du[i][q] * gamma[q] - of_channel<VECG>(p[0], q) * inv_n - f[q] * (of_channel<VECG>(p[1], q) * inv_n));
+          }
         }
         store8<T>(dx + s * a.ldo, f, n);
       }
@@ -463,10 +463,15 @@ __global__ __launch_bounds__(kWave) void k_gn_fwd_wave(GnArgs a) {
 // part[workgroup][c] = (dbeta, dgamma) of the workgroup's samples, as in the resident form.
 // Two wavefronts per SIMD; one where eight fp32 vectors and per-channel sums would spill too much
 // (8192 samples of 26 x 128, forward and backward, 32 groups: 157 us, spilling 171; 8 groups, whose
-// sums are fewer: 142, spilling 134).
+// sums are fewer: 142, spilling 134).  du stays in registers between the sums and dx (KEEP: the
+// activation's derivative, two transcendental instructions a value, is taken once), unless that
+// spills at eight vectors a lane: 16384 samples of 26 x 128 bf16, forward and backward, 8 groups 135
+// us against 146 taken twice, 32 groups 218 against 181; 8192 of fp32, 8 groups 171 against 133, 32
+// groups 148 against 158.
 template <class T, int NV, bool VECG>
 __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) == 4 ? 1 : 2) void k_gn_bwd_wave(GnArgs a) {
   using St = typename T::S;
+  constexpr bool KEEP = NV < 8 || VECG == (sizeof(St) == 2);
   float gamma[8], beta[8], sb[8] = {}, sg[8] = {};
   load_params(a, threadIdx.x & (a.CV - 1), gamma, beta);
   const int per = kWave / a.team;
@@ -483,7 +488,7 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
         rd[i] = load8_raw<T>(dy + s * a.lddy);
       }
     }
-    float shift[8], rstd[8], p0[8] = {}, p1[8] = {}, cb[8] = {}, cg[8] = {};
+    float shift[8], rstd[8], p0[8] = {}, p1[8] = {}, cb[8] = {}, cg[8] = {}, du[KEEP ? NV : 1][8];
 #pragma unroll
     for (int q = 0; q < (VECG ? 1 : 8); ++q) {
       const long at = w.on ? w.b * a.G + (w.cv * 8 + q) / a.Cg : 0;
@@ -494,12 +499,13 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (w.tr + i * a.TR < w.len) {
-        float xh[8], du[8];
-        grad8<T, VECG>(a, rx[i], rd[i], shift, rstd, gamma, beta, xh, du);
+        float xh[8];
+        float(&d)[8] = du[KEEP ? i : 0];
+        grad8<T, VECG>(a, rx[i], rd[i], shift, rstd, gamma, beta, xh, d);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          cb[q] += du[q];
-          cg[q] = fmaf(du[q], xh[q], cg[q]);
+          cb[q] += d[q];
+          cg[q] = fmaf(d[q], xh[q], cg[q]);
         }
         __builtin_amdgcn_sched_barrier(0);  // one vector's values in registers at a time
       }
@@ -522,13 +528,19 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
       if (s >= a.S) continue;
       float f[8] = {};
       if (s < w.len) {
-        float du[8];
+        float(&d)[8] = du[KEEP ? i : 0];
         forget(rx[i]);
-        forget(rd[i]);
-        grad8<T, VECG>(a, rx[i], rd[i], shift, rstd, gamma, beta, f, du);
+        if constexpr (KEEP) {
+          to_floats<T>(rx[i], f);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) f[q] = fmaf(f[q], of_channel<VECG>(rstd, q), of_channel<VECG>(shift, q));
+        } else {
+          forget(rd[i]);
+          grad8<T, VECG>(a, rx[i], rd[i], shift, rstd, gamma, beta, f, d);
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          f[q] = of_channel<VECG>(rstd, q) * fmaf(du[q], gamma[q], fmaf(f[q], of_channel<VECG>(p1, q), of_channel<VECG>(p0, q)));
+          f[q] = of_channel<VECG>(rstd, q) * fmaf(d[q], gamma[q], fmaf(f[q], of_channel<VECG>(p1, q), of_channel<VECG>(p0, q)));
         __builtin_amdgcn_sched_barrier(0);
       }
       store8<T>(dx + s * a.ldo, f, 8);
