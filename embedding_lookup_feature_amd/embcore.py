@@ -126,6 +126,19 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call on `stream`, allocated on that stream: the tensor dies when the
+    call returns, while its kernels may still run, and torch's allocator gives the freed block only
+    to later work of the stream it was allocated on, which waits for them."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # a raw handle (ExternalStream(0) would be a new stream)
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else
+                  torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _dev(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -385,7 +398,7 @@ def linear_bwd(x: torch.Tensor, w: torch.Tensor, dz: torch.Tensor, dw: torch.Ten
             raise ValueError("dx must have M rows")
     need = linear_bwd_workspace_bytes(M, K, N)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, x.device, stream)
     wp = _dev(workspace, "workspace") if workspace is not None else None
     wn = workspace.numel() if workspace is not None else 0
     _check(lib().el_linear_bwd(xp, ldx, M, K, _dev(w, "w"), N, zp, ldz, dxp, lddx,
@@ -414,7 +427,7 @@ def bce_logits(z: torch.Tensor, labels: torch.Tensor, loss: torch.Tensor, dz: to
     workspace: bytes >= bce_workspace_bytes(M) (allocated here when not given)."""
     M = labels.numel()
     if workspace is None:
-        workspace = torch.empty(max(8, bce_workspace_bytes(M)), dtype=torch.uint8, device=z.device)
+        workspace = _scratch(max(8, bce_workspace_bytes(M)), z.device, stream)
     ldz = z.stride(0) if z.dim() >= 1 else 1
     lddz = dz.stride(0) if dz.dim() >= 1 else 1
     if not (z.is_cuda and dz.is_cuda):

@@ -3,7 +3,8 @@
 Argument marshalling only, in the manner of ``embcore``: torch tensors are passed as device
 pointers plus sizes and row strides, on torch's current HIP stream unless a stream is given;
 outputs and workspaces belong to the caller (a workspace that is not given is allocated here
-for the call).  Two-dimensional operands may be row-strided views (last dimension dense).
+for the call, on the call's stream).  Two-dimensional operands may be row-strided views (last
+dimension dense).
 """
 import ctypes
 import os
@@ -124,9 +125,9 @@ def _rows_cols(t: torch.Tensor, name: str):
     return s
 
 
-def _workspace(ws, need: int, device):
+def _workspace(ws, need: int, device, stream):
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = ec._scratch(need, device, stream)
     if ws is None:
         return None, 0, None
     return ec._dev(ws, "workspace"), ws.numel() * ws.element_size(), ws
@@ -178,7 +179,8 @@ def dense_fwd(x: torch.Tensor, w: torch.Tensor, bias, y: torch.Tensor, act: str 
     rp, ldr = _mat(residual, "residual", (M, N), x.dtype)
     pp, ldp = _mat(pre, "pre", (M, N), x.dtype)
     yp, ldy = _mat(y, "y", (M, N), x.dtype)
-    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_fwd_workspace_bytes(M, K, N), x.device)
+    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_fwd_workspace_bytes(M, K, N),
+                                x.device, stream)
     ec._check(lib().el_dense_fwd(xp, ldx, M, K, ec._dev(w, "w"), _vec(bias, "bias", N), N, _act(act), _drop(dropout),
                                  rp, ldr, pp, ldp, yp, ldy, ec._dtype(x, "x"), wsp, wsn, _stream(stream, x)))
     return y
@@ -200,7 +202,8 @@ def dense_bwd(x: torch.Tensor, w: torch.Tensor, dz: torch.Tensor, dw: torch.Tens
     rp, ldr = _mat(dres, "dres", (M, K), x.dtype)
     bp, ldb = _mat(dzb, "dzb", (M, K), x.dtype)
     pp, ldp = _mat(pre, "pre", (M, K), x.dtype)
-    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_bwd_workspace_bytes(M, K, N), x.device)
+    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_bwd_workspace_bytes(M, K, N),
+                                x.device, stream)
     if dw.numel() != N * K:
         raise ValueError(f"dw must be [{N}, {K}]")
     ec._check(lib().el_dense_bwd(xp, ldx, M, K, ec._dev(w, "w"), N, zp, ldz, rp, ldr, dxp, lddx, _act(act),
@@ -234,7 +237,8 @@ def group_norm_fwd(x: torch.Tensor, gamma, beta, y: torch.Tensor, mean: torch.Te
     B, S, C, G = _samples(x, positions, groups)
     xp, ldx = _mat(x, "x", x.shape, x.dtype)
     yp, ldy = _mat(y, "y", x.shape, x.dtype)
-    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else group_norm_fwd_workspace_bytes(B, S, C, G), x.device)
+    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else group_norm_fwd_workspace_bytes(B, S, C, G),
+                                x.device, stream)
     ec._check(lib().el_group_norm_fwd(xp, ldx, B, S, C, G, _vec(lengths, "lengths", B, torch.int32),
                                       _vec(gamma, "gamma", C), _vec(beta, "beta", C), float(eps), _act(act), yp, ldy,
                                       _vec(mean, "mean", B * G), _vec(rstd, "rstd", B * G), ec._dtype(x, "x"), wsp,
@@ -251,7 +255,8 @@ def group_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma, beta, mean: torch.T
     dp, lddy = _mat(dy, "dy", x.shape, x.dtype)
     xp, ldx = _mat(x, "x", x.shape, x.dtype)
     op, lddx = _mat(dx, "dx", x.shape, x.dtype)
-    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else group_norm_bwd_workspace_bytes(B, S, C, G), x.device)
+    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else group_norm_bwd_workspace_bytes(B, S, C, G),
+                                x.device, stream)
     ec._check(lib().el_group_norm_bwd(dp, lddy, xp, ldx, B, S, C, G, _vec(lengths, "lengths", B, torch.int32),
                                       _vec(gamma, "gamma", C), _vec(beta, "beta", C), _vec(mean, "mean", B * G),
                                       _vec(rstd, "rstd", B * G), _act(act), op, lddx, _vec(dgamma, "dgamma", C),
