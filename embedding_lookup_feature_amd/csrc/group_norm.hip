@@ -18,7 +18,8 @@
 //   resident   a sample sits in the registers of one workgroup's threads, which join its sums in
 //              LDS: read once, any width and group size;
 //   streamed   samples too large for that are cut into chunks of positions: one kernel leaves
-//              per-channel statistics of each chunk, one joins them per group, one applies them
+//              per-channel statistics of each chunk, one joins them per group (the forward of a
+//              sample in one chunk does both in one), one applies them
 //              (x, and dy, are read twice, the second time from the caches where they fit: 6
 //              samples of up to 5001 x 256 in 32 groups, fp16: stats 7.2 us, join 4.5, apply 9.1;
 //              backward 11.4, 4.3 with the parameters' sums, 10.4: six dependent launches).
@@ -638,10 +639,40 @@ __device__ inline void write_part(const GnArgs& a, const StreamPos& q, const flo
     if (i < q.n) part[i] = make_float2(x[i], y[i]);
 }
 
+// mean and rstd of the sample's groups from row 0's channel statistics, where the workgroup has the
+// whole sample: up to 64 lanes share a group's channels.
+__device__ inline void group_stats(const GnArgs& a, const StreamPos& q, const float (&mean)[8], const float (&m2)[8]) {
+  __shared__ float2 chan[kStream * 8];
+  if (q.on && q.tr == 0)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < q.n) chan[q.cv * 8 + i] = make_float2(mean[i], m2[i]);
+  __syncthreads();
+  const int len = sample_len(a, q.b);
+  const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
+  int lanes = 1;
+  while (lanes < a.Cg && lanes < 64) lanes *= 2;
+  const int lane = threadIdx.x % lanes;
+  for (int g = threadIdx.x / lanes; g < a.G; g += kStream / lanes) {
+    const float2* ch = chan + g * a.Cg;
+    float s = 0.f, v = 0.f;
+    for (int c = lane; c < a.Cg; c += lanes) s += ch[c].x;
+    for (int m = lanes / 2; m > 0; m /= 2) s += __shfl_xor(s, m);
+    s /= static_cast<float>(a.Cg);
+    for (int c = lane; c < a.Cg; c += lanes) v += ch[c].y + static_cast<float>(len) * (ch[c].x - s) * (ch[c].x - s);
+    for (int m = lanes / 2; m > 0; m /= 2) v += __shfl_xor(v, m);
+    if (lane == 0) {
+      a.mean[static_cast<long>(q.b) * a.G + g] = s;
+      a.rstd[static_cast<long>(q.b) * a.G + g] = 1.f / sqrtf(v * inv_n + a.eps);
+    }
+  }
+}
+
 // part[b][chunk][c] = (mean, sum of squares about it) of channel c over the chunk's valid
 // positions.  A thread sums differences from its first value; threads are joined by the
-// pairwise update of Chan, Golub and LeVeque (1979).
-template <class T>
+// pairwise update of Chan, Golub and LeVeque (1979).  WHOLE: the workgroup has the whole sample and
+// writes the groups' mean and rstd instead.
+template <class T, bool WHOLE>
 __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
   using St = typename T::S;
   const StreamPos q = stream_pos(a, a.chunks, a.per_chunk);
@@ -685,7 +716,8 @@ __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
       s += o.y + d * d * (na * w);
     }
   });
-  write_part(a, q, mean, m2);
+  if constexpr (WHOLE) group_stats(a, q, mean, m2);
+  else write_part(a, q, mean, m2);
 }
 
 // Sum of v over the workgroup's threads, in a fixed order, for every thread.
@@ -925,7 +957,9 @@ struct GnPlan {
   Form form = STREAMED;
   int NV = 1, TR = 0, team = 0, spw = 1, threads = 0, blocks_fwd = 0, blocks_bwd = 0;
   int chunks = 1, per_chunk = 1, pieces = 1, per_piece = 1, colblocks = 1, TC = 1;
+  bool whole = false;                // streamed: one workgroup has a sample's statistics
   size_t fwd_bytes = 0, bwd_bytes = 0;
+  size_t part_bytes = 0;             // streamed backward: the channel sums, before gsum
 };
 
 // LDS of group_sums for nval values: entries, their first sums, the groups' sums.
@@ -995,8 +1029,13 @@ GnPlan plan_gn(int B, int S, int C, int G) {
   while (static_cast<long>(B) * p.colblocks * ((S + static_cast<long>(p.per_piece) - 1) / p.per_piece) > (1l << 22) && p.per_piece < S)
     p.per_piece = static_cast<int>(std::min<long>(S, 2l * p.per_piece));
   p.pieces = static_cast<int>((S + static_cast<long>(p.per_piece) - 1) / p.per_piece);
-  p.fwd_bytes = round256(static_cast<size_t>(B) * p.chunks * C * sizeof(float2));
-  p.bwd_bytes = p.fwd_bytes + round256(static_cast<size_t>(B) * G * 2 * sizeof(float));
+  // The forward leaves channel statistics only where they have to be joined across workgroups, so
+  // the 8 MB above hold for every batch of up to 8 kStream channels (1492 samples of 9 x 1888 bf16:
+  // 45.1 us, with channel statistics of 22 MB and a join 65.9; 600 of 200 x 128: 26.2, 30.0).
+  p.whole = p.chunks == 1 && p.colblocks == 1;
+  p.part_bytes = round256(static_cast<size_t>(B) * p.chunks * C * sizeof(float2));
+  p.fwd_bytes = p.whole ? 0 : p.part_bytes;
+  p.bwd_bytes = p.part_bytes + round256(static_cast<size_t>(B) * G * 2 * sizeof(float));
   return p;
 }
 
@@ -1064,8 +1103,12 @@ void launch_gn(const GnArgs& a, const GnPlan& p, hipStream_t st) {
     params = params && !beside;
     hipLaunchKernelGGL((k_gn_bwd_apply<T>), pieces, block, 0, st, a);
   } else {
-    hipLaunchKernelGGL((k_gn_stats<T>), grid, block, 0, st, a);
-    hipLaunchKernelGGL(k_gn_join, groups, join, 0, st, a);
+    if (p.whole) {
+      hipLaunchKernelGGL((k_gn_stats<T, true>), grid, block, 0, st, a);
+    } else {
+      hipLaunchKernelGGL((k_gn_stats<T, false>), grid, block, 0, st, a);
+      hipLaunchKernelGGL(k_gn_join, groups, join, 0, st, a);
+    }
     hipLaunchKernelGGL((k_gn_apply<T>), pieces, block, 0, st, a);
   }
   if (params) hipLaunchKernelGGL(k_gn_params, dim3(quads), dim3(1024), 0, st, a, rows);
@@ -1193,7 +1236,7 @@ el_status el_group_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t
       a.part = dgamma || dbeta ? static_cast<float2*>(workspace) : nullptr;
     } else {
       a.part = static_cast<float2*>(workspace);
-      a.gsum = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.fwd_bytes);
+      a.gsum = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_bytes);
     }
     return run_gn<true>(fn, a, p, dtype, stream);
   });

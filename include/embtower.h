@@ -109,7 +109,8 @@ EL_API el_status el_dense_bwd(const void* x, int64_t ldx, int32_t M, int32_t K, 
                               size_t workspace_bytes, hipStream_t stream);
 
 /* [host, pure] Bytes of device workspace el_group_norm_fwd / _bwd need for B samples of S
- * positions, C channels in G groups; 0 for invalid or empty sizes. */
+ * positions, C channels in G groups; 0 for invalid or empty sizes.  The forward's are at most
+ * 8 MiB for up to 2048 channels. */
 EL_API size_t el_group_norm_fwd_workspace_bytes(int32_t B, int32_t S, int32_t C, int32_t G);
 EL_API size_t el_group_norm_bwd_workspace_bytes(int32_t B, int32_t S, int32_t C, int32_t G);
 
