@@ -670,21 +670,22 @@ WgradPlan plan_wgrad(int M, int K, int N, bool shared) {
   return p;
 }
 
-// Tiles of `a` (all splits) in shape C; 0 if there are too many for one launch.
+// What one launch takes of the forward's and the data gradient's R x C outputs (shape L, where there
+// are many); the weight gradient's, N K < 2^29 of them, are always fewer.
+bool tiles_fit(long R, long C) { return ceil_div(R, kEdge[SHAPE_L]) * ceil_div(C, kEdge[SHAPE_L]) < (1l << 21); }
+el_status too_many_tiles(const char* fn) { return tower::unsupported(fn, "an output must have fewer than 2^21 tiles of 256 x 256"); }
+
+// Tiles of `a` (all splits) in shape C.
 template <class C>
 int set_tiles(GemmArgs& a, int splits) {
   a.tiles_c = static_cast<int>(ceil_div(a.C, C::BC));
-  const long tiles = ceil_div(a.R, C::BR) * a.tiles_c;
-  if (tiles * splits >= (1l << 21)) return 0;
-  a.tiles = static_cast<int>(tiles);
+  a.tiles = static_cast<int>(ceil_div(a.R, C::BR) * a.tiles_c);
   return a.tiles * splits;
 }
-el_status too_many_tiles(const char* fn) { return tower::unsupported(fn, "the output has too many tiles for one launch"); }
 
 template <class T, class C, int PROD>
 el_status launch_tiles(const char* fn, GemmArgs a, int splits, hipStream_t st) {
   const int n = set_tiles<C>(a, splits);
-  if (!n) return too_many_tiles(fn);
   hipLaunchKernelGGL((k_dense<T, C, PROD>), dim3(n), dim3(C::NW * 64), 0, st, a);
   return check_launch(fn);
 }
@@ -698,7 +699,6 @@ el_status launch_product(const char* fn, const GemmArgs& a, Shape s, int splits,
 template <class T, class CD, class CW>
 el_status launch_both(const char* fn, GemmArgs d, GemmArgs w, int splits, hipStream_t st) {
   const int nd = set_tiles<CD>(d, 1), nw = set_tiles<CW>(w, splits);
-  if (!nd || !nw) return too_many_tiles(fn);
   hipLaunchKernelGGL((k_dense_bwd<T, CD, CW>), dim3(nd + nw), dim3(CD::NW * 64), 0, st, d, w, nd);
   return check_launch(fn);
 }
@@ -850,7 +850,7 @@ el_status run_bwd(const char* fn, const uint16_t* x, long ldx, int M, int K, con
 extern "C" {
 
 size_t el_dense_fwd_workspace_bytes(int32_t M, int32_t K, int32_t N) {
-  if (!dense_sizes_ok(M, K, N) || plan_few(M, N)) return 0;
+  if (!dense_sizes_ok(M, K, N) || plan_few(M, N) || !tiles_fit(M, N)) return 0;
   return packed_bytes(M, K) + packed_bytes(N, K);
 }
 
@@ -874,6 +874,7 @@ el_status el_dense_fwd(const void* x, int64_t ldx, int32_t M, int32_t K, const v
     EL_TRY(tower::check_rows(fn, "pre", pre, ldpre, N, false, 2));
     EL_TRY(tower::check_rows(fn, "y", y, ldy, N, M > 0, 2));
     if (M == 0) return EL_OK;
+    if (!tiles_fit(M, N)) return too_many_tiles(fn);
     const size_t need = plan_few(M, N) ? 0 : copy_bytes(x, ldx, M, K) + copy_bytes(w, K, N, K);
     EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, need));
     a.P = u16(x), a.ldp = ldx, a.Q = u16(w), a.ldq = K, a.R = M, a.C = N, a.red = K, a.act = act;
@@ -906,6 +907,7 @@ el_status el_dense_bwd(const void* x, int64_t ldx, int32_t M, int32_t K, const v
       if (db) hipLaunchKernelGGL(k_zero, dim3(static_cast<unsigned>(ceil_div(N, 256))), dim3(256), 0, stream, db, static_cast<long>(N));
       return check_launch(fn);
     }
+    if (dx && !tiles_fit(M, K)) return too_many_tiles(fn);
     const size_t need = copy_bytes(dz, lddz, M, N) + copy_bytes(x, ldx, M, K) + (dx ? copy_bytes(w, K, N, K) : 0) +
                         plan_wgrad(M, K, N, wgrad_shares(M, K, dx)).bytes;
     EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, need));

@@ -64,7 +64,7 @@ EL_API el_status el_act_dropout_bwd(const void* dy, int64_t lddy, const void* x,
                                     void* dx, int64_t lddx, el_dtype dtype, hipStream_t stream);
 
 /* [host, pure] Bytes of device workspace el_dense_fwd / el_dense_bwd can need for these sizes,
- * whatever the strides and alignments; 0 for invalid sizes or M == 0. */
+ * whatever the strides and alignments; 0 for invalid or unsupported sizes or M == 0. */
 EL_API size_t el_dense_fwd_workspace_bytes(int32_t M, int32_t K, int32_t N);
 EL_API size_t el_dense_bwd_workspace_bytes(int32_t M, int32_t K, int32_t N);
 
@@ -76,9 +76,11 @@ EL_API size_t el_dense_bwd_workspace_bytes(int32_t M, int32_t K, int32_t N);
  * x: [M] rows of stride ldx (first K used); w: [N][K] row-major; bias: fp32 [N] or NULL;
  * residual, pre, y: [M] rows of strides ldr, ldpre, ldy.  dtype: EL_BF16 or EL_F16 (one for x,
  * w, residual, pre and y).  Products accumulate in fp32 (MFMA); y is computed from the fp32 z,
- * one rounding each.  Any K, N from 1 to 2^20 with N K < 2^29 (EL_ERR_UNSUPPORTED beyond).
- * workspace: >= el_dense_fwd_workspace_bytes(M, K, N),
- * 256-byte aligned, contents irrelevant (NULL when that is 0).
+ * one rounding each.  Any K, N from 1 to 2^20 with N K < 2^29 and ceil(M/256) ceil(N/256) < 2^21
+ * (EL_ERR_UNSUPPORTED beyond).  x and w are copied to the workspace where their rows are not
+ * whole 16-byte aligned vectors; such operands may have fewer than 2^35 elements together.
+ * workspace: >= el_dense_fwd_workspace_bytes(M, K, N), 256-byte aligned, contents irrelevant
+ * (NULL when that is 0).
  */
 EL_API el_status el_dense_fwd(const void* x, int64_t ldx, int32_t M, int32_t K, const void* w,
                               const float* bias, int32_t N, uint32_t act, const el_dropout* drop,
@@ -97,8 +99,11 @@ EL_API el_status el_dense_fwd(const void* x, int64_t ldx, int32_t M, int32_t K, 
  * dres is the gradient that reaches x by another way (the skip connection of a residual
  * layer).  dzb is the dz of the layer below, whose output is x: act, drop and pre are that
  * layer's; it is computed from the fp32 dx, so a tower's backward is one call per layer.  pre
- * may be NULL with EL_ACT_NONE; dzb needs dx.  The sums over m are split into fixed slices
- * whose fp32 partials are added in a fixed order: bitwise reproducible.  M == 0 gives zero dw, db.
+ * may be NULL with EL_ACT_NONE; dzb needs dx.  The sums over m are split into fixed slices (by
+ * the sizes, and by whether dx is asked for) whose fp32 partials are added in a fixed order:
+ * bitwise reproducible.  M == 0 gives zero dw, db.  K and N as in the
+ * forward, and ceil(M/256) ceil(K/256) < 2^21 where dx is asked for; dz, x and (for dx) w are
+ * copied as x and w are there, with the same limit.
  * workspace: >= el_dense_bwd_workspace_bytes(M, K, N), 256-byte aligned.
  */
 EL_API el_status el_dense_bwd(const void* x, int64_t ldx, int32_t M, int32_t K, const void* w,

@@ -39,3 +39,30 @@ def test_workspaces_of_the_measured_range_fit_a_programs_buffers():
         else:
             continue
         assert need <= give[c["op"]], (c["op"], a, need)
+
+
+A = 0x7F0000000000  # fake, aligned: every call below ends at its checks
+
+
+@pytest.mark.parametrize("M,N,extra", [(1 << 29, 8, 1), (2**31 - 1, 8, 0), (1 << 29, 1, 8), (1 << 24, 1 << 13, 1)])
+def test_dense_outputs_of_too_many_tiles_are_refused_before_any_work(M, N, extra):
+    """Also where operands would be copied first (odd row strides): nothing is enqueued, so the
+    refusal is the call's and no launch is tried."""
+    from embedding_lookup_feature_amd import embcore as ec
+    L, K, big = tw.lib(), 8, 1 << 50
+    rc = L.el_dense_fwd(A, K + extra, M, K, A, None, N, 0, None, None, 0, None, 0, A, N, ec.EL_BF16, A, big, None)
+    assert rc == ec.EL_ERR_UNSUPPORTED and "tiles" in ec.el_last_error()
+    assert tw.dense_fwd_workspace_bytes(M, K, N) == 0
+    # the data gradient's output is [M, K]: the sizes the other way round
+    rc = L.el_dense_bwd(A, N + extra, M, N, A, K, A, K + extra, None, 0, A, N, 0, None, None, 0, None, 0, A, None,
+                        ec.EL_BF16, A, big, None)
+    assert rc == ec.EL_ERR_UNSUPPORTED and "tiles" in ec.el_last_error()
+
+
+def test_dense_sizes_up_to_the_limit_pass_the_checks():
+    """One tile below the limit the call goes on to ask for its workspace."""
+    from embedding_lookup_feature_amd import embcore as ec
+    M, K, N = (1 << 29) - 256, 8, 8
+    rc = tw.lib().el_dense_fwd(A, K + 1, M, K, A, None, N, 0, None, None, 0, None, 0, A, N, ec.EL_BF16, None, 0, None)
+    assert rc == ec.EL_ERR_WORKSPACE
+    assert tw.dense_fwd_workspace_bytes(M, K, N) >= 16 * M
