@@ -272,7 +272,8 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
   const int split = lid / a.tiles, t = lid - split * a.tiles;
   const int tr = t / a.tiles_c, tc = t - tr * a.tiles_c;
   const int row0 = tr * C::BR, col0 = tc * C::BC;
-  const int kbeg = split * a.per_split, kend = min(a.red, kbeg + a.per_split);
+  const int kbeg = split * a.per_split;
+  const int kend = a.red - kbeg < a.per_split ? a.red : kbeg + a.per_split;  // (the sum may pass 2^31)
   const int nk = (kend - kbeg + BK - 1) / BK;
   const int wr = wave / WC, wc = wave % WC;
   OP op;
@@ -661,7 +662,7 @@ WgradPlan plan_wgrad(int M, int K, int N, bool shared) {
     if (s == SHAPE_S) splits = std::min(splits, ceil_div(M, 256));
     else if (M / splits >= (s == SHAPE_L ? 2048 : 512)) break;
   }
-  p.per = static_cast<int>(ceil_div(ceil_div(M, splits), 64) * 64);
+  p.per = static_cast<int>(std::min(ceil_div(ceil_div(M, splits), 64) * 64, (1l << 31) - 64));
   p.splits = static_cast<int>(ceil_div(M, p.per));
   const int wc = p.shape == SHAPE_L ? CfgL::WC : p.shape == SHAPE_M ? CfgM::WC : CfgS::WC;
   p.db_rows = p.splits * static_cast<int>(ceil_div(K, kEdge[p.shape])) * wc;

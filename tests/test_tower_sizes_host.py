@@ -66,3 +66,11 @@ def test_dense_sizes_up_to_the_limit_pass_the_checks():
     rc = tw.lib().el_dense_fwd(A, K + 1, M, K, A, None, N, 0, None, None, 0, None, 0, A, N, ec.EL_BF16, None, 0, None)
     assert rc == ec.EL_ERR_WORKSPACE
     assert tw.dense_fwd_workspace_bytes(M, K, N) >= 16 * M
+
+
+def test_dense_bwd_partials_are_counted_for_the_longest_batches():
+    r256, pad8 = (lambda n: -(-n // 256) * 256), (lambda n: -(-n // 8) * 8)
+    for M in (2**31 - 1, 2**31 - 64, 2**31 - 65, 2**31 - 4096):
+        for K, N in ((8, 1 << 20), (1 << 20, 8), (8, 8), (512, 1024)):
+            copies = sum(r256(a * pad8(b) * 2) for a, b in ((M, N), (M, K), (N, K)))
+            assert tw.dense_bwd_workspace_bytes(M, K, N) - copies >= 4 * N * K, (M, K, N)
