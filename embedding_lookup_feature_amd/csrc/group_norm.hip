@@ -127,9 +127,10 @@ __device__ inline void group_sums(const GnArgs& a, float* lds, int tid, int team
 template <bool VECG>
 __device__ inline float of_channel(const float (&p)[8], int i) { return p[VECG ? 0 : i]; }
 
-// xh = x rstd + shift (shift = -mean rstd) and du of eight values.
+// xh = (x - mean) rstd and du of eight values.  (Centred before it is scaled, as in the forward:
+// x rstd - mean rstd loses |mean| rstd steps of fp32, also where x - mean is exact.)
 template <class T, bool VECG>
-__device__ inline void grad8(const GnArgs& a, const Raw8<T>& rx, const Raw8<T>& rd, const float (&shift)[8],
+__device__ inline void grad8(const GnArgs& a, const Raw8<T>& rx, const Raw8<T>& rd, const float (&mean)[8],
                              const float (&rstd)[8], const float (&gamma)[8], const float (&beta)[8], float (&xh)[8],
                              float (&du)[8]) {
   float u[8];
@@ -137,7 +138,7 @@ __device__ inline void grad8(const GnArgs& a, const Raw8<T>& rx, const Raw8<T>& 
   to_floats<T>(rd, du);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    xh[q] = fmaf(xh[q], of_channel<VECG>(rstd, q), of_channel<VECG>(shift, q));
+    xh[q] = (xh[q] - of_channel<VECG>(mean, q)) * of_channel<VECG>(rstd, q);
     u[q] = fmaf(xh[q], gamma[q], beta[q]);
   }
   act8_grad(a.act, u, du);
@@ -274,18 +275,16 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
         rd[i] = load8_raw<T>(dy + s * a.lddy, n);
       }
     }
-    float shift[8], rstd[8];
+    float mean[8], rstd[8];
     load_groups(a, a.rstd + (on ? b * a.G : 0), cv, rstd);
-    load_groups(a, a.mean + (on ? b * a.G : 0), cv, shift);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) shift[q] *= -rstd[q];
+    load_groups(a, a.mean + (on ? b * a.G : 0), cv, mean);
     const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
     float p[2][8] = {}, cb[8] = {}, cg[8] = {}, du[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (tr + i * a.TR < len) {
         float xh[8];
-        grad8<T, false>(a, rx[i], rd[i], shift, rstd, gamma, beta, xh, du[i]);  // du is zero past the last channel
+        grad8<T, false>(a, rx[i], rd[i], mean, rstd, gamma, beta, xh, du[i]);  // du is zero past the last channel
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           cb[q] += du[i][q];
@@ -301,6 +300,8 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
     }
     group_sums<VECG, 2>(a, lds, tid, team_id, r, cv, on, p);
     if (on) {
+#pragma unroll
+      for (int q = 0; q < (VECG ? 1 : 8); ++q) p[0][q] *= -inv_n, p[1][q] *= -inv_n * rstd[q];
       St* dx = static_cast<St*>(a.out) + b * a.S * a.ldo + cv * 8;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -312,8 +313,8 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
           to_floats<T>(rx[i], f);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            f[q] = fmaf(f[q], rstd[q], shift[q]);
-            f[q] = rstd[q] * (du[i][q] * gamma[q] - of_channel<VECG>(p[0], q) * inv_n - f[q] * (of_channel<VECG>(p[1], q) * inv_n));
+            f[q] -= mean[q];
+            f[q] = rstd[q] * fmaf(du[i][q], gamma[q], fmaf(f[q], of_channel<VECG>(p[1], q), of_channel<VECG>(p[0], q)));
           }
         }
         store8<T>(dx + s * a.ldo, f, n);
@@ -490,12 +491,12 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
         rd[i] = load8_raw<T>(dy + s * a.lddy);
       }
     }
-    float shift[8], rstd[8], p0[8] = {}, p1[8] = {}, cb[8] = {}, cg[8] = {}, du[KEEP ? NV : 1][8];
+    float mean[8], rstd[8], p0[8] = {}, p1[8] = {}, cb[8] = {}, cg[8] = {}, du[KEEP ? NV : 1][8];
 #pragma unroll
     for (int q = 0; q < (VECG ? 1 : 8); ++q) {
       const long at = w.on ? w.b * a.G + (w.cv * 8 + q) / a.Cg : 0;
       rstd[q] = a.rstd[at];
-      shift[q] = -a.mean[at] * rstd[q];
+      mean[q] = a.mean[at];
     }
     const float inv_n = w.len > 0 ? 1.f / (static_cast<float>(w.len) * a.Cg) : 0.f;
 #pragma unroll
@@ -503,7 +504,7 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
       if (w.tr + i * a.TR < w.len) {
         float xh[8];
         float(&d)[8] = du[KEEP ? i : 0];
-        grad8<T, VECG>(a, rx[i], rd[i], shift, rstd, gamma, beta, xh, d);
+        grad8<T, VECG>(a, rx[i], rd[i], mean, rstd, gamma, beta, xh, d);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           cb[q] += d[q];
@@ -522,7 +523,7 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
     lane_sums<VECG>(a, p1);
     if (!w.on) continue;
 #pragma unroll
-    for (int q = 0; q < (VECG ? 1 : 8); ++q) p0[q] *= -inv_n, p1[q] *= -inv_n;
+    for (int q = 0; q < (VECG ? 1 : 8); ++q) p0[q] *= -inv_n, p1[q] *= KEEP ? -inv_n * rstd[q] : -inv_n;
     St* dx = static_cast<St*>(a.out) + w.b * a.S * a.ldo + w.cv * 8;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -535,10 +536,10 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
         if constexpr (KEEP) {
           to_floats<T>(rx[i], f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) f[q] = fmaf(f[q], of_channel<VECG>(rstd, q), of_channel<VECG>(shift, q));
+          for (int q = 0; q < 8; ++q) f[q] -= of_channel<VECG>(mean, q);
         } else {
           forget(rd[i]);
-          grad8<T, VECG>(a, rx[i], rd[i], shift, rstd, gamma, beta, f, d);
+          grad8<T, VECG>(a, rx[i], rd[i], mean, rstd, gamma, beta, f, d);
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -769,14 +770,10 @@ __global__ __launch_bounds__(1024) void k_gn_join(GnArgs a) {
   }
 }
 
-// (mean, rstd) of the thread's channels; SHIFT: -mean rstd in the mean's place.
-template <bool SHIFT>
+// (mean, rstd) of the thread's channels.
 __device__ inline void load_stats(const GnArgs& a, const StreamPos& q, float (&mean)[8], float (&rstd)[8]) {
   load_groups(a, a.rstd + static_cast<long>(q.b) * a.G, q.cv, rstd);
   load_groups(a, a.mean + static_cast<long>(q.b) * a.G, q.cv, mean);
-  if (SHIFT)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mean[i] *= -rstd[i];
 }
 
 template <class T>
@@ -789,7 +786,7 @@ __global__ __launch_bounds__(kStream) void k_gn_apply(GnArgs a) {
   St* y = static_cast<St*>(a.out) + static_cast<long>(q.b) * a.S * a.ldo + q.cv * 8;
   float gamma[8], beta[8], mean[8], rstd[8];
   load_params(a, q.cv, gamma, beta);
-  load_stats<false>(a, q, mean, rstd);
+  load_stats(a, q, mean, rstd);
   for (int s0 = q.s0 + q.tr; s0 < q.s1; s0 += kAhead * q.TR) {
     Raw8<T> r[kAhead];
 #pragma unroll
@@ -821,9 +818,9 @@ __global__ __launch_bounds__(kStream) void k_gn_bwd_stats(GnArgs a) {
   if (q.on) {
     const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
     const St* dy = static_cast<const St*>(a.dy) + static_cast<long>(q.b) * a.S * a.lddy + q.cv * 8;
-    float gamma[8], beta[8], shift[8], rstd[8];
+    float gamma[8], beta[8], mean[8], rstd[8];
     load_params(a, q.cv, gamma, beta);
-    load_stats<true>(a, q, shift, rstd);
+    load_stats(a, q, mean, rstd);
     for (int s = q.s0 + q.tr; s < end; s += kAhead * q.TR) {
       Raw8<T> rx[kAhead], rd[kAhead];
 #pragma unroll
@@ -836,7 +833,7 @@ __global__ __launch_bounds__(kStream) void k_gn_bwd_stats(GnArgs a) {
       for (int u = 0; u < kAhead; ++u) {
         if (s + u * q.TR >= end) break;
         float f[8], d[8];
-        grad8<T, false>(a, rx[u], rd[u], shift, rstd, gamma, beta, f, d);
+        grad8<T, false>(a, rx[u], rd[u], mean, rstd, gamma, beta, f, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           s1[i] += d[i];
@@ -919,9 +916,9 @@ __global__ __launch_bounds__(kStream) void k_gn_bwd_apply(GnArgs a) {
   const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
   const St* dy = static_cast<const St*>(a.dy) + static_cast<long>(q.b) * a.S * a.lddy + q.cv * 8;
   St* dx = static_cast<St*>(a.out) + static_cast<long>(q.b) * a.S * a.ldo + q.cv * 8;
-  float gamma[8], beta[8], shift[8], rstd[8], m1[8], m2[8];
+  float gamma[8], beta[8], mean[8], rstd[8], m1[8], m2[8];
   load_params(a, q.cv, gamma, beta);
-  load_stats<true>(a, q, shift, rstd);
+  load_stats(a, q, mean, rstd);
   load_groups(a, a.gsum + static_cast<long>(q.b) * a.G, q.cv, m1);
   load_groups(a, a.gsum + (static_cast<long>(a.B) + q.b) * a.G, q.cv, m2);
   for (int s0 = q.s0 + q.tr; s0 < q.s1; s0 += kAhead * q.TR) {
@@ -939,7 +936,7 @@ __global__ __launch_bounds__(kStream) void k_gn_bwd_apply(GnArgs a) {
       float f[8] = {};
       if (s < len) {
         float d[8];
-        grad8<T, false>(a, rx[u], rd[u], shift, rstd, gamma, beta, f, d);
+        grad8<T, false>(a, rx[u], rd[u], mean, rstd, gamma, beta, f, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = rstd[i] * (d[i] * gamma[i] - m1[i] - f[i] * m2[i]);
       }

@@ -42,3 +42,31 @@ def test_dense_bwd_of_the_longest_batch():
     ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
     elf.dense_bwd(x[:M], w=torch.ones(N, K, dtype=torch.bfloat16, device=DEV), dz=dz[:M], dw=dw, db=db, workspace=ws)
     assert (dw.cpu().numpy() == zs.T @ xs).all() and (db.cpu().numpy() == zs.sum(0)).all()
+
+
+@pytest.mark.parametrize("B,S,C,G,dt", [
+    (70, 26, 128, 8, "bf16"), (70, 26, 128, 8, "f32"), (40, 30, 128, 32, "f32"), (33, 1, 64, 1, "f16"), (50, 5, 32, 4, "f32"),
+    (20, 40, 96, 6, "f32"), (21, 33, 30, 3, "bf16"), (9, 20, 520, 5, "f32"), (3, 2000, 64, 8, "f32"), (2, 900, 257, 1, "f16"),
+    (6, 1, 40, 40, "f32"), (4, 1, 64, 64, "f32"),
+])
+def test_group_norm_gradients_do_not_see_an_offset(B, S, C, G, dt):
+    """x and mean moved by one number, every value exact before and after: the centred values are the
+    same bits, and so are the gradients (all forms; also where a group is one value and xh is 0)."""
+    g = torch.Generator(DEV).manual_seed(B + C)
+    move = {"f32": 4096.0, "f16": 1024.0, "bf16": 240.0}[dt]
+    x = torch.randint(0, 16, (B * S, C), generator=g, device=DEV).to(base.DT[dt])
+    dy = torch.randn(B * S, C, generator=g, device=DEV).to(base.DT[dt])
+    gm, bt = (torch.randn(C, generator=g, device=DEV) for _ in range(2))
+    mean = torch.randint(0, 128, (B, G), generator=g, device=DEV) / 8.0
+    if C == G and S == 1:
+        mean = x.float()
+    rstd = torch.rand(B, G, generator=g, device=DEV) + 0.5
+    got = []
+    for m in (0.0, move):
+        dx, dg, db = torch.full_like(x, float("nan")), torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+        elf.group_norm_bwd(dy, x + m, gm, bt, mean + m, rstd, dx, dg, db, positions=S, groups=G, act="silu")
+        got.append((dx, dg, db))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    if C == G and S == 1:  # xh = 0, dh = avg dh: nothing but the rounding of du gamma (|du| <= 1.1 |dy|)
+        assert (got[1][1] == 0).all()
+        assert (got[1][0].abs() <= 4 * 2.0**-24 * (dy * gm).abs() * rstd).all()
