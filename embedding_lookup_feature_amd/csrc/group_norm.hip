@@ -250,41 +250,52 @@ __global__ __launch_bounds__(kResident) void k_gn_fwd_resident(GnArgs a) {
 }
 
 // Every workgroup takes samples blockIdx.x * spw + team, then gridDim.x * spw further on, and
-// keeps dgamma / dbeta of its samples in registers; part[workgroup][c] = (dbeta, dgamma).
+// keeps dgamma / dbeta of its samples in registers; part[workgroup][c] = (dbeta, dgamma).  A sample's
+// mean and rstd are one value each where a vector lies inside a group (65536 rows of 1024 bf16: 161
+// us, eight of each 244).
 template <class T, int NV, bool VECG>
 __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
   extern __shared__ float lds[];
   using St = typename T::S;
   const int tid = threadIdx.x, team_id = tid / a.team, r = tid - team_id * a.team;
   const int tr = r / a.CV, cv = r - tr * a.CV;
-  const int n = min(8, a.C - cv * 8);
+  const int n = min(8, a.C - cv * 8), group = VECG ? cv * 8 / a.Cg : 0;
   float gamma[8], beta[8], sb[8] = {}, sg[8] = {};
   load_params(a, cv, gamma, beta);
-  for (long b0 = static_cast<long>(blockIdx.x) * a.spw; b0 < a.B; b0 += static_cast<long>(gridDim.x) * a.spw) {
+  const long first = static_cast<long>(blockIdx.x) * a.spw, step = static_cast<long>(gridDim.x) * a.spw;
+  const long row0 = (first + team_id) * a.S + tr, rows = step * a.S;
+  const St* x = static_cast<const St*>(a.x) + row0 * a.ldx + cv * 8;
+  const St* dy = static_cast<const St*>(a.dy) + row0 * a.lddy + cv * 8;
+  St* dx = static_cast<St*>(a.out) + row0 * a.ldo + cv * 8;
+  for (long b0 = first; b0 < a.B; b0 += step, x += rows * a.ldx, dy += rows * a.lddy, dx += rows * a.ldo) {
     const long b = b0 + team_id;
     const bool on = team_id < a.spw && b < a.B;
     const int len = on ? sample_len(a, static_cast<int>(b)) : 0;
-    const St* x = static_cast<const St*>(a.x) + (on ? b * a.S * a.ldx : 0) + cv * 8;
-    const St* dy = static_cast<const St*>(a.dy) + (on ? b * a.S * a.lddy : 0) + cv * 8;
+    float mean[8], rstd[8];  // before the sample's vectors, so that those are waited for once
+    const long at = on ? b * a.G : 0;
+    if constexpr (VECG) {
+      rstd[0] = a.rstd[at + group];
+      mean[0] = a.mean[at + group];
+    } else {
+      load_groups(a, a.rstd + at, cv, rstd);
+      load_groups(a, a.mean + at, cv, mean);
+    }
     Raw8<T> rx[NV], rd[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int s = tr + i * a.TR;
       if (s < len) {
-        rx[i] = load8_raw<T>(x + s * a.ldx, n);
-        rd[i] = load8_raw<T>(dy + s * a.lddy, n);
+        rx[i] = load8_raw<T>(x + i * (a.TR * a.ldx), n);
+        rd[i] = load8_raw<T>(dy + i * (a.TR * a.lddy), n);
       }
     }
-    float mean[8], rstd[8];
-    load_groups(a, a.rstd + (on ? b * a.G : 0), cv, rstd);
-    load_groups(a, a.mean + (on ? b * a.G : 0), cv, mean);
     const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
     float p[2][8] = {}, cb[8] = {}, cg[8] = {}, du[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (tr + i * a.TR < len) {
         float xh[8];
-        grad8<T, false>(a, rx[i], rd[i], mean, rstd, gamma, beta, xh, du[i]);  // du is zero past the last channel
+        grad8<T, VECG>(a, rx[i], rd[i], mean, rstd, gamma, beta, xh, du[i]);  // du is zero past the last channel
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           cb[q] += du[i][q];
@@ -302,7 +313,6 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
     if (on) {
 #pragma unroll
       for (int q = 0; q < (VECG ? 1 : 8); ++q) p[0][q] *= -inv_n, p[1][q] *= -inv_n * rstd[q];
-      St* dx = static_cast<St*>(a.out) + b * a.S * a.ldo + cv * 8;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int s = tr + i * a.TR;
@@ -313,11 +323,11 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
           to_floats<T>(rx[i], f);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            f[q] -= mean[q];
-            f[q] = rstd[q] * fmaf(du[i][q], gamma[q], fmaf(f[q], of_channel<VECG>(p[1], q), of_channel<VECG>(p[0], q)));
+            f[q] -= of_channel<VECG>(mean, q);
+            f[q] = of_channel<VECG>(rstd, q) * fmaf(du[i][q], gamma[q], fmaf(f[q], of_channel<VECG>(p[1], q), of_channel<VECG>(p[0], q)));
           }
         }
-        store8<T>(dx + s * a.ldo, f, n);
+        store8<T>(dx + i * (a.TR * a.ldo), f, n);
       }
     }
   }
@@ -464,31 +474,37 @@ __global__ __launch_bounds__(kWave) void k_gn_fwd_wave(GnArgs a) {
 }
 
 // part[workgroup][c] = (dbeta, dgamma) of the workgroup's samples, as in the resident form.
-// Two wavefronts per SIMD; one where eight fp32 vectors and per-channel sums would spill too much
-// (8192 samples of 26 x 128, forward and backward, 32 groups: 157 us, spilling 171; 8 groups, whose
-// sums are fewer: 142, spilling 134).  du stays in registers between the sums and dx (KEEP: the
-// activation's derivative, two transcendental instructions a value, is taken once), unless that
-// spills at eight vectors a lane: 16384 samples of 26 x 128 bf16, forward and backward, 8 groups 135
-// us against 146 taken twice, 32 groups 218 against 181; 8192 of fp32, 8 groups 171 against 133, 32
-// groups 148 against 158.
+// Pointers walk from sample to sample and rows lie a uniform stride apart, so that no lane keeps an
+// offset per vector (48 registers; 16384 samples of 26 x 128 bf16, 8 groups: 76.8 us against 91.1).
+// Two wavefronts per SIMD; one where eight fp32 vectors and per-channel sums would spill (8192
+// samples of 26 x 128, 32 groups: 102.6 us, spilling 134.8).  du stays in registers between the sums
+// and dx (KEEP: the activation's derivative, two transcendental instructions a value, is taken once),
+// unless that spills, with eight fp32 vectors a lane at two wavefronts per SIMD: 16384 samples of
+// bf16, 8 groups 76.8 us against 101.7 taken twice, 32 groups 94.1 against 108.5; 8192 of fp32, 32
+// groups 102.6 against 114.6, but 8 groups 113.2 against 79.0.
 template <class T, int NV, bool VECG>
 __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) == 4 ? 1 : 2) void k_gn_bwd_wave(GnArgs a) {
   using St = typename T::S;
-  constexpr bool KEEP = NV < 8 || VECG == (sizeof(St) == 2);
+  constexpr bool KEEP = NV < 8 || !VECG || sizeof(St) == 2;
   float gamma[8], beta[8], sb[8] = {}, sg[8] = {};
   load_params(a, threadIdx.x & (a.CV - 1), gamma, beta);
   const int per = kWave / a.team;
-  for (long first = static_cast<long>(blockIdx.x) * per; first < a.B; first += static_cast<long>(gridDim.x) * per) {
+  const long step = static_cast<long>(gridDim.x) * per, rows = step * a.S;
+  const WavePos w0 = wave_pos(a, static_cast<long>(blockIdx.x) * per);
+  const long row0 = w0.b * a.S + w0.tr;
+  const St* x = static_cast<const St*>(a.x) + row0 * a.ldx + w0.cv * 8;
+  const St* dy = static_cast<const St*>(a.dy) + row0 * a.lddy + w0.cv * 8;
+  St* dx = static_cast<St*>(a.out) + row0 * a.ldo + w0.cv * 8;
+  for (long first = static_cast<long>(blockIdx.x) * per; first < a.B;
+       first += step, x += rows * a.ldx, dy += rows * a.lddy, dx += rows * a.ldo) {
     const WavePos w = wave_pos(a, first);
-    const St* x = static_cast<const St*>(a.x) + w.b * a.S * a.ldx + w.cv * 8;
-    const St* dy = static_cast<const St*>(a.dy) + w.b * a.S * a.lddy + w.cv * 8;
     Raw8<T> rx[NV], rd[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int s = w.tr + i * a.TR;
       if (s < w.len) {
-        rx[i] = load8_raw<T>(x + s * a.ldx);
-        rd[i] = load8_raw<T>(dy + s * a.lddy);
+        rx[i] = load8_raw<T>(x + i * (a.TR * a.ldx));
+        rd[i] = load8_raw<T>(dy + i * (a.TR * a.lddy));
       }
     }
     float mean[8], rstd[8], p0[8] = {}, p1[8] = {}, cb[8] = {}, cg[8] = {}, du[KEEP ? NV : 1][8];
@@ -524,7 +540,6 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
     if (!w.on) continue;
 #pragma unroll
     for (int q = 0; q < (VECG ? 1 : 8); ++q) p0[q] *= -inv_n, p1[q] *= KEEP ? -inv_n * rstd[q] : -inv_n;
-    St* dx = static_cast<St*>(a.out) + w.b * a.S * a.ldo + w.cv * 8;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int s = w.tr + i * a.TR;
@@ -546,7 +561,7 @@ __global__ __launch_bounds__(kWave, NV == 8 && !VECG && sizeof(typename T::S) ==
           f[q] = of_channel<VECG>(rstd, q) * fmaf(d[q], gamma[q], fmaf(f[q], of_channel<VECG>(p1, q), of_channel<VECG>(p0, q)));
         __builtin_amdgcn_sched_barrier(0);
       }
-      store8<T>(dx + s * a.ldo, f, 8);
+      store8<T>(dx + i * (a.TR * a.ldo), f, 8);
     }
   }
   if (!a.part) return;
