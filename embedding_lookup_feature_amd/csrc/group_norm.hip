@@ -263,31 +263,41 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
   float gamma[8], beta[8], sb[8] = {}, sg[8] = {};
   load_params(a, cv, gamma, beta);
   const long first = static_cast<long>(blockIdx.x) * a.spw, step = static_cast<long>(gridDim.x) * a.spw;
-  const long row0 = (first + team_id) * a.S + tr, rows = step * a.S;
+  // VECG: pointers walk from sample to sample and a thread's rows lie a uniform stride apart.  With
+  // per-channel statistics the scalar registers do not hold that too: a sample's pointers are
+  // computed and the rows' offsets kept (65536 rows of 600 in 50 groups 165 us, walking 178).
+  const auto place = [&](int i, long ld) { return VECG ? i * (a.TR * ld) : (tr + i * a.TR) * ld; };
+  const long row0 = (first + team_id) * a.S + (VECG ? tr : 0), rows = step * a.S;
   const St* x = static_cast<const St*>(a.x) + row0 * a.ldx + cv * 8;
   const St* dy = static_cast<const St*>(a.dy) + row0 * a.lddy + cv * 8;
   St* dx = static_cast<St*>(a.out) + row0 * a.ldo + cv * 8;
   for (long b0 = first; b0 < a.B; b0 += step, x += rows * a.ldx, dy += rows * a.lddy, dx += rows * a.ldo) {
     const long b = b0 + team_id;
     const bool on = team_id < a.spw && b < a.B;
+    if constexpr (!VECG) {
+      x = static_cast<const St*>(a.x) + (on ? b * a.S * a.ldx : 0) + cv * 8;
+      dy = static_cast<const St*>(a.dy) + (on ? b * a.S * a.lddy : 0) + cv * 8;
+      dx = static_cast<St*>(a.out) + b * a.S * a.ldo + cv * 8;
+    }
     const int len = on ? sample_len(a, static_cast<int>(b)) : 0;
-    float mean[8], rstd[8];  // before the sample's vectors, so that those are waited for once
+    float mean[8], rstd[8];  // VECG: before the sample's vectors, so that those are waited for once
     const long at = on ? b * a.G : 0;
     if constexpr (VECG) {
       rstd[0] = a.rstd[at + group];
       mean[0] = a.mean[at + group];
-    } else {
-      load_groups(a, a.rstd + at, cv, rstd);
-      load_groups(a, a.mean + at, cv, mean);
     }
     Raw8<T> rx[NV], rd[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int s = tr + i * a.TR;
       if (s < len) {
-        rx[i] = load8_raw<T>(x + i * (a.TR * a.ldx), n);
-        rd[i] = load8_raw<T>(dy + i * (a.TR * a.lddy), n);
+        rx[i] = load8_raw<T>(x + place(i, a.ldx), n);
+        rd[i] = load8_raw<T>(dy + place(i, a.lddy), n);
       }
+    }
+    if constexpr (!VECG) {
+      load_groups(a, a.rstd + at, cv, rstd);
+      load_groups(a, a.mean + at, cv, mean);
     }
     const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
     float p[2][8] = {}, cb[8] = {}, cg[8] = {}, du[NV][8];
@@ -327,7 +337,7 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
             f[q] = of_channel<VECG>(rstd, q) * fmaf(du[i][q], gamma[q], fmaf(f[q], of_channel<VECG>(p[1], q), of_channel<VECG>(p[0], q)));
           }
         }
-        store8<T>(dx + i * (a.TR * a.ldo), f, n);
+        store8<T>(dx + place(i, a.ldo), f, n);
       }
     }
   }
