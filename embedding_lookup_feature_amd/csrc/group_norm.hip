@@ -1144,15 +1144,14 @@ el_status run_gn(const char* fn, const GnArgs& a, const GnPlan& p, el_dtype dtyp
   return check_launch(fn);
 }
 
-// What one launch's grid can hold: samples that fit a workgroup take up to one workgroup each,
-// streamed ones a workgroup per group and per block of columns.
+// What one launch's grid can hold (2^32 threads): samples that fit a workgroup take up to one
+// workgroup each, streamed ones a workgroup per group and per block of columns.
 bool gn_sizes_ok(int32_t B, int32_t S, int32_t C, int32_t G) {
-  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0 || C > (1 << 20) || B > (1 << 22) || S > (1 << 30))
-    return false;
+  if (B < 1 || S < 1 || C < 1 || G < 1 || C % G != 0 || C > (1 << 20) || S > (1 << 30)) return false;
   if (static_cast<int64_t>(B) * G >= (int64_t{1} << 25)) return false;
   const GnPlan p = plan_gn(B, S, C, G);
-  return p.form != STREAMED ||
-         (static_cast<int64_t>(B) * G < (int64_t{1} << 22) && static_cast<int64_t>(B) * p.colblocks <= (int64_t{1} << 22));
+  if (p.form != STREAMED) return static_cast<int64_t>(p.blocks_fwd) * p.threads < (int64_t{1} << 32);
+  return static_cast<int64_t>(B) * G < (int64_t{1} << 22) && static_cast<int64_t>(B) * p.colblocks <= (int64_t{1} << 22);
 }
 
 el_status check_gn(const char* fn, const void* x, int64_t ldx, int32_t B, int32_t S, int32_t C, int32_t G,
@@ -1164,7 +1163,7 @@ el_status check_gn(const char* fn, const void* x, int64_t ldx, int32_t B, int32_
   if (G < 1 || C % G != 0) return tower::bad(fn, "G must be >= 1 and divide C");
   if (!dtype_valid(dtype)) return tower::bad(fn, "unknown dtype");
   if (B > 0 && S > 0 && !gn_sizes_ok(B, S, C, G))
-    return tower::unsupported(fn, "more channels (2^20), samples (2^22), positions (2^30) or groups in all than one launch takes");
+    return tower::unsupported(fn, "more channels (2^20), positions (2^30), groups in all (2^25) or samples than one launch takes");
   const el_status s = tower::check_act(fn, act);
   if (s != EL_OK) return s;
   if (!tower::al(lengths, 4) || !tower::al(gamma, 4) || !tower::al(beta, 4))

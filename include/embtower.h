@@ -131,8 +131,10 @@ EL_API size_t el_group_norm_bwd_workspace_bytes(int32_t B, int32_t S, int32_t C,
  * pooled vectors [B][F][D] normalises each sample's embeddings over its F tables.
  * x, y: rows of strides ldx, ldy, dtype EL_F32 / EL_F16 / EL_BF16; gamma, beta: fp32 [C] or
  * NULL (1, 0); mean, rstd: fp32 [B][G], overwritten; statistics and arithmetic in fp32, the
- * variance from centred values.  C % G == 0, eps >= 0 finite.  Up to C = 2^20, B = 2^22,
- * S = 2^30 and B G = 2^25 (EL_ERR_UNSUPPORTED beyond).  workspace: >=
+ * variance from centred values.  C % G == 0, eps >= 0 finite.  Up to C = 2^20 and S = 2^30, with
+ * B G < 2^25 (EL_ERR_UNSUPPORTED beyond, as for batches that one launch cannot hold: B below 2^22
+ * always fits where a sample has at most 512 vectors of eight channels, and rows, S = 1, of up to
+ * 2048 channels with G = 1 below 2^24; longer samples B G < 2^22).  workspace: >=
  * el_group_norm_fwd_workspace_bytes(B, S, C, G), 256-byte aligned (NULL when that is 0).
  */
 EL_API el_status el_group_norm_fwd(const void* x, int64_t ldx, int32_t B, int32_t S, int32_t C,

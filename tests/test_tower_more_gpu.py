@@ -6,6 +6,7 @@ import torch
 
 import embedding_lookup_feature_amd as elf
 from tests import test_tower_gpu as base
+from tests import tower_plain as tp
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -70,3 +71,37 @@ def test_group_norm_gradients_do_not_see_an_offset(B, S, C, G, dt):
     if C == G and S == 1:  # xh = 0, dh = avg dh: nothing but the rounding of du gamma (|du| <= 1.1 |dy|)
         assert (got[1][1] == 0).all()
         assert (got[1][0].abs() <= 4 * 2.0**-24 * (dy * gm).abs() * rstd).all()
+
+
+def test_group_norm_rows_of_the_largest_batch():
+    """Every pooled vector of 262144 samples of 26 tables as a row (S = 1, one group): the same bits as
+    in two halves, rows against the plain form, parameter gradients against sums in 64 bits."""
+    B, C, kw = 26 * 262144, 128, dict(positions=1, groups=1)
+    g = torch.Generator(DEV).manual_seed(3)
+    x = torch.empty(B, C, dtype=torch.bfloat16, device=DEV).normal_(0.5, 1.5, generator=g)
+    dy = torch.empty(B, C, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    gm, bt = (torch.randn(C, generator=g, device=DEV) for _ in range(2))
+    y, dx, y2, dx2 = (torch.full_like(x, float("nan")) for _ in range(4))
+    st, st2 = (torch.full((2, B, 1), float("nan"), device=DEV) for _ in range(2))
+    dg, db = torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+    elf.group_norm_fwd(x, gm, bt, y, st[0], st[1], act="silu", **kw)
+    elf.group_norm_bwd(dy, x, gm, bt, st[0], st[1], dx, dg, db, act="none", **kw)
+    for h in (slice(0, B // 2), slice(B // 2, B)):
+        elf.group_norm_fwd(x[h], gm, bt, y2[h], st2[0, h], st2[1, h], act="silu", **kw)
+        elf.group_norm_bwd(dy[h], x[h], gm, bt, st2[0, h], st2[1, h], dx2[h], None, None, act="none", **kw)
+    assert torch.equal(y, y2) and torch.equal(dx, dx2) and torch.equal(st, st2)
+    for at in (0, B // 2 - 50, B - 100):
+        h, n = slice(at, at + 100), base.np64
+        ry, ey, rm, rr = tp.gn_fwd(n(x[h]), 1, 1, None, n(gm), n(bt), 1e-5, "silu", torch.bfloat16)
+        tp.check(y[h], (ry, ey), "y")
+        ref = tp.gn_bwd(n(dy[h]), n(x[h]), 1, 1, None, n(gm), n(bt), n(st[0, h]), n(st[1, h]), "none", torch.bfloat16)
+        tp.check(dx[h], ref["dx"], "dx")
+    want, size = (torch.zeros(2, C, dtype=torch.float64, device=DEV) for _ in range(2))
+    for at in range(0, B, 1 << 19):
+        h = slice(at, at + (1 << 19))
+        d = dy[h].double()
+        q = d * (x[h].double() - st[0, h].double()) * st[1, h].double()
+        want += torch.stack([q.sum(0), d.sum(0)])
+        size += torch.stack([q.abs().sum(0), d.abs().sum(0)])
+    # 416 samples behind each other in a thread, then joins of at most 64 additions; xh within 4 steps
+    assert ((torch.stack([dg, db]).double() - want).abs() <= 512 * 2.0**-24 * size).all()

@@ -74,3 +74,22 @@ def test_dense_bwd_partials_are_counted_for_the_longest_batches():
         for K, N in ((8, 1 << 20), (1 << 20, 8), (8, 8), (512, 1024)):
             copies = sum(r256(a * pad8(b) * 2) for a, b in ((M, N), (M, K), (N, K)))
             assert tw.dense_bwd_workspace_bytes(M, K, N) - copies >= 4 * N * K, (M, K, N)
+
+
+def test_group_norm_takes_every_pooled_vector_of_the_largest_batch_as_a_row():
+    """26 tables x 262144 samples of 128 channels as rows (one position each), and as many as one
+    launch's grid of several samples per workgroup holds."""
+    from embedding_lookup_feature_amd import embcore as ec
+    L, big = tw.lib(), 1 << 50
+    fwd = lambda B, S, C, G, ws=A, n=big: L.el_group_norm_fwd(  # noqa: E731
+        A, C, B, S, C, G, None, None, None, -1.0, 0, A, C, A, A, ec.EL_BF16, ws, n, None)
+    bwd = lambda B, S, C, G, ws, n: L.el_group_norm_bwd(  # noqa: E731
+        A, C, A, C, B, S, C, G, None, None, None, A, A, 0, A, C, A, A, ec.EL_BF16, ws, n, None)
+    for B, C, G in ((26 * 262144, 128, 1), ((1 << 25) - 1, 64, 1), ((1 << 24), 512, 1), ((1 << 22) + 1, 4096, 1)):
+        assert fwd(B, 1, C, G) == ec.EL_ERR_INVALID_ARG and "eps" in ec.el_last_error(), (B, C, G)  # past the sizes
+        assert bwd(B, 1, C, G, None, 0) == ec.EL_ERR_WORKSPACE
+        assert tw.group_norm_bwd_workspace_bytes(B, 1, C, G) > 0
+    for B, S, C, G in ((1 << 25, 1, 64, 1), ((1 << 23) + 1, 1, 4096, 1), ((1 << 22), 1, 64, 8), ((1 << 22) + 1, 4096, 64, 1)):
+        assert fwd(B, S, C, G) == ec.EL_ERR_UNSUPPORTED, (B, S, C, G)
+        assert bwd(B, S, C, G, A, big) == ec.EL_ERR_UNSUPPORTED
+        assert tw.group_norm_bwd_workspace_bytes(B, S, C, G) == 0 == tw.group_norm_fwd_workspace_bytes(B, S, C, G)
