@@ -105,3 +105,102 @@ def test_group_norm_rows_of_the_largest_batch():
         size += torch.stack([q.abs().sum(0), d.abs().sum(0)])
     # 416 samples behind each other in a thread, then joins of at most 64 additions; xh within 4 steps
     assert ((torch.stack([dg, db]).double() - want).abs() <= 512 * 2.0**-24 * size).all()
+
+
+# ------------------------------------------------------------------------- dense layer, every tile shape
+FWD = [
+    # M, K, N, extra row stride: L, M and S tiles; whole vectors, then operands that are copied first
+    (33_000, 40, 264, 8), (4_200, 72, 1_032, 8), (2_200, 72, 520, 0), (40_000, 24, 1, 8),
+    (33_000, 43, 257, 5), (4_099, 479, 1_001, 33), (2_200, 71, 523, 1), (2_200, 72, 520, 3),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K,N,extra", FWD)
+def test_dense_fwd_tiles(M, K, N, extra, dt):
+    rng = np.random.default_rng(M + K)
+    x, w = base.rows(rng, M, K, K + extra, dt), base.rows(rng, N, K, K, dt, 1 / np.sqrt(K)).contiguous()
+    bias = torch.from_numpy(rng.normal(size=N)).float().to(DEV)
+    r, y, pre = (base.rows(rng, M, N, N + extra, dt), base.out(M, N, N + extra, dt), base.out(M, N, N + extra, dt))
+    d, seed, offset = base.make_drop(0.3)
+    n = base.np64
+    ws = torch.full((elf.dense_fwd_workspace_bytes(M, K, N) // 4,), float("nan"), device=DEV)
+    elf.dense_fwd(x, w, bias, y, act="silu", dropout=d, residual=r, pre=pre, workspace=ws)
+    ry, ey, rz, ez = tp.dense_fwd(n(x), n(w), n(bias), "silu", tp.drop_factors(M, N, 0.3, seed, offset), n(r), base.DT[dt])
+    tp.check(y, (ry, ey), "y")
+    tp.check(pre, (rz, ez), "pre")
+    assert base.gap_untouched(y) and base.gap_untouched(pre)
+
+
+BWD = [
+    # M, K, N, extra: both products L, both M, M and S, S and M, L and S; then copied operands
+    (24_600, 1_000, 1_032, 0), (5_000, 1_032, 1_032, 0), (4_200, 1_032, 136, 8), (5_700, 520, 1_032, 0),
+    (33_000, 264, 72, 8), (33_000, 261, 70, 3), (5_001, 1_031, 1_030, 1), (4_099, 517, 260, 0), (4_099, 512, 257, 7),
+]
+
+
+@pytest.mark.parametrize("M,K,N,extra,dt", [(*c, "f16") for c in BWD] + [(*c, "bf16") for c in BWD[5:]])
+def test_dense_bwd_tiles(M, K, N, extra, dt):
+    rng = np.random.default_rng(M + K)
+    x, w = base.rows(rng, M, K, K + extra, dt), base.rows(rng, N, K, K, dt, 1 / np.sqrt(N)).contiguous()
+    dz, dres, pre = (base.rows(rng, M, c, c + extra, dt, s) for c, s in ((N, 1.0), (K, 1.0), (K, 1.5)))
+    dx, dzb = base.out(M, K, K + extra, dt), base.out(M, K, K + extra, dt)
+    dw, db = torch.full((N, K), float("nan"), device=DEV), torch.full((N,), float("nan"), device=DEV)
+    d, seed, offset = base.make_drop(0.3)
+    n = base.np64
+    ws = torch.full((elf.dense_bwd_workspace_bytes(M, K, N) // 4,), float("nan"), device=DEV)
+    elf.dense_bwd(x, w, dz, dw, db, dx=dx, dres=dres, dzb=dzb, pre=pre, act="gelu", dropout=d, workspace=ws)
+    ref = tp.dense_bwd(n(x), n(w), n(dz), n(dres), n(pre), "gelu", tp.drop_factors(M, K, 0.3, seed, offset), base.DT[dt])
+    for name, got in (("dw", dw), ("db", db), ("dx", dx), ("dzb", dzb)):
+        tp.check(got, ref[name], name)
+    assert base.gap_untouched(dx) and base.gap_untouched(dzb)
+    dw2 = torch.empty_like(dw)
+    if M < 20_000:  # (shape L has other slices without dx)
+        elf.dense_bwd(x, w, dz, dw2, workspace=ws)
+        assert torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K,N", [(33_000, 40, 264), (4_200, 72, 1_032), (2_200, 72, 520), (4_099, 479, 1_001)])
+def test_non_finite_rows_stay_in_their_rows_in_every_tile_shape(M, K, N, dt):
+    rng = np.random.default_rng(N)
+    x, w = base.rows(rng, M, K, K, dt).contiguous(), base.rows(rng, N, K, K, dt).contiguous()
+    bad = [0, 5, 63, 64, 127, 255, 256, M // 2, M - 2, M - 1]
+    x2 = x.clone()
+    x2[bad] = torch.tensor([float("nan"), float("inf")], device=DEV).to(base.DT[dt]).repeat(5)[:, None]
+    ok = torch.ones(M, dtype=torch.bool, device=DEV)
+    ok[bad] = False
+    y, y2 = torch.empty(M, N, dtype=base.DT[dt], device=DEV), torch.empty(M, N, dtype=base.DT[dt], device=DEV)
+    elf.dense_fwd(x, w, None, y, act="silu")
+    elf.dense_fwd(x2, w, None, y2, act="silu")
+    assert torch.equal(y[ok], y2[ok]) and torch.isfinite(y[ok].float()).all()
+    assert not torch.isfinite(y2[bad].float()).any()
+    # the data gradient's rows likewise
+    dw, dx, dx2 = torch.empty(K, N, device=DEV), torch.empty_like(y), torch.empty_like(y)
+    wt = w.t().contiguous()
+    elf.dense_bwd(y, wt, x, dw, dx=dx)
+    elf.dense_bwd(y, wt, x2, dw, dx=dx2)
+    assert torch.equal(dx[ok], dx2[ok]) and torch.isnan(dx2[bad[0]].float()).all()
+
+
+# ------------------------------------------------------------------------- group norm, several samples a workgroup in turn
+LOOPS = [
+    # B, S, C, G, ld, dtype, act, lengths, affine: more samples than one round of workgroups takes
+    (2501, 26, 128, 8, 128, "bf16", "silu", "mixed", True),    # wavefronts, eight vectors a lane
+    (2501, 26, 128, 32, 128, "f16", "gelu", "mixed", True),    # per-channel sums, 16 bits
+    (2501, 26, 128, 32, 136, "f32", "silu", None, True),
+    (2501, 26, 128, 8, 128, "f32", "none", "mixed", False),
+    (262_403, 1, 8, 1, 8, "bf16", "silu", "mixed", True),      # one lane a sample
+    (17_001, 3, 64, 64, 64, "f16", "none", None, True),
+    (4501, 10, 30, 3, 31, "bf16", "silu", "mixed", True),      # one wavefront of threads, partial vectors
+    (4501, 20, 96, 6, 96, "f16", "gelu", None, True),
+    (1101, 40, 96, 4, 96, "f32", "silu", "mixed", True),       # 256 threads
+    (3500, 1, 600, 50, 600, "bf16", "silu", None, True),       # three samples a workgroup
+    (500, 1, 2304, 9, 2304, "f32", "gelu", "mixed", True),     # 288 threads
+    (500, 2, 2040, 1, 2048, "f16", "silu", "mixed", True),     # 510 threads
+]
+
+
+@pytest.mark.parametrize("case", LOOPS, ids=lambda c: "-".join(map(str, c)))
+def test_group_norm_loops(case):
+    base.test_group_norm(case)
