@@ -21,6 +21,8 @@ extern "C" {
 
 /* Activations, next to EL_ACT_NONE and EL_ACT_RELU:
  *   EL_ACT_GELU  u Phi(u) = u (1 + erf(u / sqrt 2)) / 2
+ *                (absolute error in fp32 at most 2.2e-7 for |u| <= 8; the error relative to the
+ *                value passes 1e-3 below u = -4.6, where the value is smaller than 1e-5)
  *   EL_ACT_SILU  u / (1 + exp(-u)) */
 enum { EL_ACT_GELU = 2u, EL_ACT_SILU = 3u };
 
