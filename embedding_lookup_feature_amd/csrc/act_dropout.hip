@@ -96,12 +96,6 @@ el_status check_common(const char* fn, int32_t M, int32_t N, uint32_t act, el_dt
 
 using namespace el;
 
-#define EL_TRY(x)                    \
-  do {                               \
-    const el_status st_ = (x);       \
-    if (st_ != EL_OK) return st_;    \
-  } while (0)
-
 extern "C" {
 
 el_status el_act_dropout_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t M,

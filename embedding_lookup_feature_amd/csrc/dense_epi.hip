@@ -804,12 +804,6 @@ el_status run_fwd(const char* fn, GemmArgs a, char* ws, hipStream_t st) {
 
 using namespace el;
 
-#define EL_TRY(x)                    \
-  do {                               \
-    const el_status st_ = (x);       \
-    if (st_ != EL_OK) return st_;    \
-  } while (0)
-
 namespace {
 
 // Device bytes of the copies that these operands need (none when they are whole vectors).

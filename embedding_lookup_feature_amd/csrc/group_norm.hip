@@ -1188,12 +1188,6 @@ __global__ __launch_bounds__(256) void k_gn_empty(float* mean, float* rstd, long
 
 using namespace el;
 
-#define EL_TRY(x)                    \
-  do {                               \
-    const el_status st_ = (x);       \
-    if (st_ != EL_OK) return st_;    \
-  } while (0)
-
 extern "C" {
 
 size_t el_group_norm_fwd_workspace_bytes(int32_t B, int32_t S, int32_t C, int32_t G) {

@@ -250,6 +250,13 @@ __device__ inline bool keep_of(const u32x4& bits, int i, uint32_t top) {
 // ---------------------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------------------
+// Leaves the function with a status other than EL_OK.
+#define EL_TRY(x)                    \
+  do {                               \
+    const el_status st_ = (x);       \
+    if (st_ != EL_OK) return st_;    \
+  } while (0)
+
 namespace tower {
 
 inline bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
