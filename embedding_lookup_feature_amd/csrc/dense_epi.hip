@@ -15,12 +15,12 @@
 // plain 16-byte LDS reads, output-contiguous ones gfx950's transposing LDS reads, both from
 // layouts whose 16-byte units are permuted so that the reads touch every bank once.
 //
-// What bounds it: the large products run at the matrix units' rate under the power limit (the
-// main loop alone, 65536 x 1024 x 1024 bf16, 125 us = 1.1 PFLOP/s, a library's product 121), and
-// behind each tile's products its epilogue moves residual, pre and y at the memory's rate with
-// the matrix units idle, the generator and the activation beside it: 213 us forward with GELU,
-// dropout, residual and pre, 360 us for both products of the backward, their partials' sums
-// included (floors 121 and 242 of products, 105 and 158 of memory).
+// What bounds it: the large products run at the matrix units' rate under the power limit (65536 x
+// 1024 x 1024 bf16, y alone stored: 148 us, a library's product 115; with operands of zeros, the
+// same work, 107 and 87), and behind each tile's products its epilogue moves residual, pre and y at
+// the memory's rate with the matrix units idle, the generator and the activation beside it: 215 us
+// forward with GELU, dropout, residual and pre, 363 us for both products of the backward, their
+// partials' sums included (floors 121 and 242 of products, 105 and 158 of memory).
 #include <algorithm>
 
 #include "tower_common.hpp"

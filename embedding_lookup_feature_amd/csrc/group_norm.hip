@@ -10,19 +10,21 @@
 //
 // Bound by memory: x in, y out (forward); x, dy in, dx out (backward).  Three forms:
 //   wavefront  a sample sits in the registers of some lanes of one wavefront, which exchange its
-//              sums: read once, no barrier (16384 samples of 26 x 128 in 8 groups, bf16: forward
-//              41.5 us, 5.2 TB/s, the rate of a copy; backward 81.5 us, 4.0 TB/s: the
-//              activation's derivative, two quarter-rate instructions a value, and the two
-//              wavefronts per SIMD that its 256 registers leave; with fewer registers, three
-//              or four per SIMD, it spills and takes 220 us and more);
+//              sums: read once, no barrier (16384 samples of 26 x 128 in 8 groups, bf16, SiLU:
+//              forward 42 us, 5.2 TB/s, the rate of a copy; backward 76.8 us, 4.3 TB/s, without an
+//              activation 72.8: two wavefronts per SIMD, which its 223 registers leave, do not keep
+//              more loads in flight; at three it spills and takes 214 us);
 //   resident   a sample sits in the registers of one workgroup's threads, which join its sums in
-//              LDS: read once, any width and group size;
+//              LDS: read once, any width and group size (16384 samples of 26 x 96 in 6 groups, bf16:
+//              forward 71 us, backward 127, floors 32 and 47; 65536 rows of 1024: 128 and 160, floors
+//              52 and 78: one to four vectors a thread in flight, and four barriers for every join
+//              of sums, of which the forward has two a sample);
 //   streamed   samples too large for that are cut into chunks of positions: one kernel leaves
 //              per-channel statistics of each chunk, one joins them per group (the forward of a
 //              sample in one chunk does both in one), one applies them
 //              (x, and dy, are read twice, the second time from the caches where they fit: 6
-//              samples of up to 5001 x 256 in 32 groups, fp16: stats 7.2 us, join 4.5, apply 9.1;
-//              backward 11.4, 4.3 with the parameters' sums, 10.4: six dependent launches).
+//              samples of up to 5001 x 256 in 32 groups, fp16: stats 7.3 us, join 4.5, apply 9.0;
+//              backward 11.6, 4.7 with the parameters' sums, 10.9: six dependent launches).
 // A thread owns eight consecutive channels of some positions, so every access is a 16-byte
 // vector whatever the group width; sums are kept per channel and joined into groups afterwards
 // where a vector crosses groups.
