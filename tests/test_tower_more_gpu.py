@@ -204,3 +204,29 @@ LOOPS = [
 @pytest.mark.parametrize("case", LOOPS, ids=lambda c: "-".join(map(str, c)))
 def test_group_norm_loops(case):
     base.test_group_norm(case)
+
+
+@pytest.mark.parametrize("B,S,C,G,dt,outlier", [
+    (513, 4000, 1040, 1040, "bf16", 1000.0),  # one chunk a sample: a thread sums 4000 positions
+    (513, 4000, 1040, 65, "bf16", 1000.0),
+    (2, 90_000, 64, 64, "f32", 3000.0),       # chunks of positions
+    (513, 4000, 1040, 1040, "bf16", 0.5),     # and none
+])
+def test_group_norm_statistics_behind_a_large_first_position(B, S, C, G, dt, outlier):
+    """Histories whose first position is far from all others: mean and rstd of a few samples against 64 bits."""
+    g = torch.Generator(DEV).manual_seed(S)
+    x = torch.empty(B * S, C, dtype=base.DT[dt], device=DEV).normal_(0.5, 1.0, generator=g)
+    x[::S] = x[::S] + outlier
+    y, mean, rstd = torch.empty_like(x), torch.empty(B, G, device=DEV), torch.empty(B, G, device=DEV)
+    elf.group_norm_fwd(x, None, None, y, mean, rstd, positions=S, groups=G)
+    for b in (0, B // 2, B - 1):
+        v = x[b * S:(b + 1) * S].double().view(S, G, C // G)
+        m = v.mean((0, 2))
+        var = ((v - m[:, None]) ** 2).mean((0, 2))
+        want = (var + 1e-5).rsqrt()
+        # sums in fp32 of n positions a thread, n / 2 half steps for each of the sums of values and of
+        # squares (four positions are added at a time), and trees behind them
+        n = S if B > 2 else S // 16
+        bound = (n / 2 + 64) * 2.0**-24
+        assert ((mean[b].double() - m).abs() <= bound * v.abs().mean((0, 2))).all()
+        assert ((rstd[b].double() / want - 1).abs() <= bound).all(), float((rstd[b].double() / want - 1).abs().max())
