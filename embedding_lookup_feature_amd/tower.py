@@ -125,6 +125,12 @@ def _rows_cols(t: torch.Tensor, name: str):
     return s
 
 
+def _sizes(*n: int):
+    """Sizes that the ABI takes in 32 bits (ctypes would cut larger ones without a word)."""
+    if max(n) >= 2**31:
+        raise ValueError(f"sizes must be below 2^31, got {list(n)}")
+
+
 def _workspace(ws, need: int, device, stream):
     if ws is None and need > 0:
         ws = ec._scratch(need, device, stream)
@@ -137,6 +143,7 @@ def act_dropout_fwd(x: torch.Tensor, y: torch.Tensor, act: str = "none", dropout
                     residual: torch.Tensor = None, stream=None):
     """y = residual + drop(act(x)); x, y, residual [M, N] of one dtype (fp32, fp16, bf16)."""
     shape = M, N = _rows_cols(x, "x")
+    _sizes(M, N)
     xp, ldx = _mat(x, "x", shape, x.dtype)
     rp, ldr = _mat(residual, "residual", shape, x.dtype)
     yp, ldy = _mat(y, "y", shape, x.dtype)
@@ -150,6 +157,7 @@ def act_dropout_bwd(dy: torch.Tensor, x: torch.Tensor, dx: torch.Tensor, act: st
     """dx = drop(dy * act'(x)), the mask of the forward with the same dropout (x may be None
     with act "none")."""
     shape = M, N = _rows_cols(dy, "dy")
+    _sizes(M, N)
     dp, lddy = _mat(dy, "dy", shape, dy.dtype)
     xp, ldx = _mat(x, "x", shape, dy.dtype)
     op, lddx = _mat(dx, "dx", shape, dy.dtype)
@@ -173,6 +181,7 @@ def dense_fwd(x: torch.Tensor, w: torch.Tensor, bias, y: torch.Tensor, act: str 
     contiguous, bias fp32 [N] or None, y / residual / pre [M, N], bf16 or fp16."""
     M, K = _rows_cols(x, "x")
     N = _rows_cols(w, "w")[0]
+    _sizes(M, K, N)
     if w.shape != (N, K) or w.dtype is not x.dtype:
         raise ValueError(f"w must be [N, {K}] of {x.dtype}")
     xp, ldx = _mat(x, "x", (M, K), x.dtype)
@@ -194,6 +203,7 @@ def dense_bwd(x: torch.Tensor, w: torch.Tensor, dz: torch.Tensor, dw: torch.Tens
     dz of the layer below (act, dropout and pre are that layer's).  dx, dres, dzb, pre [M, K]."""
     M, K = _rows_cols(x, "x")
     N = _rows_cols(w, "w")[0]
+    _sizes(M, K, N)
     if w.shape != (N, K) or w.dtype is not x.dtype:
         raise ValueError(f"w must be [N, {K}] of {x.dtype}")
     xp, ldx = _mat(x, "x", (M, K), x.dtype)
@@ -225,6 +235,7 @@ def _samples(x: torch.Tensor, positions: int, groups: int):
     S = int(positions)
     if S < 1 or rows % S != 0:
         raise ValueError(f"x must have a whole number of samples of {S} rows, got {rows}")
+    _sizes(rows // S, S, C, int(groups))
     return rows // S, S, C, int(groups)
 
 

@@ -93,3 +93,42 @@ def test_group_norm_takes_every_pooled_vector_of_the_largest_batch_as_a_row():
         assert fwd(B, S, C, G) == ec.EL_ERR_UNSUPPORTED, (B, S, C, G)
         assert bwd(B, S, C, G, A, big) == ec.EL_ERR_UNSUPPORTED
         assert tw.group_norm_bwd_workspace_bytes(B, S, C, G) == 0 == tw.group_norm_fwd_workspace_bytes(B, S, C, G)
+
+
+def test_binding_refuses_sizes_beyond_32_bits(monkeypatch):
+    """A row count that a 32-bit argument would cut (2^32 + 4 rows to 4) is refused by the binding,
+    not handed on; samples times positions may pass 2^31."""
+    import torch
+    calls = []
+
+    class FakeLibrary:
+        def __getattr__(self, name):
+            return (lambda *a: 4096) if name.endswith("workspace_bytes") else (lambda *a: calls.append((name, a)) or 0)
+
+    monkeypatch.setattr(tw, "lib", FakeLibrary)
+    monkeypatch.setattr(tw, "_mat", lambda t, name, shape, dtype: (A, shape[1]))
+    monkeypatch.setattr(tw, "_vec", lambda *a: A)
+    monkeypatch.setattr(tw, "_stream", lambda *a: 0)
+    monkeypatch.setattr(tw.ec, "_dev", lambda t, name: A)
+    m = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device="meta")  # noqa: E731
+    ws = torch.empty(4096, dtype=torch.uint8)
+    many, few = 2**32 + 4, 16
+    for bad in (
+            lambda: tw.act_dropout_fwd(m(many, 1), m(many, 1)),
+            lambda: tw.act_dropout_fwd(m(1, many), m(1, many)),
+            lambda: tw.act_dropout_bwd(m(many, 1), None, m(many, 1)),
+            lambda: tw.dense_fwd(m(many, 8), m(8, 8), None, m(many, 8), workspace=ws),
+            lambda: tw.dense_fwd(m(few, 8), m(many, 8), None, m(few, many), workspace=ws),
+            lambda: tw.dense_fwd(m(few, many), m(8, many), None, m(few, 8), workspace=ws),
+            lambda: tw.dense_bwd(m(many, 8), m(8, 8), m(many, 8), m(8, 8), workspace=ws),
+            lambda: tw.group_norm_fwd(m(many, 8), None, None, m(many, 8), None, None, positions=1, groups=1, workspace=ws),
+            lambda: tw.group_norm_fwd(m(many, 8), None, None, m(many, 8), None, None, positions=many, groups=1, workspace=ws),
+            lambda: tw.group_norm_fwd(m(few, 8), None, None, m(few, 8), None, None, positions=1, groups=many, workspace=ws),
+            lambda: tw.group_norm_bwd(m(many, 8), m(many, 8), None, None, None, None, m(many, 8), None, None, positions=1,
+                                      groups=1, workspace=ws)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            bad()
+    assert not calls
+    tw.group_norm_fwd(m(2**33, 8), None, None, m(2**33, 8), None, None, positions=2**13, groups=1, workspace=ws)
+    tw.act_dropout_fwd(m(2**31 - 1, 1), m(2**31 - 1, 1))
+    assert [c[0] for c in calls] == ["el_group_norm_fwd", "el_act_dropout_fwd"]
