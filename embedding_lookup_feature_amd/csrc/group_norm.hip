@@ -282,11 +282,14 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
       dx = static_cast<St*>(a.out) + b * a.S * a.ldo + cv * 8;
     }
     const int len = on ? sample_len(a, static_cast<int>(b)) : 0;
-    float mean[8], rstd[8];  // VECG: before the sample's vectors, so that those are waited for once
+    float mean[8], rstd[8];  // before the sample's vectors, so that those are waited for once
     const long at = on ? b * a.G : 0;
     if constexpr (VECG) {
       rstd[0] = a.rstd[at + group];
       mean[0] = a.mean[at + group];
+    } else {
+      load_groups(a, a.rstd + at, cv, rstd);
+      load_groups(a, a.mean + at, cv, mean);
     }
     Raw8<T> rx[NV], rd[NV];
 #pragma unroll
@@ -296,10 +299,6 @@ __global__ __launch_bounds__(kResident) void k_gn_bwd_resident(GnArgs a) {
         rx[i] = load8_raw<T>(x + place(i, a.ldx), n);
         rd[i] = load8_raw<T>(dy + place(i, a.lddy), n);
       }
-    }
-    if constexpr (!VECG) {
-      load_groups(a, a.rstd + at, cv, rstd);
-      load_groups(a, a.mean + at, cv, mean);
     }
     const float inv_n = len > 0 ? 1.f / (static_cast<float>(len) * a.Cg) : 0.f;
     float p[2][8] = {}, cb[8] = {}, cg[8] = {}, du[NV][8];
