@@ -696,11 +696,11 @@ __device__ inline void group_stats(const GnArgs& a, const StreamPos& q, const fl
 }
 
 // part[b][chunk][c] = (mean, sum of squares about it) of channel c over the chunk's valid
-// positions.  A thread takes kAhead positions at a time about the mean so far, which it keeps to twice
-// fp32's bits (differences from its first value lose the others behind a large one: 4000 positions,
-// the first 1000 standard deviations away, left the mean off by 5e-4 of them and rstd by 1 %);
-// batches and threads are joined by the pairwise update of Chan, Golub and LeVeque (1979).  WHOLE: the workgroup has the whole sample and
-// writes the groups' mean and rstd instead.
+// positions.  A thread sums differences from its mean so far, which is brought up to date each time
+// the positions have doubled (differences from its first value all along lose the others behind a
+// large one: 4000 positions, the first 1000 standard deviations away, left the mean off by 5e-4 of
+// them and rstd by 1 %); threads are joined by the pairwise update of Chan, Golub and LeVeque
+// (1979).  WHOLE: the workgroup has the whole sample and writes the groups' mean and rstd instead.
 template <class T, bool WHOLE>
 __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
   using St = typename T::S;
@@ -709,13 +709,24 @@ __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
   float mean[8] = {}, m2[8] = {}, cnt = 0.f;
   if (q.on) {
     const St* x = static_cast<const St*>(a.x) + static_cast<long>(q.b) * a.S * a.ldx + q.cv * 8;
-    float low[8] = {};  // mean + low is the mean so far
+    float s1[8] = {}, s2[8] = {}, fresh = 0.f;  // of the positions since the last fold
+    const auto fold = [&] {
+      cnt += fresh;
+      const float inv = 1.f / cnt;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = s1[i] * inv;
+        mean[i] += d;
+        m2[i] += s2[i] - s1[i] * d;
+        s1[i] = s2[i] = 0.f;
+      }
+      fresh = 0.f;
+    };
     for (int s = q.s0 + q.tr; s < end; s += kAhead * q.TR) {
       Raw8<T> r[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
         if (s + u * q.TR < end) r[u] = load8_raw<T>(x + (s + u * q.TR) * a.ldx, q.n);
-      float s1[8] = {}, s2[8] = {};
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (s + u * q.TR >= end) break;
@@ -723,23 +734,16 @@ __global__ __launch_bounds__(kStream) void k_gn_stats(GnArgs a) {
         to_floats<T>(r[u], f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (cnt == 0.f) mean[i] = f[i];
-          const float d = f[i] - mean[i] - low[i];
+          if (cnt + fresh == 0.f) mean[i] = f[i];
+          const float d = f[i] - mean[i];
           s1[i] += d;
           s2[i] = fmaf(d, d, s2[i]);
         }
-        cnt += 1.f;
+        fresh += 1.f;
       }
-      const float inv = 1.f / cnt;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = s1[i] * inv, step = low[i] + d;
-        m2[i] += s2[i] - s1[i] * d;
-        const float next = mean[i] + step, got = next - mean[i];  // the sum and its rounding error, exactly
-        low[i] = (mean[i] - (next - got)) + (step - got);
-        mean[i] = next;
-      }
+      if (fresh >= cnt) fold();
     }
+    if (fresh > 0.f) fold();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m2[i] = fmaxf(m2[i], 0.f);
   }
