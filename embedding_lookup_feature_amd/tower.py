@@ -125,10 +125,9 @@ def _rows_cols(t: torch.Tensor, name: str):
     return s
 
 
-def _sizes(*n: int):
-    """Sizes that the ABI takes in 32 bits (ctypes would cut larger ones without a word)."""
-    if max(n) >= 2**31:
-        raise ValueError(f"sizes must be below 2^31, got {list(n)}")
+def _too_large(*n: int):
+    """The ABI takes sizes in 32 bits, and ctypes would cut larger ones without a word."""
+    raise ValueError(f"sizes must be below 2^31, got {list(n)}")
 
 
 def _workspace(ws, need: int, device, stream):
@@ -143,7 +142,8 @@ def act_dropout_fwd(x: torch.Tensor, y: torch.Tensor, act: str = "none", dropout
                     residual: torch.Tensor = None, stream=None):
     """y = residual + drop(act(x)); x, y, residual [M, N] of one dtype (fp32, fp16, bf16)."""
     shape = M, N = _rows_cols(x, "x")
-    _sizes(M, N)
+    if (M | N) >> 31:
+        _too_large(M, N)
     xp, ldx = _mat(x, "x", shape, x.dtype)
     rp, ldr = _mat(residual, "residual", shape, x.dtype)
     yp, ldy = _mat(y, "y", shape, x.dtype)
@@ -157,7 +157,8 @@ def act_dropout_bwd(dy: torch.Tensor, x: torch.Tensor, dx: torch.Tensor, act: st
     """dx = drop(dy * act'(x)), the mask of the forward with the same dropout (x may be None
     with act "none")."""
     shape = M, N = _rows_cols(dy, "dy")
-    _sizes(M, N)
+    if (M | N) >> 31:
+        _too_large(M, N)
     dp, lddy = _mat(dy, "dy", shape, dy.dtype)
     xp, ldx = _mat(x, "x", shape, dy.dtype)
     op, lddx = _mat(dx, "dx", shape, dy.dtype)
@@ -181,7 +182,8 @@ def dense_fwd(x: torch.Tensor, w: torch.Tensor, bias, y: torch.Tensor, act: str 
     contiguous, bias fp32 [N] or None, y / residual / pre [M, N], bf16 or fp16."""
     M, K = _rows_cols(x, "x")
     N = _rows_cols(w, "w")[0]
-    _sizes(M, K, N)
+    if (M | K | N) >> 31:
+        _too_large(M, K, N)
     if w.shape != (N, K) or w.dtype is not x.dtype:
         raise ValueError(f"w must be [N, {K}] of {x.dtype}")
     xp, ldx = _mat(x, "x", (M, K), x.dtype)
@@ -203,7 +205,8 @@ def dense_bwd(x: torch.Tensor, w: torch.Tensor, dz: torch.Tensor, dw: torch.Tens
     dz of the layer below (act, dropout and pre are that layer's).  dx, dres, dzb, pre [M, K]."""
     M, K = _rows_cols(x, "x")
     N = _rows_cols(w, "w")[0]
-    _sizes(M, K, N)
+    if (M | K | N) >> 31:
+        _too_large(M, K, N)
     if w.shape != (N, K) or w.dtype is not x.dtype:
         raise ValueError(f"w must be [N, {K}] of {x.dtype}")
     xp, ldx = _mat(x, "x", (M, K), x.dtype)
@@ -235,8 +238,10 @@ def _samples(x: torch.Tensor, positions: int, groups: int):
     S = int(positions)
     if S < 1 or rows % S != 0:
         raise ValueError(f"x must have a whole number of samples of {S} rows, got {rows}")
-    _sizes(rows // S, S, C, int(groups))
-    return rows // S, S, C, int(groups)
+    B, G = rows // S, int(groups)
+    if (B | S | C | G) >> 31 > 0:  # (a negative G is refused as such)
+        _too_large(B, S, C, G)
+    return B, S, C, G
 
 
 def group_norm_fwd(x: torch.Tensor, gamma, beta, y: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
