@@ -23,8 +23,8 @@
 //              per-channel statistics of each chunk, one joins them per group (the forward of a
 //              sample in one chunk does both in one), one applies them
 //              (x, and dy, are read twice, the second time from the caches where they fit: 6
-//              samples of up to 5001 x 256 in 32 groups, fp16: stats 8.2 us, join 4.8, apply 9.0;
-//              backward 10.8, 4.5 with the parameters' sums, 10.2: six dependent launches).
+//              samples of up to 5001 x 256 in 32 groups, fp16: stats 7.4 us, join 5.0, apply 9.4;
+//              backward 11.4, 4.8 with the parameters' sums, 10.9: six dependent launches).
 // A thread owns eight consecutive channels of some positions, so every access is a 16-byte
 // vector whatever the group width; sums are kept per channel and joined into groups afterwards
 // where a vector crosses groups.
