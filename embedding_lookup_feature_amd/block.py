@@ -1,0 +1,341 @@
+"""Python binding of the residual block's operators (the C ABI in ``include/embblock.h``).
+
+Argument marshalling only, in the manner of ``tower``: torch tensors are passed as device
+pointers plus sizes and row strides, on torch's current HIP stream unless a stream is given, with
+the operands' device made current for the call; outputs and workspaces belong to the caller (a
+workspace that is not given is allocated here for the call, on the call's stream).
+Two-dimensional operands may be row-strided views (last dimension dense).
+"""
+import ctypes
+import os
+import re
+
+import torch
+
+from . import embcore as ec
+from . import tower as tw
+
+HEADER = os.path.join(os.path.dirname(ec.HERE), "include", "embblock.h")
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+GATES = {"none": 0, "sigmoid": 1}
+MICRO_BLOCK, FP4_PAD = 32, 128
+
+
+class ElBlockNorm(ctypes.Structure):
+    _fields_ = [("post", ctypes.c_uint32), ("pre", ctypes.c_uint32), ("gate_act", ctypes.c_uint32),
+                ("gate_rows", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("post_gamma", ctypes.c_void_p), ("post_beta", ctypes.c_void_p),
+                ("pre_gamma", ctypes.c_void_p), ("pre_beta", ctypes.c_void_p)]
+
+
+_bound = None
+
+
+def lib() -> ctypes.CDLL:
+    """The loaded library with this header's functions declared."""
+    global _bound
+    if _bound is None:
+        L = ec.lib()
+        vp, i32, i64, u32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t)
+        dt, D, P = ctypes.c_int, ctypes.POINTER(tw.ElDropout), ctypes.POINTER(ElBlockNorm)
+        L.el_block_norm_fwd.argtypes = [P, vp, i64, vp, i64, vp, i64, i32, i32, vp, i64, vp, i64, vp, vp, dt, vp]
+        L.el_block_norm_bwd.argtypes = [P, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, vp, vp, vp, i64, vp,
+                                        i64, vp, i64, vp, vp, vp, vp, dt, vp, sz, vp]
+        L.el_ckpt_pack.argtypes = [vp, i64, i32, i32, dt, vp, vp, vp]
+        L.el_ckpt_act_dropout_fwd.argtypes = [vp, vp, i32, i32, u32, D, vp, i64, dt, vp]
+        L.el_ckpt_act_dropout_bwd.argtypes = [vp, i64, vp, vp, i32, i32, u32, D, vp, i64, dt, vp]
+        L.el_dense_bwd_ckpt.argtypes = [vp, vp, i32, i32, vp, i32, vp, i64, vp, i64, vp, i64, u32, D, vp, vp, vp, i64,
+                                        vp, vp, dt, vp, sz, vp]
+        L.el_fp4_pack.argtypes = [vp, i64, i32, i32, dt, vp, vp, vp]
+        L.el_fp4_unpack.argtypes = [vp, vp, i32, i32, vp, i64, dt, vp]
+        L.el_dense_fwd_fp4.argtypes = [vp, i64, i32, i32, vp, vp, vp, i32, u32, vp, i64, vp, i64, dt, vp, sz, vp]
+        for name in header_functions():
+            getattr(L, name).restype = ctypes.c_int
+        for name in ("el_block_norm_bwd_workspace_bytes", "el_dense_bwd_ckpt_workspace_bytes",
+                     "el_dense_fwd_fp4_workspace_bytes"):
+            getattr(L, name).argtypes = [i32] * 3
+            getattr(L, name).restype = sz
+        _bound = L
+    return _bound
+
+
+def header_functions():
+    """Names of the functions `include/embblock.h` declares."""
+    text = open(HEADER).read()
+    return re.findall(r"EL_API\s+[\w\s\*]+?\b(\w+)\s*\(", text)
+
+
+def _launch(fn, t: torch.Tensor, stream, *args):
+    """Calls fn(*args, stream) with t's device current (the default stream's handle names none)."""
+    i = t.get_device()
+    if i == torch.cuda.current_device():
+        ec._check(fn(*args, tw._stream(stream, t)))
+    else:
+        with torch.cuda.device(i):
+            ec._check(fn(*args, tw._stream(stream, t)))
+
+
+def _mat(t, name: str, shape, like: torch.Tensor):
+    """(pointer, row stride) of a row-strided operand of like's type, on its device; (None, cols) of
+    None."""
+    if t is not None and t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return tw._mat(t, name, shape, like.dtype)
+
+
+def _vec(t, name: str, n: int, like: torch.Tensor):
+    if t is None:
+        return None
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return tw._vec(t, name, n)
+
+
+def _workspace(ws, need: int, like: torch.Tensor, stream):
+    if ws is not None and ws.get_device() != like.get_device():
+        raise ValueError(f"workspace must be on {like.device}, got {ws.device}")
+    return tw._workspace(ws, need, like.device, stream)
+
+
+class BlockNorm:
+    """The parameters around one residual block of C columns: the norms `post` behind it ("none",
+    "rms", "layer") and `pre` before the next ("rms", "layer") with their gammas and betas (fp32 [C]
+    or None), the gate's activation ("none", "sigmoid"), the number of consecutive rows that share
+    one row of the gate, and the residual scale."""
+
+    def __init__(self, C: int, post: str = "none", pre: str = "rms", post_gamma: torch.Tensor = None,
+                 post_beta: torch.Tensor = None, pre_gamma: torch.Tensor = None, pre_beta: torch.Tensor = None,
+                 gate_act: str = "none", gate_rows: int = 1, scale: float = 1.0, eps: float = 1e-5):
+        if post not in NORMS:
+            raise ValueError(f"post must be one of {sorted(NORMS)}, got {post!r}")
+        if pre not in NORMS or pre == "none":
+            raise ValueError(f"pre must be \"rms\" or \"layer\", got {pre!r}")
+        if gate_act not in GATES:
+            raise ValueError(f"gate_act must be one of {sorted(GATES)}, got {gate_act!r}")
+        if not 1 <= gate_rows < 2**31:
+            raise ValueError(f"gate_rows must be from 1 to 2^31 - 1, got {gate_rows}")
+        self.C = int(C)
+        self.params = (post_gamma, post_beta, pre_gamma, pre_beta)
+        names = ("post_gamma", "post_beta", "pre_gamma", "pre_beta")
+        self.device = next((p.get_device() for p in self.params if p is not None), None)
+        for p, name in zip(self.params, names):
+            if p is not None and p.get_device() != self.device:
+                raise ValueError(f"{name} must be on the other parameters' device")
+        self.c = ElBlockNorm(NORMS[post], NORMS[pre], GATES[gate_act], int(gate_rows), float(scale), float(eps),
+                             *(tw._vec(p, name, self.C) for p, name in zip(self.params, names)))
+        self.ref = ctypes.byref(self.c)
+
+    def gates(self, M: int) -> int:
+        """Rows of the gate for M rows."""
+        return -(-M // self.c.gate_rows)
+
+
+def _norm_shape(norm: BlockNorm, t: torch.Tensor, name: str):
+    M, C = tw._rows_cols(t, name)
+    if C != norm.C:
+        raise ValueError(f"{name} must have {norm.C} columns, got {C}")
+    if M >> 31:
+        tw._too_large(M, C)
+    if norm.device is not None and t.get_device() != norm.device:
+        raise ValueError(f"{name} must be on the parameters' device")
+    return M, C
+
+
+def block_norm_fwd(norm: BlockNorm, x, y=None, h=None, f: torch.Tensor = None, gate: torch.Tensor = None,
+                   post_stats: torch.Tensor = None, pre_stats: torch.Tensor = None, stream=None):
+    """y = x + scale gate (post_gamma post(f) + post_beta), h = pre_gamma pre(y) + pre_beta; x (or
+    None: nothing added), f, y, h [M, C], gate [ceil(M / gate_rows), C] of one dtype.  Without f, h
+    is the norm of x.  y or h may be None.  post_stats, pre_stats: fp32 [M, 2], written when given."""
+    like = x if x is not None else f
+    if like is None:
+        raise ValueError("x or f must be given")
+    shape = M, C = _norm_shape(norm, like, "x" if x is not None else "f")
+    xp, ldx = _mat(x, "x", shape, like)
+    fp, ldf = _mat(f, "f", shape, like)
+    gp, ldg = _mat(gate, "gate", (norm.gates(M), C), like)
+    yp, ldy = _mat(y, "y", shape, like)
+    hp, ldh = _mat(h, "h", shape, like)
+    _launch(lib().el_block_norm_fwd, like, stream, norm.ref, xp, ldx, fp, ldf, gp, ldg, M, C, yp, ldy, hp, ldh,
+            _vec(post_stats, "post_stats", 2 * M, like), _vec(pre_stats, "pre_stats", 2 * M, like), ec._dtype(like, "x"))
+    return y, h
+
+
+def block_norm_bwd_workspace_bytes(norm: BlockNorm, M: int) -> int:
+    return int(lib().el_block_norm_bwd_workspace_bytes(M, norm.C, norm.c.gate_rows))
+
+
+def block_norm_bwd(norm: BlockNorm, y, dx, dy: torch.Tensor = None, dh: torch.Tensor = None, f: torch.Tensor = None,
+                   gate: torch.Tensor = None, df: torch.Tensor = None, dgate: torch.Tensor = None,
+                   post_stats: torch.Tensor = None, pre_stats: torch.Tensor = None, dpost_gamma: torch.Tensor = None,
+                   dpost_beta: torch.Tensor = None, dpre_gamma: torch.Tensor = None, dpre_beta: torch.Tensor = None,
+                   workspace: torch.Tensor = None, stream=None):
+    """Gradients of block_norm_fwd from dy and / or dh, the stored y (x where f was None; may be None
+    without dh), f, gate and statistics: dx, df [M, C], dgate like the gate, the parameters' fp32
+    [C]; every output may be None."""
+    like = dh if dh is not None else dy
+    if like is None:
+        raise ValueError("dy or dh must be given")
+    shape = M, C = _norm_shape(norm, like, "dh" if dh is not None else "dy")
+    dyp, lddy = _mat(dy, "dy", shape, like)
+    dhp, lddh = _mat(dh, "dh", shape, like)
+    yp, ldy = _mat(y, "y", shape, like)
+    fp, ldf = _mat(f, "f", shape, like)
+    gp, ldg = _mat(gate, "gate", (norm.gates(M), C), like)
+    dxp, lddx = _mat(dx, "dx", shape, like)
+    dfp, lddf = _mat(df, "df", shape, like)
+    dgp, lddg = _mat(dgate, "dgate", (norm.gates(M), C), like)
+    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else block_norm_bwd_workspace_bytes(norm, M), like,
+                                stream)
+    _launch(lib().el_block_norm_bwd, like, stream, norm.ref, dyp, lddy, dhp, lddh, yp, ldy, fp, ldf, gp, ldg, M, C,
+            _vec(post_stats, "post_stats", 2 * M, like), _vec(pre_stats, "pre_stats", 2 * M, like), dxp, lddx, dfp, lddf,
+            dgp, lddg, _vec(dpost_gamma, "dpost_gamma", C, like), _vec(dpost_beta, "dpost_beta", C, like),
+            _vec(dpre_gamma, "dpre_gamma", C, like), _vec(dpre_beta, "dpre_beta", C, like), ec._dtype(like, "dh"), wsp,
+            wsn)
+    return dx, df
+
+
+class _Packed:
+    """[rows, cols] values in microscaled codes: blocks of 32 columns share a scale byte."""
+
+    def __init__(self, rows: int, cols: int, device, pad: int, per_byte: int):
+        if not 0 <= rows < 2**31 or not 1 <= cols < 2**31:
+            raise ValueError(f"rows must be from 0 and cols from 1 to 2^31 - 1, got {rows} x {cols}")
+        self.rows, self.cols = int(rows), int(cols)
+        width = -(-self.cols // pad) * pad
+        self.codes = torch.empty((self.rows, width // per_byte), dtype=torch.uint8, device=device)
+        self.scales = torch.empty((self.rows, width // MICRO_BLOCK), dtype=torch.uint8, device=device)
+        self.ptrs = (ec._dev(self.codes, "codes"), ec._dev(self.scales, "scales")) if self.rows else (None, None)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+class Checkpoint(_Packed):
+    """Activations kept in 8 bits (e4m3): codes [rows, cols rounded up to 32], scales."""
+
+    def __init__(self, rows: int, cols: int, device="cuda"):
+        super().__init__(rows, cols, device, MICRO_BLOCK, 1)
+
+
+class Fp4(_Packed):
+    """Weights in 4 bits (e2m1), two to a byte: codes [rows, cols rounded up to 128 / 2], scales."""
+
+    def __init__(self, rows: int, cols: int, device="cuda"):
+        super().__init__(rows, cols, device, FP4_PAD, 2)
+
+
+def _packed(p, kind, name: str, shape, like: torch.Tensor):
+    """Pointers of a packed operand of `kind`; (None, None) of None."""
+    if p is None:
+        return None, None
+    if type(p) is not kind:
+        raise ValueError(f"{name} must be a {kind.__name__}")
+    if (p.rows, p.cols) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {[p.rows, p.cols]}")
+    if p.codes.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on {like.device}, got {p.codes.device}")
+    return p.ptrs
+
+
+def ckpt_pack(x: torch.Tensor, ckpt: Checkpoint, stream=None) -> Checkpoint:
+    """Keeps x [M, K] (fp32, fp16, bf16) in 8 bits."""
+    M, K = tw._rows_cols(x, "x")
+    codes, scales = _packed(ckpt, Checkpoint, "ckpt", (M, K), x)
+    xp, ldx = _mat(x, "x", (M, K), x)
+    _launch(lib().el_ckpt_pack, x, stream, xp, ldx, M, K, ec._dtype(x, "x"), codes, scales)
+    return ckpt
+
+
+def ckpt_act_dropout_fwd(ckpt: Checkpoint, y: torch.Tensor, act: str = "none", dropout=None, stream=None):
+    """y = drop(act(kept values)): what act_dropout_fwd gives on them; with neither, the kept values."""
+    M, K = tw._rows_cols(y, "y")
+    codes, scales = _packed(ckpt, Checkpoint, "ckpt", (M, K), y)
+    yp, ldy = _mat(y, "y", (M, K), y)
+    _launch(lib().el_ckpt_act_dropout_fwd, y, stream, codes, scales, M, K, tw._act(act), tw._drop(dropout), yp, ldy,
+            ec._dtype(y, "y"))
+    return y
+
+
+def ckpt_act_dropout_bwd(dy: torch.Tensor, ckpt: Checkpoint, dx: torch.Tensor, act: str = "none", dropout=None,
+                         stream=None):
+    """dx = drop(dy * act'(kept values)), the mask of the forward with the same dropout."""
+    M, K = tw._rows_cols(dy, "dy")
+    codes, scales = _packed(ckpt, Checkpoint, "ckpt", (M, K), dy)
+    dp, lddy = _mat(dy, "dy", (M, K), dy)
+    op, lddx = _mat(dx, "dx", (M, K), dy)
+    _launch(lib().el_ckpt_act_dropout_bwd, dy, stream, dp, lddy, codes, scales, M, K, tw._act(act), tw._drop(dropout), op,
+            lddx, ec._dtype(dy, "dy"))
+    return dx
+
+
+def dense_bwd_ckpt_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().el_dense_bwd_ckpt_workspace_bytes(M, K, N))
+
+
+def dense_bwd_ckpt(x: Checkpoint, w: torch.Tensor, dz: torch.Tensor, dw: torch.Tensor, db: torch.Tensor = None,
+                   dx: torch.Tensor = None, dres: torch.Tensor = None, dzb: torch.Tensor = None, pre: Checkpoint = None,
+                   act: str = "none", dropout=None, workspace: torch.Tensor = None, stream=None):
+    """dense_bwd with x [M, K] and pre [M, K] kept in 8 bits."""
+    M, N = tw._rows_cols(dz, "dz")
+    K = tw._rows_cols(w, "w")[1]
+    if (M | K | N) >> 31:
+        tw._too_large(M, K, N)
+    if w.shape != (N, K) or w.dtype is not dz.dtype or w.get_device() != dz.get_device():
+        raise ValueError(f"w must be [{N}, K] of {dz.dtype} on {dz.device}")
+    xc, xs = _packed(x, Checkpoint, "x", (M, K), dz)
+    pc, ps = _packed(pre, Checkpoint, "pre", (M, K), dz)
+    zp, ldz = _mat(dz, "dz", (M, N), dz)
+    dxp, lddx = _mat(dx, "dx", (M, K), dz)
+    rp, ldr = _mat(dres, "dres", (M, K), dz)
+    bp, ldb = _mat(dzb, "dzb", (M, K), dz)
+    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_bwd_ckpt_workspace_bytes(M, K, N), dz,
+                                stream)
+    if dw.numel() != N * K:
+        raise ValueError(f"dw must be [{N}, {K}]")
+    _launch(lib().el_dense_bwd_ckpt, dz, stream, xc, xs, M, K, ec._dev(w, "w"), N, zp, ldz, rp, ldr, dxp, lddx,
+            tw._act(act), tw._drop(dropout), pc, ps, bp, ldb, _vec(dw, "dw", N * K, dz), _vec(db, "db", N, dz),
+            ec._dtype(dz, "dz"), wsp, wsn)
+    return dx, dw, db
+
+
+def fp4_pack(x: torch.Tensor, packed: Fp4, stream=None) -> Fp4:
+    """Rounds x [M, K] (fp32, fp16, bf16) to 4 bits."""
+    M, K = tw._rows_cols(x, "x")
+    codes, scales = _packed(packed, Fp4, "packed", (M, K), x)
+    xp, ldx = _mat(x, "x", (M, K), x)
+    _launch(lib().el_fp4_pack, x, stream, xp, ldx, M, K, ec._dtype(x, "x"), codes, scales)
+    return packed
+
+
+def fp4_unpack(packed: Fp4, y: torch.Tensor, stream=None):
+    """The values that the codes stand for."""
+    M, K = tw._rows_cols(y, "y")
+    codes, scales = _packed(packed, Fp4, "packed", (M, K), y)
+    yp, ldy = _mat(y, "y", (M, K), y)
+    _launch(lib().el_fp4_unpack, y, stream, codes, scales, M, K, yp, ldy, ec._dtype(y, "y"))
+    return y
+
+
+def dense_fwd_fp4_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().el_dense_fwd_fp4_workspace_bytes(M, K, N))
+
+
+def dense_fwd_fp4(x: torch.Tensor, w: Fp4, bias, y: torch.Tensor, act: str = "none", residual: torch.Tensor = None,
+                  workspace: torch.Tensor = None, stream=None):
+    """y = residual + act(x4 @ w4.T + bias), x [M, K] (bf16, fp16) rounded to 4 bits within the call,
+    w a packed [N, K]; bias fp32 [N] or None; y, residual [M, N]."""
+    M, K = tw._rows_cols(x, "x")
+    N = y.shape[-1]
+    if (M | K | N) >> 31:
+        tw._too_large(M, K, N)
+    wc, wsc = _packed(w, Fp4, "w", (N, K), x)
+    xp, ldx = _mat(x, "x", (M, K), x)
+    rp, ldr = _mat(residual, "residual", (M, N), x)
+    yp, ldy = _mat(y, "y", (M, N), x)
+    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_fwd_fp4_workspace_bytes(M, K, N), x,
+                                stream)
+    _launch(lib().el_dense_fwd_fp4, x, stream, xp, ldx, M, K, wc, wsc, _vec(bias, "bias", N, x), N, tw._act(act), rp, ldr,
+            yp, ldy, ec._dtype(x, "x"), wsp, wsn)
+    return y

@@ -1,0 +1,119 @@
+// micro.hpp -- microscaled 8-bit (e4m3) and 4-bit (e2m1) numbers: 32 columns share a power of two
+// (the format stands in embblock.h).
+#pragma once
+
+#include "embblock.h"
+#include "tower_common.hpp"
+
+namespace el {
+
+constexpr int kMicroBlock = 32;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// 2^e of a scale byte e + 127 (1 .. 254); 255 (NaN) gives infinity.
+__device__ inline float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// The scale byte of a block whose largest finite magnitude has the bits `amax`, for T = top: the
+// smallest e with amax <= top 2^e.  With top = (1 + f) 2^t and amax = (1 + g) 2^E that is E - t,
+// and one more where g > f.  (Subnormal magnitudes have the exponent bits 0, E = -127 or less.)
+template <bool FP4>
+__device__ inline uint32_t scale_byte(uint32_t amax) {
+  constexpr uint32_t top_frac = FP4 ? 0x400000u : 0x600000u;  // 6 = 1.5 * 2^2, 448 = 1.75 * 2^8
+  constexpr int top_exp = FP4 ? 2 : 8;
+  const int e = static_cast<int>(amax >> 23) - top_exp + ((amax & 0x7fffffu) > top_frac);
+  return static_cast<uint32_t>(max(e, 1));
+}
+
+// Largest magnitude over the four lanes that hold a block of 32 columns, eight each.
+__device__ inline uint32_t quad_max(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xf, 0xf, true)));  // lane ^ 1
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xf, 0xf, true)));  // lane ^ 2
+}
+__device__ inline uint32_t quad_or(uint32_t v) {
+  v |= static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xf, 0xf, true));
+  return v | static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xf, 0xf, true));
+}
+
+// This lane's eight columns of a block held by four neighbouring lanes, as 8-bit codes; the block's
+// scale byte to `byte`.
+struct Codes8 { uint32_t lo, hi; };
+__device__ inline Codes8 pack8(const float (&v)[8], uint32_t& byte) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
+    amax = max(amax, m < 0x7f800000u ? m : 0u);
+  }
+  byte = scale_byte<false>(quad_max(amax));
+  const float inv = __uint_as_float((254u - byte) << 23);  // 2^-e, exact (e <= 120)
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // an infinity becomes NaN; the conversion keeps NaN
+    const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
+    q[i] = m == 0x7f800000u ? __uint_as_float(0x7fc00000u) : v[i] * inv;
+  }
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
+  return Codes8{static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
+}
+__device__ inline void unpack8(uint32_t lo, uint32_t hi, float scale, float (&v)[8]) {
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), true);
+  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(hi), false), d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(hi), true);
+  v[0] = a[0] * scale, v[1] = a[1] * scale, v[2] = b[0] * scale, v[3] = b[1] * scale;
+  v[4] = c[0] * scale, v[5] = c[1] * scale, v[6] = d[0] * scale, v[7] = d[1] * scale;
+}
+
+// The same in 4 bits: eight codes in one word.
+__device__ inline uint32_t pack4(const float (&v)[8], uint32_t& byte) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  amax = quad_max(amax);  // NaN and infinities compare as the largest
+  if (amax >= 0x7f800000u) {
+    byte = 255u;
+    return 0u;
+  }
+  byte = scale_byte<true>(amax);
+  const float inv = __uint_as_float((254u - byte) << 23);
+  uint32_t q = 0;
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0] * inv, v[1] * inv, 1.f, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2] * inv, v[3] * inv, 1.f, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4] * inv, v[5] * inv, 1.f, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6] * inv, v[7] * inv, 1.f, 3);
+  return q;
+}
+__device__ inline void unpack4(uint32_t q, uint32_t byte, float (&v)[8]) {
+  const float scale = byte == 255u ? __uint_as_float(0x7fc00000u) : scale_of(byte);
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
+  v[0] = a[0] * scale, v[1] = a[1] * scale, v[2] = b[0] * scale, v[3] = b[1] * scale;
+  v[4] = c[0] * scale, v[5] = c[1] * scale, v[6] = d[0] * scale, v[7] = d[1] * scale;
+}
+
+namespace tower {
+
+constexpr int kMaxMicroCols = 1 << 20;
+inline int64_t pad_to(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// Sizes of a packed [M][K] array whose rows are padded to `pad` columns.  (2^34 elements are 2^31
+// threads of eight.)
+inline el_status check_packed_sizes(const char* fn, int64_t M, int64_t K, int pad) {
+  if (M < 0) return bad(fn, "the number of rows must be >= 0");
+  if (K < 1) return bad(fn, "K must be >= 1");
+  if (K > kMaxMicroCols) return unsupported(fn, "K must be <= 2^20");
+  if (M * pad_to(K, pad) > (int64_t{1} << 34)) return unsupported(fn, "rows times padded columns must be <= 2^34");
+  return EL_OK;
+}
+inline el_status check_packed(const char* fn, const char* name, const void* codes, const void* scales, bool needed) {
+  if (!codes || !scales) return needed ? bad(fn, std::string("the codes and scales of ") + name + " must not be null") : EL_OK;
+  if (!al(codes, 16)) return bad(fn, std::string("the codes of ") + name + " must be 16-byte aligned");
+  if (!al(scales, 4)) return bad(fn, std::string("the scales of ") + name + " must be 4-byte aligned");
+  return EL_OK;
+}
+
+}  // namespace tower
+}  // namespace el

@@ -1,0 +1,211 @@
+"""The residual block's entry points: exported, and bad arguments refused on the host before
+anything reaches a GPU (no compute call is made here)."""
+import ctypes
+
+import pytest
+import torch
+
+from embedding_lookup_feature_amd import block as bk
+from embedding_lookup_feature_amd import embcore as ec
+from embedding_lookup_feature_amd import tower as tw
+
+INVALID, UNSUPPORTED, WORKSPACE, OK = ec.EL_ERR_INVALID_ARG, ec.EL_ERR_UNSUPPORTED, ec.EL_ERR_WORKSPACE, ec.EL_OK
+A = 0x7F0000000000  # fake, aligned: every call below ends at its checks
+BIG = 1 << 40
+NAN, INF = float("nan"), float("inf")
+
+
+def drop(p):
+    return ctypes.byref(tw.ElDropout(p, 1, 2, None))
+
+
+def test_library_exports_every_declared_function():
+    L = bk.lib()
+    names = bk.header_functions()
+    assert set(names) == {"el_block_norm_fwd", "el_block_norm_bwd", "el_block_norm_bwd_workspace_bytes", "el_ckpt_pack",
+                          "el_ckpt_act_dropout_fwd", "el_ckpt_act_dropout_bwd", "el_dense_bwd_ckpt",
+                          "el_dense_bwd_ckpt_workspace_bytes", "el_fp4_pack", "el_fp4_unpack", "el_dense_fwd_fp4",
+                          "el_dense_fwd_fp4_workspace_bytes"}
+    for n in names:
+        assert hasattr(L, n), n
+
+
+NP = dict(post=1, pre=1, gate_act=0, gate_rows=1, scale=1.0, eps=1e-5, gp=A, bp=A, gq=A, bq=A)
+
+
+def params(a):
+    return ctypes.byref(bk.ElBlockNorm(*(a[k] for k in NP)))
+
+
+NF = dict(x=A, ldx=64, f=A, ldf=64, gate=A, ldg=64, M=8, C=64, y=A, ldy=64, h=A, ldh=64, ps=A, qs=A, dt=ec.EL_BF16)
+BAD_PARAMS = [
+    (dict(post=3), INVALID), (dict(pre=0), INVALID), (dict(pre=3), INVALID), (dict(gate_act=2), INVALID),
+    (dict(gate_rows=0), INVALID), (dict(gate_rows=-3), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID),
+    (dict(eps=-1e-6), INVALID), (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID), (dict(gp=A + 2), INVALID),
+    (dict(bq=A + 1), INVALID), (dict(M=-1), INVALID), (dict(C=0), INVALID), (dict(C=32769, ldx=1 << 16), UNSUPPORTED),
+    (dict(dt=3), INVALID), (dict(dt=-1), INVALID),
+]
+
+
+@pytest.mark.parametrize("change,status", BAD_PARAMS + [
+    (dict(x=None, f=None, gate=None, y=None, ps=None), INVALID), (dict(f=None), INVALID), (dict(f=None, gate=None), INVALID),
+    (dict(f=None, gate=None, y=None), INVALID), (dict(y=None, h=None), INVALID), (dict(h=None), INVALID),
+    (dict(post=0), INVALID), (dict(ldx=63), INVALID), (dict(ldf=63), INVALID), (dict(ldg=8), INVALID), (dict(ldy=0), INVALID),
+    (dict(ldh=-64), INVALID), (dict(x=A + 1), INVALID), (dict(gate=A + 1), INVALID), (dict(ps=A + 4), INVALID),
+    (dict(qs=A + 4), INVALID), (dict(ldx=1 << 40), INVALID), (dict(M=0, x=None, f=None, y=None, h=None), OK),
+])
+def test_block_norm_fwd_refusals(change, status):
+    a = {**NP, **NF, **change}
+    rc = bk.lib().el_block_norm_fwd(params(a), a["x"], a["ldx"], a["f"], a["ldf"], a["gate"], a["ldg"], a["M"], a["C"],
+                                    a["y"], a["ldy"], a["h"], a["ldh"], a["ps"], a["qs"], a["dt"], None)
+    assert rc == status
+    if status != OK:
+        assert "el_block_norm_fwd" in ec.el_last_error()
+
+
+NB = dict(dy=A, lddy=64, dh=A, lddh=64, y=A, ldy=64, f=A, ldf=64, gate=A, ldg=64, M=8, C=64, ps=A, qs=A, dx=A, lddx=64,
+          df=A, lddf=64, dg=A, lddg=64, dgp=A, dbp=A, dgq=A, dbq=A, dt=ec.EL_F16, ws=A, wsn=BIG)
+
+
+@pytest.mark.parametrize("change,status", [c for c in BAD_PARAMS if "ldx" not in c[0]] + [
+    (dict(C=32769, **{k: 1 << 16 for k in ("lddy", "lddh", "ldy", "ldf", "ldg", "lddx", "lddf", "lddg")}), UNSUPPORTED),
+    (dict(dy=None, dh=None), INVALID), (dict(y=None), INVALID), (dict(qs=None), INVALID), (dict(ps=None), INVALID),
+    (dict(dh=None), INVALID), (dict(dh=None, dgq=None), INVALID), (dict(f=None), INVALID), (dict(f=None, gate=None), INVALID),
+    (dict(f=None, gate=None, df=None, dg=None), INVALID), (dict(gate=None), INVALID), (dict(lddy=63), INVALID),
+    (dict(lddh=63), INVALID), (dict(ldy=63), INVALID), (dict(lddx=63), INVALID), (dict(lddf=1), INVALID),
+    (dict(lddg=63), INVALID), (dict(dgp=A + 2), INVALID), (dict(dbq=A + 1), INVALID), (dict(dy=A + 1), INVALID),
+    (dict(qs=A + 4), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=A + 128), WORKSPACE), (dict(wsn=64), WORKSPACE),
+])
+def test_block_norm_bwd_refusals(change, status):
+    a = {**NP, **NB, **change}
+    rc = bk.lib().el_block_norm_bwd(params(a), a["dy"], a["lddy"], a["dh"], a["lddh"], a["y"], a["ldy"], a["f"], a["ldf"],
+                                    a["gate"], a["ldg"], a["M"], a["C"], a["ps"], a["qs"], a["dx"], a["lddx"], a["df"],
+                                    a["lddf"], a["dg"], a["lddg"], a["dgp"], a["dbp"], a["dgq"], a["dbq"], a["dt"], a["ws"],
+                                    a["wsn"], None)
+    assert rc == status
+    assert "el_block_norm_bwd" in ec.el_last_error()
+
+
+def test_null_parameters_are_refused():
+    assert bk.lib().el_block_norm_fwd(None, A, 8, None, 0, None, 0, 1, 8, None, 0, A, 8, None, None, 0, None) == INVALID
+
+
+PACK = dict(x=A, ldx=64, M=8, K=64, dt=ec.EL_F32, codes=A, scales=A)
+
+
+@pytest.mark.parametrize("fn", ["el_ckpt_pack", "el_fp4_pack"])
+@pytest.mark.parametrize("change,status", [
+    (dict(x=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(codes=A + 8), INVALID),
+    (dict(scales=A + 2), INVALID), (dict(ldx=63), INVALID), (dict(x=A + 2), INVALID), (dict(M=-1), INVALID),
+    (dict(K=0), INVALID), (dict(K=(1 << 20) + 1, ldx=1 << 21), UNSUPPORTED),
+    (dict(M=(1 << 24) + 1, K=1024, ldx=1024), UNSUPPORTED), (dict(dt=5), INVALID), (dict(M=0, x=None, codes=None), OK),
+])
+def test_pack_refusals(fn, change, status):
+    a = {**PACK, **change}
+    rc = getattr(bk.lib(), fn)(a["x"], a["ldx"], a["M"], a["K"], a["dt"], a["codes"], a["scales"], None)
+    assert rc == status
+    if status != OK:
+        assert fn in ec.el_last_error()
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(x=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(codes=A + 4), INVALID),
+    (dict(scales=A + 1), INVALID), (dict(ldx=63), INVALID), (dict(M=-1), INVALID), (dict(K=0), INVALID), (dict(dt=9), INVALID),
+    (dict(M=(1 << 24) + 1, K=1024, ldx=1024), UNSUPPORTED),
+])
+def test_unpacking_refusals(change, status):
+    a = {**PACK, **change}
+    L = bk.lib()
+    assert L.el_fp4_unpack(a["codes"], a["scales"], a["M"], a["K"], a["x"], a["ldx"], a["dt"], None) == status
+    assert L.el_ckpt_act_dropout_fwd(a["codes"], a["scales"], a["M"], a["K"], 2, None, a["x"], a["ldx"], a["dt"], None) == status
+    assert "el_ckpt_act_dropout_fwd" in ec.el_last_error()
+    assert L.el_ckpt_act_dropout_bwd(A, 1 << 21, a["codes"], a["scales"], a["M"], a["K"], 2, None, a["x"], a["ldx"], a["dt"], None) == status
+
+
+def test_ckpt_act_refusals():
+    L = bk.lib()
+    fwd = lambda act, d: L.el_ckpt_act_dropout_fwd(A, A, 4, 64, act, d, A, 64, ec.EL_BF16, None)  # noqa: E731
+    assert fwd(4, None) == INVALID and fwd(1, drop(-0.5)) == INVALID and fwd(1, drop(NAN)) == INVALID
+    bwd = lambda dy, ld: L.el_ckpt_act_dropout_bwd(dy, ld, A, A, 4, 64, 1, None, A, 64, ec.EL_BF16, None)  # noqa: E731
+    assert bwd(None, 64) == INVALID and bwd(A, 63) == INVALID and bwd(A + 1, 64) == INVALID
+
+
+DB = dict(xc=A, xs=A, M=4, K=32, w=A, N=16, dz=A, ldz=16, dres=None, ldr=0, dx=A, lddx=32, act=1, drop=None, pc=A, ps=A,
+          dzb=A, ldb=32, dw=A, db=A, dt=ec.EL_BF16, ws=A, wsn=BIG)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(xc=None), INVALID), (dict(xs=None), INVALID), (dict(xc=A + 8), INVALID), (dict(xs=A + 1), INVALID),
+    (dict(w=None), INVALID), (dict(w=A + 1), INVALID), (dict(dz=None), INVALID), (dict(dw=None), INVALID),
+    (dict(pc=None), INVALID), (dict(ps=None), INVALID), (dict(pc=A + 4), INVALID), (dict(dx=None), INVALID),
+    (dict(dx=None, dzb=None, dres=A, ldr=32), INVALID), (dict(ldz=15), INVALID), (dict(lddx=31), INVALID),
+    (dict(ldb=31), INVALID), (dict(dres=A, ldr=31), INVALID), (dict(dw=A + 2), INVALID), (dict(db=A + 1), INVALID),
+    (dict(act=5), INVALID), (dict(dt=ec.EL_F32), UNSUPPORTED), (dict(dt=7), INVALID), (dict(ws=None), WORKSPACE),
+    (dict(ws=A + 16), WORKSPACE), (dict(wsn=1), WORKSPACE), (dict(M=-2), INVALID), (dict(K=0), INVALID), (dict(N=0), INVALID),
+    (dict(drop=drop(-1.0)), INVALID), (dict(K=1 << 16, N=1 << 15), UNSUPPORTED),
+])
+def test_dense_bwd_ckpt_refusals(change, status):
+    a = {**DB, **change}
+    rc = bk.lib().el_dense_bwd_ckpt(a["xc"], a["xs"], a["M"], a["K"], a["w"], a["N"], a["dz"], a["ldz"], a["dres"], a["ldr"],
+                                    a["dx"], a["lddx"], a["act"], a["drop"], a["pc"], a["ps"], a["dzb"], a["ldb"], a["dw"],
+                                    a["db"], a["dt"], a["ws"], a["wsn"], None)
+    assert rc == status
+    assert "el_dense_bwd_ckpt" in ec.el_last_error()
+
+
+DF = dict(x=A, ldx=2048, M=300, K=2048, wc=A, ws=A, bias=A, N=512, act=1, r=None, ldr=0, y=A, ldy=512, dt=ec.EL_BF16, wk=A,
+          wkn=BIG)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(x=None), INVALID), (dict(wc=None), INVALID), (dict(ws=None), INVALID), (dict(y=None), INVALID),
+    (dict(wc=A + 8), INVALID), (dict(ws=A + 2), INVALID), (dict(bias=A + 2), INVALID), (dict(ldx=2047), INVALID),
+    (dict(ldy=511), INVALID), (dict(r=A, ldr=511), INVALID), (dict(r=A + 1, ldr=512), INVALID), (dict(M=-1), INVALID),
+    (dict(K=0), INVALID), (dict(N=0), INVALID), (dict(act=4), INVALID), (dict(dt=ec.EL_F32), UNSUPPORTED),
+    (dict(dt=44), INVALID), (dict(K=1 << 16, N=1 << 15, ldx=1 << 16, ldy=1 << 15), UNSUPPORTED),
+    (dict(M=(1 << 24) + 1, K=1024, N=16), UNSUPPORTED), (dict(M=0, x=None, y=None), OK),
+])
+def test_dense_fwd_fp4_refusals(change, status):
+    a = {**DF, **change}
+    rc = bk.lib().el_dense_fwd_fp4(a["x"], a["ldx"], a["M"], a["K"], a["wc"], a["ws"], a["bias"], a["N"], a["act"], a["r"],
+                                   a["ldr"], a["y"], a["ldy"], a["dt"], a["wk"], a["wkn"], None)
+    assert rc == status
+    if status != OK:
+        assert "el_dense_fwd_fp4" in ec.el_last_error()
+
+
+def test_workspace_queries_are_host_pure_and_bounded():
+    L = bk.lib()
+    sizes = (-2**31, -1, 0, 1, 2, 7, 26, 127, 129, 1024, 4099, 65536, 1 << 20, 2**31 - 1)
+    for fn in (L.el_block_norm_bwd_workspace_bytes, L.el_dense_bwd_ckpt_workspace_bytes, L.el_dense_fwd_fp4_workspace_bytes):
+        for a in sizes:
+            for b in sizes:
+                for c in sizes:
+                    n = fn(a, b, c)
+                    assert n % 256 == 0
+                    if min(a, b, c) < 1:
+                        assert n == 0
+
+
+def test_python_binding_refuses_mismatched_operands():
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="post must be"):
+        bk.BlockNorm(8, post="batch")
+    with pytest.raises(ValueError, match="pre must be"):
+        bk.BlockNorm(8, pre="none")
+    with pytest.raises(ValueError, match="gate_act"):
+        bk.BlockNorm(8, gate_act="tanh")
+    with pytest.raises(ValueError, match="gate_rows"):
+        bk.BlockNorm(8, gate_rows=0)
+    with pytest.raises(ValueError, match="device tensor"):
+        bk.block_norm_fwd(bk.BlockNorm(8), x, h=x)
+    with pytest.raises(ValueError, match="columns"):
+        bk.block_norm_fwd(bk.BlockNorm(9), x, h=x)
+    with pytest.raises(ValueError, match="x or f"):
+        bk.block_norm_fwd(bk.BlockNorm(8), None)
+    with pytest.raises(ValueError, match="dy or dh"):
+        bk.block_norm_bwd(bk.BlockNorm(8), x, x)
+    with pytest.raises(ValueError, match="cols"):
+        bk.Checkpoint(4, 0, "cpu")
+    with pytest.raises(ValueError, match="device tensor"):
+        bk.Checkpoint(4, 8, "cpu")
