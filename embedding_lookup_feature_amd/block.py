@@ -19,7 +19,7 @@ HEADER = os.path.join(os.path.dirname(ec.HERE), "include", "embblock.h")
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 GATES = {"none": 0, "sigmoid": 1}
-MICRO_BLOCK, FP4_PAD = 32, 128
+MICRO_BLOCK = 32
 
 
 class ElBlockNorm(ctypes.Structure):
@@ -198,13 +198,13 @@ def block_norm_bwd(norm: BlockNorm, y, dx, dy: torch.Tensor = None, dh: torch.Te
 class _Packed:
     """[rows, cols] values in microscaled codes: blocks of 32 columns share a scale byte."""
 
-    def __init__(self, rows: int, cols: int, device, pad: int, per_byte: int):
+    def __init__(self, rows: int, cols: int, device):
         if not 0 <= rows < 2**31 or not 1 <= cols < 2**31:
             raise ValueError(f"rows must be from 0 and cols from 1 to 2^31 - 1, got {rows} x {cols}")
         self.rows, self.cols = int(rows), int(cols)
-        width = -(-self.cols // pad) * pad
-        self.codes = torch.empty((self.rows, width // per_byte), dtype=torch.uint8, device=device)
-        self.scales = torch.empty((self.rows, width // MICRO_BLOCK), dtype=torch.uint8, device=device)
+        codes, scales = self._shapes()
+        self.codes = torch.empty(codes, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(scales, dtype=torch.uint8, device=device)
         self.ptrs = (ec._dev(self.codes, "codes"), ec._dev(self.scales, "scales")) if self.rows else (None, None)
 
     @property
@@ -213,17 +213,26 @@ class _Packed:
 
 
 class Checkpoint(_Packed):
-    """Activations kept in 8 bits (e4m3): codes [rows, cols rounded up to 32], scales."""
+    """Activations kept in 8 bits (e4m3): codes [rows, cols rounded up to 32], scales [rows, blocks]."""
 
     def __init__(self, rows: int, cols: int, device="cuda"):
-        super().__init__(rows, cols, device, MICRO_BLOCK, 1)
+        super().__init__(rows, cols, device)
+
+    def _shapes(self):
+        blocks = -(-self.cols // MICRO_BLOCK)
+        return (self.rows, blocks * MICRO_BLOCK), (self.rows, blocks)
 
 
 class Fp4(_Packed):
-    """Weights in 4 bits (e2m1), two to a byte: codes [rows, cols rounded up to 128 / 2], scales."""
+    """Weights in 4 bits (e2m1), two to a byte, in the order that the matrix instructions take: tiles
+    of 32 rows by 128 columns (codes) and by 512 (scales)."""
 
     def __init__(self, rows: int, cols: int, device="cuda"):
-        super().__init__(rows, cols, device, FP4_PAD, 2)
+        super().__init__(rows, cols, device)
+
+    def _shapes(self):
+        tiles = -(-self.rows // 32)
+        return (tiles, -(-self.cols // 128), 2, 64, 16), (tiles, -(-self.cols // 512), 2, 64, 4)
 
 
 def _packed(p, kind, name: str, shape, like: torch.Tensor):

@@ -7,42 +7,159 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 constexpr int kThreads = 256;
 constexpr int kPad = 128;  // columns of a padded row: whole products of 128
 
+// ---------------------------------------------------------------------------------------
+// The layout: tiles of 32 rows by 128 columns in the order in which the matrix instructions take
+// them.  Fragment i (of two) of a tile is 64 lanes of 16 bytes: lane l holds the block l / 16 of 32
+// columns of row 8 (l % 16 / 4) + 4 i + l % 4.  With w as the first operand the accumulators of
+// both fragments are then eight consecutive output columns of a lane, and every load of a fragment
+// is one contiguous KiB (straight from row-major codes a load touched 64 separate pieces, and the
+// cache's address rate, not its bytes, bounded the product: 184 us for 65536 x 1024 x 1024).
+// ---------------------------------------------------------------------------------------
+constexpr int kTileRows = 32, kFrag = 1024;  // bytes of a fragment's codes; 64 words hold its scales of four steps
+__device__ inline int lane_of_row(int r) { return (r >> 3 & 3) * 4 + (r & 3); }  // row of a tile -> l % 16
+__device__ inline int frag_of_row(int r) { return r >> 2 & 1; }
+__device__ inline int row_of_lane(int frag, int l16) { return (frag >> 1) * kTileRows + (l16 >> 2) * 8 + (frag & 1) * 4 + (l16 & 3); }
+
+// Byte of the codes of row r's eight columns 8 q .. 8 q + 7 of step k, and of its scale of their block.
+__device__ inline long code_at(long r, int k, int q, int steps) {
+  const int t = static_cast<int>(r & 31);
+  return (((r >> 5) * steps + k) * 2 + frag_of_row(t)) * kFrag + ((q >> 2) * 16 + lane_of_row(t)) * 16 + (q & 3) * 4;
+}
+__device__ inline long scale_at(long r, int k, int g, int groups) {
+  const int t = static_cast<int>(r & 31);
+  return (((r >> 5) * groups + (k >> 2)) * 2 + frag_of_row(t)) * 256 + (g * 16 + lane_of_row(t)) * 4 + (k & 3);
+}
+
+// Eight values of a 16-bit type straight to 4 bits: the largest magnitude is found on the bits
+// (ordered like unsigned numbers), and the conversion divides by the scale.
+template <class T>
+__device__ inline uint32_t pack4_raw(const Raw8<T>& raw, uint32_t& byte) {
+  if constexpr (T::code == EL_F32) {
+    float v[8];
+    to_floats<T>(raw, v);
+    return pack4(v, byte);
+  } else {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, raw.v[0][i] & 0x7fff7fffu));
+    const uint32_t top = quad_max(max(static_cast<uint32_t>(m[0]), static_cast<uint32_t>(m[1])));
+    const uint32_t amax = __float_as_uint(T::to_f(static_cast<uint16_t>(top)));
+    if (amax >= 0x7f800000u) {  // NaN and infinities compare as the largest
+      byte = 255u;
+      return 0u;
+    }
+    byte = scale_byte<true>(amax);
+    const float scale = scale_of(byte);
+    const uint32_t w0 = raw.v[0][0], w1 = raw.v[0][1], w2 = raw.v[0][2], w3 = raw.v[0][3];
+    uint32_t q = 0;
+    if constexpr (T::code == EL_BF16) {
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, w0), scale, 0);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, w1), scale, 1);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, w2), scale, 2);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, w3), scale, 3);
+    } else {
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, __builtin_bit_cast(f16x2, w0), scale, 0);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, __builtin_bit_cast(f16x2, w1), scale, 1);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, __builtin_bit_cast(f16x2, w2), scale, 2);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, __builtin_bit_cast(f16x2, w3), scale, 3);
+    }
+    return q;
+  }
+}
+
+// Lane d of the result holds what lane `from` (the same in no two lanes) holds.
+__device__ inline u32x4 lanes_from(int from, const u32x4& v) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(from * 4, static_cast<int>(v[i])));
+  return r;
+}
+
+// Two values to a word in one conversion.
+template <class T>
+__device__ inline u32x4 to_16bit(const float (&f)[8]) {
+  u32x4 a;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 p = {f[2 * i], f[2 * i + 1]};
+    uint32_t w;
+    if constexpr (T::code == EL_BF16) w = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+    else w = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, f16x2));
+    a[i] = w;
+  }
+  return a;
+}
+
+__device__ inline void store8_raw(uint16_t* p, const u32x4& v, int n) {
+  if (n >= 8) {
+    *reinterpret_cast<u32x4_any*>(p) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = static_cast<uint16_t>(v[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+template <class T>
+__device__ inline Raw8<T> zeros8() {
+  Raw8<T> r;
+#pragma unroll
+  for (int w = 0; w < Raw8<T>::W; ++w) r.v[w] = u32x4{0, 0, 0, 0};
+  return r;
+}
+
 struct PackArgs {
   const void* x;
   long ldx;
-  int K, groups;  // columns, padded columns / 8
-  int64_t items;  // M * groups
+  int M, K, steps;
   uint8_t *codes, *scales;
 };
 
-// One thread owns eight columns; four neighbouring lanes a block of 32, which never crosses a row.
+// 16 lanes pack the 128 columns of a step of one row; a workgroup takes four steps of 16 rows at a
+// time, so that whole words of scales and whole lines of codes are written.
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_fp4_pack(PackArgs a) {
-  using S = typename T::S;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads;
-  const int64_t i = first + threadIdx.x;
-  if (i >= a.items) return;
-  const int64_t row0 = first / a.groups;  // uniform: one 64-bit division per workgroup
-  const uint32_t local = static_cast<uint32_t>(first - row0 * a.groups) + threadIdx.x;
-  const uint32_t dr = local / static_cast<uint32_t>(a.groups), grp = local - dr * a.groups;
-  const int n = a.K - static_cast<int>(grp) * 8;
-  float v[8] = {};
-  if (n > 0) to_floats<T>(load8_raw<T>(static_cast<const S*>(a.x) + (row0 + dr) * a.ldx + grp * 8l, n), v);
-  uint32_t byte;
-  const uint32_t q = pack4(v, byte);
-  reinterpret_cast<uint32_t*>(a.codes)[i] = q;
-  if ((threadIdx.x & 3) == 0) a.scales[i >> 2] = static_cast<uint8_t>(byte);
+  __shared__ uint8_t sc[16][4][4];  // [row][block][step]
+  const int groups = (a.steps + 3) / 4;
+  const int64_t rows16 = blockIdx.x / groups;
+  const int grp = static_cast<int>(blockIdx.x - rows16 * groups);
+  const int u = threadIdx.x >> 4, q = threadIdx.x & 15;
+  const int64_t row = rows16 * 16 + u;
+  Raw8<T> raw[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int k = grp * 4 + s, c = k * kPad + q * 8, n = a.K - c;
+    raw[s] = zeros8<T>();
+    if (row < a.M && n > 0) raw[s] = load8_raw<T>(static_cast<const typename T::S*>(a.x) + row * a.ldx + c, n);
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int k = grp * 4 + s;
+    uint32_t byte;
+    const uint32_t w = pack4_raw<T>(raw[s], byte);
+    if (k < a.steps) *reinterpret_cast<uint32_t*>(a.codes + code_at(row, k, q, a.steps)) = w;
+    if ((q & 3) == 0) sc[u][q >> 2][s] = static_cast<uint8_t>(byte);
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {  // (steps behind the last have the scales of zeros)
+    const int r = threadIdx.x >> 2, g = threadIdx.x & 3;
+    *reinterpret_cast<uint32_t*>(a.scales + scale_at(rows16 * 16 + r, grp * 4, g, groups)) = *reinterpret_cast<const uint32_t*>(sc[r][g]);
+  }
 }
 
 struct UnpackArgs {
   const uint8_t *codes, *scales;
   void* y;
   long ldy;
-  int K, groups, vecs;
+  int K, steps, vecs;
   int64_t items;  // M * vecs
 };
 template <class T>
@@ -52,15 +169,26 @@ __global__ __launch_bounds__(kThreads) void k_fp4_unpack(UnpackArgs a) {
   const int64_t row0 = first / a.vecs;
   const uint32_t local = static_cast<uint32_t>(first - row0 * a.vecs) + threadIdx.x;
   const uint32_t dr = local / static_cast<uint32_t>(a.vecs), grp = local - dr * a.vecs;
-  const int64_t row = row0 + dr, i = row * a.groups + grp;
+  const int64_t row = row0 + dr;
+  const int k = static_cast<int>(grp >> 4), q = static_cast<int>(grp & 15);
   float v[8];
-  unpack4(reinterpret_cast<const uint32_t*>(a.codes)[i], a.scales[i >> 2], v);
+  unpack4(*reinterpret_cast<const uint32_t*>(a.codes + code_at(row, k, q, a.steps)),
+          a.scales[scale_at(row, k, q >> 2, (a.steps + 3) / 4)], v);
   store8<T>(static_cast<typename T::S*>(a.y) + row * a.ldy + grp * 8l, v, a.K - static_cast<int>(grp) * 8);
 }
 
+// ---------------------------------------------------------------------------------------
+// The product.  A workgroup of four wavefronts packs 16 J rows of x into LDS once (their whole
+// length), then walks over its columns, 32 to a wavefront; the weights' fragments come straight
+// from the L2, which holds them all.
+// ---------------------------------------------------------------------------------------
 struct DenseArgs {
-  const uint8_t *xc, *xs, *wc, *ws;
-  int M, N, steps;  // steps of 128 columns
+  const void* x;             // 16-bit rows, packed here
+  const uint8_t *xc, *xs;    // or rows packed before (XG)
+  const uint8_t *wc, *ws;
+  long ldx;
+  int M, N, K, steps;        // steps of 128 columns
+  int passes, row_blocks;    // column passes of a workgroup; blocks of 16 J rows
   const float* bias;
   const uint16_t* add;
   uint16_t* out;
@@ -68,53 +196,209 @@ struct DenseArgs {
   uint32_t act;
 };
 
-// 16 x 16 outputs from 128 columns: lane l holds row l % 16 of each operand, the block of 32 columns
-// l / 16, and that block's scale byte; the accumulators of lane l are rows 4 (l / 16) .. +3 of the
-// first operand and row l % 16 of the second.
+// 16 x 16 outputs from 128 columns; the scale of a lane's block is byte SEL of its scale word.  The
+// accumulators of lane l are rows 4 (l / 16) .. +3 of the first operand's fragment and row l % 16
+// of the second's.
+template <int SEL>
 __device__ inline f32x4 mfma_fp4(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb, const f32x4& c) {
   const i32x8 av = {static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]), 0, 0, 0, 0};
   const i32x8 bv = {static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3]), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, static_cast<int>(sa), 0, static_cast<int>(sb));
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, SEL, static_cast<int>(sa), SEL, static_cast<int>(sb));
 }
 
-template <class T>
-__global__ __launch_bounds__(kThreads) void k_dense_fp4(DenseArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
-  const int tiles_c = (a.N + 63) / 64;
-  const int tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
-  const int row0 = tr * 64 + (wave >> 1) * 32, col0 = tc * 64 + (wave & 1) * 32;
-  f32x4 acc[2][2] = {};
-  for (int k = 0; k < a.steps; ++k) {
-    u32x4 x[2], w[2];
-    uint32_t xs[2], ws[2];
+// The n (1 .. 7) last elements of eight, moved to the front, zeros behind them.
+__device__ inline u32x4 last_to_front(u32x4 v, int n) {
+  const int s = 8 - n;
+  if (s & 4) v = u32x4{v[2], v[3], 0, 0};
+  if (s & 2) v = u32x4{v[1], v[2], v[3], 0};
+  if (s & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  return v;
+}
+
+// Eight columns from c of a row of `cols` (at least eight) at p, zeros behind its end, by one load
+// without a branch: a vector that the end cuts is loaded from the row's last eight.
+__device__ inline u32x4 load_cut(const uint16_t* p, int c, int cols) {
+  return *reinterpret_cast<const u32x4_any*>(p + min(c, cols - 8));
+}
+__device__ inline u32x4 settle_cut(const u32x4& v, int c, int cols) {
+  const int n = cols - c;
+  if (n >= 8) return v;
+  return n > 0 ? last_to_front(v, n) : u32x4{0, 0, 0, 0};
+}
+
+__device__ inline void settle_cut(float (&v)[8], int n) {
+  const int s = n > 0 && n < 8 ? 8 - n : 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const long r = min(row0 + i * 16 + l16, a.M - 1), c = min(col0 + i * 16 + l16, a.N - 1);
-      x[i] = *reinterpret_cast<const u32x4*>(a.xc + ((r * a.steps + k) * 4 + g) * 16);
-      w[i] = *reinterpret_cast<const u32x4*>(a.wc + ((c * a.steps + k) * 4 + g) * 16);
-      xs[i] = a.xs[(r * a.steps + k) * 4 + g];
-      ws[i] = a.ws[(c * a.steps + k) * 4 + g];
-    }
+  for (int b = 4; b; b >>= 1)
+    if (s & b)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int e = 0; e + b < 8; ++e) v[e] = v[e + b];
+}
+
+// What bounds it, and the shape that follows: loads and stores share one in-order counter, so every
+// load is issued at a fixed distance in front of its use, without a branch around it (a wait that
+// cannot count waits for everything, the stores before it too: 124 us against 98).  The weights of
+// the step three ahead, of the next columns where the row ends, are fetched while a step multiplies;
+// the residual during a pass's last three steps.  EIGHT: K and N are at least 8.
+template <class T, int J, bool XG, bool EIGHT, bool ADD, bool BIAS>
+__global__ __launch_bounds__(kThreads, 4) void k_dense_fp4(DenseArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [step][J][64 lanes][16], then [group][J][64 lanes][4]
+  constexpr int BR = 16 * J, WC = 32;
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rb = blockIdx.x % a.row_blocks, cb = blockIdx.x / a.row_blocks;
+  const int row0 = rb * BR, groups = (a.steps + 3) / 4;
+  uint8_t* lsc = lds + a.steps * J * kFrag;
+  if constexpr (!XG) {
+    // 16 lanes pack the 128 columns of a step of one row
+    const int u = threadIdx.x >> 4, q = threadIdx.x & 15;
+    const uint16_t* px = static_cast<const uint16_t*>(a.x);
+    const uint16_t* p[J];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_fp4(w[i], ws[i], x[j], xs[j], acc[i][j]);
-  }
+    for (int j = 0; j < J; ++j) p[j] = px + static_cast<long>(min(row0 + j * 16 + u, a.M - 1)) * a.ldx;
+#pragma unroll 2
+    for (int k = 0; k < a.steps; ++k) {
+      const int c = k * kPad + q * 8, n = a.K - c;
+      Raw8<T> raw[J];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < J; ++j) {
+        if constexpr (EIGHT) {
+          raw[j].v[0] = load_cut(p[j], c, a.K);
+        } else {
+          raw[j] = zeros8<T>();
+          if (n > 0) raw[j] = load8_raw<T>(p[j] + c, n);
+        }
+      }
+      const bool cut = k * kPad + kPad > a.K;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = row0 + j * 16 + l16, c = col0 + i * 16 + g * 4;
-      if (r >= a.M) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (c + e >= a.N) continue;
-        float v[8] = {acc[i][j][e] + (a.bias ? a.bias[c + e] : 0.f)};
-        act8(a.act, v);
-        if (a.add) v[0] += T::to_f(a.add[r * a.ldadd + c + e]);
-        a.out[r * a.ldo + c + e] = T::from_f(v[0]);
+      for (int j = 0; j < J; ++j) {
+        if (EIGHT && cut) raw[j].v[0] = settle_cut(raw[j].v[0], c, a.K);
+        uint32_t byte;
+        const uint32_t w = pack4_raw<T>(raw[j], byte);
+        *reinterpret_cast<uint32_t*>(lds + (k * J + j) * kFrag + ((q >> 2) * 16 + u) * 16 + (q & 3) * 4) = w;
+        if ((q & 3) == 0) lsc[((k >> 2) * J + j) * 256 + ((q >> 2) * 16 + u) * 4 + (k & 3)] = static_cast<uint8_t>(byte);
       }
     }
+    __syncthreads();
+  }
+  constexpr int SETS = 4;  // steps of w in flight or in use
+  u32x4 w[SETS][2];
+  uint32_t wsc[2][2], xsc[J];
+  const int tiles = (a.N + kTileRows - 1) / kTileRows;
+  int tile = cb * a.passes * 4 + wave;
+  if (tile >= tiles) return;
+  const auto rc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.wc), 0, tiles * a.steps * 2 * kFrag, 0x00027000);
+  const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.ws), 0, tiles * groups * 512, 0x00027000);
+  // Step k of the tile, or of the tile after it from 4 groups on; what does not exist is replaced by
+  // what does, and not used.
+  const auto fetch = [&](int set, int k) {
+    const bool next = k >= groups * 4;
+    const int t = min(next ? tile + 4 : tile, tiles - 1), kk = min(next ? k - groups * 4 : k, a.steps - 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[set][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, lane * 16, ((t * a.steps + kk) * 2 + i) * kFrag, 0));
+  };
+  const auto fetch_scales = [&](int set, int group) {
+    const bool next = group >= groups;
+    const int t = min(next ? tile + 4 : tile, tiles - 1), gg = next ? 0 : group;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) wsc[set][i] = __builtin_amdgcn_raw_buffer_load_b32(rs, lane * 4, ((t * groups + gg) * 2 + i) * 256, 0);
+  };
+  fetch_scales(0, 0);
+#pragma unroll
+  for (int t = 0; t < SETS - 1; ++t) fetch(t, t);
+  // Fragment j's row of this lane in memory is row_of(j, l) = first row of the fragment + l (or l's
+  // place in a tile): the lane's part of its address is formed once.
+  const int lrow = XG ? row_of_lane(0, lane >> 2) : lane >> 2;
+  const auto frag_row = [&](int j) { return XG ? row_of_lane(rb * J + j, 0) : row0 + j * 16; };
+  const long add_lane = lrow * a.ldadd, out_lane = lrow * a.ldo;
+  for (int pass = 0; pass < a.passes && tile < tiles; ++pass, tile += 4) {
+    const int c = tile * WC + 8 * g;              // this lane's columns in the accumulators,
+    const int cm = tile * WC + 8 * (lane & 3);    // and in memory, where four neighbours share a row
+    f32x4 acc[2][J] = {};
+    float bias[8] = {};
+    Raw8<T> add[J];
+    const auto fetch_ends = [&]() {  // the bias and the residual
+      if constexpr (BIAS) {
+        if constexpr (EIGHT) {
+          const f32x4_any* p = reinterpret_cast<const f32x4_any*>(a.bias + min(c, a.N - 8));
+          const f32x4 lo = p[0], hi = p[1];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bias[e] = lo[e], bias[4 + e] = hi[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) bias[e] = a.bias[min(c + e, a.N - 1)];
+        }
+      }
+      if constexpr (ADD)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int fr = frag_row(j);  // (a row that does not exist is replaced by the workgroup's first)
+          const uint16_t* p = a.add + (lrow < a.M - fr ? fr * a.ldadd + add_lane : min(row0, a.M - 1) * a.ldadd);
+          if constexpr (EIGHT) add[j].v[0] = load_cut(p, cm, a.N);
+          else if (cm < a.N) add[j] = load8_raw<T>(p + cm, a.N - cm);
+        }
+    };
+    const auto step = [&](int k, auto sel) {
+      constexpr int SEL = decltype(sel)::value;
+      fetch((SEL + SETS - 1) % SETS, k + SETS - 1);
+      if (k >= a.steps) return;
+      u32x4 x[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if constexpr (XG) {
+          const long f = rb * J + j;
+          x[j] = *reinterpret_cast<const u32x4*>(a.xc + (((f >> 1) * a.steps + k) * 2 + (f & 1)) * kFrag + lane * 16);
+          if (SEL == 0) xsc[j] = *reinterpret_cast<const uint32_t*>(a.xs + (((f >> 1) * groups + (k >> 2)) * 2 + (f & 1)) * 256 + lane * 4);
+        } else {
+          x[j] = *reinterpret_cast<const u32x4*>(lds + (k * J + j) * kFrag + lane * 16);
+          if (SEL == 0) xsc[j] = *reinterpret_cast<const uint32_t*>(lsc + ((k >> 2) * J + j) * 256 + lane * 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) acc[i][j] = mfma_fp4<SEL>(w[SEL][i], wsc[0][i], x[j], xsc[j], acc[i][j]);
+    };
+    static_assert(SETS == 4, "one set for each scale byte");
+    const auto group = [&](int k, auto last) {
+      fetch_scales(1, (k >> 2) + 1);
+      step(k, std::integral_constant<int, 0>{});
+      if constexpr (decltype(last)::value) fetch_ends();
+      step(k + 1, std::integral_constant<int, 1>{});
+      step(k + 2, std::integral_constant<int, 2>{});
+      step(k + 3, std::integral_constant<int, 3>{});
+      wsc[0][0] = wsc[1][0], wsc[0][1] = wsc[1][1];
+    };
+    int k = 0;
+    for (; k < groups * 4 - 4; k += 4) group(k, std::false_type{});
+    group(k, std::true_type{});
+    const bool cut = tile * WC + WC > a.N;
+    if (BIAS && EIGHT && cut) settle_cut(bias, a.N - c);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float v[8], f[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = acc[0][j][e] + bias[e], v[4 + e] = acc[1][j][e] + bias[4 + e];
+      act8(a.act, v);
+      if constexpr (ADD) {
+        Raw8<T> mine = add[j];
+        if (EIGHT && cut) mine.v[0] = settle_cut(mine.v[0], cm, a.N);
+        mine.v[0] = lanes_from(l16 * 4 + g, mine.v[0]);
+        to_floats<T>(mine, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += f[e];
+      }
+      const u32x4 o = lanes_from((lane & 3) * 16 + (lane >> 2), to_16bit<T>(v));
+      const int fr = frag_row(j);
+      uint16_t* p = a.out + (fr * a.ldo + out_lane) + cm;
+      if (lrow < a.M - fr) {
+        if (!cut) *reinterpret_cast<u32x4_any*>(p) = o;
+        else if (cm < a.N) store8_raw(p, o, a.N - cm);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one vector's values at a time in registers
+    }
+  }
 }
 
 template <class F>
@@ -127,20 +411,66 @@ void with_type(el_dtype dtype, F&& f) {
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 long steps_of(long K) { return ceil_div(K, kPad); }
-size_t code_bytes(long M, long K) { return round256(static_cast<size_t>(M) * steps_of(K) * kPad / 2); }
-size_t scale_bytes(long M, long K) { return round256(static_cast<size_t>(M) * steps_of(K) * kPad / kMicroBlock); }
+long groups_of(long K) { return ceil_div(steps_of(K), 4); }
+long tile_rows(long M) { return tower::pad_to(M, kTileRows); }
+size_t code_bytes(long M, long K) { return round256(static_cast<size_t>(tile_rows(M)) * steps_of(K) * kPad / 2); }
+size_t scale_bytes(long M, long K) { return round256(static_cast<size_t>(tile_rows(M)) * groups_of(K) * 16); }
 
 void launch_pack(const void* x, long ldx, int M, int K, el_dtype dtype, uint8_t* codes, uint8_t* scales, hipStream_t st) {
-  PackArgs a{x, ldx, K, static_cast<int>(steps_of(K) * kPad / 8), 0, codes, scales};
-  a.items = static_cast<int64_t>(M) * a.groups;
+  const PackArgs a{x, ldx, M, K, static_cast<int>(steps_of(K)), codes, scales};
+  const long units = tile_rows(M) / 16 * groups_of(K);
   with_type(dtype, [&](auto t) {
-    hipLaunchKernelGGL((k_fp4_pack<decltype(t)>), dim3(static_cast<unsigned>(ceil_div(a.items, kThreads))), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((k_fp4_pack<decltype(t)>), dim3(static_cast<unsigned>(units)), dim3(kThreads), 0, st, a);
   });
+}
+
+size_t x_lds(int rows, long K) { return rows * (steps_of(K) * 64 + groups_of(K) * 16); }
+
+// How a call is cut: 16 J rows x 16 I columns a wavefront, `passes` column passes of a workgroup.
+struct Plan {
+  bool few, packed;  // few rows (J = 1, I = 2); x packed in the workspace
+  int row_blocks, passes;
+  long blocks;
+};
+Plan plan_dense(long M, long K, long N) {
+  Plan p{};
+  p.few = ceil_div(M, 64) * ceil_div(N, 128) < 512;
+  const int rows = p.few ? 16 : 64, cols = 128;
+  p.packed = x_lds(rows, K) > 150 * 1024;
+  p.row_blocks = static_cast<int>(ceil_div(p.packed ? tile_rows(M) : M, rows));  // packed rows come in whole tiles
+  const long all = ceil_div(N, cols);  // column passes there are
+  const long split = std::min(all, std::max<long>(1, ceil_div(p.few ? 1l << 30 : 1024, p.row_blocks)));
+  p.passes = static_cast<int>(ceil_div(all, split));
+  p.blocks = p.row_blocks * ceil_div(all, p.passes);
+  return p;
+}
+
+template <class T>
+void launch_dense(const Plan& p, const DenseArgs& a, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(p.blocks));
+  const size_t lds = p.packed ? 0 : x_lds(p.few ? 16 : 64, a.K);
+  const bool eight = a.K >= 8 && a.N >= 8;
+#define EL_FP4_ONE(J, XG, EIGHT, ADD, BIAS) \
+  hipLaunchKernelGGL((k_dense_fp4<T, J, XG, EIGHT, ADD, BIAS>), grid, dim3(kThreads), lds, st, a)
+#define EL_FP4(J, XG, EIGHT)                                        \
+  if (a.add && a.bias) EL_FP4_ONE(J, XG, EIGHT, true, true);        \
+  else if (a.add) EL_FP4_ONE(J, XG, EIGHT, true, false);            \
+  else if (a.bias) EL_FP4_ONE(J, XG, EIGHT, false, true);           \
+  else EL_FP4_ONE(J, XG, EIGHT, false, false)
+#define EL_FP4_J(J)                                   \
+  if (p.packed && eight) { EL_FP4(J, true, true); }   \
+  else if (p.packed) { EL_FP4(J, true, false); }      \
+  else if (eight) { EL_FP4(J, false, true); }         \
+  else { EL_FP4(J, false, false); }
+  if (p.few) { EL_FP4_J(1) } else { EL_FP4_J(4) }
+#undef EL_FP4_J
+#undef EL_FP4
+#undef EL_FP4_ONE
 }
 
 bool dense_fp4_sizes_ok(int64_t M, int64_t K, int64_t N) {
   return M >= 1 && K >= 1 && N >= 1 && K <= tower::kMaxMicroCols && N <= tower::kMaxMicroCols && N * K < (int64_t{1} << 29) &&
-         ceil_div(M, 256) * ceil_div(N, 256) < (1l << 21) && M * tower::pad_to(K, kPad) <= (int64_t{1} << 34);
+         ceil_div(M, 256) * ceil_div(N, 256) < (1l << 21) && tower::pad_to(M, kTileRows) * tower::pad_to(K, kPad) <= (int64_t{1} << 34);
 }
 
 }  // namespace
@@ -155,7 +485,7 @@ el_status el_fp4_pack(const void* x, int64_t ldx, int32_t M, int32_t K, el_dtype
   const char* fn = "el_fp4_pack";
   return tower::guarded(fn, [&]() -> el_status {
     if (!dtype_valid(dtype)) return tower::bad(fn, "unknown dtype");
-    EL_TRY(tower::check_packed_sizes(fn, M, K, kPad));
+    EL_TRY(tower::check_packed_sizes(fn, M, K, kPad, kTileRows));
     EL_TRY(tower::check_rows(fn, "x", x, ldx, K, M > 0, dtype_size(dtype)));
     EL_TRY(tower::check_packed(fn, "the output", codes, scales, M > 0));
     if (M == 0) return EL_OK;
@@ -169,11 +499,11 @@ el_status el_fp4_unpack(const uint8_t* codes, const uint8_t* scales, int32_t M, 
   const char* fn = "el_fp4_unpack";
   return tower::guarded(fn, [&]() -> el_status {
     if (!dtype_valid(dtype)) return tower::bad(fn, "unknown dtype");
-    EL_TRY(tower::check_packed_sizes(fn, M, K, kPad));
+    EL_TRY(tower::check_packed_sizes(fn, M, K, kPad, kTileRows));
     EL_TRY(tower::check_packed(fn, "x", codes, scales, M > 0));
     EL_TRY(tower::check_rows(fn, "y", y, ldy, K, M > 0, dtype_size(dtype)));
     if (M == 0) return EL_OK;
-    UnpackArgs a{codes, scales, y, ldy, K, static_cast<int>(steps_of(K) * kPad / 8), (K + 7) / 8, 0};
+    UnpackArgs a{codes, scales, y, ldy, K, static_cast<int>(steps_of(K)), (K + 7) / 8, 0};
     a.items = static_cast<int64_t>(M) * a.vecs;
     with_type(dtype, [&](auto t) {
       hipLaunchKernelGGL((k_fp4_unpack<decltype(t)>), dim3(static_cast<unsigned>(ceil_div(a.items, kThreads))), dim3(kThreads), 0, stream, a);
@@ -183,7 +513,8 @@ el_status el_fp4_unpack(const uint8_t* codes, const uint8_t* scales, int32_t M, 
 }
 
 size_t el_dense_fwd_fp4_workspace_bytes(int32_t M, int32_t K, int32_t N) {
-  return dense_fp4_sizes_ok(M, K, N) ? code_bytes(M, K) + scale_bytes(M, K) : 0;
+  if (!dense_fp4_sizes_ok(M, K, N) || !plan_dense(M, K, N).packed) return 0;
+  return code_bytes(M, K) + scale_bytes(M, K);
 }
 
 el_status el_dense_fwd_fp4(const void* x, int64_t ldx, int32_t M, int32_t K, const uint8_t* w_codes,
@@ -207,17 +538,21 @@ el_status el_dense_fwd_fp4(const void* x, int64_t ldx, int32_t M, int32_t K, con
     EL_TRY(tower::check_rows(fn, "y", y, ldy, N, M > 0, 2));
     if (M == 0) return EL_OK;
     EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, el_dense_fwd_fp4_workspace_bytes(M, K, N)));
+    const Plan p = plan_dense(M, K, N);
     DenseArgs a{};
-    uint8_t* xc = static_cast<uint8_t*>(workspace);
-    uint8_t* xs = xc + code_bytes(M, K);
-    launch_pack(x, ldx, M, K, dtype, xc, xs, stream);
-    EL_TRY(check_launch(fn));
-    a.xc = xc, a.xs = xs, a.wc = w_codes, a.ws = w_scales, a.M = M, a.N = N, a.steps = static_cast<int>(steps_of(K));
+    a.x = x, a.ldx = ldx, a.wc = w_codes, a.ws = w_scales, a.M = M, a.N = N, a.K = K, a.steps = static_cast<int>(steps_of(K));
+    a.passes = p.passes, a.row_blocks = p.row_blocks;
     a.bias = bias, a.add = static_cast<const uint16_t*>(residual), a.ldadd = ldr;
     a.out = static_cast<uint16_t*>(y), a.ldo = ldy, a.act = act;
-    const dim3 grid(static_cast<unsigned>(ceil_div(M, 64) * ceil_div(N, 64)));
-    if (dtype == EL_BF16) hipLaunchKernelGGL((k_dense_fp4<BF16T>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((k_dense_fp4<F16T>), grid, dim3(kThreads), 0, stream, a);
+    if (p.packed) {
+      uint8_t* xc = static_cast<uint8_t*>(workspace);
+      uint8_t* xs = xc + code_bytes(M, K);
+      launch_pack(x, ldx, M, K, dtype, xc, xs, stream);
+      EL_TRY(check_launch(fn));
+      a.xc = xc, a.xs = xs;
+    }
+    if (dtype == EL_BF16) launch_dense<BF16T>(p, a, stream);
+    else launch_dense<F16T>(p, a, stream);
     return check_launch(fn);
   });
 }

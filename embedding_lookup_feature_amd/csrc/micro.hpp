@@ -101,11 +101,11 @@ inline int64_t pad_to(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 // Sizes of a packed [M][K] array whose rows are padded to `pad` columns.  (2^34 elements are 2^31
 // threads of eight.)
-inline el_status check_packed_sizes(const char* fn, int64_t M, int64_t K, int pad) {
+inline el_status check_packed_sizes(const char* fn, int64_t M, int64_t K, int pad, int pad_rows = 1) {
   if (M < 0) return bad(fn, "the number of rows must be >= 0");
   if (K < 1) return bad(fn, "K must be >= 1");
   if (K > kMaxMicroCols) return unsupported(fn, "K must be <= 2^20");
-  if (M * pad_to(K, pad) > (int64_t{1} << 34)) return unsupported(fn, "rows times padded columns must be <= 2^34");
+  if (pad_to(M, pad_rows) * pad_to(K, pad) > (int64_t{1} << 34)) return unsupported(fn, "padded rows times padded columns must be <= 2^34");
   return EL_OK;
 }
 inline el_status check_packed(const char* fn, const char* name, const void* codes, const void* scales, bool needed) {

@@ -89,11 +89,15 @@ EL_API el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64
  *   4 bits: e2m1 (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives), T = 6, two to a byte, the even
  *           column in the low half.  A block that holds a NaN or an infinity has the scale byte 255
  *           and stands for NaN altogether.
- * Columns behind the last are zeros up to the padded width, so rows hold whole blocks:
- *   8 bits: codes [M][Kp],   scales [M][Kp / 32],  Kp = K rounded up to 32
- *   4 bits: codes [M][Kp/2], scales [M][Kp / 32],  Kp = K rounded up to 128
- * Codes are 16-byte aligned, scales 4-byte aligned.  K from 1 to 2^20, M Kp <= 2^34
- * (EL_ERR_UNSUPPORTED beyond).
+ * Columns behind the last are zeros up to the padded width Kp, so rows hold whole blocks.
+ *   8 bits: codes [M][Kp], scales [M][Kp / 32], Kp = K rounded up to 32.
+ *   4 bits: in the order that the matrix instructions take, rows padded with zeros to 32, Kp = K
+ *           rounded up to 128 for the codes and to 512 for the scales.  Codes [M / 32][Kp / 128][2]
+ *           [64][16]: lane l of fragment i holds the 16 bytes of block l / 16 (of a step of 128
+ *           columns) of row 8 (l % 16 / 4) + 4 i + l % 4 (of 32).  Scales [M / 32][Kp / 512][2][64][4]:
+ *           the same lanes, their blocks' scales of four steps.
+ * Codes are 16-byte aligned, scales 4-byte aligned.  K from 1 to 2^20, padded rows times padded
+ * columns of codes <= 2^34 (EL_ERR_UNSUPPORTED beyond).
  */
 
 /* x [M] rows of stride ldx, K columns, of dtype -> 8 bits. */
@@ -140,7 +144,7 @@ EL_API el_status el_fp4_unpack(const uint8_t* codes, const uint8_t* scales, int3
                                int64_t ldy, el_dtype dtype, hipStream_t stream);
 
 /* [host, pure] Bytes of device workspace el_dense_fwd_fp4 can need; 0 for invalid or unsupported
- * sizes or M == 0. */
+ * sizes or M == 0, and where the rows are rounded within the product's launch. */
 EL_API size_t el_dense_fwd_fp4_workspace_bytes(int32_t M, int32_t K, int32_t N);
 
 /*

@@ -18,10 +18,35 @@ def vec(rng, n, base=0.0, scale=0.3):
 
 def codes_of(p, fp4):
     """(codes one per value, scale bytes) of a packed array, as int64 numpy arrays."""
-    c = p.codes.cpu().numpy().astype(np.int64)
+    c, s = (t.cpu().numpy().astype(np.int64) for t in (p.codes, p.scales))
     if fp4:
-        c = np.stack([c & 15, c >> 4], -1).reshape(c.shape[0], -1)
-    return c, p.scales.cpu().numpy().astype(np.int64)
+        c, s = rows_of_codes(np.stack([c & 15, c >> 4], -1)), rows_of_scales(s)
+        assert (c[p.rows:] == 0).all() and (c[:, -(-p.cols // 128) * 128:] == 0).all()
+        c, s = c[:p.rows], s[:p.rows, :c.shape[1] // 32]
+    return c, s
+
+
+def rows_of_codes(c):
+    """[tiles, steps, 2, 64, 16, 2] -> [rows, columns]: lane l of fragment i holds block l / 16 of row
+    8 (l % 16 / 4) + 4 i + l % 4."""
+    T, S = c.shape[:2]
+    return c.reshape(T, S, 2, 4, 4, 4, 32).transpose(0, 4, 2, 5, 1, 3, 6).reshape(T * 32, S * 128)
+
+
+def rows_of_scales(s):
+    T, S = s.shape[:2]
+    return s.reshape(T, S, 2, 4, 4, 4, 4).transpose(0, 4, 2, 5, 1, 6, 3).reshape(T * 32, S * 16)
+
+
+def codes_from_rows(c):
+    """The inverses for whole tiles."""
+    T, S = c.shape[0] // 32, c.shape[1] // 128
+    return c.reshape(T, 4, 2, 4, S, 4, 32).transpose(0, 4, 2, 5, 1, 3, 6).reshape(T, S, 2, 64, 16, 2)
+
+
+def scales_from_rows(s):
+    T, S = s.shape[0] // 32, s.shape[1] // 16
+    return s.reshape(T, 4, 2, 4, S, 4, 4).transpose(0, 4, 2, 6, 1, 3, 5).reshape(T, S, 2, 64, 4)
 
 
 def new(fp4, M, K):
@@ -95,16 +120,19 @@ def test_unpacking_every_code_and_scale():
     """All codes under all scale bytes, to every type (fp32 exactly, 16 bits rounded once)."""
     for fp4 in (False, True):
         n = 16 if fp4 else 256
-        K = 128
-        code = np.tile(np.arange(K) % n, (254 * (256 // K), 1)) if not fp4 else np.tile(np.arange(K) % n, (254, 1))
+        K = 512 if fp4 else 128
+        code = np.tile(np.arange(K) % n, (508 if not fp4 else 256, 1))
         if not fp4:
             code = (code + 128 * (np.arange(code.shape[0])[:, None] % 2)) % 256
         byte = np.repeat((np.arange(code.shape[0]) % 254 + 1)[:, None], K // 32, 1)
         M = code.shape[0]
         p = new(fp4, M, K)
-        raw = code[:, ::2] + 16 * code[:, 1::2] if fp4 else code
-        p.codes.copy_(torch.from_numpy(raw.astype(np.uint8)))
-        p.scales.copy_(torch.from_numpy(byte.astype(np.uint8)))
+        raw, rs = code, byte
+        if fp4:
+            raw, rs = codes_from_rows(code), scales_from_rows(byte)
+            raw = raw[..., 0] + 16 * raw[..., 1]
+        p.codes.copy_(torch.from_numpy(np.ascontiguousarray(raw).astype(np.uint8)))
+        p.scales.copy_(torch.from_numpy(np.ascontiguousarray(rs).astype(np.uint8)))
         sign = 8 if fp4 else 128
         mag = code % sign
         want = bp.values(np.where(code >= sign, mag + (8 if fp4 else 128), mag), byte, K, fp4)
@@ -391,6 +419,8 @@ DENSE_FP4 = [
     (4099, 479, 1001, 1, "f16", "relu", False, True), (9000, 256, 264, 0, "bf16", "gelu", True, True),
     (33_000, 40, 264, 0, "bf16", "silu", True, True), (2, 5000, 33, 0, "f16", "none", False, True),
     (40_000, 24, 1, 0, "bf16", "none", False, True), (64, 4096, 2048, 0, "bf16", "gelu", False, True),
+    (9_000, 4096, 520, 0, "bf16", "none", False, True), (8_300, 8_200, 520, 0, "bf16", "silu", True, True),
+    (8_200, 8_201, 515, 1, "f16", "none", False, False), (37, 70_000, 100, 0, "bf16", "none", True, True),
 ]
 
 
