@@ -5,12 +5,12 @@
 // (L lanes of a wavefront, or W whole wavefronts) owns a row: its columns stay in registers, eight
 // to a vector, NV vectors a lane, between the one read of the row and the one write.
 //
-// Two forms of each direction.  The aligned form (rows of whole, 16-byte aligned vectors, C <= 4096)
-// reaches memory through buffer descriptors of the rows at hand: an operand that is left out, a row
-// behind the last and a lane behind the last column all read zeros and write nothing, without a
-// branch, so the number of loads and stores in flight is known at every wait (they share one
-// in-order counter) and the next rows' loads stay in flight behind this row's arithmetic and stores.
-// The general form takes any alignment, width and stride with a branch around each access.
+// The kernels see their operands through views, of two kinds.  The aligned view (rows of whole,
+// 16-byte aligned vectors, C <= 4096) is a buffer descriptor of the rows at hand: an operand that is
+// left out, a row behind the last and a lane behind the last column all read zeros and write
+// nothing, without a branch, so the number of loads and stores in flight is known at every wait (they
+// share one in-order counter) and the next rows' loads stay in flight behind this row's arithmetic
+// and stores.  The loose view takes any alignment, width and stride with a branch around each access.
 #pragma once
 
 #include <algorithm>
@@ -19,10 +19,6 @@
 #include "tower_common.hpp"
 
 namespace el {
-namespace {
-
-constexpr int kMaxCols = 32768;
-constexpr int kMaxAlignedCols = 4096;  // wider rows do not fit the registers of the aligned form
 
 struct NormArgs {
   uint32_t post, pre, gate_act;
@@ -36,14 +32,15 @@ struct NormArgs {
   long ldx, ldf, ldg, ldy, ldh, lddy, lddh, lddx, lddf, lddg;
   float *post_stats, *pre_stats;
   int M, C;
-  // backward: units of rows that share a gate row
-  int chunk;        // rows of a unit
-  int per_gate;     // units of a gate row
-  int units;
-  float* gate_part;  // [units][C] where a gate row has several units
+  float* gate_part;  // [slots][2][C]: sums of the gate rows that a slot's rows begin and end in
   float* part;       // [grid][4][C]: the parameters' partial sums
   uint32_t want;     // bit k: parameter sum k is asked for
 };
+
+namespace {
+
+constexpr int kMaxCols = 32768;
+constexpr int kMaxAlignedCols = 4096;  // wider rows do not fit the registers of the aligned form
 
 // A slot: L lanes of one wavefront (W = 1), or W whole wavefronts (L = 64), NV vectors a lane.
 template <int L_, int W_, int NV_>
@@ -113,30 +110,9 @@ __device__ inline void load_vec(const float* p, float fill, int c, int n, float 
   }
 }
 
-template <class T, class SL>
-struct RowRaw {
-  Raw8<T> v[SL::NV];
-  __device__ inline void load(const void* base, long ld, long row, int c0, int C) {
-    const typename T::S* p = static_cast<const typename T::S*>(base) + row * ld;
-#pragma unroll
-    for (int j = 0; j < SL::NV; ++j) {
-      const int c = c0 + j * SL::L * SL::W * 8, n = C - c;
-      if (n > 0) v[j] = load8_raw<T>(p + c, n);
-      else
-#pragma unroll
-        for (int w = 0; w < Raw8<T>::W; ++w) v[j].v[w] = u32x4{0, 0, 0, 0};
-    }
-  }
-};
-
-template <class T, class SL>
-__device__ inline void store_row(void* base, long ld, long row, int c0, int C, const float (&v)[SL::NV][8]) {
-  typename T::S* p = static_cast<typename T::S*>(base) + row * ld;
-#pragma unroll
-  for (int j = 0; j < SL::NV; ++j) {
-    const int c = c0 + j * SL::L * SL::W * 8, n = C - c;
-    if (n > 0) store8<T>(p + c, v[j], n);
-  }
+// Row statistics are two fp32 numbers a row; absent ones read (0, 0) and are not written.
+__device__ inline __amdgpu_buffer_rsrc_t stats_span(const float* p, long first, int rows) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p) + first * 2, 0, p && rows > 0 ? rows * 8 : 0, 0x00027000);
 }
 
 // Mean and rstd of a slot's row (values past its end are zero).
@@ -193,42 +169,43 @@ __device__ inline u32x4 to_16bit(const float (&f)[8]) {
 }
 
 // ---------------------------------------------------------------------------------------
-// The aligned form's view of one operand's rows.
+// Views of one operand's rows: init() and at() fix this lane's slot's row of the view and its
+// columns, span() the rows that the view covers, load() and store() row `t` behind the slot's row.
 // ---------------------------------------------------------------------------------------
 constexpr uint32_t kNowhere = 0x80000000u;  // behind the end of every view (they are shorter than 2^31)
 constexpr int kStream = 2;                  // non-temporal: rows are read and written once
 
 template <class T, class SL>
-struct View {
+struct Aligned {
   static constexpr int ES = sizeof(typename T::S), STEP = SL::L * SL::W * 8 * ES;
+  typedef __amdgpu_buffer_rsrc_t Span;
   const char* base;
-  long row_bytes;
-  uint32_t voff[SL::NV];  // this lane's vectors: its slot's row of the view, its columns
+  int row_bytes;
+  uint32_t voff[SL::NV];
   __device__ inline void init(const void* p, long ld, long slot_row, int c0, int C) {
     base = static_cast<const char*>(p);
-    row_bytes = ld * ES;
+    row_bytes = static_cast<int>(ld * ES);
     at(slot_row, c0, C);
   }
   __device__ inline void at(long slot_row, int c0, int C) {
 #pragma unroll
     for (int j = 0; j < SL::NV; ++j)
-      voff[j] = c0 + j * SL::L * SL::W * 8 < C ? static_cast<uint32_t>(slot_row * row_bytes) + c0 * ES + j * STEP : kNowhere;
+      voff[j] = c0 + j * SL::L * SL::W * 8 < C ? static_cast<uint32_t>(slot_row) * row_bytes + c0 * ES + j * STEP : kNowhere;
   }
   // `rows` rows from row `first` on (0: nothing there), C columns of the last.
-  __device__ inline auto rsrc(long first, int rows, int C) const {
-    const int bytes = base && rows > 0 ? static_cast<int>((rows - 1) * row_bytes) + C * ES : 0;
+  __device__ inline Span span(long first, int rows, int C) const {
+    const int bytes = base && rows > 0 ? (rows - 1) * row_bytes + C * ES : 0;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base) + first * row_bytes, 0, bytes, 0x00027000);
   }
-  template <class R>
-  __device__ inline void load(R rs, Raw8<T> (&raw)[SL::NV], uint32_t more = 0) const {
+  __device__ inline uint32_t place(int j, int t, bool valid) const { return valid ? voff[j] + static_cast<uint32_t>(t) * row_bytes : kNowhere; }
+  __device__ inline void load(Span rs, Raw8<T> (&raw)[SL::NV], int t = 0, bool valid = true) const {
 #pragma unroll
     for (int j = 0; j < SL::NV; ++j)
 #pragma unroll
       for (int w = 0; w < Raw8<T>::W; ++w)
-        raw[j].v[w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff[j] + more + 16 * w, 0, kStream));
+        raw[j].v[w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, place(j, t, valid) + 16 * w, 0, kStream));
   }
-  template <class R>
-  __device__ inline void store(R rs, const float (&v)[SL::NV][8], uint32_t more = 0) const {
+  __device__ inline void store(Span rs, const float (&v)[SL::NV][8], int t = 0, bool valid = true) const {
 #pragma unroll
     for (int j = 0; j < SL::NV; ++j) {
       u32x4 q[Raw8<T>::W];
@@ -239,7 +216,45 @@ struct View {
         q[0] = to_16bit<T>(v[j]);
       }
 #pragma unroll
-      for (int w = 0; w < Raw8<T>::W; ++w) __builtin_amdgcn_raw_buffer_store_b128(q[w], rs, voff[j] + more + 16 * w, 0, kStream);
+      for (int w = 0; w < Raw8<T>::W; ++w) __builtin_amdgcn_raw_buffer_store_b128(q[w], rs, place(j, t, valid) + 16 * w, 0, kStream);
+    }
+  }
+};
+
+template <class T, class SL>
+struct Loose {
+  typedef typename T::S S;
+  struct Span {
+    S* p;
+    int rows;
+  };
+  S* base;
+  long ld;
+  long row;
+  int c, cols;
+  __device__ inline void init(const void* p, long ld_, long slot_row, int c0, int C) {
+    base = static_cast<S*>(const_cast<void*>(p));
+    ld = ld_, row = slot_row, c = c0, cols = C;
+  }
+  __device__ inline void at(long slot_row, int, int) { row = slot_row; }
+  __device__ inline Span span(long first, int rows, int) const { return Span{base ? base + first * ld : nullptr, rows}; }
+  __device__ inline void load(Span s, Raw8<T> (&raw)[SL::NV], int t = 0, bool valid = true) const {
+    const S* p = s.p + (row + t) * ld;
+#pragma unroll
+    for (int j = 0; j < SL::NV; ++j) {
+      const int cj = c + j * SL::L * SL::W * 8;
+      if (s.p && valid && row + t < s.rows && cj < cols) raw[j] = load8_raw<T>(p + cj, cols - cj);
+      else
+#pragma unroll
+        for (int w = 0; w < Raw8<T>::W; ++w) raw[j].v[w] = u32x4{0, 0, 0, 0};
+    }
+  }
+  __device__ inline void store(Span s, const float (&v)[SL::NV][8], int t = 0, bool valid = true) const {
+    S* p = s.p + (row + t) * ld;
+#pragma unroll
+    for (int j = 0; j < SL::NV; ++j) {
+      const int cj = c + j * SL::L * SL::W * 8;
+      if (s.p && valid && row + t < s.rows && cj < cols) store8<T>(p + cj, v[j], cols - cj);
     }
   }
 };
@@ -258,6 +273,7 @@ __device__ inline void load_param(const float* p, float fill, int c0, int C, flo
 // Host side.
 // ---------------------------------------------------------------------------------------
 constexpr int kCus = 256;
+
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -313,11 +329,18 @@ NormArgs common(const el_block_norm* p, int M, int C) {
 }
 
 
-// An operand as the aligned form takes it: absent, or rows of 16-byte aligned vectors so close that
-// `rows` of them span less than 2^31 bytes.
+// An operand as the aligned view takes it: absent, or rows of 16-byte aligned vectors so close that
+// `rows` of them span less than 2^30 bytes.
 bool aligned_rows(const void* p, int64_t ld, size_t elem, int64_t rows) {
   return !p || (tower::al(p, 16) && ld * static_cast<int64_t>(elem) % 16 == 0 && ld * static_cast<int64_t>(elem) < (int64_t{1} << 30) / rows);
 }
 
 }  // namespace
+
+// One direction's launch for a type of data, each in a source file of its own (dozens of kernels).
+template <class T>
+void launch_norm_fwd(const NormArgs& a, bool aligned, hipStream_t st);
+template <class T>
+void launch_norm_bwd(const NormArgs& a, bool aligned, bool shared, int grid, hipStream_t st);
+
 }  // namespace el

@@ -1,0 +1,329 @@
+// block_norm_bwd.hpp -- the block norm's backward: gradients of both norms' inputs, of the gate and
+// of the parameters in one pass over the rows (formulas in embblock.h).
+#pragma once
+
+#include "block_norm.hpp"
+
+namespace el {
+namespace {
+
+// Gradient at a norm's input from g, the one at its output (gamma in it), and the normalised row.
+template <class SL>
+__device__ inline void norm_grad(float (&g)[SL::NV][8], const float (&vh)[SL::NV][8], uint32_t kind, float rstd,
+                                 const NormArgs& a, float (*lds)[SL::W][2], int& turn) {
+  float s[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < SL::NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0] = fmaf(g[j][e], vh[j][e], s[0]), s[1] += g[j][e];
+  slot_sums<SL>(s, lds, turn);
+  const float m2 = s[0] * a.inv_c, m1 = kind == EL_NORM_LAYER ? s[1] * a.inv_c : 0.f;
+#pragma unroll
+  for (int j = 0; j < SL::NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[j][e] = (fmaf(-vh[j][e], m2, g[j][e]) - m1) * rstd;
+}
+
+// Rows [first, first + n) of slot s where M rows are dealt out to `slots` slots in order.
+struct RowRange {
+  int first, n;
+};
+__host__ __device__ inline RowRange rows_of_slot(int s, int slots, int M) {
+  const int base = M / slots, rem = M - base * slots;
+  return RowRange{s * base + (s < rem ? s : rem), base + (s < rem)};
+}
+__device__ inline int slot_of_row(int r, int slots, int M) {
+  const int base = M / slots, rem = M - base * slots, wide = rem * (base + 1);
+  return r < wide ? r / (base + 1) : rem + (r - wide) / base;
+}
+
+// SHARED: rows share gate rows, so a slot takes a run of consecutive rows (all slots the same number
+// within one, whatever the number of rows that share) and adds up the gate's gradient over the gate
+// rows in it: one that lies in the run is finished here, the others are left as partial sums
+// (gate_part[slot][0] where the gate row began before this slot, [1] where it begins here).  Not
+// SHARED: a workgroup's slots take consecutive rows, and every row has its own gate row, if any.
+template <class T, class SL, template <class, class> class View, bool SHARED, bool BETA>
+__global__ __launch_bounds__(SL::THREADS, SL::THREADS > 256 ? 4 : SL::NV > 1 ? 2 : 3) void k_norm_bwd(NormArgs a) {
+  __shared__ float lds[2][SL::W][2];
+  __shared__ float join[SL::PER_WG > 1 ? SL::THREADS * SL::NV * 8 : 1];
+  int turn = 0;
+  constexpr int NV = SL::NV, PER = SL::PER_WG;
+  const int in_slot = threadIdx.x % (SL::L * SL::W), c0 = in_slot * 8, sl = threadIdx.x / (SL::L * SL::W);
+  const int slots = gridDim.x * PER, slot = blockIdx.x * PER + sl;
+  // the rows of this workgroup's first slot and of this slot
+  const RowRange wg = rows_of_slot(blockIdx.x * PER, slots, a.M), mine = rows_of_slot(slot, slots, a.M);
+  const int local = SHARED ? mine.first - wg.first : sl;
+  const int steps = SHARED ? wg.n : static_cast<int>(max(0l, (static_cast<long>(a.M) - blockIdx.x * PER + slots - 1) / slots));
+  View<T, SL> vdy, vdh, vy, vf, vg, vdx, vdf, vdg;
+  vdy.init(a.dy, a.lddy, local, c0, a.C), vdh.init(a.dh, a.lddh, local, c0, a.C), vy.init(a.y_in, a.ldy, local, c0, a.C);
+  vf.init(a.f, a.ldf, local, c0, a.C), vdx.init(a.dx, a.lddx, local, c0, a.C), vdf.init(a.df, a.lddf, local, c0, a.C);
+  float gp[NV][8], gq[NV][8], bp[BETA ? NV : 1][8];
+  load_param<SL>(a.gp, 1.f, c0, a.C, gp);
+  load_param<SL>(a.gq, 1.f, c0, a.C, gq);
+  if constexpr (BETA) load_param<SL>(a.bp, 0.f, c0, a.C, bp);
+  float acc_gp[NV][8] = {}, acc_gq[NV][8] = {}, acc_bp[BETA ? NV : 1][8] = {}, acc_bq[BETA ? NV : 1][8] = {};
+
+  // the gate
+  float g[NV][8], gsum[NV][8] = {};
+  Raw8<T> rg[NV];
+  int grow = 0, left = 0;  // SHARED: gate row of the current row, rows of it left in this slot's run
+  const int g0 = SHARED ? wg.first / a.gate_rows : 0, gates = SHARED ? (a.M + a.gate_rows - 1) / a.gate_rows : 0;
+  const auto gate_values = [&]() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      to_floats<T>(rg[j], g[j]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[j][e] = a.gate ? (a.gate_act == EL_GATE_SIGMOID ? sigmoid(g[j][e]) : g[j][e]) : 1.f;
+    }
+  };
+  const auto through_gate = [&](float (&v)[NV][8]) {  // times the derivative of its activation
+    if (a.gate_act == EL_GATE_SIGMOID)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= g[j][e] * (1.f - g[j][e]);
+  };
+  const int span_gates = SHARED ? min(gates - g0, PER * wg.n + 1) : 0;  // those of the workgroup's rows
+  if constexpr (SHARED) {
+    grow = mine.first / a.gate_rows;
+    left = static_cast<int>(min((grow + 1l) * a.gate_rows, static_cast<long>(mine.first) + mine.n) - mine.first);
+    vg.init(a.gate, a.ldg, grow - g0, c0, a.C), vdg.init(a.dgate, a.lddg, grow - g0, c0, a.C);
+    vg.load(vg.span(g0, span_gates, a.C), rg, 0, mine.n > 0);
+    gate_values();
+  } else {
+    vg.init(a.gate, a.ldg, sl, c0, a.C), vdg.init(a.dgate, a.lddg, sl, c0, a.C);
+  }
+
+  Raw8<T> rdy[NV], rdh[NV], ry[NV], rf[NV];
+  u32x2 spre, spost;
+  const auto first_of = [&](int t) { return SHARED ? static_cast<long>(wg.first) : static_cast<long>(t) * slots + blockIdx.x * PER; };
+  const auto rows_at = [&](int t) {
+    if constexpr (SHARED) return min(a.M - wg.first, PER * wg.n);
+    else return static_cast<int>(max(0l, min(static_cast<long>(PER), a.M - first_of(t))));
+  };
+  const auto valid_at = [&](int t) { return !SHARED || t < mine.n; };
+  const auto fetch = [&](int t) {
+    const long first = first_of(t);
+    const int rows = rows_at(t), tt = SHARED ? t : 0;
+    const bool ok = valid_at(t);
+    vdy.load(vdy.span(first, rows, a.C), rdy, tt, ok);
+    vdh.load(vdh.span(first, rows, a.C), rdh, tt, ok);
+    vy.load(vy.span(first, a.dh ? rows : 0, a.C), ry, tt, ok);
+    vf.load(vf.span(first, rows, a.C), rf, tt, ok);
+    if constexpr (!SHARED) vg.load(vg.span(first, rows, a.C), rg);
+    const uint32_t at = ok ? static_cast<uint32_t>(local + tt) * 8u : kNowhere;
+    spre = __builtin_amdgcn_raw_buffer_load_b64(stats_span(a.pre_stats, first, rows), at, 0, 0);
+    spost = __builtin_amdgcn_raw_buffer_load_b64(stats_span(a.post_stats, first, rows), at, 0, 0);
+  };
+  fetch(0);
+  for (int t = 0; t < steps; ++t) {
+    const long first = first_of(t);
+    const int rows = rows_at(t), tt = SHARED ? t : 0;
+    const bool ok = valid_at(t);
+    float D[NV][8], v[NV][8], fh[NV][8], dy[NV][8];
+    const float mq = __uint_as_float(spre[0]), rq = __uint_as_float(spre[1]);
+    const float mp = a.post != EL_NORM_NONE ? __uint_as_float(spost[0]) : 0.f;
+    const float rp = a.post != EL_NORM_NONE ? __uint_as_float(spost[1]) : 1.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      to_floats<T>(rdh[j], D[j]), to_floats<T>(ry[j], v[j]), to_floats<T>(rf[j], fh[j]), to_floats<T>(rdy[j], dy[j]);
+    if constexpr (!SHARED) gate_values();
+    fetch(t + 1);
+    if (a.dh) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[j][e] = (v[j][e] - mq) * rq;
+          acc_gq[j][e] = fmaf(D[j][e], v[j][e], acc_gq[j][e]);
+          if constexpr (BETA) acc_bq[j][e] += D[j][e];
+          D[j][e] *= gq[j][e];
+        }
+      norm_grad<SL>(D, v, a.pre, rq, a, lds, turn);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) D[j][e] += dy[j][e];
+    vdx.store(vdx.span(first, rows, a.C), D, tt, ok);
+    if (a.f) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          fh[j][e] = (fh[j][e] - mp) * rp;
+          const float sD = a.scale * D[j][e];
+          float tv;
+          if constexpr (BETA) tv = fmaf(fh[j][e], gp[j][e], bp[j][e]);
+          else tv = fh[j][e] * gp[j][e];
+          if constexpr (SHARED) gsum[j][e] = fmaf(sD, tv, gsum[j][e]);
+          else gsum[j][e] = sD * tv;
+          const float u = g[j][e] * sD;
+          acc_gp[j][e] = fmaf(u, fh[j][e], acc_gp[j][e]);
+          if constexpr (BETA) acc_bp[j][e] += u;
+          D[j][e] = u * gp[j][e];
+        }
+      if (a.df && a.post != EL_NORM_NONE) norm_grad<SL>(D, fh, a.post, rp, a, lds, turn);
+    }
+    vdf.store(vdf.span(first, rows, a.C), D, tt, ok);
+    if constexpr (!SHARED) {
+      through_gate(gsum);
+      vdg.store(vdg.span(first, rows, a.C), gsum);
+    } else if (ok && --left == 0) {
+      // the last row of this gate row in the run
+      const long gfirst = static_cast<long>(grow) * a.gate_rows, row = static_cast<long>(mine.first) + t;
+      const bool begins = gfirst >= mine.first, ends = row + 1 == min(gfirst + a.gate_rows, static_cast<long>(a.M));
+      if (a.dgate) {
+        if (begins && ends) {
+          through_gate(gsum);
+          vdg.store(vdg.span(g0, span_gates, a.C), gsum);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            const int c = c0 + j * SL::L * SL::W * 8;
+            if (c < a.C) store8<F32T>(a.gate_part + (2l * slot + begins) * a.C + c, gsum[j], a.C - c);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gsum[j][e] = 0.f;
+      ++grow;
+      left = static_cast<int>(min((grow + 1l) * a.gate_rows, static_cast<long>(mine.first) + mine.n) - (row + 1));
+      vg.at(grow - g0, c0, a.C), vdg.at(grow - g0, c0, a.C);
+      if (left > 0) {
+        vg.load(vg.span(g0, span_gates, a.C), rg);
+        gate_values();
+      }
+    }
+  }
+  // The workgroup's sums of each asked parameter: its slots' added in slot order.
+  const auto put = [&](int k, const float (&acc)[NV][8]) {
+    if (!(a.want >> k & 1)) return;
+    float* out = a.part + (static_cast<long>(blockIdx.x) * 4 + k) * a.C;
+    if constexpr (PER == 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * SL::L * SL::W * 8;
+        if (c < a.C) store8<F32T>(out + c, acc[j], a.C - c);
+      }
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) join[sl * SL::COLS + c0 + j * SL::L * 8 + e] = acc[j][e];
+      __syncthreads();
+      for (int c = threadIdx.x; c < SL::COLS && c < a.C; c += SL::THREADS) {
+        float s = join[c];
+        for (int p = 1; p < PER; ++p) s += join[p * SL::COLS + c];
+        out[c] = s;
+      }
+    }
+  };
+  put(0, acc_gp);
+  put(2, acc_gq);
+  if constexpr (BETA) put(1, acc_bp), put(3, acc_bq);
+}
+
+// dgate of the gate rows that lie in several slots: their partial sums in slot order, times the
+// gate's derivative.  A thread takes eight columns of a gate row (few partial sums a row).
+template <class T>
+__device__ inline void finish_gate(const NormArgs& a, long r, int c, float (&v)[8]) {
+  if (a.gate_act == EL_GATE_SIGMOID) {
+    float g[8];
+    to_floats<T>(load8_raw<T>(static_cast<const typename T::S*>(a.gate) + r * a.ldg + c, a.C - c), g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float s = sigmoid(g[e]);
+      v[e] *= s * (1.f - s);
+    }
+  }
+  store8<T>(static_cast<typename T::S*>(a.dgate) + r * a.lddg + c, v, a.C - c);
+}
+template <class T>
+__global__ __launch_bounds__(256) void k_join_gate(NormArgs a, int gates, int slots) {
+  const int vecs = (a.C + 7) / 8;
+  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  const long r = i / vecs;
+  if (r >= gates) return;
+  const int c = static_cast<int>(i - r * vecs) * 8;
+  const int s0 = slot_of_row(static_cast<int>(r * a.gate_rows), slots, a.M);
+  const int s1 = slot_of_row(static_cast<int>(min((r + 1) * a.gate_rows, static_cast<long>(a.M)) - 1), slots, a.M);
+  if (s0 == s1) return;
+  float v[8];
+  to_floats<F32T>(load8_raw<F32T>(a.gate_part + (2l * s0 + 1) * a.C + c, a.C - c), v);
+  for (int s = s0 + 1; s <= s1; ++s) {
+    float p[8];
+    to_floats<F32T>(load8_raw<F32T>(a.gate_part + 2l * s * a.C + c, a.C - c), p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += p[e];
+  }
+  finish_gate<T>(a, r, c, v);
+}
+// The same where a gate row lies in many slots: a workgroup takes eight columns of a gate row, thread
+// p the slots s0 + p, s0 + p + 256, ...; the threads' sums are added by halves.
+template <class T>
+__global__ __launch_bounds__(256) void k_join_gate_long(NormArgs a, int slots) {
+  __shared__ float red[256][9];
+  const int vecs = (a.C + 7) / 8;
+  const long r = blockIdx.x / vecs;
+  const int c = static_cast<int>(blockIdx.x - r * vecs) * 8, p = threadIdx.x;
+  const int s0 = slot_of_row(static_cast<int>(r * a.gate_rows), slots, a.M);
+  const int s1 = slot_of_row(static_cast<int>(min((r + 1) * a.gate_rows, static_cast<long>(a.M)) - 1), slots, a.M);
+  if (s0 == s1) return;
+  float v[8] = {};
+  for (int s = s0 + p; s <= s1; s += 256) {
+    float q[8];
+    to_floats<F32T>(load8_raw<F32T>(a.gate_part + (2l * s + (s == s0)) * a.C + c, a.C - c), q);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += q[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[p][e] = v[e];
+  for (int h = 128; h > 0; h >>= 1) {
+    __syncthreads();
+    if (p < h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) red[p][e] += red[p + h][e];
+  }
+  if (p == 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = red[0][e];
+    finish_gate<T>(a, r, c, v);
+  }
+}
+
+template <class T, class SL, template <class, class> class View, bool BETA>
+void launch_one_bwd(const NormArgs& a, bool shared, int grid, hipStream_t st) {
+  if (shared) hipLaunchKernelGGL((k_norm_bwd<T, SL, View, true, BETA>), dim3(grid), dim3(SL::THREADS), 0, st, a);
+  else hipLaunchKernelGGL((k_norm_bwd<T, SL, View, false, BETA>), dim3(grid), dim3(SL::THREADS), 0, st, a);
+}
+
+}  // namespace
+
+template <class T>
+void launch_norm_bwd(const NormArgs& a, bool aligned, bool shared, int grid, hipStream_t st) {
+  with_slot(a.C, [&](auto s) {
+    using SL = decltype(s);
+    if constexpr (SL::COLS <= kMaxAlignedCols) {
+      if (aligned) {
+        if (a.bp || (a.want & 10u)) launch_one_bwd<T, SL, Aligned, true>(a, shared, grid, st);
+        else launch_one_bwd<T, SL, Aligned, false>(a, shared, grid, st);
+        return;
+      }
+    }
+    launch_one_bwd<T, SL, Loose, true>(a, shared, grid, st);
+  });
+  if (!shared || !a.dgate) return;
+  int per = 1;
+  with_slot(a.C, [&](auto s) { per = decltype(s)::PER_WG; });
+  const int slots = grid * per, gates = static_cast<int>(ceil_div(a.M, a.gate_rows));
+  const long vecs = (a.C + 7) / 8;
+  // a gate row in more than 16 slots is worth a workgroup
+  if (slots / gates > 16) hipLaunchKernelGGL((k_join_gate_long<T>), dim3(static_cast<unsigned>(gates * vecs)), dim3(256), 0, st, a, slots);
+  else hipLaunchKernelGGL((k_join_gate<T>), dim3(static_cast<unsigned>(ceil_div(gates * vecs, 256))), dim3(256), 0, st, a, gates, slots);
+}
+
+}  // namespace el

@@ -1,0 +1,6 @@
+// block_norm_bwd_bf16.hip -- the block norm's backward kernels for one type of data.
+#include "block_norm_bwd.hpp"
+
+namespace el {
+template void launch_norm_bwd<BF16T>(const NormArgs&, bool, bool, int, hipStream_t);
+}
