@@ -15,8 +15,7 @@
 
 #include <algorithm>
 
-#include "embblock.h"
-#include "tower_common.hpp"
+#include "micro.hpp"
 
 namespace el {
 
@@ -149,24 +148,6 @@ __device__ inline void row_stats(const float (&v)[SL::NV][8], uint32_t kind, con
 }
 
 __device__ inline float gate_value(uint32_t act, float u) { return act == EL_GATE_SIGMOID ? sigmoid(u) : u; }
-
-// Eight values as four words, two to a word in one conversion.
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-template <class T>
-__device__ inline u32x4 to_16bit(const float (&f)[8]) {
-  u32x4 a;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f32x2 p = {f[2 * i], f[2 * i + 1]};
-    uint32_t w;
-    if constexpr (T::code == EL_BF16) w = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
-    else w = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, f16x2));
-    a[i] = w;
-  }
-  return a;
-}
 
 // ---------------------------------------------------------------------------------------
 // Views of one operand's rows: init() and at() fix this lane's slot's row of the view and its

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_act(ActArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = keep_of(bits, e, a.drop.top) ? v[e] * a.drop.scale : 0.f;
   }
-  store8<T>(static_cast<S*>(a.y) + row * a.ldy + grp * 8l, v, n);
+  put_whole8<T>(static_cast<S*>(a.y) + row * a.ldy + grp * 8l, v, n);
 }
 
 template <class F>

@@ -7,8 +7,6 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 constexpr int kThreads = 256;
@@ -81,21 +79,6 @@ __device__ inline u32x4 lanes_from(int from, const u32x4& v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(from * 4, static_cast<int>(v[i])));
   return r;
-}
-
-// Two values to a word in one conversion.
-template <class T>
-__device__ inline u32x4 to_16bit(const float (&f)[8]) {
-  u32x4 a;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f32x2 p = {f[2 * i], f[2 * i + 1]};
-    uint32_t w;
-    if constexpr (T::code == EL_BF16) w = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
-    else w = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, f16x2));
-    a[i] = w;
-  }
-  return a;
 }
 
 __device__ inline void store8_raw(uint16_t* p, const u32x4& v, int n) {
@@ -174,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void k_fp4_unpack(UnpackArgs a) {
   float v[8];
   unpack4(*reinterpret_cast<const uint32_t*>(a.codes + code_at(row, k, q, a.steps)),
           a.scales[scale_at(row, k, q >> 2, (a.steps + 3) / 4)], v);
-  store8<T>(static_cast<typename T::S*>(a.y) + row * a.ldy + grp * 8l, v, a.K - static_cast<int>(grp) * 8);
+  put_whole8<T>(static_cast<typename T::S*>(a.y) + row * a.ldy + grp * 8l, v, a.K - static_cast<int>(grp) * 8);
 }
 
 // ---------------------------------------------------------------------------------------

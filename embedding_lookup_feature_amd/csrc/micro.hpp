@@ -10,6 +10,23 @@ namespace el {
 constexpr int kMicroBlock = 32;
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+// Eight values as four words, two to a word in one conversion.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+template <class T>
+__device__ inline u32x4 to_16bit(const float (&f)[8]) {
+  u32x4 a;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 p = {f[2 * i], f[2 * i + 1]};
+    uint32_t w;
+    if constexpr (T::code == EL_BF16) w = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+    else w = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, f16x2));
+    a[i] = w;
+  }
+  return a;
+}
+
 // 2^e of a scale byte e + 127 (1 .. 254); 255 (NaN) gives infinity.
 __device__ inline float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
@@ -61,10 +78,10 @@ __device__ inline Codes8 pack8(const float (&v)[8], uint32_t& byte) {
   return Codes8{static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
 }
 __device__ inline void unpack8(uint32_t lo, uint32_t hi, float scale, float (&v)[8]) {
-  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), true);
-  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(hi), false), d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(hi), true);
-  v[0] = a[0] * scale, v[1] = a[1] * scale, v[2] = b[0] * scale, v[3] = b[1] * scale;
-  v[4] = c[0] * scale, v[5] = c[1] * scale, v[6] = d[0] * scale, v[7] = d[1] * scale;
+  // (the conversion multiplies by the scale)
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, scale, false), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, scale, true);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, scale, false), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, scale, true);
+  v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
 }
 
 // The same in 4 bits: eight codes in one word.
@@ -87,11 +104,25 @@ __device__ inline uint32_t pack4(const float (&v)[8], uint32_t& byte) {
   return q;
 }
 __device__ inline void unpack4(uint32_t q, uint32_t byte, float (&v)[8]) {
-  const float scale = byte == 255u ? __uint_as_float(0x7fc00000u) : scale_of(byte);
-  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
-  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
-  v[0] = a[0] * scale, v[1] = a[1] * scale, v[2] = b[0] * scale, v[3] = b[1] * scale;
-  v[4] = c[0] * scale, v[5] = c[1] * scale, v[6] = d[0] * scale, v[7] = d[1] * scale;
+  const float scale = scale_of(byte);
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 1);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 3);
+  v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
+  if (byte == 255u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(0x7fc00000u);
+}
+
+// The first n of eight values, a whole vector in 16-bit pairs.
+template <class T>
+__device__ inline void put_whole8(typename T::S* p, const float (&v)[8], int n) {
+  if constexpr (sizeof(typename T::S) == 2) {
+    if (n >= 8) {
+      *reinterpret_cast<u32x4_any*>(p) = to_16bit<T>(v);
+      return;
+    }
+  }
+  store8<T>(p, v, n);
 }
 
 namespace tower {
