@@ -1,25 +1,35 @@
 // dense_ckpt.hip -- a dense layer's backward with its input and the pre-activation of the layer
 // below read from 8 bits:  dw = dz^T xq,  dx = dz w + dres,  dzb = drop(dx act'(preq)).
+//
+// The tiles of dense_tile.hpp, with two changes.  The data gradient's epilogue reads half the bytes
+// for the pre-activation.  The weight gradient's 256 x 256 tiles take x's codes through registers,
+// where the conversion to 16 bits applies the scale, to the LDS places that direct loads would fill.
+// Smaller tiles, whose batches are small, take a 16-bit copy that shares a launch with the copies of
+// unaligned operands.
 #include "dense_tile.hpp"
-#include "micro.hpp"
 
 namespace el {
 namespace {
 
-// Codes to 16-bit rows of `groups` whole vectors (x and pre in one launch).
+// Codes to 16-bit rows of whole vectors.
 struct UnpackJob {
   const uint8_t *codes, *scales;
   uint16_t* dst;
+  long items;
+  unsigned blocks;  // 0: nothing to copy
 };
 template <class T>
-__global__ __launch_bounds__(256) void k_unpack16(UnpackJob a, UnpackJob b, long items) {
-  const UnpackJob j = blockIdx.y ? b : a;
-  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= items) return;
-  const uint2 q = reinterpret_cast<const uint2*>(j.codes)[i];
+__global__ __launch_bounds__(256) void k_copies(PackJob a, PackJob b, UnpackJob x) {
+  unsigned blk = blockIdx.x;
+  if (blk < a.blocks) return pack_rows(a, blk);
+  blk -= a.blocks;
+  if (blk < b.blocks) return pack_rows(b, blk);
+  const long i = static_cast<long>(blk - b.blocks) * 256 + threadIdx.x;
+  if (i >= x.items) return;
+  const uint2 q = reinterpret_cast<const uint2*>(x.codes)[i];
   float v[8];
-  unpack8(q.x, q.y, scale_of(j.scales[i >> 2]), v);
-  store8<T>(j.dst + i * 8, v, 8);
+  unpack8(q.x, q.y, scale_of(x.scales[i >> 2]), v);
+  reinterpret_cast<u32x4*>(x.dst)[i] = to_16bit<T>(v);
 }
 
 long padded(long K) { return tower::pad_to(K, kMicroBlock); }
@@ -29,19 +39,25 @@ template <class T>
 el_status run(const char* fn, const uint8_t* xc, const uint8_t* xs, int M, int K, const uint16_t* w, int N,
               const uint16_t* dz, long lddz, GemmArgs a, const uint8_t* pc, const uint8_t* ps, float* dw, float* db,
               char* ws, hipStream_t st) {
-  const long items = M * padded(K) / 8;
-  UnpackJob jx{xc, xs, reinterpret_cast<uint16_t*>(ws)}, jp{pc, ps, reinterpret_cast<uint16_t*>(ws + unpacked_bytes(M, K))};
-  ws += 2 * unpacked_bytes(M, K);
-  hipLaunchKernelGGL((k_unpack16<T>), dim3(static_cast<unsigned>(ceil_div(items, 256)), pc ? 2 : 1), dim3(256), 0, st, jx, jp, items);
-  EL_TRY(check_launch(fn));
+  const WgradPlan pl = plan_wgrad(M, K, N, wgrad_shares(M, K, a.out));
+  UnpackJob jx{xc, xs, reinterpret_cast<uint16_t*>(ws), 0, 0};
+  if (!reads_codes(pl.shape)) {
+    jx.items = M * padded(K) / 8;
+    jx.blocks = static_cast<unsigned>(ceil_div(jx.items, 256));
+    ws += unpacked_bytes(M, K);
+  }
   Packs packs;
   packs.add(&dz, &lddz, M, N, &ws);
   long ldw = K;
   if (a.out) packs.add(&w, &ldw, N, K, &ws);
-  EL_TRY(packs.run(fn, st));
-  const WgradPlan pl = plan_wgrad(M, K, N, wgrad_shares(M, K, a.out));
+  const long blocks = static_cast<long>(packs.job[0].blocks) + packs.job[1].blocks + jx.blocks;
+  if (blocks >= (1l << 24)) return tower::unsupported(fn, "copied operands of more than 2^35 elements");
+  if (blocks > 0) {
+    hipLaunchKernelGGL((k_copies<T>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, packs.job[0], packs.job[1], jx);
+    EL_TRY(check_launch(fn));
+  }
   GemmArgs b{};
-  b.P = dz, b.ldp = lddz, b.Q = jx.dst, b.ldq = padded(K), b.R = N, b.C = K, b.red = b.red_q = M, b.per_split = pl.per;
+  b.P = dz, b.ldp = lddz, b.Q = jx.dst, b.ldq = padded(K), b.codes = xc, b.scales = xs, b.kp = padded(K), b.R = N, b.C = K, b.red = b.red_q = M, b.per_split = pl.per;
   b.part = pl.splits > 1 ? reinterpret_cast<float*>(ws) : dw;
   float* dbp = reinterpret_cast<float*>(ws + pl.dw_bytes);
   b.dbp = db ? dbp : nullptr;
@@ -49,10 +65,10 @@ el_status run(const char* fn, const uint8_t* xc, const uint8_t* xs, int M, int K
     a.P = dz, a.ldp = lddz, a.Q = w, a.ldq = ldw, a.R = M, a.C = K;
     a.red = a.per_split = static_cast<int>(pad8(N));
     a.red_q = N;
-    if (pc) a.pre = jp.dst, a.ldpre = padded(K);
-    EL_TRY(launch_backward<T>(fn, a, plan_tiles(M, K), b, pl.shape, pl.splits, st));
+    a.codes = pc, a.scales = ps, a.kp = padded(K);
+    EL_TRY((launch_backward<T, true>(fn, a, plan_tiles(M, K), b, pl.shape, pl.splits, st)));
   } else {
-    EL_TRY((launch_product<T, WGRAD>(fn, b, pl.shape, pl.splits, st)));
+    EL_TRY((launch_product<T, WGRAD, true>(fn, b, pl.shape, pl.splits, st)));
   }
   launch_sums(Sums{b.part, dw, pl.splits > 1 ? static_cast<long>(N) * K : 0, pl.splits},
               Sums{dbp, db, db ? static_cast<long>(N) : 0, pl.db_rows}, st);
@@ -68,8 +84,12 @@ extern "C" {
 
 size_t el_dense_bwd_ckpt_workspace_bytes(int32_t M, int32_t K, int32_t N) {
   if (!dense_sizes_ok(M, K, N) || M * padded(K) > (int64_t{1} << 34)) return 0;
-  return 2 * unpacked_bytes(M, K) + packed_bytes(M, N) + packed_bytes(N, K) +
-         std::max(plan_wgrad(M, K, N, false).bytes, plan_wgrad(M, K, N, true).bytes);
+  size_t most = 0;
+  for (bool shared : {false, true}) {
+    const WgradPlan p = plan_wgrad(M, K, N, shared);
+    most = std::max(most, p.bytes + (reads_codes(p.shape) ? 0 : unpacked_bytes(M, K)));
+  }
+  return most + packed_bytes(M, N) + packed_bytes(N, K);
 }
 
 el_status el_dense_bwd_ckpt(const uint8_t* x_codes, const uint8_t* x_scales, int32_t M, int32_t K, const void* w,

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_dense_few(GemmArgs a) {
   for (int w = 0; w < kFewWaves; ++w)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += lds[w][threadIdx.x / 2 * PITCH + threadIdx.x % 2 * 8 + e];
-  epilogue8<T, FWD, false>(a, a.drop.top ? drop_offset(a.drop) : 0, r, c, n, v, add, add);
+  epilogue8<T, FWD, false>(a, a.drop.top ? drop_offset(a.drop) : 0, r, c, n, v, add, Pre8<T, false>{});
 }
 
 // A forward of few outputs: at most 64 tiles of 64 x 64 (512 x 512 x 512: 7.6 us against 9.1 in

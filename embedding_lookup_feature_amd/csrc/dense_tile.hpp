@@ -5,7 +5,7 @@
 
 #include <algorithm>
 
-#include "tower_common.hpp"
+#include "micro.hpp"
 
 namespace el {
 namespace {
@@ -33,6 +33,22 @@ struct GemmArgs {
   float *part, *dbp;
   DropArgs drop;
   uint32_t act;
+  // activations kept in 8 bits: pre of the data gradient, Q of the weight gradient, rows of kp codes
+  const uint8_t *codes, *scales;
+  long kp;
+};
+
+// Eight columns of the data gradient's pre-activation, in 16 or in 8 bits.
+template <class T, bool KEPT>
+struct Pre8 {
+  Raw8<T> raw;
+  __device__ inline void floats(float (&f)[8]) const { to_floats<T>(raw, f); }
+};
+template <class T>
+struct Pre8<T, true> {
+  uint2 q;
+  uint32_t scale;
+  __device__ inline void floats(float (&f)[8]) const { unpack8(q.x, q.y, scale_of(scale), f); }
 };
 
 // ---------------------------------------------------------------------------------------
@@ -61,9 +77,9 @@ __device__ inline Raw8<T> get8(const uint16_t* p, int n) {
   return r;
 }
 
-template <class T, int PROD, bool NT>
+template <class T, int PROD, bool NT, class PRE>
 __device__ inline void epilogue8(const GemmArgs& a, uint64_t offset, long r, int c, int n, float (&v)[8],
-                                 const Raw8<T>& add, const Raw8<T>& pre) {
+                                 const Raw8<T>& add, const PRE& pre) {
   float f[8];
   if (a.add) to_floats<T>(add, f);
   if constexpr (PROD == FWD) {
@@ -76,7 +92,7 @@ __device__ inline void epilogue8(const GemmArgs& a, uint64_t offset, long r, int
     put8<T, NT>(a.out + r * a.ldo + c, v, n);
     if (!a.aux) return;
     if (a.act != EL_ACT_NONE) {
-      to_floats<T>(pre, f);
+      pre.floats(f);
       act8_grad(a.act, f, v);
     }
   }
@@ -211,6 +227,69 @@ struct Operand {
   }
 };
 
+// The weight gradient's Q kept in 8 bits: the same tile in LDS (output-contiguous, [BK][W] of 16-bit
+// values, the same permutation), but its codes pass through registers, where they get their scales.
+// A stage's codes are loaded when its slot is freed and written to it one stage later.
+template <class T, int W, int BK, int NW>
+struct Operand8 {
+  using Tile = Operand<W, BK, false, NW>;
+  static constexpr int BYTES = Tile::BYTES, N = Tile::N;
+  const uint8_t *codes, *scales;  // where the next stage to load begins
+  int64_t left;                   // rows from there to the end
+  int kp;
+  uint32_t voff[N], soff[N];
+  uint2 q[N];
+  uint32_t sc[N];
+  __device__ inline void init(const uint8_t* c8, const uint8_t* s8, long kp_, int i0, int n, long kbeg, long kend, int wave, int lane) {
+    kp = static_cast<int>(kp_);
+    codes = c8 + kbeg * kp_ + i0;
+    scales = s8 + kbeg * (kp_ / kMicroBlock) + i0 / kMicroBlock;
+    left = kend - kbeg;
+    const int cols = min(W, n - i0);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int u = (j * NW + wave) * 64 + lane;
+      const int k = u / (W / 8), c = (u % (W / 8)) ^ Tile::perm(k);
+      voff[j] = c * 8 < cols ? static_cast<uint32_t>(k) * kp + c * 8 : kOut;
+      soff[j] = c * 8 < cols ? static_cast<uint32_t>(k) * (kp / kMicroBlock) + c * 8 / kMicroBlock : kOut;
+    }
+  }
+  __device__ inline void load(int j) {
+    const int rows = static_cast<int>(max(int64_t{0}, min(left, int64_t{BK})));
+    const auto rc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(codes), 0, rows * kp, 0x00027000);
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales), 0, rows * (kp / kMicroBlock), 0x00027000);
+    const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, voff[j], 0, 0));
+    q[j] = uint2{v[0], v[1]};
+    sc[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, soff[j], 0, 0);
+  }
+  __device__ inline void advance() {
+    codes += static_cast<long>(BK) * kp;
+    scales += static_cast<long>(BK) * (kp / kMicroBlock);
+    left -= BK;
+  }
+  // This lane's vectors to their places behind `tile` (this wavefront's first piece).
+  __device__ inline void put(lds_char* tile, int lane) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float s = scale_of(sc[j]);
+      u32x4 v;
+      if constexpr (T::code == EL_BF16) {
+        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[j].x, s, false));
+        v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[j].x, s, true));
+        v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[j].y, s, false));
+        v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[j].y, s, true));
+      } else {
+        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[j].x, s, false));
+        v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[j].x, s, true));
+        v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[j].y, s, false));
+        v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[j].y, s, true));
+      }
+      *reinterpret_cast<lds_u32x4*>(tile + j * NW * 1024 + lane * 16) = v;
+    }
+  }
+  __device__ static inline u32x4 frag(const lds_char* tile, int i, int kk, int lane) { return Tile::frag(tile, i, kk, lane); }
+};
+
 // Orders this wavefront's LDS writes before its later reads by other lanes (the hardware keeps a
 // wavefront's LDS accesses in order; this keeps the compiler from moving them).
 __device__ inline void wave_sync() {
@@ -243,11 +322,14 @@ using CfgM = Cfg<128, 128, 2, 4, 2, 4, false, 2>;  // 64 KB, two of 8 wavefronts
 using CfgS = Cfg<64, 64, 2, 2, 4, 2, false, 1>;    // 64 KB, two per CU
 
 // One tile (of one split): `lid` in tiles of all splits, in the order that shares panels.
-template <class T, class C, int PROD>
+// KEPT: the data gradient's pre or the weight gradient's Q is read from 8 bits.
+template <class T, class C, int PROD, bool KEPT = false>
 __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds) {
   constexpr int NW = C::NW, FR = C::FR, FC = C::FC, BK = C::BK, ST = C::ST, WC = C::WC;
   using OP = Operand<C::BR, BK, PROD != WGRAD, NW>;
-  using OQ = Operand<C::BC, BK, PROD == FWD, NW>;
+  constexpr bool Q8 = KEPT && PROD == WGRAD;
+  static_assert(!Q8 || ST == 2, "the registers hold one stage of codes");
+  using OQ = std::conditional_t<Q8, Operand8<T, C::BC, BK, NW>, Operand<C::BC, BK, PROD == FWD, NW>>;
   constexpr int SB = OP::BYTES + OQ::BYTES, LOADS = OP::N + OQ::N;
   const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = static_cast<int>(uniform(threadIdx.x >> 6));
@@ -261,12 +343,21 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
   OP op;
   OQ oq;
   op.init(a.P, a.ldp, row0, a.R, kbeg, kend, wave, lane);
-  oq.init(a.Q, a.ldq, col0, a.C, kbeg, min(kend, a.red_q), wave, lane);
+  if constexpr (Q8) oq.init(a.codes, a.scales, a.kp, col0, a.C, kbeg, min(kend, a.red_q), wave, lane);
+  else oq.init(a.Q, a.ldq, col0, a.C, kbeg, min(kend, a.red_q), wave, lane);
   const lds_char* base = (const lds_char*)lds;
   const uint32_t mine = uniform(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base)) + wave * 1024);
+  const auto rsrc_q = [&]() {
+    if constexpr (Q8) return u32x4{};
+    else return oq.rsrc();
+  };
   const auto load_one = [&](int m, uint32_t slot, const u32x4& rp, const u32x4& rq) {
     if (m < OP::N) op.load(mine + slot, m, rp);
+    else if constexpr (Q8) oq.load(m - OP::N);
     else oq.load(mine + slot + OP::BYTES, m - OP::N, rq);
+  };
+  const auto put_q = [&](uint32_t slot) {
+    if constexpr (Q8) oq.put((lds_char*)lds + slot + OP::BYTES + wave * 1024, lane);
   };
   f32x16 acc[FC][FR];
   // register 4 g + e of acc[i][j]: column 32 i + 8 g + 4 half + e of row 32 j + l32; the forward's
@@ -286,11 +377,12 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
   // number of loads in flight at every wait is known at compile time.
 #pragma unroll
   for (int s = 0; s < ST; ++s) {
-    const u32x4 rp = op.rsrc(), rq = oq.rsrc();
+    const u32x4 rp = op.rsrc(), rq = rsrc_q();
 #pragma unroll
     for (int m = 0; m < LOADS; ++m) load_one(m, s * SB, rp, rq);
     op.advance();
     oq.advance();
+    if (s < ST - 1) put_q(s * SB);  // (the last stage's codes wait for the loop)
   }
 
   // Two register sets of fragments: while one K16 step multiplies, the next one's are read.  The
@@ -320,6 +412,8 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
   for (int kt = 0; kt < nk; ++kt) {
 #pragma unroll
     for (int kk = 0; kk < KK - 1; ++kk) {
+      // the next stage's codes, loaded a stage ago, to the slot that was freed then
+      if (Q8 && kk == KK - 2) put_q(slot + SB == ST * SB ? 0 : slot + SB);
       read((kk + 1) & 1, slot, kk + 1);
 #pragma unroll
       for (int j = 0; j < FR; ++j)
@@ -340,7 +434,7 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
     __builtin_amdgcn_sched_barrier(0);
     const uint32_t freed = slot;
     slot = slot + SB == ST * SB ? 0 : slot + SB;
-    const u32x4 rp = op.rsrc(), rq = oq.rsrc();
+    const u32x4 rp = op.rsrc(), rq = rsrc_q();
     add_rows((KK - 1) & 1, kt);
     read(0, slot, 0);
     __builtin_amdgcn_sched_barrier(0);
@@ -397,7 +491,9 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
     float* blk = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
     const int gr = lane % GR, rr = lane / GR;
     const int c = col0 + wc * WCOLS + gr * 8, n = min(8, a.C - c);
-    Raw8<T> add[AHEAD][PASS], pre[AHEAD][PASS];
+    constexpr bool P8 = KEPT && PROD == DGRAD;
+    Raw8<T> add[AHEAD][PASS];
+    Pre8<T, P8> pre[AHEAD][PASS];
     const auto fetch = [&](int j) {
 #pragma unroll
       for (int s = 0; s < PASS; ++s) {
@@ -405,7 +501,14 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
         if (r < a.R && n > 0) {
           constexpr bool NTL = C::NT && PROD == DGRAD;
           if (a.add) add[j % AHEAD][s] = get8<T, NTL>(a.add + r * a.ldadd + c, n);
-          if (PROD == DGRAD && a.pre) pre[j % AHEAD][s] = get8<T, NTL>(a.pre + r * a.ldpre + c, n);
+          if constexpr (P8) {
+            if (a.codes) {
+              pre[j % AHEAD][s].q = *reinterpret_cast<const uint2*>(a.codes + r * a.kp + c);
+              pre[j % AHEAD][s].scale = a.scales[r * (a.kp / kMicroBlock) + c / kMicroBlock];
+            }
+          } else {
+            if (PROD == DGRAD && a.pre) pre[j % AHEAD][s].raw = get8<T, NTL>(a.pre + r * a.ldpre + c, n);
+          }
         }
       }
     };
@@ -436,10 +539,10 @@ __device__ __forceinline__ void dense_tile(const GemmArgs& a, int lid, char* lds
   }
 }
 
-template <class T, class C, int PROD>
+template <class T, class C, int PROD, bool KEPT>
 __global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
-  dense_tile<T, C, PROD>(a, xcd_order(blockIdx.x, gridDim.x), lds);
+  dense_tile<T, C, PROD, KEPT>(a, xcd_order(blockIdx.x, gridDim.x), lds);
 }
 
 // The two products of the backward in one launch: nd tiles of the data gradient `d`, and the
@@ -447,7 +550,7 @@ __global__ __launch_bounds__(C::NW * 64, C::WPE) void k_dense(GemmArgs a) {
 // gradient's long tiles first, so that the data gradient's short ones fill the gaps behind them
 // and one tail replaces two (65536 x 1024 x 1024: 374 us; two launches 383; every third
 // workgroup a weight gradient's 394).
-template <class T, class CD, class CW>
+template <class T, class CD, class CW, bool KD, bool KW>
 __global__ __launch_bounds__(CD::NW * 64, CD::WPE) void k_dense_bwd(GemmArgs d, GemmArgs w, int nd) {
   static_assert(CD::NW == CW::NW, "one workgroup shape");
   __shared__ __attribute__((aligned(1024))) char lds[std::max(CD::LDS, CW::LDS)];
@@ -456,9 +559,9 @@ __global__ __launch_bounds__(CD::NW * 64, CD::WPE) void k_dense_bwd(GemmArgs d, 
   const int dcount = (nd >> 3) + (x < (nd & 7)), dfirst = x * (nd >> 3) + min(x, nd & 7);
   const int wcount = count - dcount;
   if (i < wcount)
-    dense_tile<T, CW, WGRAD>(w, first - dfirst + i, lds);
+    dense_tile<T, CW, WGRAD, KW>(w, first - dfirst + i, lds);
   else
-    dense_tile<T, CD, DGRAD>(d, dfirst + i - wcount, lds);
+    dense_tile<T, CD, DGRAD, KD>(d, dfirst + i - wcount, lds);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -473,6 +576,14 @@ struct PackJob {
   int cols, vecs;
   unsigned blocks;  // 0: nothing to copy
 };
+__device__ inline void pack_rows(const PackJob& j, unsigned blk) {
+  const long i = static_cast<long>(blk) * 256 + threadIdx.x;
+  const long r = i / j.vecs;
+  const int v = static_cast<int>(i - r * j.vecs);
+  if (r >= j.rows) return;
+  // (bits: one loader serves both 16-bit types)
+  reinterpret_cast<u32x4*>(j.dst)[i] = load8_raw<BF16T>(j.src + r * j.ld + v * 8, j.cols - v * 8).v[0];
+}
 __global__ __launch_bounds__(256) void k_pack(PackJob a, PackJob b, PackJob c) {
   unsigned blk = blockIdx.x;
   PackJob j = a;
@@ -484,12 +595,7 @@ __global__ __launch_bounds__(256) void k_pack(PackJob a, PackJob b, PackJob c) {
       j = c;
     }
   }
-  const long i = static_cast<long>(blk) * 256 + threadIdx.x;
-  const long r = i / j.vecs;
-  const int v = static_cast<int>(i - r * j.vecs);
-  if (r >= j.rows) return;
-  // (bits: one loader serves both 16-bit types)
-  reinterpret_cast<u32x4*>(j.dst)[i] = load8_raw<BF16T>(j.src + r * j.ld + v * 8, j.cols - v * 8).v[0];
+  pack_rows(j, blk);
 }
 
 // out[i] = the sum over p < parts of part[p][i], i < n: 16 threads share one vector's parts
@@ -605,33 +711,37 @@ int set_tiles(GemmArgs& a, int splits) {
   return a.tiles * splits;
 }
 
-template <class T, class C, int PROD>
+// The shape whose weight gradient reads Q from 8 bits itself (the others take a copy in 16).
+constexpr bool reads_codes(Shape s) { return s == SHAPE_L; }
+
+template <class T, class C, int PROD, bool KEPT>
 el_status launch_tiles(const char* fn, GemmArgs a, int splits, hipStream_t st) {
   const int n = set_tiles<C>(a, splits);
-  hipLaunchKernelGGL((k_dense<T, C, PROD>), dim3(n), dim3(C::NW * 64), 0, st, a);
+  hipLaunchKernelGGL((k_dense<T, C, PROD, KEPT>), dim3(n), dim3(C::NW * 64), 0, st, a);
   return check_launch(fn);
 }
-template <class T, int PROD>
+template <class T, int PROD, bool KEPT = false>
 el_status launch_product(const char* fn, const GemmArgs& a, Shape s, int splits, hipStream_t st) {
-  return s == SHAPE_L   ? launch_tiles<T, CfgL, PROD>(fn, a, splits, st)
-         : s == SHAPE_M ? launch_tiles<T, CfgM, PROD>(fn, a, splits, st)
-                        : launch_tiles<T, CfgS, PROD>(fn, a, splits, st);
+  constexpr bool small = KEPT && (PROD != WGRAD || reads_codes(SHAPE_M));
+  return s == SHAPE_L   ? launch_tiles<T, CfgL, PROD, KEPT>(fn, a, splits, st)
+         : s == SHAPE_M ? launch_tiles<T, CfgM, PROD, small>(fn, a, splits, st)
+                        : launch_tiles<T, CfgS, PROD, small>(fn, a, splits, st);
 }
 
-template <class T, class CD, class CW>
+template <class T, class CD, class CW, bool KD, bool KW>
 el_status launch_both(const char* fn, GemmArgs d, GemmArgs w, int splits, hipStream_t st) {
   const int nd = set_tiles<CD>(d, 1), nw = set_tiles<CW>(w, splits);
-  hipLaunchKernelGGL((k_dense_bwd<T, CD, CW>), dim3(nd + nw), dim3(CD::NW * 64), 0, st, d, w, nd);
+  hipLaunchKernelGGL((k_dense_bwd<T, CD, CW, KD, KW>), dim3(nd + nw), dim3(CD::NW * 64), 0, st, d, w, nd);
   return check_launch(fn);
 }
 // The backward's two products: in one launch where their workgroups have one shape.
-template <class T>
+template <class T, bool KEPT = false>
 el_status launch_backward(const char* fn, const GemmArgs& d, Shape sd, const GemmArgs& w, Shape sw, int splits, hipStream_t st) {
-  if (sd == SHAPE_L && sw == SHAPE_L) return launch_both<T, CfgL, CfgL>(fn, d, w, splits, st);
-  if (sd == SHAPE_M && sw == SHAPE_M) return launch_both<T, CfgM, CfgM>(fn, d, w, splits, st);
-  if (sd == SHAPE_S && sw == SHAPE_S) return launch_both<T, CfgS, CfgS>(fn, d, w, splits, st);
-  const el_status s = launch_product<T, DGRAD>(fn, d, sd, 1, st);
-  return s == EL_OK ? launch_product<T, WGRAD>(fn, w, sw, splits, st) : s;
+  if (sd == SHAPE_L && sw == SHAPE_L) return launch_both<T, CfgL, CfgL, KEPT, KEPT>(fn, d, w, splits, st);
+  if (sd == SHAPE_M && sw == SHAPE_M) return launch_both<T, CfgM, CfgM, KEPT, false>(fn, d, w, splits, st);
+  if (sd == SHAPE_S && sw == SHAPE_S) return launch_both<T, CfgS, CfgS, KEPT, false>(fn, d, w, splits, st);
+  const el_status s = launch_product<T, DGRAD, KEPT>(fn, d, sd, 1, st);
+  return s == EL_OK ? launch_product<T, WGRAD, KEPT>(fn, w, sw, splits, st) : s;
 }
 
 bool wgrad_shares(long M, long K, const void* dx) { return dx && plan_tiles(M, K) == SHAPE_L; }
