@@ -2,62 +2,27 @@
 // below read from 8 bits:  dw = dz^T xq,  dx = dz w + dres,  dzb = drop(dx act'(preq)).
 //
 // The tiles of dense_tile.hpp, with two changes.  The data gradient's epilogue reads half the bytes
-// for the pre-activation.  The weight gradient's 256 x 256 tiles take x's codes through registers,
-// where the conversion to 16 bits applies the scale, to the LDS places that direct loads would fill.
-// Smaller tiles, whose batches are small, take a 16-bit copy that shares a launch with the copies of
-// unaligned operands.
+// for the pre-activation.  The weight gradient takes x's codes through registers, where the
+// conversion to 16 bits applies the scale, to the LDS places that direct loads would fill.
 #include "dense_tile.hpp"
 
 namespace el {
 namespace {
 
-// Codes to 16-bit rows of whole vectors.
-struct UnpackJob {
-  const uint8_t *codes, *scales;
-  uint16_t* dst;
-  long items;
-  unsigned blocks;  // 0: nothing to copy
-};
-template <class T>
-__global__ __launch_bounds__(256) void k_copies(PackJob a, PackJob b, UnpackJob x) {
-  unsigned blk = blockIdx.x;
-  if (blk < a.blocks) return pack_rows(a, blk);
-  blk -= a.blocks;
-  if (blk < b.blocks) return pack_rows(b, blk);
-  const long i = static_cast<long>(blk - b.blocks) * 256 + threadIdx.x;
-  if (i >= x.items) return;
-  const uint2 q = reinterpret_cast<const uint2*>(x.codes)[i];
-  float v[8];
-  unpack8(q.x, q.y, scale_of(x.scales[i >> 2]), v);
-  reinterpret_cast<u32x4*>(x.dst)[i] = to_16bit<T>(v);
-}
-
 long padded(long K) { return tower::pad_to(K, kMicroBlock); }
-size_t unpacked_bytes(long M, long K) { return round256(static_cast<size_t>(M) * padded(K) * 2); }
 
 template <class T>
 el_status run(const char* fn, const uint8_t* xc, const uint8_t* xs, int M, int K, const uint16_t* w, int N,
               const uint16_t* dz, long lddz, GemmArgs a, const uint8_t* pc, const uint8_t* ps, float* dw, float* db,
               char* ws, hipStream_t st) {
   const WgradPlan pl = plan_wgrad(M, K, N, wgrad_shares(M, K, a.out));
-  UnpackJob jx{xc, xs, reinterpret_cast<uint16_t*>(ws), 0, 0};
-  if (!reads_codes(pl.shape)) {
-    jx.items = M * padded(K) / 8;
-    jx.blocks = static_cast<unsigned>(ceil_div(jx.items, 256));
-    ws += unpacked_bytes(M, K);
-  }
   Packs packs;
   packs.add(&dz, &lddz, M, N, &ws);
   long ldw = K;
   if (a.out) packs.add(&w, &ldw, N, K, &ws);
-  const long blocks = static_cast<long>(packs.job[0].blocks) + packs.job[1].blocks + jx.blocks;
-  if (blocks >= (1l << 24)) return tower::unsupported(fn, "copied operands of more than 2^35 elements");
-  if (blocks > 0) {
-    hipLaunchKernelGGL((k_copies<T>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, packs.job[0], packs.job[1], jx);
-    EL_TRY(check_launch(fn));
-  }
+  EL_TRY(packs.run(fn, st));
   GemmArgs b{};
-  b.P = dz, b.ldp = lddz, b.Q = jx.dst, b.ldq = padded(K), b.codes = xc, b.scales = xs, b.kp = padded(K), b.R = N, b.C = K, b.red = b.red_q = M, b.per_split = pl.per;
+  b.P = dz, b.ldp = lddz, b.codes = xc, b.scales = xs, b.kp = padded(K), b.R = N, b.C = K, b.red = b.red_q = M, b.per_split = pl.per;
   b.part = pl.splits > 1 ? reinterpret_cast<float*>(ws) : dw;
   float* dbp = reinterpret_cast<float*>(ws + pl.dw_bytes);
   b.dbp = db ? dbp : nullptr;
@@ -84,12 +49,7 @@ extern "C" {
 
 size_t el_dense_bwd_ckpt_workspace_bytes(int32_t M, int32_t K, int32_t N) {
   if (!dense_sizes_ok(M, K, N) || M * padded(K) > (int64_t{1} << 34)) return 0;
-  size_t most = 0;
-  for (bool shared : {false, true}) {
-    const WgradPlan p = plan_wgrad(M, K, N, shared);
-    most = std::max(most, p.bytes + (reads_codes(p.shape) ? 0 : unpacked_bytes(M, K)));
-  }
-  return most + packed_bytes(M, N) + packed_bytes(N, K);
+  return packed_bytes(M, N) + packed_bytes(N, K) + std::max(plan_wgrad(M, K, N, false).bytes, plan_wgrad(M, K, N, true).bytes);
 }
 
 el_status el_dense_bwd_ckpt(const uint8_t* x_codes, const uint8_t* x_scales, int32_t M, int32_t K, const void* w,

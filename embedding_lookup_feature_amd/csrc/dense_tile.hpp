@@ -320,6 +320,7 @@ struct Cfg {
 using CfgL = Cfg<256, 256, 4, 4, 2, 4, true, 1>;   // 136 KB of LDS, one workgroup of 16 wavefronts per CU
 using CfgM = Cfg<128, 128, 2, 4, 2, 4, false, 2>;  // 64 KB, two of 8 wavefronts per CU
 using CfgS = Cfg<64, 64, 2, 2, 4, 2, false, 1>;    // 64 KB, two per CU
+using CfgS2 = Cfg<64, 64, 2, 2, 2, 4, false, 1>;   // 32 KB, four per CU: for codes, of which the registers hold one stage
 
 // One tile (of one split): `lid` in tiles of all splits, in the order that shares panels.
 // KEPT: the data gradient's pre or the weight gradient's Q is read from 8 bits.
@@ -711,9 +712,6 @@ int set_tiles(GemmArgs& a, int splits) {
   return a.tiles * splits;
 }
 
-// The shape whose weight gradient reads Q from 8 bits itself (the others take a copy in 16).
-constexpr bool reads_codes(Shape s) { return s == SHAPE_L; }
-
 template <class T, class C, int PROD, bool KEPT>
 el_status launch_tiles(const char* fn, GemmArgs a, int splits, hipStream_t st) {
   const int n = set_tiles<C>(a, splits);
@@ -722,10 +720,10 @@ el_status launch_tiles(const char* fn, GemmArgs a, int splits, hipStream_t st) {
 }
 template <class T, int PROD, bool KEPT = false>
 el_status launch_product(const char* fn, const GemmArgs& a, Shape s, int splits, hipStream_t st) {
-  constexpr bool small = KEPT && (PROD != WGRAD || reads_codes(SHAPE_M));
+  using S = std::conditional_t<KEPT, CfgS2, CfgS>;
   return s == SHAPE_L   ? launch_tiles<T, CfgL, PROD, KEPT>(fn, a, splits, st)
-         : s == SHAPE_M ? launch_tiles<T, CfgM, PROD, small>(fn, a, splits, st)
-                        : launch_tiles<T, CfgS, PROD, small>(fn, a, splits, st);
+         : s == SHAPE_M ? launch_tiles<T, CfgM, PROD, KEPT>(fn, a, splits, st)
+                        : launch_tiles<T, S, PROD, KEPT>(fn, a, splits, st);
 }
 
 template <class T, class CD, class CW, bool KD, bool KW>
@@ -738,8 +736,9 @@ el_status launch_both(const char* fn, GemmArgs d, GemmArgs w, int splits, hipStr
 template <class T, bool KEPT = false>
 el_status launch_backward(const char* fn, const GemmArgs& d, Shape sd, const GemmArgs& w, Shape sw, int splits, hipStream_t st) {
   if (sd == SHAPE_L && sw == SHAPE_L) return launch_both<T, CfgL, CfgL, KEPT, KEPT>(fn, d, w, splits, st);
-  if (sd == SHAPE_M && sw == SHAPE_M) return launch_both<T, CfgM, CfgM, KEPT, false>(fn, d, w, splits, st);
-  if (sd == SHAPE_S && sw == SHAPE_S) return launch_both<T, CfgS, CfgS, KEPT, false>(fn, d, w, splits, st);
+  using S = std::conditional_t<KEPT, CfgS2, CfgS>;
+  if (sd == SHAPE_M && sw == SHAPE_M) return launch_both<T, CfgM, CfgM, KEPT, KEPT>(fn, d, w, splits, st);
+  if (sd == SHAPE_S && sw == SHAPE_S) return launch_both<T, S, S, KEPT, KEPT>(fn, d, w, splits, st);
   const el_status s = launch_product<T, DGRAD, KEPT>(fn, d, sd, 1, st);
   return s == EL_OK ? launch_product<T, WGRAD, KEPT>(fn, w, sw, splits, st) : s;
 }
