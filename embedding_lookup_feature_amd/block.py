@@ -66,36 +66,64 @@ def header_functions():
     return re.findall(r"EL_API\s+[\w\s\*]+?\b(\w+)\s*\(", text)
 
 
-def _launch(fn, t: torch.Tensor, stream, *args):
-    """Calls fn(*args, stream) with t's device current (the default stream's handle names none)."""
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of t's device; t must be on one."""
     i = t.get_device()
-    if i == torch.cuda.current_device():
-        ec._check(fn(*args, tw._stream(stream, t)))
+    if i < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return i
+
+
+def _launch(fn, dev: int, stream, *args):
+    """Calls fn(*args, stream) with the operands' device current (the default stream's handle names
+    none); without a stream, on torch's current one there."""
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else ec._stream(stream)
+    if dev == _current_device():
+        status = fn(*args, handle)
     else:
-        with torch.cuda.device(i):
-            ec._check(fn(*args, tw._stream(stream, t)))
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status:
+        ec._check(status)
 
 
-def _mat(t, name: str, shape, like: torch.Tensor):
-    """(pointer, row stride) of a row-strided operand of like's type, on its device; (None, cols) of
-    None."""
-    if t is not None and t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    return tw._mat(t, name, shape, like.dtype)
+def _mat(t, name: str, shape, dtype, dev: int):
+    """(pointer, row stride) of a row-strided [rows, cols] operand on device dev; (None, cols) of None."""
+    if t is None:
+        return None, shape[1]
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {list(shape)} of {dtype} on device {dev}, got {list(t.shape)} of {t.dtype} on "
+                         f"{t.device}")
+    ld, cs = t.stride()
+    if cs != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    # the row stride of one row (or none) says nothing
+    return t.data_ptr(), ld if shape[0] > 1 else max(ld, shape[1])
 
 
-def _vec(t, name: str, n: int, like: torch.Tensor):
+def _vec(t, name: str, n: int, dev: int):
+    """The pointer of n contiguous fp32 values."""
     if t is None:
         return None
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    return tw._vec(t, name, n)
+    if t.numel() != n or t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous values of float32 on device {dev}")
+    return t.data_ptr()
 
 
-def _workspace(ws, need: int, like: torch.Tensor, stream):
-    if ws is not None and ws.get_device() != like.get_device():
-        raise ValueError(f"workspace must be on {like.device}, got {ws.device}")
-    return tw._workspace(ws, need, like.device, stream)
+def _workspace(ws, need, like: torch.Tensor, dev: int, stream):
+    """(pointer, bytes, the tensor that holds them); `need` is asked where none is given."""
+    if ws is None:
+        n = need()
+        if n == 0:
+            return None, 0, None
+        ws = ec._scratch(n, like.device, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on device {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 class BlockNorm:
@@ -115,31 +143,35 @@ class BlockNorm:
             raise ValueError(f"gate_act must be one of {sorted(GATES)}, got {gate_act!r}")
         if not 1 <= gate_rows < 2**31:
             raise ValueError(f"gate_rows must be from 1 to 2^31 - 1, got {gate_rows}")
-        self.C = int(C)
+        if not 1 <= C < 2**31:
+            raise ValueError(f"C must be from 1 to 2^31 - 1, got {C}")
+        self.C, self.gate_rows = int(C), int(gate_rows)
         self.params = (post_gamma, post_beta, pre_gamma, pre_beta)
         names = ("post_gamma", "post_beta", "pre_gamma", "pre_beta")
-        self.device = next((p.get_device() for p in self.params if p is not None), None)
+        self.device = next((_device(p, name) for p, name in zip(self.params, names) if p is not None), None)
         for p, name in zip(self.params, names):
             if p is not None and p.get_device() != self.device:
                 raise ValueError(f"{name} must be on the other parameters' device")
-        self.c = ElBlockNorm(NORMS[post], NORMS[pre], GATES[gate_act], int(gate_rows), float(scale), float(eps),
-                             *(tw._vec(p, name, self.C) for p, name in zip(self.params, names)))
+        self.c = ElBlockNorm(NORMS[post], NORMS[pre], GATES[gate_act], self.gate_rows, float(scale), float(eps),
+                             *(_vec(p, name, self.C, self.device) for p, name in zip(self.params, names)))
         self.ref = ctypes.byref(self.c)
 
     def gates(self, M: int) -> int:
         """Rows of the gate for M rows."""
-        return -(-M // self.c.gate_rows)
+        return -(-M // self.gate_rows)
 
 
 def _norm_shape(norm: BlockNorm, t: torch.Tensor, name: str):
-    M, C = tw._rows_cols(t, name)
+    """(shape, device) of an operand of the norm."""
+    shape = M, C = tw._rows_cols(t, name)
     if C != norm.C:
         raise ValueError(f"{name} must have {norm.C} columns, got {C}")
     if M >> 31:
         tw._too_large(M, C)
-    if norm.device is not None and t.get_device() != norm.device:
+    dev = _device(t, name)
+    if norm.device is not None and dev != norm.device:
         raise ValueError(f"{name} must be on the parameters' device")
-    return M, C
+    return shape, dev
 
 
 def block_norm_fwd(norm: BlockNorm, x, y=None, h=None, f: torch.Tensor = None, gate: torch.Tensor = None,
@@ -150,19 +182,21 @@ def block_norm_fwd(norm: BlockNorm, x, y=None, h=None, f: torch.Tensor = None, g
     like = x if x is not None else f
     if like is None:
         raise ValueError("x or f must be given")
-    shape = M, C = _norm_shape(norm, like, "x" if x is not None else "f")
-    xp, ldx = _mat(x, "x", shape, like)
-    fp, ldf = _mat(f, "f", shape, like)
-    gp, ldg = _mat(gate, "gate", (norm.gates(M), C), like)
-    yp, ldy = _mat(y, "y", shape, like)
-    hp, ldh = _mat(h, "h", shape, like)
-    _launch(lib().el_block_norm_fwd, like, stream, norm.ref, xp, ldx, fp, ldf, gp, ldg, M, C, yp, ldy, hp, ldh,
-            _vec(post_stats, "post_stats", 2 * M, like), _vec(pre_stats, "pre_stats", 2 * M, like), ec._dtype(like, "x"))
+    shape, dev = _norm_shape(norm, like, "x" if x is not None else "f")
+    M, C = shape
+    dt = like.dtype
+    xp, ldx = _mat(x, "x", shape, dt, dev)
+    fp, ldf = _mat(f, "f", shape, dt, dev)
+    gp, ldg = (None, C) if gate is None else _mat(gate, "gate", (norm.gates(M), C), dt, dev)
+    yp, ldy = _mat(y, "y", shape, dt, dev)
+    hp, ldh = _mat(h, "h", shape, dt, dev)
+    _launch(lib().el_block_norm_fwd, dev, stream, norm.ref, xp, ldx, fp, ldf, gp, ldg, M, C, yp, ldy, hp, ldh,
+            _vec(post_stats, "post_stats", 2 * M, dev), _vec(pre_stats, "pre_stats", 2 * M, dev), ec._dtype(like, "x"))
     return y, h
 
 
 def block_norm_bwd_workspace_bytes(norm: BlockNorm, M: int) -> int:
-    return int(lib().el_block_norm_bwd_workspace_bytes(M, norm.C, norm.c.gate_rows))
+    return int(lib().el_block_norm_bwd_workspace_bytes(M, norm.C, norm.gate_rows))
 
 
 def block_norm_bwd(norm: BlockNorm, y, dx, dy: torch.Tensor = None, dh: torch.Tensor = None, f: torch.Tensor = None,
@@ -176,22 +210,22 @@ def block_norm_bwd(norm: BlockNorm, y, dx, dy: torch.Tensor = None, dh: torch.Te
     like = dh if dh is not None else dy
     if like is None:
         raise ValueError("dy or dh must be given")
-    shape = M, C = _norm_shape(norm, like, "dh" if dh is not None else "dy")
-    dyp, lddy = _mat(dy, "dy", shape, like)
-    dhp, lddh = _mat(dh, "dh", shape, like)
-    yp, ldy = _mat(y, "y", shape, like)
-    fp, ldf = _mat(f, "f", shape, like)
-    gp, ldg = _mat(gate, "gate", (norm.gates(M), C), like)
-    dxp, lddx = _mat(dx, "dx", shape, like)
-    dfp, lddf = _mat(df, "df", shape, like)
-    dgp, lddg = _mat(dgate, "dgate", (norm.gates(M), C), like)
-    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else block_norm_bwd_workspace_bytes(norm, M), like,
-                                stream)
-    _launch(lib().el_block_norm_bwd, like, stream, norm.ref, dyp, lddy, dhp, lddh, yp, ldy, fp, ldf, gp, ldg, M, C,
-            _vec(post_stats, "post_stats", 2 * M, like), _vec(pre_stats, "pre_stats", 2 * M, like), dxp, lddx, dfp, lddf,
-            dgp, lddg, _vec(dpost_gamma, "dpost_gamma", C, like), _vec(dpost_beta, "dpost_beta", C, like),
-            _vec(dpre_gamma, "dpre_gamma", C, like), _vec(dpre_beta, "dpre_beta", C, like), ec._dtype(like, "dh"), wsp,
-            wsn)
+    shape, dev = _norm_shape(norm, like, "dh" if dh is not None else "dy")
+    M, C = shape
+    dt, gates = like.dtype, (norm.gates(M), C)
+    dyp, lddy = _mat(dy, "dy", shape, dt, dev)
+    dhp, lddh = _mat(dh, "dh", shape, dt, dev)
+    yp, ldy = _mat(y, "y", shape, dt, dev)
+    fp, ldf = _mat(f, "f", shape, dt, dev)
+    gp, ldg = _mat(gate, "gate", gates, dt, dev)
+    dxp, lddx = _mat(dx, "dx", shape, dt, dev)
+    dfp, lddf = _mat(df, "df", shape, dt, dev)
+    dgp, lddg = _mat(dgate, "dgate", gates, dt, dev)
+    wsp, wsn, keep = _workspace(workspace, lambda: block_norm_bwd_workspace_bytes(norm, M), like, dev, stream)
+    _launch(lib().el_block_norm_bwd, dev, stream, norm.ref, dyp, lddy, dhp, lddh, yp, ldy, fp, ldf, gp, ldg, M, C,
+            _vec(post_stats, "post_stats", 2 * M, dev), _vec(pre_stats, "pre_stats", 2 * M, dev), dxp, lddx, dfp, lddf,
+            dgp, lddg, _vec(dpost_gamma, "dpost_gamma", C, dev), _vec(dpost_beta, "dpost_beta", C, dev),
+            _vec(dpre_gamma, "dpre_gamma", C, dev), _vec(dpre_beta, "dpre_beta", C, dev), ec._dtype(like, "dh"), wsp, wsn)
     return dx, df
 
 
@@ -203,9 +237,18 @@ class _Packed:
             raise ValueError(f"rows must be from 0 and cols from 1 to 2^31 - 1, got {rows} x {cols}")
         self.rows, self.cols = int(rows), int(cols)
         codes, scales = self._shapes()
-        self.codes = torch.empty(codes, dtype=torch.uint8, device=device)
-        self.scales = torch.empty(scales, dtype=torch.uint8, device=device)
-        self.ptrs = (ec._dev(self.codes, "codes"), ec._dev(self.scales, "scales")) if self.rows else (None, None)
+        self._codes = torch.empty(codes, dtype=torch.uint8, device=device)
+        self._scales = torch.empty(scales, dtype=torch.uint8, device=device)
+        self.device = _device(self._codes, "the packed array")
+        self.ptrs = (self._codes.data_ptr(), self._scales.data_ptr()) if self.rows else (None, None)
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._scales
 
     @property
     def nbytes(self) -> int:
@@ -235,34 +278,39 @@ class Fp4(_Packed):
         return (tiles, -(-self.cols // 128), 2, 64, 16), (tiles, -(-self.cols // 512), 2, 64, 4)
 
 
-def _packed(p, kind, name: str, shape, like: torch.Tensor):
+def _packed(p, kind, name: str, rows: int, cols: int, dev: int):
     """Pointers of a packed operand of `kind`; (None, None) of None."""
     if p is None:
         return None, None
     if type(p) is not kind:
         raise ValueError(f"{name} must be a {kind.__name__}")
-    if (p.rows, p.cols) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {[p.rows, p.cols]}")
-    if p.codes.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {p.codes.device}")
+    if p.rows != rows or p.cols != cols:
+        raise ValueError(f"{name} must be {[rows, cols]}, got {[p.rows, p.cols]}")
+    if p.device != dev:
+        raise ValueError(f"{name} must be on device {dev}, got {p.codes.device}")
     return p.ptrs
+
+
+def _with_packed(t: torch.Tensor, name: str, p, kind, pname: str):
+    """(shape, device, pointer, row stride) of t and the pointers of a packed operand of its shape."""
+    shape = M, K = tw._rows_cols(t, name)
+    if (M | K) >> 31:
+        tw._too_large(M, K)
+    dev = _device(t, name)
+    return shape, dev, _mat(t, name, shape, t.dtype, dev), _packed(p, kind, pname, M, K, dev)
 
 
 def ckpt_pack(x: torch.Tensor, ckpt: Checkpoint, stream=None) -> Checkpoint:
     """Keeps x [M, K] (fp32, fp16, bf16) in 8 bits."""
-    M, K = tw._rows_cols(x, "x")
-    codes, scales = _packed(ckpt, Checkpoint, "ckpt", (M, K), x)
-    xp, ldx = _mat(x, "x", (M, K), x)
-    _launch(lib().el_ckpt_pack, x, stream, xp, ldx, M, K, ec._dtype(x, "x"), codes, scales)
+    (M, K), dev, (xp, ldx), (codes, scales) = _with_packed(x, "x", ckpt, Checkpoint, "ckpt")
+    _launch(lib().el_ckpt_pack, dev, stream, xp, ldx, M, K, ec._dtype(x, "x"), codes, scales)
     return ckpt
 
 
 def ckpt_act_dropout_fwd(ckpt: Checkpoint, y: torch.Tensor, act: str = "none", dropout=None, stream=None):
     """y = drop(act(kept values)): what act_dropout_fwd gives on them; with neither, the kept values."""
-    M, K = tw._rows_cols(y, "y")
-    codes, scales = _packed(ckpt, Checkpoint, "ckpt", (M, K), y)
-    yp, ldy = _mat(y, "y", (M, K), y)
-    _launch(lib().el_ckpt_act_dropout_fwd, y, stream, codes, scales, M, K, tw._act(act), tw._drop(dropout), yp, ldy,
+    (M, K), dev, (yp, ldy), (codes, scales) = _with_packed(y, "y", ckpt, Checkpoint, "ckpt")
+    _launch(lib().el_ckpt_act_dropout_fwd, dev, stream, codes, scales, M, K, tw._act(act), tw._drop(dropout), yp, ldy,
             ec._dtype(y, "y"))
     return y
 
@@ -270,12 +318,10 @@ def ckpt_act_dropout_fwd(ckpt: Checkpoint, y: torch.Tensor, act: str = "none", d
 def ckpt_act_dropout_bwd(dy: torch.Tensor, ckpt: Checkpoint, dx: torch.Tensor, act: str = "none", dropout=None,
                          stream=None):
     """dx = drop(dy * act'(kept values)), the mask of the forward with the same dropout."""
-    M, K = tw._rows_cols(dy, "dy")
-    codes, scales = _packed(ckpt, Checkpoint, "ckpt", (M, K), dy)
-    dp, lddy = _mat(dy, "dy", (M, K), dy)
-    op, lddx = _mat(dx, "dx", (M, K), dy)
-    _launch(lib().el_ckpt_act_dropout_bwd, dy, stream, dp, lddy, codes, scales, M, K, tw._act(act), tw._drop(dropout), op,
-            lddx, ec._dtype(dy, "dy"))
+    shape, dev, (dp, lddy), (codes, scales) = _with_packed(dy, "dy", ckpt, Checkpoint, "ckpt")
+    op, lddx = _mat(dx, "dx", shape, dy.dtype, dev)
+    _launch(lib().el_ckpt_act_dropout_bwd, dev, stream, dp, lddy, codes, scales, *shape, tw._act(act), tw._drop(dropout),
+            op, lddx, ec._dtype(dy, "dy"))
     return dx
 
 
@@ -291,39 +337,33 @@ def dense_bwd_ckpt(x: Checkpoint, w: torch.Tensor, dz: torch.Tensor, dw: torch.T
     K = tw._rows_cols(w, "w")[1]
     if (M | K | N) >> 31:
         tw._too_large(M, K, N)
-    if w.shape != (N, K) or w.dtype is not dz.dtype or w.get_device() != dz.get_device():
-        raise ValueError(f"w must be [{N}, K] of {dz.dtype} on {dz.device}")
-    xc, xs = _packed(x, Checkpoint, "x", (M, K), dz)
-    pc, ps = _packed(pre, Checkpoint, "pre", (M, K), dz)
-    zp, ldz = _mat(dz, "dz", (M, N), dz)
-    dxp, lddx = _mat(dx, "dx", (M, K), dz)
-    rp, ldr = _mat(dres, "dres", (M, K), dz)
-    bp, ldb = _mat(dzb, "dzb", (M, K), dz)
-    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_bwd_ckpt_workspace_bytes(M, K, N), dz,
-                                stream)
-    if dw.numel() != N * K:
-        raise ValueError(f"dw must be [{N}, {K}]")
-    _launch(lib().el_dense_bwd_ckpt, dz, stream, xc, xs, M, K, ec._dev(w, "w"), N, zp, ldz, rp, ldr, dxp, lddx,
-            tw._act(act), tw._drop(dropout), pc, ps, bp, ldb, _vec(dw, "dw", N * K, dz), _vec(db, "db", N, dz),
+    dev, dt = _device(dz, "dz"), dz.dtype
+    if w.shape != (N, K) or w.dtype is not dt or w.get_device() != dev or not w.is_contiguous():
+        raise ValueError(f"w must be contiguous [{N}, K] of {dt} on {dz.device}")
+    xc, xs = _packed(x, Checkpoint, "x", M, K, dev)
+    pc, ps = _packed(pre, Checkpoint, "pre", M, K, dev)
+    zp, ldz = _mat(dz, "dz", (M, N), dt, dev)
+    dxp, lddx = _mat(dx, "dx", (M, K), dt, dev)
+    rp, ldr = _mat(dres, "dres", (M, K), dt, dev)
+    bp, ldb = _mat(dzb, "dzb", (M, K), dt, dev)
+    wsp, wsn, keep = _workspace(workspace, lambda: dense_bwd_ckpt_workspace_bytes(M, K, N), dz, dev, stream)
+    _launch(lib().el_dense_bwd_ckpt, dev, stream, xc, xs, M, K, w.data_ptr(), N, zp, ldz, rp, ldr, dxp, lddx,
+            tw._act(act), tw._drop(dropout), pc, ps, bp, ldb, _vec(dw, "dw", N * K, dev), _vec(db, "db", N, dev),
             ec._dtype(dz, "dz"), wsp, wsn)
     return dx, dw, db
 
 
 def fp4_pack(x: torch.Tensor, packed: Fp4, stream=None) -> Fp4:
     """Rounds x [M, K] (fp32, fp16, bf16) to 4 bits."""
-    M, K = tw._rows_cols(x, "x")
-    codes, scales = _packed(packed, Fp4, "packed", (M, K), x)
-    xp, ldx = _mat(x, "x", (M, K), x)
-    _launch(lib().el_fp4_pack, x, stream, xp, ldx, M, K, ec._dtype(x, "x"), codes, scales)
+    (M, K), dev, (xp, ldx), (codes, scales) = _with_packed(x, "x", packed, Fp4, "packed")
+    _launch(lib().el_fp4_pack, dev, stream, xp, ldx, M, K, ec._dtype(x, "x"), codes, scales)
     return packed
 
 
 def fp4_unpack(packed: Fp4, y: torch.Tensor, stream=None):
     """The values that the codes stand for."""
-    M, K = tw._rows_cols(y, "y")
-    codes, scales = _packed(packed, Fp4, "packed", (M, K), y)
-    yp, ldy = _mat(y, "y", (M, K), y)
-    _launch(lib().el_fp4_unpack, y, stream, codes, scales, M, K, yp, ldy, ec._dtype(y, "y"))
+    (M, K), dev, (yp, ldy), (codes, scales) = _with_packed(y, "y", packed, Fp4, "packed")
+    _launch(lib().el_fp4_unpack, dev, stream, codes, scales, M, K, yp, ldy, ec._dtype(y, "y"))
     return y
 
 
@@ -335,16 +375,17 @@ def dense_fwd_fp4(x: torch.Tensor, w: Fp4, bias, y: torch.Tensor, act: str = "no
                   workspace: torch.Tensor = None, stream=None):
     """y = residual + act(x4 @ w4.T + bias), x [M, K] (bf16, fp16) rounded to 4 bits within the call,
     w a packed [N, K]; bias fp32 [N] or None; y, residual [M, N]."""
-    M, K = tw._rows_cols(x, "x")
-    N = y.shape[-1]
+    shape = M, K = tw._rows_cols(x, "x")
+    out = tw._rows_cols(y, "y")
+    N = out[1]
     if (M | K | N) >> 31:
         tw._too_large(M, K, N)
-    wc, wsc = _packed(w, Fp4, "w", (N, K), x)
-    xp, ldx = _mat(x, "x", (M, K), x)
-    rp, ldr = _mat(residual, "residual", (M, N), x)
-    yp, ldy = _mat(y, "y", (M, N), x)
-    wsp, wsn, keep = _workspace(workspace, 0 if workspace is not None else dense_fwd_fp4_workspace_bytes(M, K, N), x,
-                                stream)
-    _launch(lib().el_dense_fwd_fp4, x, stream, xp, ldx, M, K, wc, wsc, _vec(bias, "bias", N, x), N, tw._act(act), rp, ldr,
-            yp, ldy, ec._dtype(x, "x"), wsp, wsn)
+    dev, dt = _device(x, "x"), x.dtype
+    wc, wsc = _packed(w, Fp4, "w", N, K, dev)
+    xp, ldx = _mat(x, "x", shape, dt, dev)
+    rp, ldr = _mat(residual, "residual", (M, N), dt, dev)
+    yp, ldy = _mat(y, "y", (M, N), dt, dev)
+    wsp, wsn, keep = _workspace(workspace, lambda: dense_fwd_fp4_workspace_bytes(M, K, N), x, dev, stream)
+    _launch(lib().el_dense_fwd_fp4, dev, stream, xp, ldx, M, K, wc, wsc, _vec(bias, "bias", N, dev), N, tw._act(act), rp,
+            ldr, yp, ldy, ec._dtype(x, "x"), wsp, wsn)
     return y
