@@ -7,7 +7,6 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 constexpr int kThreads = 256;
 constexpr int kPad = 128;  // columns of a padded row: whole products of 128
@@ -223,7 +222,7 @@ __device__ inline void settle_cut(float (&v)[8], int n) {
 // cannot count waits for everything, the stores before it too: 124 us against 98).  The weights of
 // the step three ahead, of the next columns where the row ends, are fetched while a step multiplies;
 // the residual during a pass's last three steps.  EIGHT: K and N are at least 8.
-template <class T, int J, bool XG, bool EIGHT, bool ADD, bool BIAS>
+template <class T, int J, bool XG, bool EIGHT, bool ADD>
 __global__ __launch_bounds__(kThreads, 4) void k_dense_fp4(DenseArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [step][J][64 lanes][16], then [group][J][64 lanes][4]
   constexpr int BR = 16 * J, WC = 32;
@@ -272,6 +271,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_dense_fp4(DenseArgs a) {
   if (tile >= tiles) return;
   const auto rc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.wc), 0, tiles * a.steps * 2 * kFrag, 0x00027000);
   const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.ws), 0, tiles * groups * 512, 0x00027000);
+  const auto rbias = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(a.bias), 0, a.bias ? a.N * 4 : 0, 0x00027000);  // none: zeros
   // Step k of the tile, or of the tile after it from 4 groups on; what does not exist is replaced by
   // what does, and not used.
   const auto fetch = [&](int set, int k) {
@@ -302,16 +302,15 @@ __global__ __launch_bounds__(kThreads, 4) void k_dense_fp4(DenseArgs a) {
     float bias[8] = {};
     Raw8<T> add[J];
     const auto fetch_ends = [&]() {  // the bias and the residual
-      if constexpr (BIAS) {
-        if constexpr (EIGHT) {
-          const f32x4_any* p = reinterpret_cast<const f32x4_any*>(a.bias + min(c, a.N - 8));
-          const f32x4 lo = p[0], hi = p[1];
+      if constexpr (EIGHT) {
+        const int at = min(c, a.N - 8) * 4;
+        const f32x4 lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rbias, at, 0, 0));
+        const f32x4 hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rbias, at + 16, 0, 0));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) bias[e] = lo[e], bias[4 + e] = hi[e];
-        } else {
+        for (int e = 0; e < 4; ++e) bias[e] = lo[e], bias[4 + e] = hi[e];
+      } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) bias[e] = a.bias[min(c + e, a.N - 1)];
-        }
+        for (int e = 0; e < 8; ++e) bias[e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rbias, min(c + e, a.N - 1) * 4, 0, 0));
       }
       if constexpr (ADD)
 #pragma unroll
@@ -357,7 +356,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_dense_fp4(DenseArgs a) {
     for (; k < groups * 4 - 4; k += 4) group(k, std::false_type{});
     group(k, std::true_type{});
     const bool cut = tile * WC + WC > a.N;
-    if (BIAS && EIGHT && cut) settle_cut(bias, a.N - c);
+    if (EIGHT && cut) settle_cut(bias, a.N - c);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       float v[8], f[8];
@@ -409,46 +408,47 @@ void launch_pack(const void* x, long ldx, int M, int K, el_dtype dtype, uint8_t*
 
 size_t x_lds(int rows, long K) { return rows * (steps_of(K) * 64 + groups_of(K) * 16); }
 
-// How a call is cut: 16 J rows x 16 I columns a wavefront, `passes` column passes of a workgroup.
+// How a call is cut.  A workgroup packs its rows once for all columns it walks over, so columns are
+// split over workgroups only to have 512 of them; 64 rows a workgroup (J = 4) read the weights least
+// often, fewer fill the CUs sooner.  Measured with N = K = 1024, J = 1, 2, 4: 1024 rows 6.3, 7.0,
+// 9.6 us; 8192 rows 18.7, 17.0, 18.0; 32768 rows 59.3, 46.9, 44.8; columns split for 1024 workgroups
+// rather than 512: 4099 rows 15.0 against 13.6, 16384 rows 28.6 against 27.4.
 struct Plan {
-  bool few, packed;  // few rows (J = 1, I = 2); x packed in the workspace
+  int J;        // 16 J rows a workgroup
+  bool packed;  // x is packed in the workspace: its rows would not fit LDS
   int row_blocks, passes;
   long blocks;
 };
 Plan plan_dense(long M, long K, long N) {
   Plan p{};
-  p.few = ceil_div(M, 64) * ceil_div(N, 128) < 512;
-  const int rows = p.few ? 16 : 64, cols = 128;
-  p.packed = x_lds(rows, K) > 150 * 1024;
-  p.row_blocks = static_cast<int>(ceil_div(p.packed ? tile_rows(M) : M, rows));  // packed rows come in whole tiles
-  const long all = ceil_div(N, cols);  // column passes there are
-  const long split = std::min(all, std::max<long>(1, ceil_div(p.few ? 1l << 30 : 1024, p.row_blocks)));
+  p.J = ceil_div(M, 64) >= 512 ? 4 : ceil_div(M, 32) >= 256 ? 2 : 1;
+  p.packed = x_lds(16 * p.J, K) > 150 * 1024;
+  p.row_blocks = static_cast<int>(ceil_div(p.packed ? tile_rows(M) : M, 16 * p.J));  // packed rows come in whole tiles
+  const long all = ceil_div(N, 128);  // column passes there are
+  const long split = std::min(all, std::max<long>(1, ceil_div(512, p.row_blocks)));
   p.passes = static_cast<int>(ceil_div(all, split));
   p.blocks = p.row_blocks * ceil_div(all, p.passes);
   return p;
 }
 
+template <class T, int J, bool XG, bool EIGHT>
+void launch_tiles(const Plan& p, const DenseArgs& a, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(p.blocks));
+  const size_t lds = XG ? 0 : x_lds(16 * J, a.K);
+  if (a.add) hipLaunchKernelGGL((k_dense_fp4<T, J, XG, EIGHT, true>), grid, dim3(kThreads), lds, st, a);
+  else hipLaunchKernelGGL((k_dense_fp4<T, J, XG, EIGHT, false>), grid, dim3(kThreads), lds, st, a);
+}
+template <class T, int J>
+void launch_rows(const Plan& p, const DenseArgs& a, hipStream_t st) {
+  const bool eight = a.K >= 8 && a.N >= 8;
+  if (p.packed) eight ? launch_tiles<T, J, true, true>(p, a, st) : launch_tiles<T, J, true, false>(p, a, st);
+  else eight ? launch_tiles<T, J, false, true>(p, a, st) : launch_tiles<T, J, false, false>(p, a, st);
+}
 template <class T>
 void launch_dense(const Plan& p, const DenseArgs& a, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(p.blocks));
-  const size_t lds = p.packed ? 0 : x_lds(p.few ? 16 : 64, a.K);
-  const bool eight = a.K >= 8 && a.N >= 8;
-#define EL_FP4_ONE(J, XG, EIGHT, ADD, BIAS) \
-  hipLaunchKernelGGL((k_dense_fp4<T, J, XG, EIGHT, ADD, BIAS>), grid, dim3(kThreads), lds, st, a)
-#define EL_FP4(J, XG, EIGHT)                                        \
-  if (a.add && a.bias) EL_FP4_ONE(J, XG, EIGHT, true, true);        \
-  else if (a.add) EL_FP4_ONE(J, XG, EIGHT, true, false);            \
-  else if (a.bias) EL_FP4_ONE(J, XG, EIGHT, false, true);           \
-  else EL_FP4_ONE(J, XG, EIGHT, false, false)
-#define EL_FP4_J(J)                                   \
-  if (p.packed && eight) { EL_FP4(J, true, true); }   \
-  else if (p.packed) { EL_FP4(J, true, false); }      \
-  else if (eight) { EL_FP4(J, false, true); }         \
-  else { EL_FP4(J, false, false); }
-  if (p.few) { EL_FP4_J(1) } else { EL_FP4_J(4) }
-#undef EL_FP4_J
-#undef EL_FP4
-#undef EL_FP4_ONE
+  if (p.J == 4) launch_rows<T, 4>(p, a, st);
+  else if (p.J == 2) launch_rows<T, 2>(p, a, st);
+  else launch_rows<T, 1>(p, a, st);
 }
 
 bool dense_fp4_sizes_ok(int64_t M, int64_t K, int64_t N) {
