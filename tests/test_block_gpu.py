@@ -589,3 +589,129 @@ def test_packed_arrays_past_32_bit_offsets():
     assert torch.equal(y[0], y[-1])
     ref = torch.from_numpy(bp.rounded(np64(x[:1, :4096].contiguous()), False))
     assert torch.equal(y[-1:, :4096].cpu().double(), ref)
+
+
+# ------------------------------------------------------------------------- more of the block norm
+@pytest.mark.parametrize("M,C,ld,gr,dt", [
+    (70_001, 16, 16, 26, "f32"),      # runs of one row and fewer
+    (70_000, 24, 25, 26, "bf16"),     # rows at odd addresses
+    (30_000, 128, 128, 29_999, "f16"),  # two gate rows, each in thousands of slots
+    (40_000, 64, 64, 40_000, "f32"),  # one gate row
+    (2_000, 1024, 1024, 7, "bf16"), (1_500, 1024, 1025, 100, "f16"), (700, 2048, 2048, 3, "f32"),
+    (900, 4096, 4096, 50, "bf16"), (300, 8200, 8200, 11, "f16"), (100_003, 8, 8, 2, "bf16"),
+])
+def test_block_norm_shared_gates(M, C, ld, gr, dt):
+    """Gate rows inside a slot's run of rows, across two and across very many; the last one cut."""
+    t, nm, act = norm_case((M, C, ld, 0, dt, "rms", "layer", "sigmoid", gr, 0.5, True, 0.1))
+    R = -(-M // gr)
+    y, h, dx, df, dg = out(M, C, ld, dt), out(M, C, ld, dt), out(M, C, ld, dt), out(M, C, ld, dt), out(R, C, ld, dt)
+    ps, qs = torch.empty((M, 2), device=DEV), torch.empty((M, 2), device=DEV)
+    g = [torch.full((C,), float("nan"), device=DEV) for _ in range(4)]
+    elf.block_norm_fwd(nm, t["x"], y, h, f=t["f"], gate=t["gate"], post_stats=ps, pre_stats=qs)
+    elf.block_norm_bwd(nm, y, dx, dy=t["dy"], dh=t["dh"], f=t["f"], gate=t["gate"], df=df, dgate=dg, post_stats=ps,
+                       pre_stats=qs, dpost_gamma=g[0], dpost_beta=g[1], dpre_gamma=g[2], dpre_beta=g[3])
+    n = {k: np64(v) for k, v in t.items()}
+    eps = np.float64(np.float32(0.1))
+    ref = bp.block_norm_fwd(n["x"], n["f"], n["gate"], "rms", "layer", n["gp"], n["bp"], n["gq"], n["bq"], act, gr, 0.5, eps, DT[dt])
+    tp.check(y, ref["y"], "y")
+    tp.check(h, ref["h"], "h")
+    ref = bp.block_norm_bwd(n["dy"], n["dh"], np64(y), n["f"], n["gate"], "rms", "layer", n["gp"], n["bp"], n["gq"], n["bq"],
+                            act, gr, 0.5, np64(ps), np64(qs), DT[dt])
+    for k, v in (("dx", dx), ("df", df), ("dgate", dg), ("dpost_gamma", g[0]), ("dpost_beta", g[1]), ("dpre_gamma", g[2]),
+                 ("dpre_beta", g[3])):
+        tp.check(v, ref[k], k)
+    assert all(gap_untouched(v) for v in (y, h, dx, df, dg))
+    dg2 = out(R, C, ld, dt)
+    elf.block_norm_bwd(nm, y, None, dy=t["dy"], dh=t["dh"], f=t["f"], gate=t["gate"], dgate=dg2, post_stats=ps, pre_stats=qs)
+    assert torch.equal(dg, dg2)
+
+
+def test_block_norm_aligned_and_loose_rows_agree():
+    """The same rows at aligned and at odd addresses: the same sums in the same order, the same bits."""
+    M, C = 333, 256
+    t, nm, act = norm_case((M, C, C, 0, "bf16", "layer", "rms", "plain", 5, 0.5, True, 1e-5))
+    got = []
+    for ld, at in ((C, 0), (C + 3, 1)):
+        v = {k: (lambda o: o.copy_(s))(out(s.shape[0], C, ld, "bf16", at)) if s is not None and s.dim() == 2 else s for k, s in t.items()}
+        y, h, dx, df, dg = (out(r, C, ld, "bf16", at) for r in (M, M, M, M, -(-M // 5)))
+        ps, qs = torch.empty((M, 2), device=DEV), torch.empty((M, 2), device=DEV)
+        g = [torch.empty(C, device=DEV) for _ in range(4)]
+        elf.block_norm_fwd(nm, v["x"], y, h, f=v["f"], gate=v["gate"], post_stats=ps, pre_stats=qs)
+        elf.block_norm_bwd(nm, y, dx, dy=v["dy"], dh=v["dh"], f=v["f"], gate=v["gate"], df=df, dgate=dg, post_stats=ps,
+                           pre_stats=qs, dpost_gamma=g[0], dpost_beta=g[1], dpre_gamma=g[2], dpre_beta=g[3])
+        got.append([y, h, dx, df, dg, ps, qs, *g])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_block_norm_gradients_against_differences():
+    """fp32 gradients along random directions against differences of the plain 64-bit forward."""
+    M, C, gr, s = 12, 40, 4, 0.5
+    t, nm, act = norm_case((M, C, C, 0, "f32", "layer", "rms", "sigmoid", gr, s, True, 1e-3))
+    E = lambda *z: torch.empty(z, device=DEV)  # noqa: E731
+    y, h, dx, df, dg, ps, qs = E(M, C), E(M, C), E(M, C), E(M, C), E(3, C), E(M, 2), E(M, 2)
+    g = [E(C) for _ in range(4)]
+    elf.block_norm_fwd(nm, t["x"], y, h, f=t["f"], gate=t["gate"], post_stats=ps, pre_stats=qs)
+    elf.block_norm_bwd(nm, y, dx, dy=t["dy"], dh=t["dh"], f=t["f"], gate=t["gate"], df=df, dgate=dg, post_stats=ps,
+                       pre_stats=qs, dpost_gamma=g[0], dpost_beta=g[1], dpre_gamma=g[2], dpre_beta=g[3])
+    v = {k: np64(a) for k, a in t.items()}
+
+    def loss(**k):
+        w = {**v, **k}
+        o = bp.block_norm_fwd(w["x"], w["f"], w["gate"], "layer", "rms", w["gp"], w["bp"], w["gq"], w["bq"], act, gr, s, 1e-3,
+                              torch.float32)
+        return float((o["y"][0] * v["dy"]).sum() + (o["h"][0] * v["dh"]).sum())
+
+    rng = np.random.default_rng(8)
+    for k, grad in (("x", dx), ("f", df), ("gate", dg), ("gp", g[0]), ("bp", g[1]), ("gq", g[2]), ("bq", g[3])):
+        d = rng.normal(size=v[k].shape)
+        step = 1e-5
+        diff = (loss(**{k: v[k] + step * d}) - loss(**{k: v[k] - step * d})) / (2 * step)
+        # differences are off by the third derivative times 1e-10; the gradients by some 1e3 fp32 steps
+        assert abs((np64(grad) * d).sum() - diff) <= 1e-4 * np.abs(np64(grad) * d).sum(), k
+
+
+# ------------------------------------------------------------------------- more of the dense layer in 4 bits
+@pytest.mark.parametrize("M,K,N,dt", [
+    (9, 18_000, 40, "bf16"), (9_001, 9_700, 264, "f16"), (33_000, 4_900, 136, "bf16"), (33_001, 4_700, 24, "f16"),
+    (70_001, 96, 40, "bf16"), (8_192, 520, 1_032, "bf16"), (20_000, 8, 8, "f16"), (20_000, 7, 300, "bf16"), (500, 300, 7, "bf16"),
+])
+def test_dense_fwd_fp4_forms(M, K, N, dt):
+    """Rows packed before the product and within it, 16, 32 and 64 a workgroup, narrow sizes: against
+    64-bit products of the unpacked operands (packing is tested on its own)."""
+    g = torch.Generator(DEV).manual_seed(M)
+    x = torch.randn((M, K + 1), device=DEV, generator=g).to(DT[dt])[:, 1:]
+    w = (torch.randn((N, K), device=DEV, generator=g) / K**0.5).to(DT[dt])
+    b, r = torch.randn(N, device=DEV, generator=g), torch.randn((M, N), device=DEV, generator=g).to(DT[dt])
+    y = out(M, N, N + 3, dt, 2)
+    w4 = elf.fp4_pack(w, new(True, N, K))
+    elf.dense_fwd_fp4(x, w4, b, y, act="silu", residual=r)
+    xv = elf.fp4_unpack(elf.fp4_pack(x, new(True, M, K)), torch.empty((M, K), device=DEV))
+    wv = elf.fp4_unpack(w4, torch.empty((N, K), device=DEV))
+    wd = wv.double().t().contiguous()
+    for a in range(0, M, 4096):
+        e = min(M, a + 4096)
+        z = xv[a:e].double() @ wd + b.double()
+        s = xv[a:e].double().abs() @ wd.abs() + b.double().abs()
+        act = z * torch.sigmoid(z)
+        ref = act + r[a:e].double()
+        tol = 1.13 * 2 * (-(-K // 128) * 128 + 2) * 2.0**-24 * s + z.abs() * 2.0**-20 + 4 * 2.0**-24 * (act.abs() + ref.abs())
+        tol = tol + ref.abs() * torch.finfo(DT[dt]).eps / 2 * (1 + 2 * torch.finfo(DT[dt]).eps) + torch.finfo(DT[dt]).smallest_normal * torch.finfo(DT[dt]).eps / 2
+        assert bool(((y[a:e].double() - ref).abs() <= tol).all()), a
+    assert gap_untouched(y)
+
+
+def test_a_call_on_another_devices_tensors_is_refused_or_follows_them():
+    """One device here: operands on the host next to device ones are refused by name."""
+    M, C = 4, 32
+    x = torch.randn(M, C, device=DEV)
+    nm = elf.BlockNorm(C)
+    with pytest.raises(ValueError, match="h must be"):
+        elf.block_norm_fwd(nm, x, None, torch.empty(M, C))
+    with pytest.raises(ValueError, match="y must be"):
+        elf.ckpt_act_dropout_fwd(elf.Checkpoint(M, C, DEV), torch.empty(M, C))
+    with pytest.raises(ValueError, match="ckpt must be"):
+        elf.ckpt_pack(x, elf.Checkpoint(M, C + 1, DEV))
+    with pytest.raises(ValueError, match="packed must be"):
+        elf.fp4_pack(x, elf.Checkpoint(M, C, DEV))
+    with pytest.raises(ValueError, match="workspace"):
+        elf.block_norm_bwd(nm, x, torch.empty_like(x), dh=x, pre_stats=torch.empty((M, 2), device=DEV), workspace=torch.empty(64))
