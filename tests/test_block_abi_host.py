@@ -164,6 +164,9 @@ DF = dict(x=A, ldx=2048, M=300, K=2048, wc=A, ws=A, bias=A, N=512, act=1, r=None
     (dict(K=0), INVALID), (dict(N=0), INVALID), (dict(act=4), INVALID), (dict(dt=ec.EL_F32), UNSUPPORTED),
     (dict(dt=44), INVALID), (dict(K=1 << 16, N=1 << 15, ldx=1 << 16, ldy=1 << 15), UNSUPPORTED),
     (dict(M=(1 << 24) + 1, K=1024, N=16), UNSUPPORTED), (dict(M=0, x=None, y=None), OK),
+    # rows too long to be packed within the product
+    (dict(M=16, K=1 << 15, ldx=1 << 15, wk=None), WORKSPACE), (dict(M=16, K=1 << 15, ldx=1 << 15, wk=A + 64), WORKSPACE),
+    (dict(M=16, K=1 << 15, ldx=1 << 15, wkn=1000), WORKSPACE),
 ])
 def test_dense_fwd_fp4_refusals(change, status):
     a = {**DF, **change}

@@ -715,3 +715,50 @@ def test_a_call_on_another_devices_tensors_is_refused_or_follows_them():
         elf.fp4_pack(x, elf.Checkpoint(M, C, DEV))
     with pytest.raises(ValueError, match="workspace"):
         elf.block_norm_bwd(nm, x, torch.empty_like(x), dh=x, pre_stats=torch.empty((M, 2), device=DEV), workspace=torch.empty(64))
+
+
+# ------------------------------------------------------------------------- workspaces of the binding's own
+def own_workspace_calls(stream):
+    r = lambda *s: torch.randn(*s, device=DEV, generator=torch.Generator(DEV).manual_seed(sum(s))).bfloat16()  # noqa: E731
+    M, C, K, N = 5_000, 256, 250, 264
+    nm = elf.BlockNorm(C, "rms", "layer", gate_rows=7)
+    x, dy, f, gate = r(M, C), r(M, C).flip(0).contiguous(), r(M, C) * 2, r(-(-M // 7), C)
+    st = [torch.rand((M, 2), device=DEV, generator=torch.Generator(DEV).manual_seed(k)) for k in range(2)]
+    norm = [torch.empty_like(x), torch.empty_like(x), torch.empty_like(gate), *(torch.empty(C, device=DEV) for _ in range(4))]
+    x8 = elf.ckpt_pack(r(M, K), elf.Checkpoint(M, K, DEV))
+    w, dz = r(N, K), r(M, N)
+    dense = [torch.empty((M, K), dtype=torch.bfloat16, device=DEV), torch.empty((N, K), device=DEV), torch.empty(N, device=DEV)]
+    wide = r(8_200, 9_600)
+    w4, y = elf.fp4_pack(r(24, 9_600), elf.Fp4(24, 9_600, DEV)), torch.empty((8_200, 24), dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    return {
+        "block_norm_bwd": (lambda: elf.block_norm_bwd(nm, x, norm[0], dy=dy, dh=dy, f=f, gate=gate, df=norm[1], dgate=norm[2],
+                                                      post_stats=st[0], pre_stats=st[1], dpost_gamma=norm[3], dpost_beta=norm[4],
+                                                      dpre_gamma=norm[5], dpre_beta=norm[6], stream=stream),
+                           norm, elf.block_norm_bwd_workspace_bytes(nm, M)),
+        "dense_bwd_ckpt": (lambda: elf.dense_bwd_ckpt(x8, w, dz, dense[1], dense[2], dx=dense[0], stream=stream), dense,
+                           elf.dense_bwd_ckpt_workspace_bytes(M, K, N)),
+        "dense_fwd_fp4": (lambda: elf.dense_fwd_fp4(wide, w4, None, y, stream=stream), [y],
+                          elf.dense_fwd_fp4_workspace_bytes(8_200, 9_600, 24)),
+    }
+
+
+@pytest.mark.parametrize("name", ["block_norm_bwd", "dense_bwd_ckpt", "dense_fwd_fp4"])
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_current_streams_allocations_do_not_reach_the_workspace(name, handle):
+    side = torch.cuda.Stream()
+    call, outs, need = own_workspace_calls(None)[name]
+    assert need > 0, "the case needs a workspace"
+    call()
+    want = [t.clone() for t in outs]
+    call, outs, need = own_workspace_calls(side.cuda_stream if handle else side)[name]
+    filler = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):  # work of some milliseconds in front of the call
+        for _ in range(40):
+            filler.fill_(1)
+    call()
+    junk = [torch.empty(n, dtype=torch.uint8, device=DEV).fill_(255) for n in (need, need, need // 2 + 512)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs))
+    assert all(bool((t == 255).all()) for t in junk)
