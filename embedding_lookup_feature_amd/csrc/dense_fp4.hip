@@ -217,13 +217,17 @@ __device__ inline void settle_cut(float (&v)[8], int n) {
       for (int e = 0; e + b < 8; ++e) v[e] = v[e + b];
 }
 
-// What bounds it, and the shape that follows: loads and stores share one in-order counter, so every
+// What bounds it, and the shape that follows.  Loads and stores share one in-order counter, so every
 // load is issued at a fixed distance in front of its use, without a branch around it (a wait that
-// cannot count waits for everything, the stores before it too: 124 us against 98).  The weights of
+// cannot count waits for everything, the stores before it too: 124 us against 118).  The weights of
 // the step three ahead, of the next columns where the row ends, are fetched while a step multiplies;
-// the residual during a pass's last three steps.  EIGHT: K and N are at least 8.
+// the residual during a pass's last three steps.  65536 x 1024 x 1024 in bf16 with GELU and a residual
+// take 118 us, 3.4 TB/s of x, residual and y (79 us at a copy's rate); no one part bounds it: without the
+// products it takes 93, without packing 96, without the stores 98, without the residual 97, and the
+// products alone 44.  Three wavefronts a SIMD for J = 4: at four the residual spills (131072 rows 220
+// against 206, 24000 rows 49.6 against 46.4).  EIGHT: K and N are at least 8.
 template <class T, int J, bool XG, bool EIGHT, bool ADD>
-__global__ __launch_bounds__(kThreads, 4) void k_dense_fp4(DenseArgs a) {
+__global__ __launch_bounds__(kThreads, J == 4 ? 3 : 4) void k_dense_fp4(DenseArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [step][J][64 lanes][16], then [group][J][64 lanes][4]
   constexpr int BR = 16 * J, WC = 32;
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
@@ -409,20 +413,28 @@ void launch_pack(const void* x, long ldx, int M, int K, el_dtype dtype, uint8_t*
 size_t x_lds(int rows, long K) { return rows * (steps_of(K) * 64 + groups_of(K) * 16); }
 
 // How a call is cut.  A workgroup packs its rows once for all columns it walks over, so columns are
-// split over workgroups only to have 512 of them; 64 rows a workgroup (J = 4) read the weights least
-// often, fewer fill the CUs sooner.  Measured with N = K = 1024, J = 1, 2, 4: 1024 rows 6.3, 7.0,
-// 9.6 us; 8192 rows 18.7, 17.0, 18.0; 32768 rows 59.3, 46.9, 44.8; columns split for 1024 workgroups
-// rather than 512: 4099 rows 15.0 against 13.6, 16384 rows 28.6 against 27.4.
+// split over workgroups only to have 512 of them; more rows a workgroup (16 J) read the weights less
+// often, fewer fill the CUs sooner.  Measured in us, N = K = 1024, without a residual up to 4096 rows,
+// J = 1, 2, 4: 1024 rows 6.4, 7.2, 9.6; 2048 8.0, 7.9; 4096 11.3, 10.2; 8192 21.9, 18.9, 19.4; 16384
+// 47.9, 37.2, 34.0; 65536 177, 132, 116.  Columns split for 1024 workgroups rather than 512: 4099 rows
+// 15.0 against 13.6, 16384 rows 28.6 against 27.4.
+// Two workgroups' rows must fit a CU's LDS: J = 4 holds 147 KiB at K = 4096, 16384 rows 124, J = 2 91.
+// Rows are packed in the workspace first where they are long: packing in the call, the column
+// splits of few rows pack each row again.  In the call against before it, N = 1024: K = 2048, 1024
+// rows 10.1 and 10.7; K = 4096, 1 row 13.8 and 13.6, 1024 rows 23.4 and 15.8, 2048 rows 25.9 and 20.1,
+// 4096 rows 33.7 and 34.8, 16384 rows 91 and 116; K = 8192, 256 rows 36.4 and 26.6, 4096 rows 69.3 and
+// 64.0, 16384 rows (N = 512) 170 and 155.
 struct Plan {
   int J;        // 16 J rows a workgroup
-  bool packed;  // x is packed in the workspace: its rows would not fit LDS
+  bool packed;  // x is packed in the workspace, not in LDS
   int row_blocks, passes;
   long blocks;
 };
 Plan plan_dense(long M, long K, long N) {
   Plan p{};
-  p.J = ceil_div(M, 64) >= 512 ? 4 : ceil_div(M, 32) >= 256 ? 2 : 1;
-  p.packed = x_lds(16 * p.J, K) > 150 * 1024;
+  p.J = M >= 8192 ? 4 : M >= 2048 ? 2 : 1;
+  p.packed = K > 4096 || (K > 2048 && M < 4096);
+  while (!p.packed && p.J > 1 && x_lds(16 * p.J, K) > 80 * 1024) p.J /= 2;
   p.row_blocks = static_cast<int>(ceil_div(p.packed ? tile_rows(M) : M, 16 * p.J));  // packed rows come in whole tiles
   const long all = ceil_div(N, 128);  // column passes there are
   const long split = std::min(all, std::max<long>(1, ceil_div(512, p.row_blocks)));
