@@ -234,6 +234,7 @@ __global__ __launch_bounds__(kThreads, J == 4 ? 3 : 4) void k_dense_fp4(DenseArg
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rb = blockIdx.x % a.row_blocks, cb = blockIdx.x / a.row_blocks;
   const int row0 = rb * BR, groups = (a.steps + 3) / 4;
+  const int x_frags = (a.M + kTileRows - 1) / kTileRows * 2;
   uint8_t* lsc = lds + a.steps * J * kFrag;
   if constexpr (!XG) {
     // 16 lanes pack the 128 columns of a step of one row
@@ -333,7 +334,7 @@ __global__ __launch_bounds__(kThreads, J == 4 ? 3 : 4) void k_dense_fp4(DenseArg
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if constexpr (XG) {
-          const long f = rb * J + j;
+          const long f = min(rb * J + j, x_frags - 1);  // (64 rows may end behind the last tile)
           x[j] = *reinterpret_cast<const u32x4*>(a.xc + (((f >> 1) * a.steps + k) * 2 + (f & 1)) * kFrag + lane * 16);
           if (SEL == 0) xsc[j] = *reinterpret_cast<const uint32_t*>(a.xs + (((f >> 1) * groups + (k >> 2)) * 2 + (f & 1)) * 256 + lane * 4);
         } else {

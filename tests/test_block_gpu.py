@@ -762,3 +762,17 @@ def test_current_streams_allocations_do_not_reach_the_workspace(name, handle):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, outs))
     assert all(bool((t == 255).all()) for t in junk)
+
+
+def test_dense_fwd_fp4_packed_rows_end_in_half_a_workgroup():
+    """Rows packed first, an odd number of tiles of 32 rows, 64 rows a workgroup: the tile behind the
+    last is not read (the workspace ends with the last)."""
+    M, K, N = 8_200, 4_200, 24
+    g = torch.Generator(DEV).manual_seed(1)
+    x, w = torch.randn((M, K), device=DEV, generator=g).bfloat16(), torch.randn((N, K), device=DEV, generator=g).bfloat16()
+    w4, need = elf.fp4_pack(w, new(True, N, K)), elf.dense_fwd_fp4_workspace_bytes(M, K, N)
+    room = torch.full((need + 65_536,), 0xFF, dtype=torch.uint8, device=DEV)
+    y, cut = out(M, N, N, "bf16"), out(8, N, N, "bf16")
+    elf.dense_fwd_fp4(x, w4, None, y, workspace=room[:need])
+    elf.dense_fwd_fp4(x[-8:], w4, None, cut)
+    assert torch.equal(y[-8:], cut) and bool((room[need:] == 0xFF).all())
