@@ -147,8 +147,6 @@ __device__ inline void row_stats(const float (&v)[SL::NV][8], uint32_t kind, con
   rstd = 1.f / sqrtf(s[0] * a.inv_c + a.eps);
 }
 
-__device__ inline float gate_value(uint32_t act, float u) { return act == EL_GATE_SIGMOID ? sigmoid(u) : u; }
-
 // ---------------------------------------------------------------------------------------
 // Views of one operand's rows: init() and at() fix this lane's slot's row of the view and its
 // columns, span() the rows that the view covers, load() and store() row `t` behind the slot's row.

@@ -195,6 +195,11 @@ __global__ __launch_bounds__(SL::THREADS, SL::THREADS > 256 ? 4 : SL::NV > 1 ? 2
       if (left > 0) {
         vg.load(vg.span(g0, span_gates, a.C), rg);
         gate_values();
+      } else {  // (an infinite gate times the zeros of a step behind this slot's last row)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[j][e] = 0.f;
       }
     }
   }

@@ -46,10 +46,6 @@ __device__ inline uint32_t quad_max(uint32_t v) {
   v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xf, 0xf, true)));  // lane ^ 1
   return max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xf, 0xf, true)));  // lane ^ 2
 }
-__device__ inline uint32_t quad_or(uint32_t v) {
-  v |= static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xf, 0xf, true));
-  return v | static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xf, 0xf, true));
-}
 
 // This lane's eight columns of a block held by four neighbouring lanes, as 8-bit codes; the block's
 // scale byte to `byte`.

@@ -776,3 +776,16 @@ def test_dense_fwd_fp4_packed_rows_end_in_half_a_workgroup():
     elf.dense_fwd_fp4(x, w4, None, y, workspace=room[:need])
     elf.dense_fwd_fp4(x[-8:], w4, None, cut)
     assert torch.equal(y[-8:], cut) and bool((room[need:] == 0xFF).all())
+
+
+def test_an_infinite_gate_reaches_its_own_rows_only():
+    """Slots with one row less than their workgroup's first take a step without a row: their last
+    gate row, here infinite, must not meet its zeros."""
+    M, C = 2_050, 1024
+    ones = torch.ones((M, C), device=DEV)
+    gate = torch.ones((M // 2, C), device=DEV)
+    gate[2, 5] = float("inf")  # rows 4 and 5, the third and the fourth slot's only ones
+    nm = elf.BlockNorm(C, post="none", pre="rms", gate_rows=2)
+    dgamma = torch.empty(C, device=DEV)
+    elf.block_norm_bwd(nm, None, None, dy=ones, f=ones, gate=gate, dpost_gamma=dgamma)
+    assert bool(dgamma[5].isposinf()) and bool((torch.cat([dgamma[:5], dgamma[6:]]) == M).all())
