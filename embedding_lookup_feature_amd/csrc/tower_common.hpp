@@ -225,15 +225,18 @@ struct DropArgs {
 
 __device__ inline uint64_t drop_offset(const DropArgs& d) { return d.offset + (d.step ? d.step[0] : 0); }
 
+// a ^ b ^ c in one instruction (a table of three bits; the compiler makes two).
+__device__ inline uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
+
 // The eight 16-bit numbers of columns 8 group .. 8 group + 7 of row `row`, two per word.
 __device__ inline u32x4 philox8(uint32_t group, uint32_t row, uint64_t offset, uint32_t k0, uint32_t k1) {
   uint32_t c0 = group, c1 = row, c2 = static_cast<uint32_t>(offset), c3 = static_cast<uint32_t>(offset >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c0 = xor3(static_cast<uint32_t>(b >> 32), c1, k0);
     c1 = static_cast<uint32_t>(b);
-    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c2 = xor3(static_cast<uint32_t>(a >> 32), c3, k1);
     c3 = static_cast<uint32_t>(a);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;

@@ -89,7 +89,8 @@ EL_API el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64
  *   4 bits: e2m1 (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives), T = 6, two to a byte, the even
  *           column in the low half.  A block that holds a NaN or an infinity has the scale byte 255
  *           and stands for NaN altogether.
- * Columns behind the last are zeros up to the padded width Kp, so rows hold whole blocks.
+ * Magnitudes that round to 2^128 (from 2^128 (1 - 2^-5) in 8 bits, 2^128 (1 - 2^-3) in 4) stand for
+ * infinity in fp32.  Columns behind the last are zeros up to the padded width Kp: whole blocks.
  *   8 bits: codes [M][Kp], scales [M][Kp / 32], Kp = K rounded up to 32.
  *   4 bits: in the order that the matrix instructions take, rows padded with zeros to 32, Kp = K
  *           rounded up to 128 for the codes and to 512 for the scales.  Codes [M / 32][Kp / 128][2]
