@@ -41,11 +41,11 @@ struct BwdPlan {
   int64_t span;  // rows of a workgroup where gate rows are shared
   size_t gate_bytes, bytes;
 };
-BwdPlan plan_bwd(int M, int C, int gate_rows) {
+BwdPlan plan_bwd(int M, int C, int gate_rows, bool lean) {
   BwdPlan p{};
-  with_slot(C, [&](auto s) {
+  with_bwd_slot(C, lean, [&](auto s) {
     using SL = decltype(s);
-    constexpr int most = SL::THREADS > 256 ? kCus : SL::NV > 1 ? 2 * kCus : 3 * kCus;
+    constexpr int most = kCus * (kBwdWaves<SL> * 4 / SL::WAVES);
     p.grid = static_cast<int>(std::min<long>(most, ceil_div(M, SL::PER_WG)));
     const int64_t slots = static_cast<int64_t>(p.grid) * SL::PER_WG;
     p.span = SL::PER_WG * (M / slots + 1) + 1;
@@ -94,7 +94,7 @@ el_status el_block_norm_fwd(const el_block_norm* p, const void* x, int64_t ldx, 
 
 size_t el_block_norm_bwd_workspace_bytes(int32_t M, int32_t C, int32_t gate_rows) {
   if (M < 1 || C < 1 || C > kMaxCols || gate_rows < 1) return 0;
-  return plan_bwd(M, C, gate_rows).bytes;
+  return std::max(plan_bwd(M, C, gate_rows, false).bytes, plan_bwd(M, C, gate_rows, true).bytes);
 }
 
 el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64_t lddy, const void* dh, int64_t lddh,
@@ -131,22 +131,25 @@ el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64_t lddy
       if (params) hipLaunchKernelGGL(k_zero4, dim3(static_cast<unsigned>(ceil_div(C, 256)), 4), dim3(256), 0, stream, j);
       return check_launch(fn);
     }
-    const BwdPlan pl = plan_bwd(M, C, p->gate_rows);
-    EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, pl.bytes));
+    EL_TRY(tower::check_workspace(fn, workspace, workspace_bytes, el_block_norm_bwd_workspace_bytes(M, C, p->gate_rows)));
     NormArgs a = common(p, M, C);
     a.gate_rows = std::min(p->gate_rows, M);
     a.dy = dy, a.lddy = lddy, a.dh = dh, a.lddh = lddh, a.y_in = y, a.ldy = ldy, a.f = f, a.ldf = ldf, a.gate = gate, a.ldg = ldg;
     a.dx = dx, a.lddx = lddx, a.df = df, a.lddf = lddf, a.dgate = dgate, a.lddg = lddg;
     a.post_stats = const_cast<float*>(post_stats), a.pre_stats = const_cast<float*>(pre_stats);
-    a.gate_part = static_cast<float*>(workspace);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.gate_bytes);
     for (int k = 0; k < 4; ++k) a.want |= j.out[k] ? 1u << k : 0u;
-    j.part = a.part, j.parts = pl.grid;
+    const BwdPlan plans[2] = {plan_bwd(M, C, p->gate_rows, false), plan_bwd(M, C, p->gate_rows, true)};
+    const int64_t span = std::max(plans[0].span, plans[1].span);
     const bool shared = gate && a.gate_rows > 1;
-    const auto ok = [&](const void* q, int64_t ld) { return aligned_rows(q, ld, e, shared ? pl.span : kMaxPerWg); };
+    const auto ok = [&](const void* q, int64_t ld) { return aligned_rows(q, ld, e, shared ? span : kMaxPerWg); };
     const bool aligned = C <= kMaxAlignedCols && C % 8 == 0 && ok(dy, lddy) && ok(dh, lddh) && ok(y, ldy) && ok(f, ldf) &&
                          ok(gate, ldg) && ok(dx, lddx) && ok(df, lddf) && ok(dgate, lddg);
-    with_type(dtype, [&](auto t) { launch_norm_bwd<decltype(t)>(a, aligned, shared, pl.grid, stream); });
+    const bool lean = aligned && !a.bp && !dpost_beta && !dpre_beta;
+    const BwdPlan& pl = plans[lean];
+    a.gate_part = static_cast<float*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.gate_bytes);
+    j.part = a.part, j.parts = pl.grid;
+    with_type(dtype, [&](auto t) { launch_norm_bwd<decltype(t)>(a, aligned, lean, shared, pl.grid, stream); });
     if (params) hipLaunchKernelGGL(k_join_params, dim3(static_cast<unsigned>(ceil_div(C, 16)), 4), dim3(256), 0, stream, j);
     return check_launch(fn);
   });

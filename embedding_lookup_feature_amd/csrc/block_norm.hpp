@@ -6,11 +6,13 @@
 // to a vector, NV vectors a lane, between the one read of the row and the one write.
 //
 // The kernels see their operands through views, of two kinds.  The aligned view (rows of whole,
-// 16-byte aligned vectors, C <= 4096) is a buffer descriptor of the rows at hand: an operand that is
+// 16-byte aligned vectors, C <= 8192) is a buffer descriptor of the rows at hand: an operand that is
 // left out, a row behind the last and a lane behind the last column all read zeros and write
 // nothing, without a branch, so the number of loads and stores in flight is known at every wait (they
 // share one in-order counter) and the next rows' loads stay in flight behind this row's arithmetic
 // and stores.  The loose view takes any alignment, width and stride with a branch around each access.
+// 65536 x 1024 in bf16, forward and backward: 120 and 201 us through aligned views, 135 and 226 at odd
+// addresses; 426062 x 128: 99 and 167, 149 and 236.
 #pragma once
 
 #include <algorithm>
@@ -39,16 +41,17 @@ struct NormArgs {
 namespace {
 
 constexpr int kMaxCols = 32768;
-constexpr int kMaxAlignedCols = 4096;  // wider rows do not fit the registers of the aligned form
+constexpr int kMaxAlignedCols = 8192;  // wider rows do not fit the registers of the aligned form (one vector a lane)
 
-// A slot: L lanes of one wavefront (W = 1), or W whole wavefronts (L = 64), NV vectors a lane.
+// A slot: L lanes of one wavefront (W = 1), or W whole wavefronts (L = 64), NV vectors a lane.  A
+// workgroup holds PER_WG of them, which go through the same number of rows.
 template <int L_, int W_, int NV_>
 struct Slot {
   static constexpr int L = L_, W = W_, NV = NV_;
   static constexpr int COLS = L * W * NV * 8;
   static constexpr int THREADS = W > 4 ? W * 64 : 256;
   static constexpr int PER_WG = THREADS / (L * W);
-  static_assert(W == 1 || PER_WG == 1, "a slot of several wavefronts is a workgroup");
+  static constexpr int WAVES = THREADS / 64;
 };
 
 // Adds the value of another lane: within 16 lanes by data-parallel-primitive moves (pairs, pairs of
@@ -77,7 +80,7 @@ __device__ inline float lane_sum(float v) {
 
 // Sums of N values over a slot; the same in all its lanes.
 template <class SL, int N>
-__device__ inline void slot_sums(float (&v)[N], float (*lds)[SL::W][2], int& turn) {
+__device__ inline void slot_sums(float (&v)[N], float (*lds)[SL::WAVES][2], int& turn) {
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = lane_sum<SL::L>(v[k]);
   if constexpr (SL::W > 1) {
@@ -89,6 +92,7 @@ __device__ inline void slot_sums(float (&v)[N], float (*lds)[SL::W][2], int& tur
 #pragma unroll
       for (int k = 0; k < N; ++k) b[threadIdx.x >> 6][k] = v[k];
     __syncthreads();
+    if constexpr (SL::PER_WG > 1) b += threadIdx.x / (64 * SL::W) * SL::W;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       float s = b[0][k];
@@ -117,7 +121,7 @@ __device__ inline __amdgpu_buffer_rsrc_t stats_span(const float* p, long first, 
 // Mean and rstd of a slot's row (values past its end are zero).
 template <class SL>
 __device__ inline void row_stats(const float (&v)[SL::NV][8], uint32_t kind, const NormArgs& a, int c0,
-                                 float (*lds)[SL::W][2], int& turn, float& mean, float& rstd) {
+                                 float (*lds)[SL::WAVES][2], int& turn, float& mean, float& rstd) {
   float s[1] = {0.f};
   mean = 0.f;
   if (kind == EL_NORM_LAYER) {
@@ -274,6 +278,27 @@ void with_slot(int C, F&& f) {
   else f(Slot<64, 16, 4>{});
 }
 
+// The backward's slots: one vector a lane as far as possible, for the parameters' sums stay in
+// registers beside the row (65536 rows of 1024 in bf16 with betas: two vectors a lane spill, 386 us, two
+// wavefronts a row take 211; 16384 rows of 4096: 286 and 194).  Only a wavefront with two vectors of an
+// aligned row without betas (`lean`) fits, and then has no barriers: 65536 rows of 1024 202 us against
+// 206, with gate rows shared by 26 169 against 179.
+template <class F>
+void with_bwd_slot(int C, bool lean, F&& f) {
+  const int v = (C + 7) / 8;
+  if (v <= 64 || (lean && v <= 128)) with_slot(C, f);
+  else if (v <= 128) f(Slot<64, 2, 1>{});
+  else if (v <= 256) f(Slot<64, 4, 1>{});
+  else if (v <= 512) f(Slot<64, 8, 1>{});
+  else with_slot(C, f);
+}
+template <class SL>
+constexpr bool kLeanOnly = SL::W == 1 && SL::NV == 2;
+// Wavefronts a SIMD that the backward's registers leave room for.  (Eight to a row: one workgroup a CU;
+// with two, 128 registers a lane, 16384 rows of 4096 with betas spill: 447 us.)
+template <class SL>
+constexpr int kBwdWaves = SL::W == 16 ? 4 : SL::W == 8 || SL::NV == 2 ? 2 : 3;
+
 template <class F>
 void with_type(el_dtype dtype, F&& f) {
   if (dtype == EL_F32) f(F32T{});
@@ -320,6 +345,6 @@ bool aligned_rows(const void* p, int64_t ld, size_t elem, int64_t rows) {
 template <class T>
 void launch_norm_fwd(const NormArgs& a, bool aligned, hipStream_t st);
 template <class T>
-void launch_norm_bwd(const NormArgs& a, bool aligned, bool shared, int grid, hipStream_t st);
+void launch_norm_bwd(const NormArgs& a, bool aligned, bool lean, bool shared, int grid, hipStream_t st);
 
 }  // namespace el

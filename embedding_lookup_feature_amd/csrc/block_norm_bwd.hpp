@@ -1,5 +1,12 @@
 // block_norm_bwd.hpp -- the block norm's backward: gradients of both norms' inputs, of the gate and
 // of the parameters in one pass over the rows (formulas in embblock.h).
+//
+// Memory bounds it: five rows are read (dy, dh, y, f, gate) and three written (dx, df, dgate) for some 90
+// operations a value, so every row is in registers between its one read and its one write, and the
+// parameters' sums stay there over all rows of a slot.  65536 x 1024 in bf16 with a gate: 201 us, 5.3
+// TB/s, at the rate of a copy; gate rows shared by 26 rows of 128 (426062 rows, fp16, layer norms with
+// betas): 144 us, 4.6 TB/s, 1.1 of the copy's time.  Before the views, the runs of rows and the lane sums it took
+// 450 and 328 us.
 #pragma once
 
 #include "block_norm.hpp"
@@ -10,7 +17,7 @@ namespace {
 // Gradient at a norm's input from g, the one at its output (gamma in it), and the normalised row.
 template <class SL>
 __device__ inline void norm_grad(float (&g)[SL::NV][8], const float (&vh)[SL::NV][8], uint32_t kind, float rstd,
-                                 const NormArgs& a, float (*lds)[SL::W][2], int& turn) {
+                                 const NormArgs& a, float (*lds)[SL::WAVES][2], int& turn) {
   float s[2] = {0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < SL::NV; ++j)
@@ -43,8 +50,8 @@ __device__ inline int slot_of_row(int r, int slots, int M) {
 // (gate_part[slot][0] where the gate row began before this slot, [1] where it begins here).  Not
 // SHARED: a workgroup's slots take consecutive rows, and every row has its own gate row, if any.
 template <class T, class SL, template <class, class> class View, bool SHARED, bool BETA>
-__global__ __launch_bounds__(SL::THREADS, SL::THREADS > 256 ? 4 : SL::NV > 1 ? 2 : 3) void k_norm_bwd(NormArgs a) {
-  __shared__ float lds[2][SL::W][2];
+__global__ __launch_bounds__(SL::THREADS, kBwdWaves<SL>) void k_norm_bwd(NormArgs a) {
+  __shared__ float lds[2][SL::WAVES][2];
   __shared__ float join[SL::PER_WG > 1 ? SL::THREADS * SL::NV * 8 : 1];
   int turn = 0;
   constexpr int NV = SL::NV, PER = SL::PER_WG;
@@ -218,7 +225,7 @@ __global__ __launch_bounds__(SL::THREADS, SL::THREADS > 256 ? 4 : SL::NV > 1 ? 2
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) join[sl * SL::COLS + c0 + j * SL::L * 8 + e] = acc[j][e];
+        for (int e = 0; e < 8; ++e) join[sl * SL::COLS + c0 + j * SL::L * SL::W * 8 + e] = acc[j][e];
       __syncthreads();
       for (int c = threadIdx.x; c < SL::COLS && c < a.C; c += SL::THREADS) {
         float s = join[c];
@@ -268,10 +275,13 @@ __global__ __launch_bounds__(256) void k_join_gate(NormArgs a, int gates, int sl
   finish_gate<T>(a, r, c, v);
 }
 // The same where a gate row lies in many slots: a workgroup takes eight columns of a gate row, thread
-// p the slots s0 + p, s0 + p + 256, ...; the threads' sums are added by halves.
+// p the slots s0 + p, s0 + p + 256, ...; the threads' sums are added by halves.  (One gate row for 65536
+// rows of 16: 81 us of 94, what one CU reads.  1024 threads: 102, and 219 against 174 for 64 gate rows of
+// 1024 columns.)
+constexpr int kLong = 256;
 template <class T>
-__global__ __launch_bounds__(256) void k_join_gate_long(NormArgs a, int slots) {
-  __shared__ float red[256][9];
+__global__ __launch_bounds__(kLong) void k_join_gate_long(NormArgs a, int slots) {
+  __shared__ float red[kLong][9];
   const int vecs = (a.C + 7) / 8;
   const long r = blockIdx.x / vecs;
   const int c = static_cast<int>(blockIdx.x - r * vecs) * 8, p = threadIdx.x;
@@ -279,7 +289,8 @@ __global__ __launch_bounds__(256) void k_join_gate_long(NormArgs a, int slots) {
   const int s1 = slot_of_row(static_cast<int>(min((r + 1) * a.gate_rows, static_cast<long>(a.M)) - 1), slots, a.M);
   if (s0 == s1) return;
   float v[8] = {};
-  for (int s = s0 + p; s <= s1; s += 256) {
+#pragma unroll 4
+  for (int s = s0 + p; s <= s1; s += kLong) {
     float q[8];
     to_floats<F32T>(load8_raw<F32T>(a.gate_part + (2l * s + (s == s0)) * a.C + c, a.C - c), q);
 #pragma unroll
@@ -287,7 +298,7 @@ __global__ __launch_bounds__(256) void k_join_gate_long(NormArgs a, int slots) {
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[p][e] = v[e];
-  for (int h = 128; h > 0; h >>= 1) {
+  for (int h = kLong / 2; h > 0; h >>= 1) {
     __syncthreads();
     if (p < h)
 #pragma unroll
@@ -309,25 +320,25 @@ void launch_one_bwd(const NormArgs& a, bool shared, int grid, hipStream_t st) {
 }  // namespace
 
 template <class T>
-void launch_norm_bwd(const NormArgs& a, bool aligned, bool shared, int grid, hipStream_t st) {
-  with_slot(a.C, [&](auto s) {
+void launch_norm_bwd(const NormArgs& a, bool aligned, bool lean, bool shared, int grid, hipStream_t st) {
+  with_bwd_slot(a.C, lean, [&](auto s) {
     using SL = decltype(s);
     if constexpr (SL::COLS <= kMaxAlignedCols) {
-      if (aligned) {
-        if (a.bp || (a.want & 10u)) launch_one_bwd<T, SL, Aligned, true>(a, shared, grid, st);
-        else launch_one_bwd<T, SL, Aligned, false>(a, shared, grid, st);
-        return;
-      }
+      if (lean) return launch_one_bwd<T, SL, Aligned, false>(a, shared, grid, st);
+      if constexpr (!kLeanOnly<SL>)
+        if (aligned) return launch_one_bwd<T, SL, Aligned, true>(a, shared, grid, st);
     }
-    launch_one_bwd<T, SL, Loose, true>(a, shared, grid, st);
+    if constexpr (!kLeanOnly<SL>) launch_one_bwd<T, SL, Loose, true>(a, shared, grid, st);
   });
   if (!shared || !a.dgate) return;
   int per = 1;
-  with_slot(a.C, [&](auto s) { per = decltype(s)::PER_WG; });
+  with_bwd_slot(a.C, lean, [&](auto s) { per = decltype(s)::PER_WG; });
   const int slots = grid * per, gates = static_cast<int>(ceil_div(a.M, a.gate_rows));
   const long vecs = (a.C + 7) / 8;
-  // a gate row in more than 16 slots is worth a workgroup
-  if (slots / gates > 16) hipLaunchKernelGGL((k_join_gate_long<T>), dim3(static_cast<unsigned>(gates * vecs)), dim3(256), 0, st, a, slots);
+  // A gate row in more than 32 slots is worth a workgroup: the backward of 426062 x 128 in bf16 with a
+  // gate row's slots joined by a thread and by a workgroup: 6 slots each 142 and 184 us, 29 slots 149 and
+  // 150, 1170 slots 515 and 145.
+  if (slots / gates > 32) hipLaunchKernelGGL((k_join_gate_long<T>), dim3(static_cast<unsigned>(gates * vecs)), dim3(kLong), 0, st, a, slots);
   else hipLaunchKernelGGL((k_join_gate<T>), dim3(static_cast<unsigned>(ceil_div(gates * vecs, 256))), dim3(256), 0, st, a, gates, slots);
 }
 

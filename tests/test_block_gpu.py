@@ -789,3 +789,34 @@ def test_an_infinite_gate_reaches_its_own_rows_only():
     dgamma = torch.empty(C, device=DEV)
     elf.block_norm_bwd(nm, None, None, dy=ones, f=ones, gate=gate, dpost_gamma=dgamma)
     assert bool(dgamma[5].isposinf()) and bool((torch.cat([dgamma[:5], dgamma[6:]]) == M).all())
+
+
+@pytest.mark.parametrize("M,C,ex,beta,gr", [
+    (3_001, 1000, 0, False, 1), (3_001, 1000, 0, True, 1), (3_001, 1000, 1, True, 7), (2_500, 600, 0, True, 300),
+    (1_700, 4000, 0, True, 1), (1_700, 4000, 8, False, 5), (1_300, 3001, 1, True, 3), (600, 8192, 0, False, 1),
+    (600, 8000, 8, True, 9),
+])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_block_norm_rows_of_several_wavefronts(M, C, ex, beta, gr, dt):
+    """Two, eight and sixteen wavefronts a row, one and two rows a workgroup, with betas and without."""
+    t, nm, act = norm_case((M, C, C + ex, 0, dt, "layer", "layer", "sigmoid", gr, 0.5, beta, 1e-5))
+    R = -(-M // gr)
+    y, h, dx, df, dg = out(M, C, C + ex, dt), out(M, C, C + ex, dt), out(M, C, C + ex, dt), out(M, C, C + ex, dt), out(R, C, C + ex, dt)
+    ps, qs = torch.empty((M, 2), device=DEV), torch.empty((M, 2), device=DEV)
+    g = [torch.full((C,), float("nan"), device=DEV) for _ in range(4)]
+    elf.block_norm_fwd(nm, t["x"], y, h, f=t["f"], gate=t["gate"], post_stats=ps, pre_stats=qs)
+    kw = dict(dpost_beta=g[1], dpre_beta=g[3]) if beta else {}
+    elf.block_norm_bwd(nm, y, dx, dy=t["dy"], dh=t["dh"], f=t["f"], gate=t["gate"], df=df, dgate=dg, post_stats=ps,
+                       pre_stats=qs, dpost_gamma=g[0], dpre_gamma=g[2], **kw)
+    n = {k: np64(v) for k, v in t.items()}
+    ref = bp.block_norm_fwd(n["x"], n["f"], n["gate"], "layer", "layer", n["gp"], n["bp"], n["gq"], n["bq"], act, gr, 0.5,
+                            np.float64(np.float32(1e-5)), DT[dt])
+    tp.check(y, ref["y"], "y")
+    tp.check(h, ref["h"], "h")
+    ref = bp.block_norm_bwd(n["dy"], n["dh"], np64(y), n["f"], n["gate"], "layer", "layer", n["gp"], n["bp"], n["gq"], n["bq"],
+                            act, gr, 0.5, np64(ps), np64(qs), DT[dt])
+    got = dict(dx=dx, df=df, dgate=dg, dpost_gamma=g[0], dpre_gamma=g[2])
+    got.update(dict(dpost_beta=g[1], dpre_beta=g[3]) if beta else {})
+    for k, v in got.items():
+        tp.check(v, ref[k], k)
+    assert all(gap_untouched(v) for v in (y, h, dx, df, dg))
