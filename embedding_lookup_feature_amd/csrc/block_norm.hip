@@ -34,18 +34,20 @@ __global__ __launch_bounds__(256) void k_zero4(JoinArgs a) {
   if (c < a.C && a.out[blockIdx.y]) a.out[blockIdx.y][c] = 0.f;
 }
 
-// The backward's grid is a function of the sizes alone (its partial sums are laid out by it): as many
-// workgroups as the registers let run at once.
+// The backward's grid (its partial sums are laid out by it) is a function of the sizes and of the form,
+// aligned rows without betas, aligned rows with betas or loose ones, loose rows with shared gates: as
+// many workgroups as the registers let run at once.
+enum Form { LEAN = 0, PLAIN = 1, FULL = 2 };
 struct BwdPlan {
   int grid;
   int64_t span;  // rows of a workgroup where gate rows are shared
   size_t gate_bytes, bytes;
 };
-BwdPlan plan_bwd(int M, int C, int gate_rows, bool lean) {
+BwdPlan plan_bwd(int M, int C, int gate_rows, Form form) {
   BwdPlan p{};
-  with_bwd_slot(C, lean, [&](auto s) {
+  with_bwd_slot(C, form == LEAN, [&](auto s) {
     using SL = decltype(s);
-    constexpr int most = kCus * (kBwdWaves<SL> * 4 / SL::WAVES);
+    const int most = kCus * ((form == FULL ? kBwdWaves<SL, true> : kBwdWaves<SL, false>) * 4 / SL::WAVES);
     p.grid = static_cast<int>(std::min<long>(most, ceil_div(M, SL::PER_WG)));
     const int64_t slots = static_cast<int64_t>(p.grid) * SL::PER_WG;
     p.span = SL::PER_WG * (M / slots + 1) + 1;
@@ -94,7 +96,9 @@ el_status el_block_norm_fwd(const el_block_norm* p, const void* x, int64_t ldx, 
 
 size_t el_block_norm_bwd_workspace_bytes(int32_t M, int32_t C, int32_t gate_rows) {
   if (M < 1 || C < 1 || C > kMaxCols || gate_rows < 1) return 0;
-  return std::max(plan_bwd(M, C, gate_rows, false).bytes, plan_bwd(M, C, gate_rows, true).bytes);
+  size_t bytes = 0;
+  for (const Form form : {LEAN, PLAIN, FULL}) bytes = std::max(bytes, plan_bwd(M, C, gate_rows, form).bytes);
+  return bytes;
 }
 
 el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64_t lddy, const void* dh, int64_t lddh,
@@ -138,14 +142,14 @@ el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64_t lddy
     a.dx = dx, a.lddx = lddx, a.df = df, a.lddf = lddf, a.dgate = dgate, a.lddg = lddg;
     a.post_stats = const_cast<float*>(post_stats), a.pre_stats = const_cast<float*>(pre_stats);
     for (int k = 0; k < 4; ++k) a.want |= j.out[k] ? 1u << k : 0u;
-    const BwdPlan plans[2] = {plan_bwd(M, C, p->gate_rows, false), plan_bwd(M, C, p->gate_rows, true)};
-    const int64_t span = std::max(plans[0].span, plans[1].span);
     const bool shared = gate && a.gate_rows > 1;
+    // (rows of a workgroup with shared gates: aligned in one form must be aligned in the other)
+    const int64_t span = std::max(plan_bwd(M, C, p->gate_rows, LEAN).span, plan_bwd(M, C, p->gate_rows, PLAIN).span);
     const auto ok = [&](const void* q, int64_t ld) { return aligned_rows(q, ld, e, shared ? span : kMaxPerWg); };
     const bool aligned = C <= kMaxAlignedCols && C % 8 == 0 && ok(dy, lddy) && ok(dh, lddh) && ok(y, ldy) && ok(f, ldf) &&
                          ok(gate, ldg) && ok(dx, lddx) && ok(df, lddf) && ok(dgate, lddg);
     const bool lean = aligned && !a.bp && !dpost_beta && !dpre_beta;
-    const BwdPlan& pl = plans[lean];
+    const BwdPlan pl = plan_bwd(M, C, p->gate_rows, lean ? LEAN : !aligned && shared ? FULL : PLAIN);
     a.gate_part = static_cast<float*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.gate_bytes);
     j.part = a.part, j.parts = pl.grid;

@@ -103,16 +103,6 @@ __device__ inline void slot_sums(float (&v)[N], float (*lds)[SL::WAVES][2], int&
   }
 }
 
-// Columns c .. c+7 of a parameter (`fill` where there is none), zeros from the n-th on.
-__device__ inline void load_vec(const float* p, float fill, int c, int n, float (&v)[8]) {
-  if (p && n > 0) {
-    to_floats<F32T>(load8_raw<F32T>(p + c, n), v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? fill : 0.f;
-  }
-}
-
 // Row statistics are two fp32 numbers a row; absent ones read (0, 0) and are not written.
 __device__ inline __amdgpu_buffer_rsrc_t stats_span(const float* p, long first, int rows) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p) + first * 2, 0, p && rows > 0 ? rows * 8 : 0, 0x00027000);
@@ -153,7 +143,8 @@ __device__ inline void row_stats(const float (&v)[SL::NV][8], uint32_t kind, con
 
 // ---------------------------------------------------------------------------------------
 // Views of one operand's rows: init() and at() fix this lane's slot's row of the view and its
-// columns, span() the rows that the view covers, load() and store() row `t` behind the slot's row.
+// columns, span() the rows that the view covers, load() and store() row `t` behind the slot's row;
+// settle() comes between load() and the use of what it loaded.
 // ---------------------------------------------------------------------------------------
 constexpr uint32_t kNowhere = 0x80000000u;  // behind the end of every view (they are shorter than 2^31)
 constexpr int kStream = 2;                  // non-temporal: rows are read and written once
@@ -188,6 +179,7 @@ struct Aligned {
       for (int w = 0; w < Raw8<T>::W; ++w)
         raw[j].v[w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, place(j, t, valid) + 16 * w, 0, kStream));
   }
+  __device__ inline void settle(Raw8<T> (&)[SL::NV]) const {}
   __device__ inline void store(Span rs, const float (&v)[SL::NV][8], int t = 0, bool valid = true) const {
 #pragma unroll
     for (int j = 0; j < SL::NV; ++j) {
@@ -226,11 +218,16 @@ struct Loose {
 #pragma unroll
     for (int j = 0; j < SL::NV; ++j) {
       const int cj = c + j * SL::L * SL::W * 8;
-      if (s.p && valid && row + t < s.rows && cj < cols) raw[j] = load8_raw<T>(p + cj, cols - cj);
+      if (s.p && valid && row + t < s.rows && cj < cols) raw[j] = cols >= 8 ? load8_cut<T>(p, cj, cols) : load8_raw<T>(p + cj, cols - cj);
       else
 #pragma unroll
         for (int w = 0; w < Raw8<T>::W; ++w) raw[j].v[w] = u32x4{0, 0, 0, 0};
     }
+  }
+  __device__ inline void settle(Raw8<T> (&raw)[SL::NV]) const {
+    if (cols < 8) return;
+#pragma unroll
+    for (int j = 0; j < SL::NV; ++j) settle8<T>(raw[j], c + j * SL::L * SL::W * 8, cols);
   }
   __device__ inline void store(Span s, const float (&v)[SL::NV][8], int t = 0, bool valid = true) const {
     S* p = s.p + (row + t) * ld;
@@ -242,13 +239,19 @@ struct Loose {
   }
 };
 
-// A parameter's columns of this lane, kept over all its rows.
+// A parameter's columns of this lane, kept over all its rows (`fill` where there is none, zeros behind
+// the last column).
 template <class SL>
 __device__ inline void load_param(const float* p, float fill, int c0, int C, float (&v)[SL::NV][8]) {
 #pragma unroll
   for (int j = 0; j < SL::NV; ++j) {
     const int c = c0 + j * SL::L * SL::W * 8;
-    load_vec(p, fill, c, C - c, v[j]);
+    if (p && c < C) {
+      to_floats<F32T>(load8_row<F32T>(p, c, C), v[j]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] = e < C - c ? fill : 0.f;
+    }
   }
 }
 
@@ -260,44 +263,56 @@ constexpr int kCus = 256;
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Calls f with the narrowest slot that holds C columns.
+// Calls f with the narrowest slot that holds v vectors: of at most a wavefront with one vector a lane,
+// and of sixteen wavefronts.
 template <class F>
-void with_slot(int C, F&& f) {
-  const int v = (C + 7) / 8;
+void with_narrow_slot(int v, F&& f) {
   if (v <= 2) f(Slot<2, 1, 1>{});
   else if (v <= 4) f(Slot<4, 1, 1>{});
   else if (v <= 8) f(Slot<8, 1, 1>{});
   else if (v <= 16) f(Slot<16, 1, 1>{});
   else if (v <= 32) f(Slot<32, 1, 1>{});
-  else if (v <= 64) f(Slot<64, 1, 1>{});
-  else if (v <= 128) f(Slot<64, 1, 2>{});
-  else if (v <= 256) f(Slot<64, 4, 1>{});
-  else if (v <= 512) f(Slot<64, 4, 2>{});
-  else if (v <= 1024) f(Slot<64, 16, 1>{});
+  else f(Slot<64, 1, 1>{});
+}
+template <class F>
+void with_wide_slot(int v, F&& f) {
+  if (v <= 1024) f(Slot<64, 16, 1>{});
   else if (v <= 2048) f(Slot<64, 16, 2>{});
   else f(Slot<64, 16, 4>{});
 }
-
-// The backward's slots: one vector a lane as far as possible, for the parameters' sums stay in
-// registers beside the row (65536 rows of 1024 in bf16 with betas: two vectors a lane spill, 386 us, two
+// The forward's slots.
+template <class F>
+void with_slot(int C, F&& f) {
+  const int v = (C + 7) / 8;
+  if (v <= 64) with_narrow_slot(v, f);
+  else if (v <= 128) f(Slot<64, 1, 2>{});
+  else if (v <= 256) f(Slot<64, 4, 1>{});
+  else if (v <= 512) f(Slot<64, 4, 2>{});
+  else with_wide_slot(v, f);
+}
+// The backward's: one vector a lane as far as possible, for the parameters' sums stay in registers
+// beside the row (65536 rows of 1024 in bf16 with betas: two vectors a lane spill, 386 us, two
 // wavefronts a row take 211; 16384 rows of 4096: 286 and 194).  Only a wavefront with two vectors of an
 // aligned row without betas (`lean`) fits, and then has no barriers: 65536 rows of 1024 202 us against
 // 206, with gate rows shared by 26 169 against 179.
 template <class F>
 void with_bwd_slot(int C, bool lean, F&& f) {
   const int v = (C + 7) / 8;
-  if (v <= 64 || (lean && v <= 128)) with_slot(C, f);
+  if (v <= 64) with_narrow_slot(v, f);
+  else if (v <= 128 && lean) f(Slot<64, 1, 2>{});
   else if (v <= 128) f(Slot<64, 2, 1>{});
   else if (v <= 256) f(Slot<64, 4, 1>{});
   else if (v <= 512) f(Slot<64, 8, 1>{});
-  else with_slot(C, f);
+  else with_wide_slot(v, f);
 }
 template <class SL>
 constexpr bool kLeanOnly = SL::W == 1 && SL::NV == 2;
-// Wavefronts a SIMD that the backward's registers leave room for.  (Eight to a row: one workgroup a CU;
-// with two, 128 registers a lane, 16384 rows of 4096 with betas spill: 447 us.)
-template <class SL>
-constexpr int kBwdWaves = SL::W == 16 ? 4 : SL::W == 8 || SL::NV == 2 ? 2 : 3;
+// Wavefronts a SIMD that the backward's registers leave room for.  Eight to a row: one workgroup a CU
+// (with two, 128 registers a lane, 16384 rows of 4096 with betas spill: 447 us).  Loose rows with shared
+// gates (FULL) spill at three: 30000 rows of 1001 228 us against 124; without shared gates three are
+// better, 124 against 147.
+template <class SL, bool FULL>
+constexpr int kBwdWaves = SL::W == 16 ? 4 : SL::W == 8 || SL::NV == 2 || FULL ? 2 : 3;
 
 template <class F>
 void with_type(el_dtype dtype, F&& f) {

@@ -49,8 +49,8 @@ __device__ inline int slot_of_row(int r, int slots, int M) {
 // rows in it: one that lies in the run is finished here, the others are left as partial sums
 // (gate_part[slot][0] where the gate row began before this slot, [1] where it begins here).  Not
 // SHARED: a workgroup's slots take consecutive rows, and every row has its own gate row, if any.
-template <class T, class SL, template <class, class> class View, bool SHARED, bool BETA>
-__global__ __launch_bounds__(SL::THREADS, kBwdWaves<SL>) void k_norm_bwd(NormArgs a) {
+template <class T, class SL, template <class, class> class View, bool SHARED, bool BETA, int WAVES>
+__global__ __launch_bounds__(SL::THREADS, WAVES) void k_norm_bwd(NormArgs a) {
   __shared__ float lds[2][SL::WAVES][2];
   __shared__ float join[SL::PER_WG > 1 ? SL::THREADS * SL::NV * 8 : 1];
   int turn = 0;
@@ -76,6 +76,7 @@ __global__ __launch_bounds__(SL::THREADS, kBwdWaves<SL>) void k_norm_bwd(NormArg
   int grow = 0, left = 0;  // SHARED: gate row of the current row, rows of it left in this slot's run
   const int g0 = SHARED ? wg.first / a.gate_rows : 0, gates = SHARED ? (a.M + a.gate_rows - 1) / a.gate_rows : 0;
   const auto gate_values = [&]() {
+    vg.settle(rg);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       to_floats<T>(rg[j], g[j]);
@@ -131,6 +132,7 @@ __global__ __launch_bounds__(SL::THREADS, kBwdWaves<SL>) void k_norm_bwd(NormArg
     const float mq = __uint_as_float(spre[0]), rq = __uint_as_float(spre[1]);
     const float mp = a.post != EL_NORM_NONE ? __uint_as_float(spost[0]) : 0.f;
     const float rp = a.post != EL_NORM_NONE ? __uint_as_float(spost[1]) : 1.f;
+    vdh.settle(rdh), vy.settle(ry), vf.settle(rf), vdy.settle(rdy);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       to_floats<T>(rdh[j], D[j]), to_floats<T>(ry[j], v[j]), to_floats<T>(rf[j], fh[j]), to_floats<T>(rdy[j], dy[j]);
@@ -245,7 +247,7 @@ template <class T>
 __device__ inline void finish_gate(const NormArgs& a, long r, int c, float (&v)[8]) {
   if (a.gate_act == EL_GATE_SIGMOID) {
     float g[8];
-    to_floats<T>(load8_raw<T>(static_cast<const typename T::S*>(a.gate) + r * a.ldg + c, a.C - c), g);
+    to_floats<T>(load8_row<T>(static_cast<const typename T::S*>(a.gate) + r * a.ldg, c, a.C), g);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float s = sigmoid(g[e]);
@@ -265,10 +267,10 @@ __global__ __launch_bounds__(256) void k_join_gate(NormArgs a, int gates, int sl
   const int s1 = slot_of_row(static_cast<int>(min((r + 1) * a.gate_rows, static_cast<long>(a.M)) - 1), slots, a.M);
   if (s0 == s1) return;
   float v[8];
-  to_floats<F32T>(load8_raw<F32T>(a.gate_part + (2l * s0 + 1) * a.C + c, a.C - c), v);
+  to_floats<F32T>(load8_row<F32T>(a.gate_part + (2l * s0 + 1) * a.C, c, a.C), v);
   for (int s = s0 + 1; s <= s1; ++s) {
     float p[8];
-    to_floats<F32T>(load8_raw<F32T>(a.gate_part + 2l * s * a.C + c, a.C - c), p);
+    to_floats<F32T>(load8_row<F32T>(a.gate_part + 2l * s * a.C, c, a.C), p);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += p[e];
   }
@@ -292,7 +294,7 @@ __global__ __launch_bounds__(kLong) void k_join_gate_long(NormArgs a, int slots)
 #pragma unroll 4
   for (int s = s0 + p; s <= s1; s += kLong) {
     float q[8];
-    to_floats<F32T>(load8_raw<F32T>(a.gate_part + (2l * s + (s == s0)) * a.C + c, a.C - c), q);
+    to_floats<F32T>(load8_row<F32T>(a.gate_part + (2l * s + (s == s0)) * a.C, c, a.C), q);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += q[e];
   }
@@ -313,8 +315,9 @@ __global__ __launch_bounds__(kLong) void k_join_gate_long(NormArgs a, int slots)
 
 template <class T, class SL, template <class, class> class View, bool BETA>
 void launch_one_bwd(const NormArgs& a, bool shared, int grid, hipStream_t st) {
-  if (shared) hipLaunchKernelGGL((k_norm_bwd<T, SL, View, true, BETA>), dim3(grid), dim3(SL::THREADS), 0, st, a);
-  else hipLaunchKernelGGL((k_norm_bwd<T, SL, View, false, BETA>), dim3(grid), dim3(SL::THREADS), 0, st, a);
+  constexpr bool loose = std::is_same_v<View<T, SL>, Loose<T, SL>>;
+  const auto kernel = shared ? k_norm_bwd<T, SL, View, true, BETA, kBwdWaves<SL, loose>> : k_norm_bwd<T, SL, View, false, BETA, kBwdWaves<SL, false>>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(SL::THREADS), 0, st, a);
 }
 
 }  // namespace

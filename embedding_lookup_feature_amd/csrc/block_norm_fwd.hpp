@@ -47,6 +47,7 @@ __global__ __launch_bounds__(SL::THREADS) void k_norm_fwd(NormArgs a) {
   for (; r0 < a.M; r0 += stride) {
     const int rows = static_cast<int>(min(static_cast<long>(PER), a.M - r0));
     float y[NV][8], f[NV][8], g[NV][8];
+    vx.settle(rx), vf.settle(rf), vg.settle(rg);
 #pragma unroll
     for (int j = 0; j < NV; ++j) to_floats<T>(rx[j], y[j]), to_floats<T>(rf[j], f[j]), to_floats<T>(rg[j], g[j]);
     fetch(r0 + stride);

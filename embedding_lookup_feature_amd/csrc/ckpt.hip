@@ -27,7 +27,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_pack(PackArgs a) {
   const uint32_t dr = local / static_cast<uint32_t>(a.groups), grp = local - dr * a.groups;
   const int n = a.K - static_cast<int>(grp) * 8;
   float v[8] = {};
-  if (n > 0) to_floats<T>(load8_raw<T>(static_cast<const S*>(a.x) + (row0 + dr) * a.ldx + grp * 8l, n), v);
+  if (n > 0) to_floats<T>(load8_row<T>(static_cast<const S*>(a.x) + (row0 + dr) * a.ldx, static_cast<int>(grp) * 8, a.K), v);
   uint32_t byte;
   const Codes8 q = pack8(v, byte);
   reinterpret_cast<uint2*>(a.codes)[i] = uint2{q.lo, q.hi};
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void k_ckpt_act(ActArgs a) {
   const uint2 q = reinterpret_cast<const uint2*>(a.codes)[i];
   const uint32_t byte = a.scales[i >> 2];
   float u[8], v[8];
-  if (BWD) to_floats<T>(load8_raw<T>(static_cast<const S*>(a.dy) + row * a.lddy + grp * 8l, n), v);
+  if (BWD) to_floats<T>(load8_row<T>(static_cast<const S*>(a.dy) + row * a.lddy, static_cast<int>(grp) * 8, a.K), v);
   unpack8(q.x, q.y, scale_of(byte), u);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = BWD ? v[e] * slope<T, ACT>(u[e]) : value<T, ACT>(u[e]);

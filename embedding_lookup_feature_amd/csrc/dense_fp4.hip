@@ -188,26 +188,7 @@ __device__ inline f32x4 mfma_fp4(const u32x4& a, uint32_t sa, const u32x4& b, ui
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, SEL, static_cast<int>(sa), SEL, static_cast<int>(sb));
 }
 
-// The n (1 .. 7) last elements of eight, moved to the front, zeros behind them.
-__device__ inline u32x4 last_to_front(u32x4 v, int n) {
-  const int s = 8 - n;
-  if (s & 4) v = u32x4{v[2], v[3], 0, 0};
-  if (s & 2) v = u32x4{v[1], v[2], v[3], 0};
-  if (s & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
-  return v;
-}
-
-// Eight columns from c of a row of `cols` (at least eight) at p, zeros behind its end, by one load
-// without a branch: a vector that the end cuts is loaded from the row's last eight.
-__device__ inline u32x4 load_cut(const uint16_t* p, int c, int cols) {
-  return *reinterpret_cast<const u32x4_any*>(p + min(c, cols - 8));
-}
-__device__ inline u32x4 settle_cut(const u32x4& v, int c, int cols) {
-  const int n = cols - c;
-  if (n >= 8) return v;
-  return n > 0 ? last_to_front(v, n) : u32x4{0, 0, 0, 0};
-}
-
+// The columns of a bias vector that was loaded from the last eight, moved to the front.
 __device__ inline void settle_cut(float (&v)[8], int n) {
   const int s = n > 0 && n < 8 ? 8 - n : 0;
 #pragma unroll
@@ -250,7 +231,7 @@ __global__ __launch_bounds__(kThreads, J == 4 ? 3 : 4) void k_dense_fp4(DenseArg
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if constexpr (EIGHT) {
-          raw[j].v[0] = load_cut(p[j], c, a.K);
+          raw[j] = load8_cut<T>(p[j], c, a.K);
         } else {
           raw[j] = zeros8<T>();
           if (n > 0) raw[j] = load8_raw<T>(p[j] + c, n);
@@ -259,7 +240,7 @@ __global__ __launch_bounds__(kThreads, J == 4 ? 3 : 4) void k_dense_fp4(DenseArg
       const bool cut = k * kPad + kPad > a.K;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        if (EIGHT && cut) raw[j].v[0] = settle_cut(raw[j].v[0], c, a.K);
+        if (EIGHT && cut) settle8<T>(raw[j], c, a.K);
         uint32_t byte;
         const uint32_t w = pack4_raw<T>(raw[j], byte);
         *reinterpret_cast<uint32_t*>(lds + (k * J + j) * kFrag + ((q >> 2) * 16 + u) * 16 + (q & 3) * 4) = w;
@@ -322,7 +303,7 @@ __global__ __launch_bounds__(kThreads, J == 4 ? 3 : 4) void k_dense_fp4(DenseArg
         for (int j = 0; j < J; ++j) {
           const int fr = frag_row(j);  // (a row that does not exist is replaced by the workgroup's first)
           const uint16_t* p = a.add + (lrow < a.M - fr ? fr * a.ldadd + add_lane : min(row0, a.M - 1) * a.ldadd);
-          if constexpr (EIGHT) add[j].v[0] = load_cut(p, cm, a.N);
+          if constexpr (EIGHT) add[j] = load8_cut<T>(p, cm, a.N);
           else if (cm < a.N) add[j] = load8_raw<T>(p + cm, a.N - cm);
         }
     };
@@ -370,7 +351,7 @@ __global__ __launch_bounds__(kThreads, J == 4 ? 3 : 4) void k_dense_fp4(DenseArg
       act8(a.act, v);
       if constexpr (ADD) {
         Raw8<T> mine = add[j];
-        if (EIGHT && cut) mine.v[0] = settle_cut(mine.v[0], cm, a.N);
+        if (EIGHT && cut) settle8<T>(mine, cm, a.N);
         mine.v[0] = lanes_from(l16 * 4 + g, mine.v[0]);
         to_floats<T>(mine, f);
 #pragma unroll

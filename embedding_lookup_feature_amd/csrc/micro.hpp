@@ -109,6 +109,42 @@ __device__ inline void unpack4(uint32_t q, uint32_t byte, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(0x7fc00000u);
 }
 
+// Eight columns from c of a row of `cols` (at least eight), by whole loads without a branch: a vector
+// that the row's end cuts is loaded from the row's last eight, and settle8 moves its columns to the front,
+// zeros behind them (all zeros from c = cols on).  Apart, so that the load can be in flight meanwhile.
+template <class T>
+__device__ inline Raw8<T> load8_cut(const typename T::S* row, int c, int cols) {
+  return load8_raw<T>(row + min(c, cols - 8));
+}
+template <class T>
+__device__ inline void settle8(Raw8<T>& r, int c, int cols) {
+  const int s = c + 8 - cols;
+  if (s <= 0) return;
+  if constexpr (Raw8<T>::W == 2) {
+    uint32_t w[8] = {r.v[0][0], r.v[0][1], r.v[0][2], r.v[0][3], r.v[1][0], r.v[1][1], r.v[1][2], r.v[1][3]};
+#pragma unroll
+    for (int b = 4; b; b >>= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = s & b ? (e + b < 8 ? w[(e + b) & 7] : 0u) : w[e];
+    r.v[0] = s < 8 ? u32x4{w[0], w[1], w[2], w[3]} : u32x4{0, 0, 0, 0};
+    r.v[1] = s < 8 ? u32x4{w[4], w[5], w[6], w[7]} : u32x4{0, 0, 0, 0};
+  } else {
+    u32x4 v = r.v[0];
+    if (s & 4) v = u32x4{v[2], v[3], 0, 0};
+    if (s & 2) v = u32x4{v[1], v[2], v[3], 0};
+    if (s & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    r.v[0] = s < 8 ? v : u32x4{0, 0, 0, 0};
+  }
+}
+// The same at once, of a row of any width; c < cols.
+template <class T>
+__device__ inline Raw8<T> load8_row(const typename T::S* row, int c, int cols) {
+  if (cols < 8) return load8_raw<T>(row + c, cols - c);
+  Raw8<T> r = load8_cut<T>(row, c, cols);
+  settle8<T>(r, c, cols);
+  return r;
+}
+
 // The first n of eight values, a whole vector in 16-bit pairs.
 template <class T>
 __device__ inline void put_whole8(typename T::S* p, const float (&v)[8], int n) {
