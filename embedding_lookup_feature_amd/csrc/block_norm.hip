@@ -1,33 +1,8 @@
-// block_norm.hip -- the block norm's entry points: checks, the backward's plan, and the parameters'
-// gradients joined.
+// block_norm.hip -- the block norm's entry points: checks and the backward's plan.
 #include "block_norm.hpp"
 
 namespace el {
 namespace {
-
-// out[c] = sum over p < parts of part[p * stride + c], up to four of them: 16 threads share a
-// column's parts (thread s: parts s, s + 16, ...), their sums are added in thread order.
-struct JoinArgs {
-  const float* part;
-  float* out[4];
-  int parts, C;
-};
-__global__ __launch_bounds__(256) void k_join_params(JoinArgs a) {
-  __shared__ float red[16][17];
-  const int col = threadIdx.x & 15, s = threadIdx.x >> 4, k = blockIdx.y;
-  if (!a.out[k]) return;
-  const int c = blockIdx.x * 16 + col;
-  float v = 0.f;
-  if (c < a.C)
-#pragma unroll 4
-    for (int p = s; p < a.parts; p += 16) v += a.part[(static_cast<long>(p) * 4 + k) * a.C + c];
-  red[s][col] = v;
-  __syncthreads();
-  if (s == 0 && c < a.C) {
-    for (int i = 1; i < 16; ++i) v += red[i][col];
-    a.out[k][c] = v;
-  }
-}
 
 __global__ __launch_bounds__(256) void k_zero4(JoinArgs a) {
   const int c = blockIdx.x * 256 + threadIdx.x;
@@ -153,8 +128,7 @@ el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64_t lddy
     a.gate_part = static_cast<float*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.gate_bytes);
     j.part = a.part, j.parts = pl.grid;
-    with_type(dtype, [&](auto t) { launch_norm_bwd<decltype(t)>(a, aligned, lean, shared, pl.grid, stream); });
-    if (params) hipLaunchKernelGGL(k_join_params, dim3(static_cast<unsigned>(ceil_div(C, 16)), 4), dim3(256), 0, stream, j);
+    with_type(dtype, [&](auto t) { launch_norm_bwd<decltype(t)>(a, j, aligned, lean, shared, pl.grid, stream); });
     return check_launch(fn);
   });
 }

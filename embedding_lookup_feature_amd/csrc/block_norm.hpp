@@ -38,6 +38,13 @@ struct NormArgs {
   uint32_t want;     // bit k: parameter sum k is asked for
 };
 
+// out[k][c] = sum over p < parts of part[(p * 4 + k) * C + c], for the k that are asked for.
+struct JoinArgs {
+  const float* part;
+  float* out[4];
+  int parts, C;
+};
+
 namespace {
 
 constexpr int kMaxCols = 32768;
@@ -360,6 +367,6 @@ bool aligned_rows(const void* p, int64_t ld, size_t elem, int64_t rows) {
 template <class T>
 void launch_norm_fwd(const NormArgs& a, bool aligned, hipStream_t st);
 template <class T>
-void launch_norm_bwd(const NormArgs& a, bool aligned, bool lean, bool shared, int grid, hipStream_t st);
+void launch_norm_bwd(const NormArgs& a, const JoinArgs& j, bool aligned, bool lean, bool shared, int grid, hipStream_t st);
 
 }  // namespace el

@@ -5,7 +5,7 @@
 // operations a value, so every row is in registers between its one read and its one write, and the
 // parameters' sums stay there over all rows of a slot.  65536 x 1024 in bf16 with a gate: 201 us, 5.3
 // TB/s, at the rate of a copy; gate rows shared by 26 rows of 128 (426062 rows, fp16, layer norms with
-// betas): 144 us, 4.6 TB/s, 1.1 of the copy's time.  Before the views, the runs of rows and the lane sums it took
+// betas): 141 us, 4.75 TB/s, 1.08 of the copy's time.  Before the views, the runs of rows and the lane sums it took
 // 450 and 328 us.
 #pragma once
 
@@ -241,6 +241,8 @@ __global__ __launch_bounds__(SL::THREADS, WAVES) void k_norm_bwd(NormArgs a) {
   if constexpr (BETA) put(1, acc_bp), put(3, acc_bq);
 }
 
+constexpr int kJoin = 256;
+
 // dgate of the gate rows that lie in several slots: their partial sums in slot order, times the
 // gate's derivative.  A thread takes eight columns of a gate row (few partial sums a row).
 template <class T>
@@ -257,9 +259,9 @@ __device__ inline void finish_gate(const NormArgs& a, long r, int c, float (&v)[
   store8<T>(static_cast<typename T::S*>(a.dgate) + r * a.lddg + c, v, a.C - c);
 }
 template <class T>
-__global__ __launch_bounds__(256) void k_join_gate(NormArgs a, int gates, int slots) {
+__device__ inline void join_gate(const NormArgs& a, unsigned block, int gates, int slots) {
   const int vecs = (a.C + 7) / 8;
-  const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  const long i = static_cast<long>(block) * kJoin + threadIdx.x;
   const long r = i / vecs;
   if (r >= gates) return;
   const int c = static_cast<int>(i - r * vecs) * 8;
@@ -280,19 +282,17 @@ __global__ __launch_bounds__(256) void k_join_gate(NormArgs a, int gates, int sl
 // p the slots s0 + p, s0 + p + 256, ...; the threads' sums are added by halves.  (One gate row for 65536
 // rows of 16: 81 us of 94, what one CU reads.  1024 threads: 102, and 219 against 174 for 64 gate rows of
 // 1024 columns.)
-constexpr int kLong = 256;
 template <class T>
-__global__ __launch_bounds__(kLong) void k_join_gate_long(NormArgs a, int slots) {
-  __shared__ float red[kLong][9];
+__device__ inline void join_gate_long(const NormArgs& a, unsigned block, int slots, float (*red)[9]) {
   const int vecs = (a.C + 7) / 8;
-  const long r = blockIdx.x / vecs;
-  const int c = static_cast<int>(blockIdx.x - r * vecs) * 8, p = threadIdx.x;
+  const long r = block / vecs;
+  const int c = static_cast<int>(block - r * vecs) * 8, p = threadIdx.x;
   const int s0 = slot_of_row(static_cast<int>(r * a.gate_rows), slots, a.M);
   const int s1 = slot_of_row(static_cast<int>(min((r + 1) * a.gate_rows, static_cast<long>(a.M)) - 1), slots, a.M);
   if (s0 == s1) return;
   float v[8] = {};
 #pragma unroll 4
-  for (int s = s0 + p; s <= s1; s += kLong) {
+  for (int s = s0 + p; s <= s1; s += kJoin) {
     float q[8];
     to_floats<F32T>(load8_row<F32T>(a.gate_part + (2l * s + (s == s0)) * a.C, c, a.C), q);
 #pragma unroll
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(kLong) void k_join_gate_long(NormArgs a, int slots)
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[p][e] = v[e];
-  for (int h = kLong / 2; h > 0; h >>= 1) {
+  for (int h = kJoin / 2; h > 0; h >>= 1) {
     __syncthreads();
     if (p < h)
 #pragma unroll
@@ -311,6 +311,32 @@ __global__ __launch_bounds__(kLong) void k_join_gate_long(NormArgs a, int slots)
     for (int e = 0; e < 8; ++e) v[e] = red[0][e];
     finish_gate<T>(a, r, c, v);
   }
+}
+// Sixteen columns of one parameter: 16 threads share a column's parts (thread s: parts s, s + 16, ...),
+// their sums are added in thread order.
+__device__ inline void join_params(const JoinArgs& a, unsigned block, float (*red)[9]) {
+  const int blocks = (a.C + 15) / 16, k = block / blocks;
+  if (!a.out[k]) return;
+  const int col = threadIdx.x & 15, s = threadIdx.x >> 4, c = (block - k * blocks) * 16 + col;
+  float* sums = &red[0][0];  // [16][17]
+  float v = 0.f;
+  if (c < a.C)
+#pragma unroll 4
+    for (int p = s; p < a.parts; p += 16) v += a.part[(static_cast<long>(p) * 4 + k) * a.C + c];
+  sums[s * 17 + col] = v;
+  __syncthreads();
+  if (s == 0 && c < a.C) {
+    for (int i = 1; i < 16; ++i) v += sums[i * 17 + col];
+    a.out[k][c] = v;
+  }
+}
+// All of a call's joins in one launch (a launch of its own for each: 6 us more from call to call).
+template <class T, bool LONG>
+__global__ __launch_bounds__(kJoin) void k_join(NormArgs a, JoinArgs j, unsigned param_blocks, int gates, int slots) {
+  __shared__ float red[kJoin][9];
+  if (blockIdx.x < param_blocks) join_params(j, blockIdx.x, red);
+  else if (LONG) join_gate_long<T>(a, blockIdx.x - param_blocks, slots, red);
+  else join_gate<T>(a, blockIdx.x - param_blocks, gates, slots);
 }
 
 template <class T, class SL, template <class, class> class View, bool BETA>
@@ -323,7 +349,7 @@ void launch_one_bwd(const NormArgs& a, bool shared, int grid, hipStream_t st) {
 }  // namespace
 
 template <class T>
-void launch_norm_bwd(const NormArgs& a, bool aligned, bool lean, bool shared, int grid, hipStream_t st) {
+void launch_norm_bwd(const NormArgs& a, const JoinArgs& j, bool aligned, bool lean, bool shared, int grid, hipStream_t st) {
   with_bwd_slot(a.C, lean, [&](auto s) {
     using SL = decltype(s);
     if constexpr (SL::COLS <= kMaxAlignedCols) {
@@ -333,16 +359,20 @@ void launch_norm_bwd(const NormArgs& a, bool aligned, bool lean, bool shared, in
     }
     if constexpr (!kLeanOnly<SL>) launch_one_bwd<T, SL, Loose, true>(a, shared, grid, st);
   });
-  if (!shared || !a.dgate) return;
+  const unsigned param_blocks = a.want ? 4 * static_cast<unsigned>(ceil_div(a.C, 16)) : 0;
+  const bool join = shared && a.dgate;
+  if (!param_blocks && !join) return;
   int per = 1;
   with_bwd_slot(a.C, lean, [&](auto s) { per = decltype(s)::PER_WG; });
-  const int slots = grid * per, gates = static_cast<int>(ceil_div(a.M, a.gate_rows));
+  const int slots = grid * per, gates = join ? static_cast<int>(ceil_div(a.M, a.gate_rows)) : 0;
   const long vecs = (a.C + 7) / 8;
   // A gate row in more than 32 slots is worth a workgroup: the backward of 426062 x 128 in bf16 with a
   // gate row's slots joined by a thread and by a workgroup: 6 slots each 142 and 184 us, 29 slots 149 and
   // 150, 1170 slots 515 and 145.
-  if (slots / gates > 32) hipLaunchKernelGGL((k_join_gate_long<T>), dim3(static_cast<unsigned>(gates * vecs)), dim3(kLong), 0, st, a, slots);
-  else hipLaunchKernelGGL((k_join_gate<T>), dim3(static_cast<unsigned>(ceil_div(gates * vecs, 256))), dim3(256), 0, st, a, gates, slots);
+  const bool longer = join && slots / gates > 32;
+  const long gate_blocks = longer ? gates * vecs : ceil_div(gates * vecs, kJoin);
+  const auto kernel = longer ? k_join<T, true> : k_join<T, false>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(param_blocks + gate_blocks)), dim3(kJoin), 0, st, a, j, param_blocks, gates, slots);
 }
 
 }  // namespace el

@@ -2,5 +2,5 @@
 #include "block_norm_bwd.hpp"
 
 namespace el {
-template void launch_norm_bwd<F32T>(const NormArgs&, bool, bool, bool, int, hipStream_t);
+template void launch_norm_bwd<F32T>(const NormArgs&, const JoinArgs&, bool, bool, bool, int, hipStream_t);
 }
