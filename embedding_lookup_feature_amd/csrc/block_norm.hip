@@ -10,7 +10,7 @@ __global__ __launch_bounds__(256) void k_zero4(JoinArgs a) {
 }
 
 // The backward's grid (its partial sums are laid out by it) is a function of the sizes and of the form,
-// aligned rows without betas, aligned rows with betas or loose ones, loose rows with shared gates: as
+// aligned 16-bit rows without betas, other rows, loose rows with shared gates: as
 // many workgroups as the registers let run at once.
 enum Form { LEAN = 0, PLAIN = 1, FULL = 2 };
 struct BwdPlan {
@@ -20,7 +20,7 @@ struct BwdPlan {
 };
 BwdPlan plan_bwd(int M, int C, int gate_rows, Form form) {
   BwdPlan p{};
-  with_bwd_slot(C, form == LEAN, [&](auto s) {
+  with_bwd_slot<true>(C, form == LEAN, [&](auto s) {
     using SL = decltype(s);
     const int most = kCus * ((form == FULL ? kBwdWaves<SL, true> : kBwdWaves<SL, false>) * 4 / SL::WAVES);
     p.grid = static_cast<int>(std::min<long>(most, ceil_div(M, SL::PER_WG)));
@@ -124,7 +124,7 @@ el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64_t lddy
     const bool aligned = C <= kMaxAlignedCols && C % 8 == 0 && ok(dy, lddy) && ok(dh, lddh) && ok(y, ldy) && ok(f, ldf) &&
                          ok(gate, ldg) && ok(dx, lddx) && ok(df, lddf) && ok(dgate, lddg);
     const bool lean = aligned && !a.bp && !dpost_beta && !dpre_beta;
-    const BwdPlan pl = plan_bwd(M, C, p->gate_rows, lean ? LEAN : !aligned && shared ? FULL : PLAIN);
+    const BwdPlan pl = plan_bwd(M, C, p->gate_rows, lean && e == 2 ? LEAN : !aligned && shared ? FULL : PLAIN);
     a.gate_part = static_cast<float*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.gate_bytes);
     j.part = a.part, j.parts = pl.grid;

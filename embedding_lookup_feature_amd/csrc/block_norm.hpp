@@ -300,14 +300,18 @@ void with_slot(int C, F&& f) {
 // The backward's: one vector a lane as far as possible, for the parameters' sums stay in registers
 // beside the row (65536 rows of 1024 in bf16 with betas: two vectors a lane spill, 386 us, two
 // wavefronts a row take 211; 16384 rows of 4096: 286 and 194).  Only a wavefront with two vectors of an
-// aligned row without betas (`lean`) fits, and then has no barriers: 65536 rows of 1024 202 us against
-// 206, with gate rows shared by 26 169 against 179.
-template <class F>
+// aligned row of 16-bit values without betas (`lean`, for types of which TWO holds) fits, and then has no
+// barriers: 65536 rows of 1024 202 us against 206, with gate rows shared by 26 169 against 179 (in fp32 it
+// spills: 32768 rows of 1024 349 against 219).
+template <bool TWO, class F>
 void with_bwd_slot(int C, bool lean, F&& f) {
   const int v = (C + 7) / 8;
   if (v <= 64) with_narrow_slot(v, f);
-  else if (v <= 128 && lean) f(Slot<64, 1, 2>{});
-  else if (v <= 128) f(Slot<64, 2, 1>{});
+  else if (v <= 128) {
+    if constexpr (TWO)
+      if (lean) return f(Slot<64, 1, 2>{});
+    f(Slot<64, 2, 1>{});
+  }
   else if (v <= 256) f(Slot<64, 4, 1>{});
   else if (v <= 512) f(Slot<64, 8, 1>{});
   else with_wide_slot(v, f);

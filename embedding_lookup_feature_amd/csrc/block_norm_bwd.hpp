@@ -350,7 +350,8 @@ void launch_one_bwd(const NormArgs& a, bool shared, int grid, hipStream_t st) {
 
 template <class T>
 void launch_norm_bwd(const NormArgs& a, const JoinArgs& j, bool aligned, bool lean, bool shared, int grid, hipStream_t st) {
-  with_bwd_slot(a.C, lean, [&](auto s) {
+  constexpr bool two = sizeof(typename T::S) == 2;
+  with_bwd_slot<two>(a.C, lean, [&](auto s) {
     using SL = decltype(s);
     if constexpr (SL::COLS <= kMaxAlignedCols) {
       if (lean) return launch_one_bwd<T, SL, Aligned, false>(a, shared, grid, st);
@@ -363,7 +364,7 @@ void launch_norm_bwd(const NormArgs& a, const JoinArgs& j, bool aligned, bool le
   const bool join = shared && a.dgate;
   if (!param_blocks && !join) return;
   int per = 1;
-  with_bwd_slot(a.C, lean, [&](auto s) { per = decltype(s)::PER_WG; });
+  with_bwd_slot<two>(a.C, lean, [&](auto s) { per = decltype(s)::PER_WG; });
   const int slots = grid * per, gates = join ? static_cast<int>(ceil_div(a.M, a.gate_rows)) : 0;
   const long vecs = (a.C + 7) / 8;
   // A gate row in more than 32 slots is worth a workgroup: the backward of 426062 x 128 in bf16 with a

@@ -4,6 +4,10 @@
 // The tiles of dense_tile.hpp, with two changes.  The data gradient's epilogue reads half the bytes
 // for the pre-activation.  The weight gradient takes x's codes through registers, where the
 // conversion to 16 bits applies the scale, to the LDS places that direct loads would fill.
+//
+// 65536 x 1024 x 1024 in bf16 with GELU, dropout and a skip: 355-369 us, what el_dense_bwd takes on 16-bit
+// activations (352-356), for both products (242 at the rate of a large library product) are followed by
+// their tiles' epilogues.  Unpacking both operands in front of the 16-bit kernels: 442 us.
 #include "dense_tile.hpp"
 
 namespace el {

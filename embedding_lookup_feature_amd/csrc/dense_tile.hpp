@@ -321,6 +321,7 @@ using CfgL = Cfg<256, 256, 4, 4, 2, 4, true, 1>;   // 136 KB of LDS, one workgro
 using CfgM = Cfg<128, 128, 2, 4, 2, 4, false, 2>;  // 64 KB, two of 8 wavefronts per CU
 using CfgS = Cfg<64, 64, 2, 2, 4, 2, false, 1>;    // 64 KB, two per CU
 using CfgS2 = Cfg<64, 64, 2, 2, 2, 4, false, 1>;   // 32 KB, four per CU: for codes, of which the registers hold one stage
+                                                   // (4099 x 479 x 256, fp16: 25 us; unpacked first for CfgS 27.7)
 
 // One tile (of one split): `lid` in tiles of all splits, in the order that shares panels.
 // KEPT: the data gradient's pre or the weight gradient's Q is read from 8 bits.
