@@ -174,6 +174,11 @@ def _norm_shape(norm: BlockNorm, t: torch.Tensor, name: str):
     return shape, dev
 
 
+def _query(fn, *sizes) -> int:
+    """A size query; 0 for sizes beyond the ABI's 32 bits, which it would cut."""
+    return int(fn(*sizes)) if all(0 <= s < 2**31 for s in sizes) else 0
+
+
 def block_norm_fwd(norm: BlockNorm, x, y=None, h=None, f: torch.Tensor = None, gate: torch.Tensor = None,
                    post_stats: torch.Tensor = None, pre_stats: torch.Tensor = None, stream=None):
     """y = x + scale gate (post_gamma post(f) + post_beta), h = pre_gamma pre(y) + pre_beta; x (or
@@ -196,7 +201,7 @@ def block_norm_fwd(norm: BlockNorm, x, y=None, h=None, f: torch.Tensor = None, g
 
 
 def block_norm_bwd_workspace_bytes(norm: BlockNorm, M: int) -> int:
-    return int(lib().el_block_norm_bwd_workspace_bytes(M, norm.C, norm.gate_rows))
+    return _query(lib().el_block_norm_bwd_workspace_bytes, M, norm.C, norm.gate_rows)
 
 
 def block_norm_bwd(norm: BlockNorm, y, dx, dy: torch.Tensor = None, dh: torch.Tensor = None, f: torch.Tensor = None,
@@ -326,7 +331,7 @@ def ckpt_act_dropout_bwd(dy: torch.Tensor, ckpt: Checkpoint, dx: torch.Tensor, a
 
 
 def dense_bwd_ckpt_workspace_bytes(M: int, K: int, N: int) -> int:
-    return int(lib().el_dense_bwd_ckpt_workspace_bytes(M, K, N))
+    return _query(lib().el_dense_bwd_ckpt_workspace_bytes, M, K, N)
 
 
 def dense_bwd_ckpt(x: Checkpoint, w: torch.Tensor, dz: torch.Tensor, dw: torch.Tensor, db: torch.Tensor = None,
@@ -368,7 +373,7 @@ def fp4_unpack(packed: Fp4, y: torch.Tensor, stream=None):
 
 
 def dense_fwd_fp4_workspace_bytes(M: int, K: int, N: int) -> int:
-    return int(lib().el_dense_fwd_fp4_workspace_bytes(M, K, N))
+    return _query(lib().el_dense_fwd_fp4_workspace_bytes, M, K, N)
 
 
 def dense_fwd_fp4(x: torch.Tensor, w: Fp4, bias, y: torch.Tensor, act: str = "none", residual: torch.Tensor = None,

@@ -212,3 +212,21 @@ def test_python_binding_refuses_mismatched_operands():
         bk.Checkpoint(4, 0, "cpu")
     with pytest.raises(ValueError, match="device tensor"):
         bk.Checkpoint(4, 8, "cpu")
+
+
+def test_size_queries_beyond_32_bits_are_not_cut():
+    for over in (2**31, 2**32 + 4, -1):
+        assert bk.block_norm_bwd_workspace_bytes(bk.BlockNorm(64), over) == 0
+        assert bk.dense_bwd_ckpt_workspace_bytes(over, 64, 64) == 0
+        assert bk.dense_fwd_fp4_workspace_bytes(over, 5_000, 100) == 0
+        assert bk.dense_fwd_fp4_workspace_bytes(4, over, 100) == 0
+
+
+def test_the_norms_workspace_serves_every_form():
+    """The partial sums of one workgroup at least, and with shared gates those of a slot."""
+    for C in (16, 512, 513, 600, 1024, 1025, 2048, 4096, 8192, 32768):
+        for M in (1, 5, 2_050, 65_536):
+            plain = bk.block_norm_bwd_workspace_bytes(bk.BlockNorm(C), M)
+            shared = bk.block_norm_bwd_workspace_bytes(bk.BlockNorm(C, gate_rows=3), M)
+            assert 0 < plain < shared
+            assert plain >= 4 * C * 4 and shared - plain >= 2 * C * 4
