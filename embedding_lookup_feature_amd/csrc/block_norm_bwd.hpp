@@ -10,6 +10,7 @@
 #pragma once
 
 #include "block_norm.hpp"
+#include "block_rows.hpp"
 
 namespace el {
 namespace {
@@ -29,19 +30,6 @@ __device__ inline void norm_grad(float (&g)[SL::NV][8], const float (&vh)[SL::NV
   for (int j = 0; j < SL::NV; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[j][e] = (fmaf(-vh[j][e], m2, g[j][e]) - m1) * rstd;
-}
-
-// Rows [first, first + n) of slot s where M rows are dealt out to `slots` slots in order.
-struct RowRange {
-  int first, n;
-};
-__host__ __device__ inline RowRange rows_of_slot(int s, int slots, int M) {
-  const int base = M / slots, rem = M - base * slots;
-  return RowRange{s * base + (s < rem ? s : rem), base + (s < rem)};
-}
-__device__ inline int slot_of_row(int r, int slots, int M) {
-  const int base = M / slots, rem = M - base * slots, wide = rem * (base + 1);
-  return r < wide ? r / (base + 1) : rem + (r - wide) / base;
 }
 
 // SHARED: rows share gate rows, so a slot takes a run of consecutive rows (all slots the same number
@@ -74,7 +62,9 @@ __global__ __launch_bounds__(SL::THREADS, WAVES) void k_norm_bwd(NormArgs a) {
   float g[NV][8], gsum[NV][8] = {};
   Raw8<T> rg[NV];
   int grow = 0, left = 0;  // SHARED: gate row of the current row, rows of it left in this slot's run
-  const int g0 = SHARED ? wg.first / a.gate_rows : 0, gates = SHARED ? (a.M + a.gate_rows - 1) / a.gate_rows : 0;
+  // those of the workgroup's rows (its first slot has at least one)
+  const RowRange wg_gates = SHARED ? gates_of_rows(wg.first, static_cast<long>(PER) * wg.n, a.gate_rows, a.M) : RowRange{};
+  const int g0 = wg_gates.first;
   const auto gate_values = [&]() {
     vg.settle(rg);
 #pragma unroll
@@ -91,12 +81,11 @@ __global__ __launch_bounds__(SL::THREADS, WAVES) void k_norm_bwd(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] *= g[j][e] * (1.f - g[j][e]);
   };
-  const int span_gates = SHARED ? min(gates - g0, PER * wg.n + 1) : 0;  // those of the workgroup's rows
   if constexpr (SHARED) {
     grow = mine.first / a.gate_rows;
     left = static_cast<int>(min((grow + 1l) * a.gate_rows, static_cast<long>(mine.first) + mine.n) - mine.first);
     vg.init(a.gate, a.ldg, grow - g0, c0, a.C), vdg.init(a.dgate, a.lddg, grow - g0, c0, a.C);
-    vg.load(vg.span(g0, span_gates, a.C), rg, 0, mine.n > 0);
+    vg.load(vg.span(g0, wg_gates.n, a.C), rg, 0, mine.n > 0);
     gate_values();
   } else {
     vg.init(a.gate, a.ldg, sl, c0, a.C), vdg.init(a.dgate, a.lddg, sl, c0, a.C);
@@ -185,7 +174,7 @@ __global__ __launch_bounds__(SL::THREADS, WAVES) void k_norm_bwd(NormArgs a) {
       if (a.dgate) {
         if (begins && ends) {
           through_gate(gsum);
-          vdg.store(vdg.span(g0, span_gates, a.C), gsum);
+          vdg.store(vdg.span(g0, wg_gates.n, a.C), gsum);
         } else {
 #pragma unroll
           for (int j = 0; j < NV; ++j) {
@@ -202,7 +191,7 @@ __global__ __launch_bounds__(SL::THREADS, WAVES) void k_norm_bwd(NormArgs a) {
       left = static_cast<int>(min((grow + 1l) * a.gate_rows, static_cast<long>(mine.first) + mine.n) - (row + 1));
       vg.at(grow - g0, c0, a.C), vdg.at(grow - g0, c0, a.C);
       if (left > 0) {
-        vg.load(vg.span(g0, span_gates, a.C), rg);
+        vg.load(vg.span(g0, wg_gates.n, a.C), rg);
         gate_values();
       } else {  // (an infinite gate times the zeros of a step behind this slot's last row)
 #pragma unroll

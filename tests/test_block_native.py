@@ -1,0 +1,22 @@
+"""Index arithmetic that the residual block's kernels and their launches share, on the CPU: the library's
+own headers compiled for the host with the programs in tests/native/."""
+import os
+import subprocess
+
+import pytest
+
+from tests.test_tower_sanitized import HERE, HIPCC, ROOT
+
+CSRC = os.path.join(ROOT, "embedding_lookup_feature_amd", "csrc")
+
+
+@pytest.mark.parametrize("name", ["block_rows"])
+def test_native(name, tmp_path):
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    exe = str(tmp_path / name)
+    subprocess.run([HIPCC, "-O2", "-std=c++17", "--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+                    "-Wno-unused-command-line-argument", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+                    os.path.join(HERE, "native", name + ".cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout[-3000:] + r.stderr[-1000:]
