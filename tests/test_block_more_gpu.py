@@ -26,3 +26,35 @@ def test_block_norm_shared_gates_of_more_than_2_to_the_30_rows():
     assert dgamma.item() == dbeta.item() == 2 * ones + 12
     assert torch.equal(dgate.cpu(), torch.tensor([[float(ones)], [4.0]]).bfloat16())
     assert bool((df[:-1] == 2 * dy[:-1]).all()) and df[-1].item() == 12.0
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,gr,C", [(37, 1, 64), (37, 1, 33), (40_000, 1, 24), (44, 4, 64), (44, 4, 33), (6_000, 3_000, 40),
+                                    (70_000, 70_000, 16), (3_000, 3, 1024)])
+def test_block_norm_open_and_closed_sigmoid_gates(M, gr, C, dt):
+    """dgate = s (1 - s) sum over its rows of D t and df = s D, relative to themselves, at gates from far
+    closed to far open: each in a row of its own, inside a slot's run, across two slots and across many.
+    D t is 1 in every row, so its sums are exact.
+
+    Bounds, u = 2^-24: the tail t = sigmoid(-|v|) is off by (4 + 2 |v|) u of itself (block_plain), t (1 - t)
+    by one step more and by its product with the sum, 1 - t by (5 + 2 |v|) u; below 2^-126 it may be 0."""
+    U, R = 2.0**-24, -(-M // gr)
+    v = [0.0, 1.0, 3.0, 6.0, 9.0, 12.0, 15.0, 17.0, 18.0, 25.0, 40.0, 80.0, 200.0, float("inf")]
+    v = torch.tensor(v + [-a for a in v])
+    gate = v[torch.arange(R * C) % v.numel()].view(R, C).to(DT[dt]).to(DEV)
+    ones = torch.ones((M, C), dtype=DT[dt], device=DEV)
+    df, dgate = torch.empty_like(ones), torch.empty_like(gate)
+    nm = elf.BlockNorm(C, post="none", gate_act="sigmoid", gate_rows=gr)
+    elf.block_norm_bwd(nm, None, None, dy=ones, f=ones, gate=gate, df=df, dgate=dgate)
+    w = gate.double().cpu()
+    count = torch.full((R, 1), float(gr), dtype=torch.float64)
+    count[-1] = M - (R - 1) * gr
+    f = torch.finfo(DT[dt])
+    store = lambda a: a * (f.eps / 2) * (1 + 2 * f.eps) + f.smallest_normal * f.eps / 2  # noqa: E731
+    at = 2 * w.abs().clamp(max=100.0)
+    want = torch.sigmoid(w) * torch.sigmoid(-w) * count
+    err = (dgate.cpu().double() - want).abs()
+    assert bool((err <= (7 + at) * U * want + count * 2.0**-126 + store(want)).all()), (err / want).max()
+    want = torch.sigmoid(w).repeat_interleave(gr, 0)[:M]
+    err = (df.cpu().double() - want).abs()
+    assert bool((err <= (5 + at.repeat_interleave(gr, 0)[:M]) * U * want + 2.0**-126 + store(want)).all())
