@@ -20,6 +20,7 @@ HEADER = os.path.join(os.path.dirname(ec.HERE), "include", "embblock.h")
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 GATES = {"none": 0, "sigmoid": 1}
 MICRO_BLOCK = 32
+PARAMS = ("post_gamma", "post_beta", "pre_gamma", "pre_beta")
 
 
 class ElBlockNorm(ctypes.Structure):
@@ -66,8 +67,7 @@ def header_functions():
     return re.findall(r"EL_API\s+[\w\s\*]+?\b(\w+)\s*\(", text)
 
 
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
+_current_device = torch._C._cuda_getDevice
 
 
 def _device(t: torch.Tensor, name: str) -> int:
@@ -130,7 +130,8 @@ class BlockNorm:
     """The parameters around one residual block of C columns: the norms `post` behind it ("none",
     "rms", "layer") and `pre` before the next ("rms", "layer") with their gammas and betas (fp32 [C]
     or None), the gate's activation ("none", "sigmoid"), the number of consecutive rows that share
-    one row of the gate, and the residual scale."""
+    one row of the gate, and the residual scale.  Calls read the tensors where they lie then: one whose
+    storage was replaced (same size, type and device) is followed."""
 
     def __init__(self, C: int, post: str = "none", pre: str = "rms", post_gamma: torch.Tensor = None,
                  post_beta: torch.Tensor = None, pre_gamma: torch.Tensor = None, pre_beta: torch.Tensor = None,
@@ -147,14 +148,25 @@ class BlockNorm:
             raise ValueError(f"C must be from 1 to 2^31 - 1, got {C}")
         self.C, self.gate_rows = int(C), int(gate_rows)
         self.params = (post_gamma, post_beta, pre_gamma, pre_beta)
-        names = ("post_gamma", "post_beta", "pre_gamma", "pre_beta")
-        self.device = next((_device(p, name) for p, name in zip(self.params, names) if p is not None), None)
-        for p, name in zip(self.params, names):
+        self.device = next((_device(p, name) for p, name in zip(self.params, PARAMS) if p is not None), None)
+        for p, name in zip(self.params, PARAMS):
             if p is not None and p.get_device() != self.device:
                 raise ValueError(f"{name} must be on the other parameters' device")
-        self.c = ElBlockNorm(NORMS[post], NORMS[pre], GATES[gate_act], self.gate_rows, float(scale), float(eps),
-                             *(_vec(p, name, self.C, self.device) for p, name in zip(self.params, names)))
-        self.ref = ctypes.byref(self.c)
+        self._plain = NORMS[post], NORMS[pre], GATES[gate_act], self.gate_rows, float(scale), float(eps)
+        self._bind()
+
+    def _bind(self):
+        ptrs = [_vec(p, name, self.C, self.device) for p, name in zip(self.params, PARAMS)]
+        self._ref = ctypes.byref(ElBlockNorm(*self._plain, *ptrs))
+        self._held = [(p, p.data_ptr(), p.numel()) for p in self.params if p is not None]
+
+    @property
+    def ref(self):
+        """The C structure, with the parameters' present pointers."""
+        for t, ptr, n in self._held:
+            if t.data_ptr() != ptr or t.numel() != n:
+                self._bind()
+        return self._ref
 
     def gates(self, M: int) -> int:
         """Rows of the gate for M rows."""

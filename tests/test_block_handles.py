@@ -1,0 +1,73 @@
+"""The binding's handles follow the tensors they were made of (CPU: the library is replaced by one that
+keeps what it was given): one whose storage was replaced is never read where it used to lie."""
+import gc
+
+import pytest
+import torch
+
+from embedding_lookup_feature_amd import block as bk
+from embedding_lookup_feature_amd import embcore as ec
+
+
+class KeepingLibrary:
+    """Every size query answers 0, every call succeeds and keeps its arguments."""
+
+    def __init__(self):
+        self.args = None
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_bytes"):
+            return lambda *a: 0
+
+        def call(*a):
+            self.args = a
+            return ec.EL_OK
+
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    L = KeepingLibrary()
+    monkeypatch.setattr(bk, "lib", lambda: L)
+    monkeypatch.setattr(bk, "_device", lambda t, name: t.get_device())  # host tensors stand for device -1
+    monkeypatch.setattr(bk, "_current_device", lambda: -1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
+    return L
+
+
+def norm_call(lib, nm):
+    bk.block_norm_fwd(nm, torch.zeros(4, 8), None, torch.zeros(4, 8))
+    return lib.args[0]._obj
+
+
+@pytest.mark.parametrize("name", bk.PARAMS)
+def test_block_norm_follows_its_parameters(lib, name):
+    t = torch.ones(8)
+    nm = bk.BlockNorm(8, post="rms", **{name: t})
+    assert getattr(norm_call(lib, nm), name) == t.data_ptr()
+    first = lib.args[0]._obj
+    old = t.data_ptr()
+    t.data = torch.full((8,), 2.0)
+    assert getattr(norm_call(lib, nm), name) == t.data_ptr() != old
+    assert getattr(first, name) == old, "a structure that a call may still read is not changed"
+    gc.collect()
+    assert getattr(norm_call(lib, nm), name) == t.data_ptr()
+    same = norm_call(lib, nm)
+    assert same is norm_call(lib, nm)  # nothing is built again while nothing moves
+
+
+@pytest.mark.parametrize("new", [torch.ones(7), torch.ones(9), torch.ones(8, dtype=torch.float64), torch.ones(8).half(),
+                                 torch.ones(16)[::2], torch.ones(1).expand(8)], ids=str)
+def test_block_norm_refuses_another_form_of_a_parameter(lib, new):
+    t = torch.ones(8)
+    nm = bk.BlockNorm(8, pre_gamma=t)
+    norm_call(lib, nm)
+    t.data = new
+    lib.args = None
+    for _ in range(2):
+        with pytest.raises(ValueError, match="pre_gamma must hold 8 contiguous values"):
+            norm_call(lib, nm)
+    assert lib.args is None
+    t.data = torch.ones(8)
+    assert norm_call(lib, nm).pre_gamma == t.data_ptr()

@@ -58,3 +58,16 @@ def test_block_norm_open_and_closed_sigmoid_gates(M, gr, C, dt):
     want = torch.sigmoid(w).repeat_interleave(gr, 0)[:M]
     err = (df.cpu().double() - want).abs()
     assert bool((err <= (5 + at.repeat_interleave(gr, 0)[:M]) * U * want + 2.0**-126 + store(want)).all())
+
+
+def test_block_norm_follows_a_parameter_whose_storage_was_replaced():
+    M, C = 5, 256
+    x = torch.randn((M, C), device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    gamma = torch.ones(C, device=DEV)
+    nm, h, want = elf.BlockNorm(C, pre_gamma=gamma), torch.empty_like(x), torch.empty_like(x)
+    elf.block_norm_fwd(nm, x, None, h)
+    gamma.data = torch.linspace(-2, 2, C, device=DEV)
+    junk = torch.full((C,), 77.0, device=DEV)  # (takes the old storage)
+    elf.block_norm_fwd(nm, x, None, h)
+    elf.block_norm_fwd(elf.BlockNorm(C, pre_gamma=gamma.clone()), x, None, want)
+    assert torch.equal(h, want) and bool((junk == 77.0).all())
