@@ -257,15 +257,19 @@ class _Packed:
         self._codes = torch.empty(codes, dtype=torch.uint8, device=device)
         self._scales = torch.empty(scales, dtype=torch.uint8, device=device)
         self.device = _device(self._codes, "the packed array")
-        self.ptrs = (self._codes.data_ptr(), self._scales.data_ptr()) if self.rows else (None, None)
 
     @property
+    def ptrs(self):
+        return (self._codes.data_ptr(), self._scales.data_ptr()) if self.rows else (None, None)
+
+    # (views: they share the array's memory, but giving one other storage does not take it from the array)
+    @property
     def codes(self) -> torch.Tensor:
-        return self._codes
+        return self._codes.detach()
 
     @property
     def scales(self) -> torch.Tensor:
-        return self._scales
+        return self._scales.detach()
 
     @property
     def nbytes(self) -> int:

@@ -71,3 +71,35 @@ def test_block_norm_refuses_another_form_of_a_parameter(lib, new):
     assert lib.args is None
     t.data = torch.ones(8)
     assert norm_call(lib, nm).pre_gamma == t.data_ptr()
+
+
+@pytest.mark.parametrize("kind", ["Checkpoint", "Fp4"])
+def test_packed_arrays_keep_their_memory(lib, kind):
+    p = getattr(bk, kind)(4, 40, "cpu")
+    pack = bk.ckpt_pack if kind == "Checkpoint" else bk.fp4_pack
+    pack(torch.zeros(4, 40), p)
+    first = lib.args[-3:-1]
+    assert first == (p.codes.data_ptr(), p.scales.data_ptr())
+    p.codes.fill_(7), p.scales.fill_(9)
+    assert bool((p.codes == 7).all()) and bool((p.scales == 9).all()), "written in place"
+    for name in ("codes", "scales"):
+        v = getattr(p, name)
+        v.data = torch.zeros(1, dtype=torch.uint8)  # other storage for the view
+        w = getattr(p, name)
+        w.set_(torch.zeros(1, dtype=torch.uint8))
+        with pytest.raises(AttributeError):
+            setattr(p, name, v)
+    gc.collect()
+    pack(torch.zeros(4, 40), p)
+    assert lib.args[-3:-1] == first and bool((p.codes == 7).all()) and bool((p.scales == 9).all())
+    assert p.nbytes == p.codes.numel() + p.scales.numel() > 100
+
+
+@pytest.mark.parametrize("kind", ["Checkpoint", "Fp4"])
+def test_packed_arrays_follow_storage_that_grew(lib, kind):
+    p = getattr(bk, kind)(4, 40, "cpu")
+    p.codes.fill_(7)
+    grown = p.codes
+    grown.resize_(1 << 20)  # the storage that the array shares moves
+    (bk.ckpt_pack if kind == "Checkpoint" else bk.fp4_pack)(torch.zeros(4, 40), p)
+    assert lib.args[-3] == grown.data_ptr() == p.codes.data_ptr() and bool((p.codes == 7).all())
