@@ -153,9 +153,36 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return _DTYPE[t.dtype]
 
 
-class Tables:
+class _Handle:
+    """The C structure `c` over tensors that the handle holds.  It is made again when one of them has got
+    other storage (``t.data = ...``, a module's ``to``), which needs the form that it had before."""
+
+    def _hold(self, make, **tensors):
+        """`make` gives the structure from their pointers, in order."""
+        self._make, self._tensors = make, tensors
+        self._form = {name: (t.shape, t.dtype, t.device) for name, t in tensors.items()}
+        self._bind()
+
+    def _bind(self):
+        for name, t in self._tensors.items():
+            form = shape, dtype, device = self._form[name]
+            if (t.shape, t.dtype, t.device) != form:
+                raise ValueError(f"{name} must stay {list(shape)} of {dtype} on {device}")
+        self._c = self._make(*(0 if name == "indices" and not t.numel() else _dev(t, name)
+                               for name, t in self._tensors.items()))
+        self._held = [(t, t.data_ptr(), t.numel()) for t in self._tensors.values()]
+
+    @property
+    def c(self):
+        for t, ptr, n in self._held:
+            if t.data_ptr() != ptr or t.numel() != n:
+                self._bind()
+        return self._c
+
+
+class Tables(_Handle):
     """F embedding tables in one joint [total_rows, D] buffer; table t owns rows
-    row_offset[t] .. row_offset[t+1]-1."""
+    row_offset[t] .. row_offset[t+1]-1.  Both tensors are read where they lie when a call is made."""
 
     def __init__(self, weight: torch.Tensor, row_offset: torch.Tensor, total_rows: int = None,
                  max_rows: int = None):
@@ -170,20 +197,21 @@ class Tables:
             ro = row_offset.cpu()
             max_rows = int((ro[1:] - ro[:-1]).max()) if ro.numel() > 1 else 0
         self.max_rows = int(max_rows)
-        self.c = ElTables(_dev(weight, "weight"), _dev(row_offset, "row_offset"), self.total_rows,
-                          row_offset.numel() - 1, weight.shape[1], _dtype(weight, "weight"), self.max_rows)
+        plain = (self.total_rows, row_offset.numel() - 1, weight.shape[1], _dtype(weight, "weight"), self.max_rows)
+        self._hold(lambda base, offsets: ElTables(base, offsets, *plain), weight=weight, row_offset=row_offset)
 
     @property
     def num_tables(self):
-        return self.c.num_tables
+        return self._c.num_tables
 
     @property
     def dim(self):
-        return self.c.dim
+        return self._c.dim
 
 
-class Bags:
-    """CSR lookups over F*B table-major bags (bag t*B + b)."""
+class Bags(_Handle):
+    """CSR lookups over F*B table-major bags (bag t*B + b); both tensors are read where they lie when a
+    call is made."""
 
     def __init__(self, indices: torch.Tensor, offsets: torch.Tensor, batch: int, nnz: int = None):
         if indices.dtype != torch.int32 or offsets.dtype != torch.int32:
@@ -192,8 +220,8 @@ class Bags:
         self.offsets = offsets
         self.batch = int(batch)
         self.nnz = int(indices.numel() if nnz is None else nnz)
-        ip = _dev(indices, "indices") if indices.numel() else 0
-        self.c = ElBags(ip, _dev(offsets, "offsets"), self.batch, self.nnz)
+        batch, n = self.batch, self.nnz
+        self._hold(lambda ip, op: ElBags(ip, op, batch, n), indices=indices, offsets=offsets)
 
 
 def emb_bag_fwd(tables: Tables, bags: Bags, emb_out: torch.Tensor, hash_indices=False, stream=None):
