@@ -25,7 +25,7 @@ class ElDropout(ctypes.Structure):
                 ("step", ctypes.c_void_p)]
 
 
-class Dropout:
+class Dropout(ec._Handle):
     """The mask of one dropout: keep probability 1 - p, drawn from (seed, offset, row, column).
     `step`, an int64 device tensor of one element, is added to the offset when the work runs, so
     that the replays of a captured graph draw other masks."""
@@ -34,8 +34,8 @@ class Dropout:
         if step is not None and (step.dtype != torch.int64 or step.numel() != 1):
             raise ValueError("step must be an int64 tensor of one element")
         self.step = step
-        self.c = ElDropout(float(p), int(seed) & (2**64 - 1), int(offset) & (2**64 - 1),
-                           ec._dev(step, "step") if step is not None else None)
+        plain = float(p), int(seed) & (2**64 - 1), int(offset) & (2**64 - 1)
+        self._hold(lambda at=None: ElDropout(*plain, at), **({} if step is None else {"step": step}))
 
 
 _bound = None

@@ -1,9 +1,10 @@
-"""Tables and bags follow their tensors (CPU: host tensors stand for device ones, no call is made): one
+"""Tables, bags and dropout steps follow their tensors (CPU: host tensors stand for device ones, no call is made): one
 whose storage was replaced is never read where it used to lie."""
 import pytest
 import torch
 
 from embedding_lookup_feature_amd import embcore as ec
+from embedding_lookup_feature_amd import tower as tw
 
 
 @pytest.fixture(autouse=True)
@@ -67,3 +68,19 @@ def test_fewer_indices_are_refused():
     i.data = torch.zeros(5, dtype=torch.int32)
     with pytest.raises(ValueError, match="indices must stay \\[6\\]"):
         b.c
+
+
+def test_dropout_follows_its_step():
+    step = torch.zeros(1, dtype=torch.int64)
+    d = tw.Dropout(0.25, 7, 9, step)
+    first = d.c
+    assert (first.p, first.seed, first.offset, first.step) == (0.25, 7, 9, step.data_ptr()) and d.c is first
+    step += 1
+    assert d.c is first
+    step.data = torch.zeros(1, dtype=torch.int64)
+    assert (d.c.p, d.c.seed, d.c.offset, d.c.step) == (0.25, 7, 9, step.data_ptr()) and d.c.step != first.step
+    step.data = torch.zeros(1)
+    with pytest.raises(ValueError, match="step must stay"):
+        d.c
+    none = tw.Dropout(0.25, 7)
+    assert none.c is none.c and not none.c.step
