@@ -110,7 +110,7 @@ struct PackArgs {
 // 1024 from bf16 20 us, 4.2 TB/s, and back (k_fp4_unpack) 20.
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_fp4_pack(PackArgs a) {
-  __shared__ uint8_t sc[16][4][4];  // [row][block][step]
+  __shared__ __attribute__((aligned(4))) uint8_t sc[16][4][4];  // [row][block][step], read as words
   const int groups = (a.steps + 3) / 4;
   const int64_t rows16 = blockIdx.x / groups;
   const int grp = static_cast<int>(blockIdx.x - rows16 * groups);
