@@ -55,7 +55,11 @@ struct ActArgs {
 // bits the tower's absolute 2.2e-7 is below half a step wherever the value counts.
 template <class T, int ACT>
 __device__ inline float value(float u) {
-  if constexpr (ACT == EL_ACT_GELU && T::code == EL_F32) return 0.5f * u * erfcf(-0.70710678118654752f * u);
+  if constexpr (ACT == EL_ACT_GELU && T::code == EL_F32) {
+    // (erfc(64 / sqrt 2) is 0 in fp32, and no infinity meets it; the maximum keeps NaN)
+    const float v = __builtin_elementwise_maximum(u, -64.f);
+    return 0.5f * v * erfcf(-0.70710678118654752f * v);
+  }
   return act_f<ACT>(u);
 }
 template <class T, int ACT>

@@ -71,3 +71,20 @@ def test_block_norm_follows_a_parameter_whose_storage_was_replaced():
     elf.block_norm_fwd(nm, x, None, h)
     elf.block_norm_fwd(elf.BlockNorm(C, pre_gamma=gamma.clone()), x, None, want)
     assert torch.equal(h, want) and bool((junk == 77.0).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_ckpt_activations_of_magnitudes_that_round_to_infinity(dt):
+    """fp32's largest magnitudes stand for infinities once packed (2^128): the activations' values there
+    are those of act_dropout_fwd on the kept values, GELU's 0 below."""
+    top = torch.finfo(torch.float32).max
+    x = torch.tensor([top, -top, 3.3e38, -3.3e38, -1e30, -100.0, 0.0, 1.0] * 4, device=DEV).view(1, 32)
+    ck = elf.ckpt_pack(x, elf.Checkpoint(1, 32, DEV))
+    kept = elf.ckpt_act_dropout_fwd(ck, torch.empty_like(x))
+    # (3.3e38 too: 3.3e38 / 2^120 = 248.3 lies above the middle of e4m3's 240 and 256, and 256 * 2^120 = 2^128)
+    assert bool(kept[0, 0:4:2].isposinf().all()) and bool(kept[0, 1:4:2].isneginf().all()) and bool(kept[0, 4:8].isfinite().all())
+    for act in ("relu", "gelu"):
+        y = elf.ckpt_act_dropout_fwd(ck, torch.empty((1, 32), dtype=DT[dt], device=DEV), act=act)
+        want = elf.act_dropout_fwd(kept, torch.empty_like(x), act=act).to(DT[dt])
+        assert torch.equal(y, want), (act, y[0, :8], want[0, :8])
+        assert bool(y[0, 0].isposinf()) and y[0, 1].item() == 0.0
