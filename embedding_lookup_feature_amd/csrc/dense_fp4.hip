@@ -401,7 +401,7 @@ size_t x_lds(int rows, long K) { return rows * (steps_of(K) * 64 + groups_of(K) 
 // J = 1, 2, 4: 1024 rows 6.4, 7.2, 9.6; 2048 8.0, 7.9; 4096 11.3, 10.2; 8192 21.9, 18.9, 19.4; 16384
 // 47.9, 37.2, 34.0; 65536 177, 132, 116.  Columns split for 1024 workgroups rather than 512: 4099 rows
 // 15.0 against 13.6, 16384 rows 28.6 against 27.4.
-// Two workgroups' rows must fit a CU's LDS: J = 4 holds 147 KiB at K = 4096, 16384 rows 124, J = 2 91.
+// Two workgroups' rows must fit a CU's LDS: J = 4 holds 136 KiB at K = 4096, 16384 rows 124, J = 2 91.
 // Rows are packed in the workspace first where they are long: packing in the call, the column
 // splits of few rows pack each row again.  In the call against before it, N = 1024: K = 2048, 1024
 // rows 10.1 and 10.7; K = 4096, 1 row 13.8 and 13.6, 1024 rows 23.4 and 15.8, 2048 rows 25.9 and 20.1,
