@@ -90,7 +90,8 @@ EL_API el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64
  *           column in the low half.  A block that holds a NaN or an infinity has the scale byte 255
  *           and stands for NaN altogether.
  * Magnitudes that round to 2^128 (from 2^128 (1 - 2^-5) in 8 bits, 2^128 (1 - 2^-3) in 4) stand for
- * infinity in fp32.  Columns behind the last are zeros up to the padded width Kp: whole blocks.
+ * infinity in fp32; in 8 bits, fp16's magnitudes from 63488 round to 2^16, infinity in EL_F16.
+ * Columns behind the last are zeros up to the padded width Kp: whole blocks.
  *   8 bits: codes [M][Kp], scales [M][Kp / 32], Kp = K rounded up to 32.
  *   4 bits: in the order that the matrix instructions take, rows padded with zeros to 32, Kp = K
  *           rounded up to 128 for the codes and to 512 for the scales.  Codes [M / 32][Kp / 128][2]
@@ -125,9 +126,10 @@ EL_API size_t el_dense_bwd_ckpt_workspace_bytes(int32_t M, int32_t K, int32_t N)
  * el_dense_bwd with the layer's input x and the layer below's pre-activation read from 8 bits:
  *   dw = dz^T xq,  db = sum dz,  dx = dz w + dres,  dzb = drop(dx act'(preq))
  * x_codes, x_scales, pre_codes, pre_scales: [M] rows of K columns as el_ckpt_pack writes them
- * (pre_* NULL with EL_ACT_NONE or without dzb).  xq enters the products in dtype (EL_BF16: exactly;
- * EL_F16: exactly where it was packed from EL_F16).  Everything else as in el_dense_bwd, its limits
- * and reproducibility included.
+ * (pre_* NULL with EL_ACT_NONE or without dzb).  xq enters the products in dtype: exactly where it
+ * was packed from dtype, but for EL_F16 the magnitudes that round to 2^16, as infinities; otherwise
+ * rounded (EL_BF16: magnitudes below its subnormals alone).  Everything else as in el_dense_bwd, its
+ * limits and reproducibility included.
  */
 EL_API el_status el_dense_bwd_ckpt(const uint8_t* x_codes, const uint8_t* x_scales, int32_t M, int32_t K,
                                    const void* w, int32_t N, const void* dz, int64_t lddz,

@@ -88,3 +88,26 @@ def test_ckpt_activations_of_magnitudes_that_round_to_infinity(dt):
         want = elf.act_dropout_fwd(kept, torch.empty_like(x), act=act).to(DT[dt])
         assert torch.equal(y, want), (act, y[0, :8], want[0, :8])
         assert bool(y[0, 0].isposinf()) and y[0, 1].item() == 0.0
+
+
+def test_fp16_magnitudes_that_round_to_2_to_the_16_in_8_bits():
+    """63488 lies in the middle of e4m3's 240 and 256 times 2^8 and goes to the even one: 2^16, kept as it
+    is, infinity in fp16 and nowhere else."""
+    M, K, N = 40, 64, 32
+    x = torch.ones((M, K), dtype=torch.float16, device=DEV)
+    x[3, 5], x[3, 6], x[7, 40], x[9, 33] = 63488.0, 63456.0, -65504.0, 61440.0
+    ck = elf.ckpt_pack(x, elf.Checkpoint(M, K, DEV))
+    y = elf.ckpt_act_dropout_fwd(ck, torch.empty((M, K), device=DEV))
+    assert y[3, 5:7].tolist() == [65536.0, 61440.0] and y[7, 40].item() == -65536.0 and y[9, 33].item() == 61440.0
+    for dt in (torch.float16, torch.bfloat16):
+        y = elf.ckpt_act_dropout_fwd(ck, torch.empty((M, K), dtype=dt, device=DEV))
+        w, dz = torch.zeros((N, K), dtype=dt, device=DEV), torch.full((M, N), 2.0**-6, dtype=dt, device=DEV)
+        dw = torch.empty((N, K), device=DEV)
+        elf.dense_bwd_ckpt(ck, w, dz, dw)
+        inf = dt is torch.float16
+        assert y.isinf().nonzero().tolist() == ([[3, 5], [7, 40]] if inf else [])
+        cols = sorted(set(torch.isinf(dw).nonzero()[:, 1].tolist()))
+        assert cols == ([5, 40] if inf else []) and not bool(dw.isnan().any())
+        if not inf:
+            # row 3's block has the scale 2^8, so its ones are kept as 1, as all are: 2^-6 (39 + 2^16)
+            assert bool((dw[:, 5] == (39 + 65536.0) / 64).all()) and bool((dw[:, 40] == (39 - 65536.0) / 64).all())
