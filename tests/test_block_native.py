@@ -10,7 +10,7 @@ from tests.test_tower_sanitized import HERE, HIPCC, ROOT
 CSRC = os.path.join(ROOT, "embedding_lookup_feature_amd", "csrc")
 
 
-@pytest.mark.parametrize("name", ["block_rows"])
+@pytest.mark.parametrize("name", ["block_rows", "fp4_plan"])
 def test_native(name, tmp_path):
     if not os.path.exists(HIPCC):
         pytest.skip("hipcc not available")
