@@ -4,7 +4,10 @@ import pytest
 import torch
 
 import embedding_lookup_feature_amd as elf
-from tests.test_tower_gpu import DEV, DT
+from tests import block_plain as bp
+from tests import tower_plain as tp
+from tests.test_block_gpu import norm_case
+from tests.test_tower_gpu import DEV, DT, gap_untouched, np64, out
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +114,111 @@ def test_fp16_magnitudes_that_round_to_2_to_the_16_in_8_bits():
         if not inf:
             # row 3's block has the scale 2^8, so its ones are kept as 1, as all are: 2^-6 (39 + 2^16)
             assert bool((dw[:, 5] == (39 + 65536.0) / 64).all()) and bool((dw[:, 40] == (39 - 65536.0) / 64).all())
+
+
+# ------------------------------------------------------------------------- sums over rows, exactly
+def whole(g, m, n, ld, dt, lo=-2, hi=2):
+    """Whole numbers in columns of rows ld wide, NaN behind them."""
+    full = torch.full((m, ld), float("nan"), dtype=DT[dt], device=DEV)
+    full[:, :n] = torch.randint(lo, hi + 1, (m, n), device=DEV, generator=g).to(DT[dt])
+    return full[:, :n]
+
+
+EXACT = [
+    # M, C, extra columns, dtype, gate_rows (None: no gate), betas
+    # a gate row to each row, several rows to a slot, the last step cut
+    (40_001, 128, 0, "bf16", 1, False), (40_001, 128, 0, "bf16", 1, True), (10_007, 479, 2, "f16", 1, True),
+    (10_007, 479, 1, "f16", 1, False), (7_001, 512, 0, "f32", 1, True), (7_001, 512, 0, "f32", 1, False),
+    (200_003, 16, 0, "bf16", 1, True), (200_003, 16, 0, "f32", None, False), (200_003, 13, 0, "bf16", None, True),
+    (60_001, 64, 0, "f16", None, False), (30_011, 200, 0, "bf16", 1, True), (20_011, 256, 8, "f32", None, True),
+    (9_001, 1024, 0, "bf16", 1, False), (9_001, 1024, 0, "bf16", 1, True), (9_001, 1000, 0, "f32", 1, False),
+    (5_003, 2048, 0, "bf16", 1, True), (3_001, 4096, 0, "f16", 1, False), (2_003, 8192, 0, "bf16", None, True),
+    (1_201, 16_384, 0, "bf16", 1, True), (700, 32_768, 0, "f16", None, False),
+    # gate rows shared: within a slot's run, across slots, across very many
+    (70_001, 16, 0, "f32", 26, True), (70_000, 24, 1, "bf16", 26, True), (30_000, 128, 0, "f16", 29_999, True),
+    (40_000, 64, 0, "f32", 40_000, True), (100_003, 8, 0, "bf16", 2, True), (426_062, 128, 0, "bf16", 26, False),
+    (65_536, 16, 0, "bf16", 65_536, False), (300_000, 40, 0, "f32", 7, True), (9_001, 1000, 0, "bf16", 50, True),
+    (9_001, 1024, 0, "bf16", 3, False), (9_001, 1024, 0, "f16", 9_001, False), (5_003, 4096, 0, "bf16", 11, True),
+    (2_003, 8200, 0, "f16", 5, True), (30_001, 1001, 0, "bf16", 21, True), (100_003, 32, 0, "f32", 500, False),
+]
+
+
+@pytest.mark.parametrize("case", EXACT, ids=lambda c: "-".join(map(str, c)))
+def test_block_norm_sums_over_rows_are_exact(case):
+    """Whole numbers so small that no sum passes 2^24: every order of additions gives the same bits, and a
+    row that is dropped or taken twice shows.  (At most 24 a term, for 426062 rows 1.03e7.)"""
+    M, C, ex, dt, gr, beta = case
+    g = torch.Generator(DEV).manual_seed(M + C)
+    R, ld = -(-M // (gr or 1)), C + ex
+    dy, dh, y, f = (whole(g, M, C, ld, dt) for _ in range(4))
+    gate = whole(g, R, C, ld, dt, -1, 2) if gr else None
+    gp, gq = (torch.randint(1, 3, (C,), device=DEV, generator=g).float() for _ in range(2))
+    bp, bq = ((torch.randint(-2, 3, (C,), device=DEV, generator=g).float() for _ in range(2)) if beta else (None, None))
+    nm = elf.BlockNorm(C, "none", "rms", gp, bp, gq, bq, "none", gr or 1, 2.0)
+    new = lambda r: torch.full((r, ld), float("nan"), dtype=DT[dt], device=DEV)[:, :C]  # noqa: E731
+    vec = lambda: torch.full((C,), float("nan"), device=DEV)  # noqa: E731
+    dx, df, dgate, g_post, b_post, g_pre, b_pre = new(M), new(M), new(R) if gr else None, vec(), vec(), vec(), vec()
+    betas = dict(dpost_beta=b_post) if beta else {}
+    elf.block_norm_bwd(nm, None, dx, dy=dy, f=f, gate=gate, df=df, dgate=dgate, dpost_gamma=g_post, **betas)
+    D = dy.double()
+    t = f.double() * gp + (bp if beta else 0.0)
+    rows = torch.arange(M, device=DEV) // (gr or 1)
+    u = 2.0 * D * (gate.double()[rows] if gr else 1.0)
+    assert torch.equal(dx, dy) and torch.equal(df.double(), u * gp)
+    assert torch.equal(g_post.double(), (u * f.double()).sum(0))
+    if beta:
+        assert torch.equal(b_post.double(), u.sum(0))
+    if gr:
+        want = torch.zeros((R, C), dtype=torch.float64, device=DEV).index_add_(0, rows, 2.0 * D * t)
+        assert float(want.abs().max()) < 2**24
+        assert torch.equal(dgate, want.float().to(DT[dt]))
+    del D, t, u, rows
+    # the pre norm's gradients: statistics (0, 1) make its output the stored y
+    st = torch.tensor([0.0, 1.0], device=DEV).repeat(M, 1)
+    betas = dict(dpre_beta=b_pre) if beta else {}
+    elf.block_norm_bwd(nm, y, None, dh=dh, pre_stats=st, dpre_gamma=g_pre, **betas)
+    want_g, want_b = (dh.double() * y.double()).sum(0), dh.double().sum(0)
+    assert torch.equal(g_pre.double(), want_g) and (not beta or torch.equal(b_pre.double(), want_b))
+    # all at once
+    g2, b2 = vec(), vec()
+    betas = dict(dpre_beta=b2, dpost_beta=vec()) if beta else {}
+    elf.block_norm_bwd(nm, y, dx, dy=dy, dh=dh, f=f, gate=gate, df=df, dgate=dgate, pre_stats=st, dpre_gamma=g2,
+                       dpost_gamma=vec(), **betas)
+    assert torch.equal(g2.double(), want_g) and (not beta or torch.equal(b2.double(), want_b))
+    assert ex == 0 or all(bool(torch.isnan(torch.as_strided(v, (v.shape[0], ex), (ld, 1), C).float()).all())
+                          for v in (dx, df, dgate) if v is not None)
+
+
+MANY = [(40_001, 128, 128, "bf16", 1, True), (40_001, 128, 128, "f16", 1, False), (10_007, 479, 481, "f16", 1, True),
+        (7_001, 512, 512, "f32", 1, True), (200_003, 16, 16, "f32", 1, False), (200_003, 16, 17, "bf16", None, True),
+        (9_001, 1024, 1024, "bf16", 1, False)]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(map(str, c)))
+def test_block_norm_many_rows_to_a_slot(case):
+    """A gate row to each row (or none) and several rows to a slot, so that the next rows are on their way
+    while one is worked on: every row's outputs against the 64-bit form."""
+    M, C, ld, dt, gr, beta = case
+    t, nm, act = norm_case((M, C, ld, 0, dt, "layer", "rms", "sigmoid" if gr else None, 1, 0.5, beta, 0.1))
+    y, h, dx, df = (out(M, C, ld, dt) for _ in range(4))
+    dg = out(M, C, ld, dt) if gr else None
+    ps, qs = torch.empty((M, 2), device=DEV), torch.empty((M, 2), device=DEV)
+    g = [torch.full((C,), float("nan"), device=DEV) for _ in range(4)]
+    elf.block_norm_fwd(nm, t["x"], y, h, f=t["f"], gate=t["gate"], post_stats=ps, pre_stats=qs)
+    kw = dict(dpost_beta=g[1], dpre_beta=g[3]) if beta else {}
+    elf.block_norm_bwd(nm, y, dx, dy=t["dy"], dh=t["dh"], f=t["f"], gate=t["gate"], df=df, dgate=dg, post_stats=ps,
+                       pre_stats=qs, dpost_gamma=g[0], dpre_gamma=g[2], **kw)
+    n = {k: np64(v) for k, v in t.items()}
+    args = (n["gp"], n["bp"], n["gq"], n["bq"], act, 1, 0.5)
+    ref = bp.block_norm_fwd(n["x"], n["f"], n["gate"], "layer", "rms", *args, np.float64(np.float32(0.1)), DT[dt])
+    tp.check(y, ref["y"], "y")
+    tp.check(h, ref["h"], "h")
+    tp.check(ps, ref["post_stats"], "post_stats")
+    tp.check(qs, ref["pre_stats"], "pre_stats")
+    ref = bp.block_norm_bwd(n["dy"], n["dh"], np64(y), n["f"], n["gate"], "layer", "rms", *args, np64(ps), np64(qs), DT[dt])
+    got = dict(dx=dx, df=df, dpost_gamma=g[0], dpre_gamma=g[2])
+    got.update(dict(dpost_beta=g[1], dpre_beta=g[3]) if beta else {})
+    got.update(dict(dgate=dg) if gr else {})
+    for k, v in got.items():
+        tp.check(v, ref[k], k)
+    assert all(gap_untouched(v) for v in (y, h, dx, df, dg) if v is not None)
