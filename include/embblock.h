@@ -68,8 +68,11 @@ EL_API size_t el_block_norm_bwd_workspace_bytes(int32_t M, int32_t C, int32_t ga
  *   dpre_gamma  = sum_m dh yh,  dpre_beta  = sum_m dh       (fp32 [C], overwritten)
  *   dpost_gamma = sum_m u fh,   dpost_beta = sum_m u        (fp32 [C], overwritten)
  * dy or dh may be NULL (0), not both; dh NULL: y and pre_stats are not needed.  Every output may be
- * NULL; df, dgate and the dpost_* need f (and the gate for dgate); dpre_* need dh.  Sums over rows
- * are added in a fixed order.  workspace: >= el_block_norm_bwd_workspace_bytes, 256-byte aligned.
+ * NULL; df, dgate and the dpost_* need f (and the gate for dgate); dpre_* need dh.  Sums are added in
+ * a fixed order, which depends on the sizes, on gate_rows with a gate, on whether every row is 16-byte
+ * aligned and on whether post_beta is given or a beta's gradient asked for (the other outputs may be
+ * asked for one at a time or together).  workspace: >= el_block_norm_bwd_workspace_bytes, 256-byte
+ * aligned.
  */
 EL_API el_status el_block_norm_bwd(const el_block_norm* p, const void* dy, int64_t lddy, const void* dh,
                                    int64_t lddh, const void* y, int64_t ldy, const void* f, int64_t ldf,

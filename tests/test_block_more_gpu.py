@@ -222,3 +222,29 @@ def test_block_norm_many_rows_to_a_slot(case):
     for k, v in got.items():
         tp.check(v, ref[k], k)
     assert all(gap_untouched(v) for v in (y, h, dx, df, dg) if v is not None)
+
+
+@pytest.mark.parametrize("gr", [1, 26])
+@pytest.mark.parametrize("M,C,dt", [(9_001, 1024, "bf16"), (9_001, 640, "f16"), (3_001, 1024, "f32"), (20_011, 256, "bf16")])
+def test_block_norm_outputs_together_and_one_at_a_time(M, C, dt, gr):
+    """A norm without betas: its outputs have the same bits in whatever company, as long as no beta's
+    gradient is asked for; and again with one (another slot for 513 to 1024 columns in 16 bits)."""
+    t, nm, act = norm_case((M, C, C, 0, dt, "rms", "layer", "sigmoid", gr, 0.5, False, 0.1))
+    new = lambda r=M: torch.full((r, C), float("nan"), dtype=DT[dt], device=DEV)  # noqa: E731
+    vec = lambda: torch.full((C,), float("nan"), device=DEV)  # noqa: E731
+    y, h, ps, qs = new(), new(), torch.empty((M, 2), device=DEV), torch.empty((M, 2), device=DEV)
+    elf.block_norm_fwd(nm, t["x"], y, h, f=t["f"], gate=t["gate"], post_stats=ps, pre_stats=qs)
+    make = dict(dx=new, df=new, dgate=lambda: new(-(-M // gr)), dpost_gamma=vec, dpre_gamma=vec)
+
+    def run(names, **more):
+        o = {k: make[k]() for k in names}
+        elf.block_norm_bwd(nm, y, o.get("dx"), dy=t["dy"], dh=t["dh"], f=t["f"], gate=t["gate"], post_stats=ps, pre_stats=qs,
+                           **{k: v for k, v in o.items() if k != "dx"}, **more)
+        return o
+
+    for more in ((), ("dpre_beta",), ("dpost_beta", "dpre_beta")):
+        betas = lambda: {k: vec() for k in more}  # noqa: E731
+        full = run(make, **betas())
+        assert all(bool(torch.isfinite(v).all()) for v in full.values())
+        for k in make:
+            assert torch.equal(run([k], **betas())[k], full[k]), (k, more)
