@@ -114,6 +114,12 @@ def _vec(t, name: str, n: int, dev: int):
     return t.data_ptr()
 
 
+def _drop(dropout, dev: int):
+    if dropout is not None and dropout.step is not None and dropout.step.get_device() != dev:
+        raise ValueError(f"the dropout's step must be on device {dev}, got {dropout.step.device}")
+    return tw._drop(dropout)
+
+
 def _workspace(ws, need, like: torch.Tensor, dev: int, stream):
     """(pointer, bytes, the tensor that holds them); `need` is asked where none is given."""
     if ws is None:
@@ -331,7 +337,7 @@ def ckpt_pack(x: torch.Tensor, ckpt: Checkpoint, stream=None) -> Checkpoint:
 def ckpt_act_dropout_fwd(ckpt: Checkpoint, y: torch.Tensor, act: str = "none", dropout=None, stream=None):
     """y = drop(act(kept values)): what act_dropout_fwd gives on them; with neither, the kept values."""
     (M, K), dev, (yp, ldy), (codes, scales) = _with_packed(y, "y", ckpt, Checkpoint, "ckpt")
-    _launch(lib().el_ckpt_act_dropout_fwd, dev, stream, codes, scales, M, K, tw._act(act), tw._drop(dropout), yp, ldy,
+    _launch(lib().el_ckpt_act_dropout_fwd, dev, stream, codes, scales, M, K, tw._act(act), _drop(dropout, dev), yp, ldy,
             ec._dtype(y, "y"))
     return y
 
@@ -341,7 +347,7 @@ def ckpt_act_dropout_bwd(dy: torch.Tensor, ckpt: Checkpoint, dx: torch.Tensor, a
     """dx = drop(dy * act'(kept values)), the mask of the forward with the same dropout."""
     shape, dev, (dp, lddy), (codes, scales) = _with_packed(dy, "dy", ckpt, Checkpoint, "ckpt")
     op, lddx = _mat(dx, "dx", shape, dy.dtype, dev)
-    _launch(lib().el_ckpt_act_dropout_bwd, dev, stream, dp, lddy, codes, scales, *shape, tw._act(act), tw._drop(dropout),
+    _launch(lib().el_ckpt_act_dropout_bwd, dev, stream, dp, lddy, codes, scales, *shape, tw._act(act), _drop(dropout, dev),
             op, lddx, ec._dtype(dy, "dy"))
     return dx
 
@@ -369,7 +375,7 @@ def dense_bwd_ckpt(x: Checkpoint, w: torch.Tensor, dz: torch.Tensor, dw: torch.T
     bp, ldb = _mat(dzb, "dzb", (M, K), dt, dev)
     wsp, wsn, keep = _workspace(workspace, lambda: dense_bwd_ckpt_workspace_bytes(M, K, N), dz, dev, stream)
     _launch(lib().el_dense_bwd_ckpt, dev, stream, xc, xs, M, K, w.data_ptr(), N, zp, ldz, rp, ldr, dxp, lddx,
-            tw._act(act), tw._drop(dropout), pc, ps, bp, ldb, _vec(dw, "dw", N * K, dev), _vec(db, "db", N, dev),
+            tw._act(act), _drop(dropout, dev), pc, ps, bp, ldb, _vec(dw, "dw", N * K, dev), _vec(db, "db", N, dev),
             ec._dtype(dz, "dz"), wsp, wsn)
     return dx, dw, db
 

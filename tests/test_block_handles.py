@@ -103,3 +103,25 @@ def test_packed_arrays_follow_storage_that_grew(lib, kind):
     grown.resize_(1 << 20)  # the storage that the array shares moves
     (bk.ckpt_pack if kind == "Checkpoint" else bk.fp4_pack)(torch.zeros(4, 40), p)
     assert lib.args[-3] == grown.data_ptr() == p.codes.data_ptr() and bool((p.codes == 7).all())
+
+
+def test_a_dropout_step_on_another_device_is_refused(lib):
+    class Elsewhere:  # a tensor on device 1, beside host tensors that stand for device -1
+        device = "cuda:1"
+
+        def get_device(self):
+            return 1
+
+    d = bk.tw.Dropout(0.5, 1)
+    ck, z = bk.Checkpoint(4, 8, "cpu"), torch.zeros(4, 8, dtype=torch.bfloat16)
+    w, dw = torch.zeros(8, 8, dtype=torch.bfloat16), torch.zeros(8, 8)
+    calls = [lambda: bk.ckpt_act_dropout_fwd(ck, z, dropout=d), lambda: bk.ckpt_act_dropout_bwd(z, ck, z.clone(), dropout=d),
+             lambda: bk.dense_bwd_ckpt(ck, w, z, dw, dx=z.clone(), dzb=z.clone(), dropout=d)]
+    for call in calls:
+        d.step, lib.args = None, None
+        call()
+        assert lib.args is not None
+        d.step, lib.args = Elsewhere(), None
+        with pytest.raises(ValueError, match="step must be on device -1, got cuda:1"):
+            call()
+        assert lib.args is None
