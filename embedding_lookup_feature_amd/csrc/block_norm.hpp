@@ -11,8 +11,8 @@
 // nothing, without a branch, so the number of loads and stores in flight is known at every wait (they
 // share one in-order counter) and the next rows' loads stay in flight behind this row's arithmetic
 // and stores.  The loose view takes any alignment, width and stride with a branch around each access.
-// 65536 x 1024 in bf16, forward and backward: 120 and 201 us through aligned views, 135 and 226 at odd
-// addresses; 426062 x 128: 99 and 167, 149 and 236.
+// 65536 x 1024 in bf16, forward and backward: 120 and 201 us through aligned views, 143 and 237 at odd
+// addresses; 426062 x 128: 101 and 165, 149 and 235.
 #pragma once
 
 #include <algorithm>
@@ -299,7 +299,7 @@ void with_slot(int C, F&& f) {
 }
 // The backward's: one vector a lane as far as possible, for the parameters' sums stay in registers
 // beside the row (65536 rows of 1024 in bf16 with betas: two vectors a lane spill, 386 us, two
-// wavefronts a row take 211; 16384 rows of 4096: 286 and 194).  Only a wavefront with two vectors of an
+// wavefronts a row take 211; 16384 rows of 4096: 286 and 187).  Only a wavefront with two vectors of an
 // aligned row of 16-bit values without betas (`lean`, for types of which TWO holds) fits, and then has no
 // barriers: 65536 rows of 1024 202 us against 206, with gate rows shared by 26 169 against 179 (in fp32 it
 // spills: 32768 rows of 1024 349 against 219).
@@ -320,8 +320,8 @@ template <class SL>
 constexpr bool kLeanOnly = SL::W == 1 && SL::NV == 2;
 // Wavefronts a SIMD that the backward's registers leave room for.  Eight to a row: one workgroup a CU
 // (with two, 128 registers a lane, 16384 rows of 4096 with betas spill: 447 us).  Loose rows with shared
-// gates (FULL) spill at three: 30000 rows of 1001 228 us against 124; without shared gates three are
-// better, 124 against 147.
+// gates (FULL) spill at three: 30000 rows of 1001 228 us against 122; without shared gates three are
+// better, 128 against 147.
 template <class SL, bool FULL>
 constexpr int kBwdWaves = SL::W == 16 ? 4 : SL::W == 8 || SL::NV == 2 || FULL ? 2 : 3;
 

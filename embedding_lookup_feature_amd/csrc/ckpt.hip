@@ -2,8 +2,8 @@
 // dropout and its gradient computed from them.
 //
 // Packing is bound by memory: 65536 x 1024 from bf16 41 us, 4.9 TB/s.  The activation is bound by
-// instructions: with GELU and dropout the vector units are busy for 92 % of the forward's 61 us (3.3 TB/s)
-// and 88 % of the backward's 76, some 260 and 310 issue slots of four cycles for eight values.  Twenty
+// instructions: with GELU and dropout the vector units are busy for 90 % of the forward's 61 us (3.3 TB/s)
+// and 88 % of the backward's 75, some 260 and 310 issue slots of four cycles for eight values.  Twenty
 // 64-bit products and twenty exclusive ors make the mask's number (the products, the reciprocals and the
 // exponentials take four slots each); the conversions apply the scales, two values at a time.
 // Two vectors a thread: no faster.
