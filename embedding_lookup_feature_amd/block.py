@@ -174,6 +174,10 @@ class BlockNorm:
                 self._bind()
         return self._ref
 
+    @property
+    def c(self) -> ElBlockNorm:
+        return self.ref._obj
+
     def gates(self, M: int) -> int:
         """Rows of the gate for M rows."""
         return -(-M // self.gate_rows)

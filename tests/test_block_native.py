@@ -5,8 +5,9 @@ import subprocess
 
 import pytest
 
-from tests.test_tower_sanitized import HERE, HIPCC, ROOT
-
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CSRC = os.path.join(ROOT, "embedding_lookup_feature_amd", "csrc")
 
 
