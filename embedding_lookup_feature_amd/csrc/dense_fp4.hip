@@ -331,7 +331,12 @@ __global__ __launch_bounds__(kThreads, J == 4 ? 3 : 4) void k_dense_fp4(DenseArg
       float v[8], f[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = acc[0][j][e] + bias[e], v[4 + e] = acc[1][j][e] + bias[4 + e];
-      act8(a.act, v);
+      if (a.act == EL_ACT_RELU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __builtin_elementwise_maximum(v[e], 0.f);  // (keeps the NaN of NaN blocks)
+      } else {
+        act8(a.act, v);
+      }
       if constexpr (ADD) {
         Raw8<T> mine = add[j];
         if (EIGHT && cut) settle8<T>(mine, cm, a.N);

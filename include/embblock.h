@@ -111,8 +111,8 @@ EL_API el_status el_ckpt_pack(const void* x, int64_t ldx, int32_t M, int32_t K, 
 
 /* From a kept activation xq, y = drop(act(xq)) (the forward's output computed again; with
  * EL_ACT_NONE and no dropout the kept values themselves) and its gradient dx = drop(dy act'(xq)),
- * the masks of el_act_dropout_fwd / _bwd.  ReLU'(0) = 0.  GELU for EL_F32 is accurate relative to
- * its value, also in the negative tail. */
+ * the masks of el_act_dropout_fwd / _bwd.  ReLU'(0) = 0 and ReLU(NaN) = 0, as theirs (an infinity is
+ * kept as NaN).  GELU for EL_F32 is accurate relative to its value, also in the negative tail. */
 EL_API el_status el_ckpt_act_dropout_fwd(const uint8_t* codes, const uint8_t* scales, int32_t M, int32_t K,
                                          uint32_t act, const el_dropout* drop, void* y, int64_t ldy,
                                          el_dtype dtype, hipStream_t stream);
@@ -160,7 +160,7 @@ EL_API size_t el_dense_fwd_fp4_workspace_bytes(int32_t M, int32_t K, int32_t N);
  * what el_fp4_pack makes of it); w_codes, w_scales: [N] rows of K columns from el_fp4_pack; bias:
  * fp32 [N] or NULL; residual (or NULL), y: rows of strides ldr, ldy, of dtype.  Products of 4-bit
  * numbers are exact and accumulate in fp32 (block-scaled MFMA); one rounding.  A NaN block makes
- * every output of its row (of x) or column (of w) NaN.  N, K <= 2^20, N K < 2^29 and
+ * every output of its row (of x) or column (of w) NaN, under every activation.  N, K <= 2^20, N K < 2^29 and
  * ceil(M/256) ceil(N/256) < 2^21 (EL_ERR_UNSUPPORTED beyond).  workspace: >=
  * el_dense_fwd_fp4_workspace_bytes(M, K, N), 256-byte aligned (NULL when that is 0).
  */

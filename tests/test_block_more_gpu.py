@@ -248,3 +248,26 @@ def test_block_norm_outputs_together_and_one_at_a_time(M, C, dt, gr):
         assert all(bool(torch.isfinite(v).all()) for v in full.values())
         for k in make:
             assert torch.equal(run([k], **betas())[k], full[k]), (k, more)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("M,K", [(5, 300), (2_100, 300), (8_200, 300), (40, 4_200)])
+def test_dense_fwd_fp4_nan_blocks_under_every_activation(M, K, act):
+    """A NaN block of x or w reaches every output of its row or column, rows packed within the call and
+    before it, with a residual and without."""
+    N = 70
+    g = torch.Generator(DEV).manual_seed(M)
+    x, w = torch.randn((M, K), device=DEV, generator=g).bfloat16(), torch.randn((N, K), device=DEV, generator=g).bfloat16()
+    r = torch.randn((M, N), device=DEV, generator=g).bfloat16()
+    clean = elf.fp4_pack(w, elf.Fp4(N, K, DEV))
+    w2, x2 = w.clone(), x.clone()
+    x2[2, K - 10], x2[M - 1, 0], w2[7, 3] = float("nan"), float("-inf"), float("inf")
+    w4 = elf.fp4_pack(w2, elf.Fp4(N, K, DEV))
+    bad = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+    bad[2], bad[M - 1], bad[:, 7] = True, True, True
+    for res in (None, r):
+        y, want = torch.empty((M, N), dtype=torch.bfloat16, device=DEV), torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+        elf.dense_fwd_fp4(x2, w4, None, y, act=act, residual=res)
+        elf.dense_fwd_fp4(x, clean, None, want, act=act, residual=res)
+        assert torch.equal(torch.isnan(y), bad)
+        assert torch.equal(y[~bad], want[~bad])
