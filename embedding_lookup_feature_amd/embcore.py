@@ -187,18 +187,25 @@ class Tables(_Handle):
     def __init__(self, weight: torch.Tensor, row_offset: torch.Tensor, total_rows: int = None,
                  max_rows: int = None):
         """max_rows: rows of the largest table; None reads it from row_offset (one copy to the
-        host, here and not per call), 0 leaves it unknown."""
+        host, here and when its storage was replaced, not per call), 0 leaves it unknown."""
         if weight.dim() != 2 or row_offset.dtype != torch.int64 or row_offset.dim() != 1:
             raise ValueError("weight must be [total_rows, D]; row_offset int64 [F+1]")
         self.weight = weight
         self.row_offset = row_offset
         self.total_rows = int(weight.shape[0] if total_rows is None else total_rows)
-        if max_rows is None:
-            ro = row_offset.cpu()
-            max_rows = int((ro[1:] - ro[:-1]).max()) if ro.numel() > 1 else 0
-        self.max_rows = int(max_rows)
-        plain = (self.total_rows, row_offset.numel() - 1, weight.shape[1], _dtype(weight, "weight"), self.max_rows)
-        self._hold(lambda base, offsets: ElTables(base, offsets, *plain), weight=weight, row_offset=row_offset)
+        self.max_rows = 0 if max_rows is None else int(max_rows)
+        plain = (self.total_rows, row_offset.numel() - 1, weight.shape[1], _dtype(weight, "weight"))
+        read_at = None
+
+        def make(base, offsets):
+            nonlocal read_at
+            if max_rows is None and offsets != read_at:
+                ro = row_offset.cpu()
+                self.max_rows = int((ro[1:] - ro[:-1]).max()) if ro.numel() > 1 else 0
+                read_at = offsets
+            return ElTables(base, offsets, *plain, self.max_rows)
+
+        self._hold(make, weight=weight, row_offset=row_offset)
 
     @property
     def num_tables(self):

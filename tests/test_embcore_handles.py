@@ -84,3 +84,15 @@ def test_dropout_follows_its_step():
         d.c
     none = tw.Dropout(0.25, 7)
     assert none.c is none.c and not none.c.step
+
+
+def test_tables_read_the_largest_table_again_where_row_offset_moved():
+    w, ro, t = tables()
+    assert t.c.max_rows == t.max_rows == 6
+    w.data = torch.ones(10, 8)
+    assert t.c.max_rows == 6
+    ro.data = torch.tensor([0, 1, 10])
+    assert t.c.max_rows == t.max_rows == 9
+    given = ec.Tables(w, ro, max_rows=10)
+    ro.data = torch.tensor([0, 5, 10])
+    assert given.c.max_rows == given.max_rows == 10 and t.c.max_rows == 5
